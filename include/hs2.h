@@ -267,6 +267,119 @@ hs2_status hs2_hier_reindex(hs2_idx_mode mode, const void* q_idx, const float* w
                             void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * Rows into and out of a paged cache, for prompts and single tokens.
+ * A call covers a ragged batch: row_start is int32 [batch + 1] (device), ascending from
+ * row_start[0] >= 0; rows [row_start[b], row_start[b+1]) of the packed row arrays belong to
+ * sequence b and are its LAST n_b = row_start[b+1] - row_start[b] positions, t_b - n_b ..
+ * t_b - 1 with t_b = seq_len[b] (already counting them; n_b = 0 is a sequence that takes no
+ * part, whatever its length and table). n_rows is the number of rows the arrays hold; rows
+ * outside [row_start[0], row_start[batch]) are neither read nor written.
+ * k_rows, v_rows: [n_rows][Hkv][d] of row_dtype (HS2_F32 or HS2_BF16), token r at
+ *   r * row_stride elements (row_stride >= Hkv * d: slices of a fused projection's output
+ *   fit), 16-byte aligned, row_stride * sizeof(element) a multiple of 16. v_rows is ignored
+ *   for a key-only cache (kv->v = NULL).
+ *
+ * hs2_kv_write stores the rows in the cache's type:
+ *   F32 / BF16: the value, rounded to nearest even where bfloat16 is narrower.
+ *   FP8: code = E4M3(x / S), S = scale[page][g], nearest even, saturating at +-448; NaN is NaN.
+ *   FP4: per group of 16 channels the scale s = the smallest E4M3 value with 6 s S >= max|x|
+ *     (448 where none is), then code = E2M1(x / (s S)), nearest even, saturating at +-6. A
+ *     group holding a NaN stores s = NaN, i.e. all its 16 values read as NaN.
+ *   Every code is the one exact arithmetic gives. k_scale / v_scale (one per page and KV
+ *   head) are inputs: they are set before rows are written and apply to a page's older rows
+ *   too. S outside [2^-60, 2^60] (or NaN): HS2_DEV_BAD_PAGE, the row is not written.
+ *   The pages written must belong to their sequence alone.
+ * hs2_kv_read writes the values those positions stand for to k_rows / v_rows (FP8 / FP4:
+ *   code * scales in float32, rounded once; then to bfloat16 where that is row_dtype).
+ * Device-side: t_b beyond max_pages * page_size, n_b > t_b or a descending row_start sets
+ *   HS2_DEV_BAD_LENGTH, a table entry outside [0, num_pages) HS2_DEV_BAD_PAGE; such rows are
+ *   left as they were (in the cache, or in k_rows / v_rows). */
+hs2_status hs2_kv_write(const hs2_kv* kv, const void* k_rows, const void* v_rows, hs2_dtype row_dtype,
+                        int64_t row_stride, const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream);
+hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype row_dtype, int64_t row_stride,
+                       const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of a ragged batch of query chunks over the cache: a prompt chunk, draft tokens
+ * under verification, single tokens, or any mixture ([HS2] §8: prompt rows pass through the
+ * Self-Decoder's FA and sliding-window layers, which select nothing). Rows are laid out as
+ * in hs2_kv_write: q is [n_rows][Hq][d] (bf16; float32 with an F32 cache), row r of sequence
+ * b is its position p = t_b - n_b + (r - row_start[b]), whose key is already in the cache.
+ * Head h of KV head g attends to the keys s in (p - w, p] (w = 0: s in [0, p]):
+ *   x(s) = scale * q_h . k_g(s);  Z = sum_s exp x(s) + exp(sink[h]);
+ *   o = sum_s exp x(s) v_g(s) / Z;  lse = log Z.
+ * max_n, max_t: at least the largest n_b and t_b of the call. sink: float32 [Hq] natural-log
+ * logits, or NULL (no sink). o: [n_rows][Hq][d] of o_dtype (HS2_F32 or HS2_BF16); lse:
+ * float32 [n_rows][Hq], may be NULL. scale > 0. All cache types; d 64 or 128; Hq / Hkv a
+ * power of two up to 32.
+ * Keys in pages whose table entry is bad are left out (HS2_DEV_BAD_PAGE; a row with no key
+ * left and no sink gets o = 0, lse = -inf). A sequence whose n_b > max_n, t_b > max_t,
+ * n_b > t_b, or rows beyond n_rows, sets HS2_DEV_BAD_LENGTH and its rows are not written.
+ * workspace: at least hs2_fa_chunk_workspace(...) bytes, 256-byte aligned, contents ignored;
+ * calls that run at the same time need workspaces of their own.                         */
+size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w);
+hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
+                        int max_t, int w, float scale, const float* sink, void* o, hs2_dtype o_dtype, float* lse,
+                        void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages of a pool: room for sequences, branches that share pages, defragmentation. All on
+ * the device: no call returns a count to the host, and results do not depend on timing.
+ * hs2_pages: device arrays of the caller's; ref[p] is the number of table entries that hold
+ * page p (0: free), free_list[0 .. *n_free) the free pages, taken from its end. The caches
+ * whose pages are numbered alike (the K/V pools of several groups) share one hs2_pages and
+ * one block table: kvs lists them (1 <= n_caches <= 8), with the same block_table, seq_len,
+ * batch, max_pages, num_pages (= pages->num_pages) and page_size.
+ * A call runs alone on its pool's books: calls on one hs2_pages are issued on one stream or
+ * ordered by events. All are captured and replayed like any launch. */
+typedef struct {
+  int32_t* ref;       /* [num_pages] */
+  int32_t* free_list; /* [num_pages] */
+  int32_t* n_free;    /* [1] */
+  int32_t num_pages;
+} hs2_pages;
+
+/* hs2_pages_grow: seq_len[b] += n_new[b] (n_new >= 0) for every sequence, and entries
+ * [ceil(old / 64), ceil(new / 64)) of block_table[b] ([batch][max_pages]) take free pages
+ * (ref 1) in order of (b, entry). All or nothing: where the free pages do not suffice for
+ * every sequence, HS2_DEV_BAD_PAGE is set and nothing changes. A sequence with n_new < 0, a
+ * negative length, or a new length beyond max_pages * 64 sets HS2_DEV_BAD_LENGTH and stays
+ * as it was. */
+hs2_status hs2_pages_grow(const hs2_pages* pages, int32_t* block_table, int32_t* seq_len, const int32_t* n_new,
+                          int batch, int max_pages, int32_t* dev_err, void* stream);
+/* hs2_pages_free: every page of block_table[b][0 .. ceil(seq_len[b] / 64)) loses a reference
+ * where drop[b] != 0; pages left with none go to the end of the free list in ascending
+ * order. Tables and lengths are not written. An entry outside [0, num_pages) or without a
+ * reference left sets HS2_DEV_BAD_PAGE and is skipped; a length outside [0, max_pages * 64]
+ * sets HS2_DEV_BAD_LENGTH and its sequence is skipped. */
+hs2_status hs2_pages_free(const hs2_pages* pages, const int32_t* block_table, const int32_t* seq_len,
+                          const int32_t* drop, int batch, int max_pages, int32_t* dev_err, void* stream);
+/* hs2_pages_fork: branch c < n_child becomes a sequence of its own with the keys of sequence
+ * src[c] of the caches (several branches may have one source; src[c] = -1: none, length 0).
+ * child_table ([n_child][max_pages]) shares the source's full pages (ref + 1); the rows of a
+ * last, partly filled page, and its scales, are copied in every cache to a page taken from
+ * the free list, in order of c. child_len[c] = seq_len[src[c]]; other table entries are -1.
+ * child_table and child_len do not overlap the sources'. Where the free pages do not
+ * suffice, HS2_DEV_BAD_PAGE is set and every branch has length 0 and no pages. src outside
+ * [-1, batch) sets HS2_DEV_BAD_INDEX, a source length outside [0, max_pages * 64]
+ * HS2_DEV_BAD_LENGTH: that branch is none. A source's bad table entry sets
+ * HS2_DEV_BAD_PAGE and is -1 in the branch (a bad last page: nothing is copied). */
+hs2_status hs2_pages_fork(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, const int32_t* src, int n_child,
+                          int32_t* child_table, int32_t* child_len, int32_t* dev_err, void* stream);
+/* hs2_pages_compact: with L referenced pages, moves every referenced page >= L into a free
+ * page < L, in place (i-th free page ascending takes the i-th such page ascending), in every
+ * cache with its scales, and updates the references, the free list (the pages >= L, the
+ * lowest taken first; entries behind are -1) and the entries of the caches' block table
+ * below ceil(seq_len[b] / 64). That table must hold every sequence that has pages of the
+ * pool. Bad entries (HS2_DEV_BAD_PAGE) and the rows of sequences with a bad length
+ * (HS2_DEV_BAD_LENGTH) are left as they are.
+ * workspace: at least hs2_pages_compact_workspace(pages) bytes, 256-byte aligned, contents
+ * ignored. */
+size_t hs2_pages_compact_workspace(const hs2_pages* pages);
+hs2_status hs2_pages_compact(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, void* workspace,
+                             size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Diagnostics.
  * hs2_profile_next: the next call on this host thread that runs `stage` records the
  * cudaEvent_t handles `start` and `stop` (passed as void*, created by the caller) on

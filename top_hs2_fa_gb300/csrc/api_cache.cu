@@ -1,0 +1,229 @@
+// api_cache.cu — the extern "C" boundary of the paged-cache operators: rows in and out, chunk
+// attention, pages. Validation and launches as in api.cu.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <cmath>
+
+#include "../../include/hs2.h"
+#include "api_util.h"
+#include "kernels.h"
+
+using namespace hs2::api;
+
+namespace {
+
+size_t elem_bytes(hs2_dtype t) { return t == HS2_F32 ? 4 : 2; }
+
+hs2_status kv_rows(const hs2_kv* kv, const void* k_rows, const void* v_rows, hs2_dtype row_dtype, int64_t row_stride,
+                   const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream, bool write) {
+  if (!valid_kv(kv, false) || !row_start || n_rows < 0) return HS2_ERR_ARG;
+  if (kv->v && !valid_kv(kv, true)) return HS2_ERR_ARG;
+  if (row_dtype != HS2_F32 && row_dtype != HS2_BF16) return HS2_ERR_ARG;
+  if (n_rows == 0) return HS2_OK;
+  if (!k_rows || !aligned16(k_rows) || (kv->v && (!v_rows || !aligned16(v_rows)))) return HS2_ERR_ARG;
+  if (row_stride < (int64_t)kv->Hkv * kv->d || row_stride * elem_bytes(row_dtype) % 16 != 0) return HS2_ERR_ARG;
+  if (kv->Hkv > 65535) return HS2_ERR_UNSUPPORTED;  // grid y
+  hs2::RowsArgs a{};
+  a.k = const_cast<void*>(kv->k);
+  a.v = const_cast<void*>(kv->v);
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.k_sf = const_cast<uint8_t*>(kv->k_sf);
+  a.v_sf = const_cast<uint8_t*>(kv->v_sf);
+  a.bt = kv->block_table;
+  a.seq_len = kv->seq_len;
+  a.batch = kv->batch;
+  a.num_pages = kv->num_pages;
+  a.max_pages = kv->max_pages;
+  a.Hkv = kv->Hkv;
+  a.k_rows = k_rows;
+  a.v_rows = v_rows;
+  a.row_stride = row_stride;
+  a.row_start = row_start;
+  a.n_rows = n_rows;
+  a.dev_err = dev_err;
+  const cudaError_t e = hs2::launch_kv_rows(a, kv->d, kv->dtype, write, row_dtype == HS2_F32, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+bool valid_pages(const hs2_pages* p) { return p && p->ref && p->free_list && p->n_free && p->num_pages >= 1; }
+// a sequence's entries; the bound keeps sums of 1024 sequences' pages within 32 bits
+bool valid_table(int batch, int max_pages) { return batch >= 1 && max_pages >= 1 && max_pages <= (1 << 20); }
+
+hs2::PagesArgs pages_args(const hs2_pages* p, int32_t* dev_err) {
+  hs2::PagesArgs a{};
+  a.ref = p->ref;
+  a.free_list = p->free_list;
+  a.n_free = p->n_free;
+  a.num_pages = p->num_pages;
+  a.dev_err = dev_err;
+  return a;
+}
+
+// The caches of one table: their arrays, and the table itself.
+bool page_caches(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, hs2::PagesArgs* a, hs2::PageSlabs* sl) {
+  if (!valid_pages(pages) || !kvs || n_caches < 1 || n_caches > hs2::kMaxPageCaches) return false;
+  sl->n = 0;
+  auto add = [&](const void* base, int Hkv, long long slab_bytes, int row_bytes) {
+    hs2::PageSlab& s = sl->s[sl->n];
+    s.base = (uint8_t*)const_cast<void*>(base);
+    s.slab_bytes = slab_bytes;
+    s.row_bytes = row_bytes;
+    sl->Hkv[sl->n++] = Hkv;
+  };
+  for (int c = 0; c < n_caches; ++c) {
+    const hs2_kv* kv = &kvs[c];
+    if (!valid_kv(kv, false) || (kv->v && !valid_kv(kv, true))) return false;
+    if (kv->num_pages != pages->num_pages || kv->block_table != kvs[0].block_table || kv->seq_len != kvs[0].seq_len ||
+        kv->batch != kvs[0].batch || kv->max_pages != kvs[0].max_pages)
+      return false;
+    const int row = kv->dtype == HS2_F32 ? 4 * kv->d : kv->dtype == HS2_BF16 ? 2 * kv->d
+                                                   : kv->dtype == HS2_FP8_E4M3 ? kv->d : kv->d / 2;
+    for (int side = 0; side < (kv->v ? 2 : 1); ++side) {
+      add(side ? kv->v : kv->k, kv->Hkv, 64LL * row, row);
+      if (kv->dtype == HS2_FP4_E2M1) add(side ? kv->v_sf : kv->k_sf, kv->Hkv, 64LL * (kv->d / 16), kv->d / 16);
+      if (low_precision(kv)) add(side ? kv->v_scale : kv->k_scale, kv->Hkv, 4, 0);
+    }
+  }
+  if (!valid_table(kvs[0].batch, kvs[0].max_pages)) return false;
+  a->bt = const_cast<int32_t*>(kvs[0].block_table);
+  a->seq_len = const_cast<int32_t*>(kvs[0].seq_len);
+  a->batch = kvs[0].batch;
+  a->max_pages = kvs[0].max_pages;
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+hs2_status hs2_kv_write(const hs2_kv* kv, const void* k_rows, const void* v_rows, hs2_dtype row_dtype,
+                        int64_t row_stride, const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream) {
+  return kv_rows(kv, k_rows, v_rows, row_dtype, row_stride, row_start, n_rows, dev_err, stream, true);
+}
+
+hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype row_dtype, int64_t row_stride,
+                       const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream) {
+  return kv_rows(kv, k_rows, v_rows, row_dtype, row_stride, row_start, n_rows, dev_err, stream, false);
+}
+
+size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+  if (!kv || kv->batch < 1 || kv->Hkv < 1 || Hq < 1 || n_rows < 0 || max_n < 0 || max_t < 0 || w < 0 ||
+      (kv->d != 64 && kv->d != 128))
+    return 0;
+  return 256;
+}
+
+hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
+                        int max_t, int w, float scale, const float* sink, void* o, hs2_dtype o_dtype, float* lse,
+                        void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  if (!valid_kv(kv, true) || !row_start || n_rows < 0 || Hq < 1 || Hq % kv->Hkv != 0) return HS2_ERR_ARG;
+  if (!pow2_le32(Hq / kv->Hkv)) return HS2_ERR_UNSUPPORTED;
+  if (max_n < 0 || max_n > max_t || (long long)max_t > (long long)kv->max_pages * 64 || w < 0) return HS2_ERR_ARG;
+  if (!std::isfinite(scale) || !(scale > 0.f)) return HS2_ERR_ARG;
+  if (o_dtype != HS2_F32 && o_dtype != HS2_BF16) return HS2_ERR_ARG;
+  if (n_rows == 0 || max_n == 0) return HS2_OK;
+  if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
+  if (Hq > 65535 || (kv->max_pages > (1 << 24))) return HS2_ERR_UNSUPPORTED;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < hs2_fa_chunk_workspace(n_rows, Hq, kv, max_n, max_t, w))
+    return HS2_ERR_ARG;
+  hs2::ChunkArgs a{};
+  a.q = q;
+  a.row_start = row_start;
+  a.n_rows = n_rows;
+  a.max_n = max_n;
+  a.max_t = max_t;
+  a.batch = kv->batch;
+  a.Hq = Hq;
+  a.Hkv = kv->Hkv;
+  a.G = Hq / kv->Hkv;
+  a.k = kv->k;
+  a.v = kv->v;
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.k_sf = kv->k_sf;
+  a.v_sf = kv->v_sf;
+  a.bt = kv->block_table;
+  a.seq_len = kv->seq_len;
+  a.num_pages = kv->num_pages;
+  a.max_pages = kv->max_pages;
+  a.w = w;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.sink = sink;
+  a.o = o;
+  a.o_bf16 = o_dtype == HS2_BF16;
+  a.lse = lse;
+  a.dev_err = dev_err;
+  const cudaError_t e = hs2::launch_chunk_cc(a, kv->d, kv->dtype, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+hs2_status hs2_pages_grow(const hs2_pages* pages, int32_t* block_table, int32_t* seq_len, const int32_t* n_new,
+                          int batch, int max_pages, int32_t* dev_err, void* stream) {
+  if (!valid_pages(pages) || !block_table || !seq_len || !n_new || batch < 0 || max_pages < 1) return HS2_ERR_ARG;
+  if (batch == 0) return HS2_OK;
+  if (!valid_table(batch, max_pages)) return HS2_ERR_UNSUPPORTED;
+  hs2::PagesArgs a = pages_args(pages, dev_err);
+  a.bt = block_table;
+  a.seq_len = seq_len;
+  a.n_new = n_new;
+  a.batch = batch;
+  a.max_pages = max_pages;
+  const cudaError_t e = hs2::launch_pages_grow(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+hs2_status hs2_pages_free(const hs2_pages* pages, const int32_t* block_table, const int32_t* seq_len,
+                          const int32_t* drop, int batch, int max_pages, int32_t* dev_err, void* stream) {
+  if (!valid_pages(pages) || !block_table || !seq_len || !drop || batch < 0 || max_pages < 1) return HS2_ERR_ARG;
+  if (batch == 0) return HS2_OK;
+  if (!valid_table(batch, max_pages)) return HS2_ERR_UNSUPPORTED;
+  hs2::PagesArgs a = pages_args(pages, dev_err);
+  a.bt = const_cast<int32_t*>(block_table);
+  a.seq_len = const_cast<int32_t*>(seq_len);
+  a.drop = drop;
+  a.batch = batch;
+  a.max_pages = max_pages;
+  const cudaError_t e = hs2::launch_pages_free(a, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+hs2_status hs2_pages_fork(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, const int32_t* src, int n_child,
+                          int32_t* child_table, int32_t* child_len, int32_t* dev_err, void* stream) {
+  hs2::PagesArgs a{};
+  hs2::PageSlabs sl;
+  if (!valid_pages(pages) || !src || !child_table || !child_len || n_child < 0) return HS2_ERR_ARG;
+  a = pages_args(pages, dev_err);
+  if (!page_caches(pages, n_caches, kvs, &a, &sl)) return HS2_ERR_ARG;
+  if (n_child == 0) return HS2_OK;
+  int slabs = 0;
+  for (int k = 0; k < sl.n; ++k) slabs += sl.Hkv[k];
+  if (slabs > 65535) return HS2_ERR_UNSUPPORTED;  // grid y
+  a.src = src;
+  a.n_child = n_child;
+  a.child_table = child_table;
+  a.child_len = child_len;
+  const cudaError_t e = hs2::launch_pages_fork(a, sl, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+size_t hs2_pages_compact_workspace(const hs2_pages* pages) {
+  if (!pages || pages->num_pages < 1) return 0;
+  return align256(4 * (4 + 2 * (size_t)(pages->num_pages / 2) + (size_t)pages->num_pages));
+}
+
+hs2_status hs2_pages_compact(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, void* workspace,
+                             size_t ws_bytes, int32_t* dev_err, void* stream) {
+  hs2::PagesArgs a{};
+  hs2::PageSlabs sl;
+  if (!valid_pages(pages)) return HS2_ERR_ARG;
+  a = pages_args(pages, dev_err);
+  if (!page_caches(pages, n_caches, kvs, &a, &sl)) return HS2_ERR_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < hs2_pages_compact_workspace(pages)) return HS2_ERR_ARG;
+  a.moves = (int32_t*)workspace;
+  const cudaError_t e = hs2::launch_pages_compact(a, sl, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+}  // extern "C"

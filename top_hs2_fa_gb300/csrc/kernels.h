@@ -83,6 +83,80 @@ struct AppendArgs {
   int32_t* dev_err;
 };
 
+// Rows of a ragged batch into (or out of) a paged cache.
+struct RowsArgs {
+  void* k;
+  void* v;  // null: a key-only cache
+  const float* k_scale;
+  const float* v_scale;
+  uint8_t* k_sf;
+  uint8_t* v_sf;
+  const int32_t* bt;
+  const int32_t* seq_len;
+  int batch, num_pages, max_pages, Hkv;
+  const void* k_rows;  // [n_rows][Hkv][d], token stride row_stride elements (read: written to)
+  const void* v_rows;
+  long long row_stride;
+  const int32_t* row_start;  // [batch + 1]
+  int n_rows;
+  int32_t* dev_err;
+};
+
+// Attention of a ragged batch of query chunks (the last rows of every sequence).
+struct ChunkArgs {
+  const void* q;  // [n_rows][Hq][D]
+  const int32_t* row_start;  // [batch + 1]
+  int n_rows, max_n, max_t, batch;
+  int Hq, Hkv, G;
+  const void* k;
+  const void* v;
+  const float* k_scale;
+  const float* v_scale;
+  const uint8_t* k_sf;
+  const uint8_t* v_sf;
+  const int32_t* bt;
+  const int32_t* seq_len;
+  int num_pages, max_pages;
+  int w;             // 0: every earlier key
+  float scale_log2;  // softmax scale * log2(e), > 0
+  const float* sink; // [Hq] natural log, or null
+  void* o;           // [n_rows][Hq][D]
+  int o_bf16;
+  float* lse;  // [n_rows][Hq], or null
+  int32_t* dev_err;
+};
+
+// The books of a page pool and what a call does with them.
+constexpr int kMaxPageCaches = kMaxAppendCaches;
+struct PageSlab {  // one array of a cache: page p, KV head g at base + (p * Hkv + g) * slab_bytes
+  uint8_t* base;
+  long long slab_bytes;
+  int row_bytes;  // of one of the 64 rows; 0: one entry per slab (copied whole)
+};
+constexpr int kMaxPageSlabs = kMaxPageCaches * 6;  // k, v, their scales and group scales
+struct PageSlabs {
+  PageSlab s[kMaxPageSlabs];
+  int Hkv[kMaxPageSlabs];
+  int n;
+};
+struct PagesArgs {
+  int32_t* ref;
+  int32_t* free_list;
+  int32_t* n_free;
+  int num_pages;
+  int32_t* bt;  // [batch][max_pages]
+  int32_t* seq_len;
+  int batch, max_pages;
+  const int32_t* n_new;  // grow
+  const int32_t* drop;   // free
+  const int32_t* src;    // fork: [n_child]
+  int n_child;
+  int32_t* child_table;
+  int32_t* child_len;
+  int32_t* moves;  // compact (workspace): [0] the number of moves, then src and dst lists, then the page map
+  int32_t* dev_err;
+};
+
 // Decode SA stream: units = (row, KV head, group of 8 query heads), hg groups per pair;
 // `total` = units * ms steps of 16 entries cut into nwarps equal ranges; partials hold up
 // to maxc warps per unit, 8 heads each.
@@ -202,6 +276,12 @@ struct SelectArgs {
 };
 
 cudaError_t launch_fa_decode_mma(const AttnArgs& a, int Bq, cudaStream_t s);
+cudaError_t launch_kv_rows(const RowsArgs& a, int d, int dtype, bool write, bool row_f32, cudaStream_t s);
+cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t s);
+cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t s);
+cudaError_t launch_pages_fork(const PagesArgs& a, const PageSlabs& sl, cudaStream_t s);
+cudaError_t launch_pages_compact(const PagesArgs& a, const PageSlabs& sl, cudaStream_t s);
 cudaError_t launch_kv_append(const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_attn_partial(const AttnArgs& a, int Bq, int bf16, cudaStream_t s);
 cudaError_t launch_combine(const CombineArgs& a, int Bq, cudaStream_t s);

@@ -1,0 +1,275 @@
+// kv_rows.cu — rows of a ragged batch into a paged cache (quantised on the way) and back.
+//
+// At prefill each Cross group's cache gains the prompt's bridged K/V rows, at decode one row
+// per sequence ("HySparse2：整体架构、KV 生命周期与 PD 分离", §8, §10.1); an FP4 cache keeps E2M1
+// codes with one E4M3 scale per 16 channels ("2.3.1 · CSA、HCA 与 CSA2", §3, "KV 字节与 FP4").
+//
+// FP4 of a group of 16 values x_j with slab scale S: A = max |x_j|, s the smallest E4M3 value
+// with 6 s S >= A, code_j the E2M1 value nearest to x_j / (s S), ties to the even code. No
+// division: code_j counts the borders b s S (b = 0.25 .. 5, between neighbouring codes) that
+// |x_j| reaches, and a float x reaches the real number b s S exactly when it reaches a float
+// computed from it (reach_float), so the code is the one of exact arithmetic. A product a S
+// with a of at most 7 bits is p + e, p = fl(a S), e = fma(a, S, -p), exactly, for S in
+// [2^-60, 2^60].
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "ragged.cuh"
+
+namespace hs2 {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+HS2_DEVI float e4m3_value(uint32_t code) {
+  float f;
+  asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.f32.f16 %0, l;}" : "=f"(f) : "r"(fp8x2_to_f16x2(code & 0xFFu)));
+  return f;
+}
+// two floats to E4M3 codes, nearest even, saturating (NaN: 0x7F); a in the low byte
+HS2_DEVI uint32_t e4m3_codes(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// The smallest float that is >= the real number a * S (tie) or > it (not tie).
+HS2_DEVI float reach_float(float a, float S, bool tie) {
+  const float p = a * S, e = fmaf(a, S, -p);
+  return (e < 0.f || (e == 0.f && tie)) ? p : __uint_as_float(__float_as_uint(p) + 1);
+}
+
+// The smallest E4M3 code whose value s has 6 s S >= A (A finite or inf); 126 (448) where none has.
+HS2_DEVI uint32_t group_scale(float A, float S) {
+  // the nearest code to about A / (6 S) is the one sought or the one before it
+  const uint32_t c = e4m3_codes(A / (6.f * S), 0.f) & 0xFFu;
+  const float a = 6.f * e4m3_value(c), p = a * S;
+  const bool short_of = p < A || (p == A && fmaf(a, S, -p) < 0.f);
+  return c + (short_of && c < 126u);
+}
+
+// x / S to E4M3 in exact arithmetic: the quotient rounded to odd (its last bit set where the
+// quotient is not exact) keeps what the second rounding, to 4 bits, needs to see.
+HS2_DEVI float quotient_to_odd(float x, float S, float inv) {
+  float q = x * inv;
+  if (!(fabsf(q) < 1024.f)) return q;  // saturates, or NaN
+  q = copysignf(fmaf(fmaf(-q, S, x), inv, q), x);
+  const float rest = fmaf(-q, S, x);
+  const uint32_t u = __float_as_uint(q);
+  if (rest != 0.f && !(u & 1u)) {
+    const bool away = (rest > 0.f) == !(u >> 31);  // the true magnitude is larger
+    if (away) return __uint_as_float(u + 1);
+    return (u & 0x7FFFFFFFu) ? __uint_as_float(u - 1) : q;
+  }
+  return q;
+}
+
+template <bool ROW_F32>
+HS2_DEVI void load16(const void* rows, long long at, float (&x)[16]) {
+  if constexpr (ROW_F32) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rows) + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldg(p + i);
+      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+  } else {
+    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(rows) + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 v = __ldg(p + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[8 * i + 2 * j] = bf16_lo(w[j]), x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
+    }
+  }
+}
+
+// One thread per (row, KV head, 16 channels) of K or V; a warp takes 32 / (D / 16) consecutive
+// rows of one head, so its codes and group scales fall next to each other in the page.
+template <int D, int FMT, bool ROW_F32>
+__global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a) {
+  constexpr int GPR = D / 16, TOK = 32 / GPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = (blockIdx.x * (kRowThreads / 32) + warp) * TOK;
+  const int tok = lane / GPR, grp = lane % GPR, r = r0 + tok;
+  const int g = blockIdx.y, side = blockIdx.z;
+  if (r0 >= a.n_rows) return;
+  const bool have = r < a.n_rows;
+  float x[16];
+  if (have) load16<ROW_F32>(side ? a.v_rows : a.k_rows, (long long)r * a.row_stride + g * D + 16 * grp, x);
+  int n[TOK], n_le = 0;
+  warp_rows_at_most<TOK>(a.row_start, a.batch, r0, n);
+#pragma unroll
+  for (int k = 0; k < TOK; ++k)
+    if (k == tok) n_le = n[k];
+  if (!have) return;
+  const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, r, n_le);
+  if (pl.b < 0) return;
+  if (pl.pos < 0) {
+    flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
+    return;
+  }
+  const int phys = a.bt[(size_t)pl.b * a.max_pages + pl.pos / kPage];
+  if (phys < 0 || phys >= a.num_pages) {
+    flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+    return;
+  }
+  const size_t slab = (size_t)phys * a.Hkv + g;
+  const size_t line = slab * kPage + pl.pos % kPage;  // row of the pool
+  uint8_t* pool = reinterpret_cast<uint8_t*>(side ? a.v : a.k);
+  if constexpr (FMT == HS2_F32) {
+    float4* dst = reinterpret_cast<float4*>(pool + (line * D + 16 * grp) * 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  } else if constexpr (FMT == HS2_BF16) {
+    uint4* dst = reinterpret_cast<uint4*>(pool + (line * D + 16 * grp) * 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      dst[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                          pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+  } else {
+    const float S = (side ? a.v_scale : a.k_scale)[slab];
+    if (!(S >= 0x1p-60f && S <= 0x1p60f)) {
+      flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+      return;
+    }
+    if constexpr (FMT == HS2_FP8_E4M3) {
+      const float inv = 1.f / S;
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = e4m3_codes(quotient_to_odd(x[4 * i], S, inv), quotient_to_odd(x[4 * i + 1], S, inv));
+        const uint32_t hi = e4m3_codes(quotient_to_odd(x[4 * i + 2], S, inv), quotient_to_odd(x[4 * i + 3], S, inv));
+        w[i] = lo | (hi << 16);
+      }
+      *reinterpret_cast<uint4*>(pool + line * D + 16 * grp) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+      uint32_t top = 0;  // the largest magnitude as bits: a NaN's exceed infinity's
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
+      const bool nan = top > 0x7F800000u;
+      const uint32_t s = nan ? 0x7Fu : group_scale(__uint_as_float(top), S);
+      const float sv = nan ? 0.f : e4m3_value(s);
+      const float t0 = reach_float(0.25f * sv, S, false), t1 = reach_float(0.75f * sv, S, true),
+                  t2 = reach_float(1.25f * sv, S, false), t3 = reach_float(1.75f * sv, S, true),
+                  t4 = reach_float(2.5f * sv, S, false), t5 = reach_float(3.5f * sv, S, true),
+                  t6 = reach_float(5.f * sv, S, false);
+      uint32_t w[2] = {0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const uint32_t u = __float_as_uint(x[j]);
+        const float m = fabsf(x[j]);
+        const bool b2 = m >= t3;
+        const bool b1 = m >= (b2 ? t5 : t1);
+        const bool b0 = m >= (b2 ? (b1 ? t6 : t4) : (b1 ? t2 : t0));
+        uint32_t c = (b2 ? 4u : 0u) | (b1 ? 2u : 0u) | (b0 ? 1u : 0u);
+        if (sv == 0.f) c = 0u;  // an all-zero group (or a NaN's)
+        c |= (u >> 28) & 8u;
+        w[j >> 3] |= c << (4 * (j & 7));
+      }
+      *reinterpret_cast<uint2*>(pool + line * (D / 2) + 8 * grp) = make_uint2(w[0], w[1]);
+      (side ? a.v_sf : a.k_sf)[line * GPR + grp] = (uint8_t)s;
+    }
+  }
+}
+
+// Four channels per lane, so that every store of a warp is contiguous; a warp takes as many
+// rows of one head as the writing kernel's.
+template <int D, int FMT, bool ROW_F32>
+__global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) {
+  constexpr int TOK = 512 / D;        // rows per warp
+  constexpr int LPR = D / 4;          // lanes per row
+  constexpr int RPS = 32 / LPR;       // rows per step
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = (blockIdx.x * (kRowThreads / 32) + warp) * TOK;
+  const int g = blockIdx.y, side = blockIdx.z;
+  if (r0 >= a.n_rows) return;
+  int n[TOK];
+  warp_rows_at_most<TOK>(a.row_start, a.batch, r0, n);
+  // lane k < TOK resolves row r0 + k: its pool row, or -1
+  long long mine = -1;
+  {
+    int n_le = 0;
+#pragma unroll
+    for (int k = 0; k < TOK; ++k)
+      if (k == lane) n_le = n[k];
+    if (lane < TOK && r0 + lane < a.n_rows) {
+      const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, r0 + lane, n_le);
+      if (pl.b >= 0 && pl.pos < 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
+      if (pl.b >= 0 && pl.pos >= 0) {
+        const int phys = a.bt[(size_t)pl.b * a.max_pages + pl.pos / kPage];
+        if (phys < 0 || phys >= a.num_pages) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        else mine = ((long long)phys * a.Hkv + g) * kPage + pl.pos % kPage;
+      }
+    }
+  }
+  const uint8_t* pool = reinterpret_cast<const uint8_t*>(side ? a.v : a.k);
+  void* rows = const_cast<void*>(side ? a.v_rows : a.k_rows);
+#pragma unroll
+  for (int st = 0; st < TOK / RPS; ++st) {
+    const int tok = st * RPS + lane / LPR, ch = 4 * (lane % LPR);
+    const long long line = __shfl_sync(0xffffffffu, mine, tok);
+    if (line < 0) continue;
+    float x[4];
+    if constexpr (FMT == HS2_F32) {
+      const float4 v = *reinterpret_cast<const float4*>(pool + (line * D + ch) * 4);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else if constexpr (FMT == HS2_BF16) {
+      const uint2 v = *reinterpret_cast<const uint2*>(pool + (line * D + ch) * 2);
+      x[0] = bf16_lo(v.x), x[1] = bf16_hi(v.x), x[2] = bf16_lo(v.y), x[3] = bf16_hi(v.y);
+    } else {
+      const float S = (side ? a.v_scale : a.k_scale)[line / kPage];
+      uint32_t h0, h1;  // four values as f16 pairs, exact
+      if constexpr (FMT == HS2_FP8_E4M3) {
+        fp8x4_to_f16x4(*reinterpret_cast<const uint32_t*>(pool + line * D + ch), h0, h1);
+      } else {
+        uint32_t u2, u3;
+        fp4x8_to_f16x8(*reinterpret_cast<const uint16_t*>(pool + line * (D / 2) + ch / 2), h0, h1, u2, u3);
+        const uint32_t s = (side ? a.v_sf : a.k_sf)[line * (D / 16) + ch / 16];
+        h0 = hmul2(h0, e4m3_pair(s, s));
+        h1 = hmul2(h1, e4m3_pair(s, s));
+      }
+      const float2 f0 = __half22float2(*reinterpret_cast<__half2*>(&h0));
+      const float2 f1 = __half22float2(*reinterpret_cast<__half2*>(&h1));
+      x[0] = f0.x * S, x[1] = f0.y * S, x[2] = f1.x * S, x[3] = f1.y * S;
+    }
+    const long long at = (long long)(r0 + tok) * a.row_stride + g * D + ch;
+    if constexpr (ROW_F32)
+      *reinterpret_cast<float4*>(reinterpret_cast<float*>(rows) + at) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(rows) + at) =
+          make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+  }
+}
+
+template <int D, int FMT>
+cudaError_t launch_fmt(const RowsArgs& a, bool write, bool row_f32, cudaStream_t s) {
+  const int per_cta = kRowThreads / (D / 16);
+  const dim3 grid((a.n_rows + per_cta - 1) / per_cta, a.Hkv, a.v ? 2 : 1);
+  auto kern = write ? (row_f32 ? kv_write_kernel<D, FMT, true> : kv_write_kernel<D, FMT, false>)
+                    : (row_f32 ? kv_read_kernel<D, FMT, true> : kv_read_kernel<D, FMT, false>);
+  kern<<<grid, kRowThreads, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const RowsArgs& a, int dtype, bool write, bool row_f32, cudaStream_t s) {
+  switch (dtype) {
+    case HS2_F32: return launch_fmt<D, HS2_F32>(a, write, row_f32, s);
+    case HS2_BF16: return launch_fmt<D, HS2_BF16>(a, write, row_f32, s);
+    case HS2_FP8_E4M3: return launch_fmt<D, HS2_FP8_E4M3>(a, write, row_f32, s);
+    case HS2_FP4_E2M1: return launch_fmt<D, HS2_FP4_E2M1>(a, write, row_f32, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_kv_rows(const RowsArgs& a, int d, int dtype, bool write, bool row_f32, cudaStream_t s) {
+  return d == 128 ? launch_d<128>(a, dtype, write, row_f32, s) : launch_d<64>(a, dtype, write, row_f32, s);
+}
+
+}  // namespace hs2

@@ -25,6 +25,8 @@ EXPORTS = (
     "hs2_hier_reindex_workspace", "hs2_hier_reindex", "hs2_strerror", "hs2_last_cuda_error",
     "hs2_abi_version", "hs2_profile_next", "hs2_selftest_wait_timeout", "hs2_fa_select_noalloc", "hs2_fa_select_noalloc_capacity",
     "hs2_kv_append", "hs2_fa_select_append", "hs2_fa_select_launches", "hs2_sa_reuse_launches",
+    "hs2_kv_write", "hs2_kv_read", "hs2_fa_chunk_workspace", "hs2_fa_chunk", "hs2_pages_grow", "hs2_pages_free",
+    "hs2_pages_fork", "hs2_pages_compact_workspace", "hs2_pages_compact",
 )
 STAGE_FA_SCAN, STAGE_SA_GATHER, STAGE_INDEXER = 0, 1, 2
 SA_OVERLAP = 1  # HS2_SA_OVERLAP
@@ -38,6 +40,11 @@ class hs2_kv(ctypes.Structure):
         ("d", ctypes.c_int32), ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
         ("k_sf", ctypes.c_void_p), ("v_sf", ctypes.c_void_p),
     ]
+
+
+class hs2_pages(ctypes.Structure):
+    _fields_ = [("ref", ctypes.c_void_p), ("free_list", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32)]
 
 
 class HS2Error(RuntimeError):
@@ -96,6 +103,25 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.hs2_fa_select_launches.restype = i32
     lib.hs2_sa_reuse_launches.argtypes = [i32, i32, kvp, i32, i32, i32]
     lib.hs2_sa_reuse_launches.restype = i32
+    i64, pgp = ctypes.c_int64, ctypes.POINTER(hs2_pages)
+    lib.hs2_kv_write.argtypes = [kvp, vp, vp, i32, i64, vp, i32, vp, vp]
+    lib.hs2_kv_write.restype = i32
+    lib.hs2_kv_read.argtypes = [kvp, vp, vp, i32, i64, vp, i32, vp, vp]
+    lib.hs2_kv_read.restype = i32
+    lib.hs2_fa_chunk_workspace.argtypes = [i32, i32, kvp, i32, i32, i32]
+    lib.hs2_fa_chunk_workspace.restype = sz
+    lib.hs2_fa_chunk.argtypes = [vp, vp, i32, i32, i32, kvp, i32, i32, f32, vp, vp, i32, vp, vp, sz, vp, vp]
+    lib.hs2_fa_chunk.restype = i32
+    lib.hs2_pages_grow.argtypes = [pgp, vp, vp, vp, i32, i32, vp, vp]
+    lib.hs2_pages_grow.restype = i32
+    lib.hs2_pages_free.argtypes = [pgp, vp, vp, vp, i32, i32, vp, vp]
+    lib.hs2_pages_free.restype = i32
+    lib.hs2_pages_fork.argtypes = [pgp, i32, kvp, vp, i32, vp, vp, vp, vp]
+    lib.hs2_pages_fork.restype = i32
+    lib.hs2_pages_compact_workspace.argtypes = [pgp]
+    lib.hs2_pages_compact_workspace.restype = sz
+    lib.hs2_pages_compact.argtypes = [pgp, i32, kvp, vp, sz, vp, vp]
+    lib.hs2_pages_compact.restype = i32
     if lib.hs2_abi_version() != ABI_VERSION:
         raise HS2Error(f"libhs2 ABI {lib.hs2_abi_version()} != binding ABI {ABI_VERSION}: rebuild the library")
     _lib = lib
@@ -358,3 +384,212 @@ def hs2_selftest_wait_timeout(timeout_us: int, dev_err: torch.Tensor, stream=Non
     """One warp waits (bounded, timeout_us) on an mbarrier nothing arrives on: the wait must
     give up and set DEV_TIMEOUT in dev_err."""
     _check(load().hs2_selftest_wait_timeout(int(timeout_us), _ptr(dev_err), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- paged-cache operators
+def _scratch(nbytes: int, device, ws, stream):
+    """The caller's workspace, or one of this call's own that stays alive until `stream` is done."""
+    t = _workspace(nbytes, device, ws)
+    if ws is None and stream is not None:
+        t.record_stream(stream)
+    return t
+
+
+_ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _i32(t: torch.Tensor, name: str, *shape) -> torch.Tensor:
+    """An int32 contiguous tensor of the given shape (-1: any), or an error."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
+            a not in (-1, b) for a, b in zip(shape, t.shape)):
+        raise HS2Error(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+    return t
+
+
+def _here(stream, *tensors) -> None:
+    """Every tensor on one device, and that the current one (the library launches there)."""
+    dev = {t.device for t in tensors if t is not None}
+    if len(dev) > 1:
+        raise HS2Error("tensors on several devices")
+    d = next(iter(dev))
+    if d.type != "cuda" or d.index != torch.cuda.current_device() or (stream is not None and stream.device != d):
+        raise HS2Error("the tensors must be on the current CUDA device (and the stream's)")
+
+
+def _kv_tensors(kv: KV):
+    return kv.k, kv.v, kv.block_table, kv.seq_len, kv.k_scale, kv.v_scale, kv.k_sf, kv.v_sf
+
+
+def _rows(t: torch.Tensor, kv: hs2_kv, n_rows: int, name: str):
+    """Row dtype code and token stride of [n_rows][Hkv][d] rows, heads next to each other."""
+    if t.dtype not in _ROW_DTYPES or tuple(t.shape) != (n_rows, kv.Hkv, kv.d) or t.stride(2) != 1 or (
+            kv.Hkv > 1 and t.stride(1) != kv.d):
+        raise HS2Error(f"{name} must be float32 or bfloat16 [n_rows][Hkv][d] with contiguous tokens")
+    return _ROW_DTYPES[t.dtype], int(t.stride(0)) if n_rows > 1 else kv.Hkv * kv.d
+
+
+def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
+    c = kv.c()
+    n = int(k_rows.shape[0])
+    _here(stream, k_rows, v_rows, row_start, dev_err, *_kv_tensors(kv))
+    dt, stride = _rows(k_rows, c, n, "k_rows")
+    if (v_rows is None) != (kv.v is None):
+        raise HS2Error("v_rows goes with a cache that has V")
+    if v_rows is not None and _rows(v_rows, c, n, "v_rows") != (dt, stride):
+        raise HS2Error("v_rows must have k_rows' dtype and token stride")
+    _i32(row_start, "row_start", c.batch + 1)
+    _check(call(ctypes.byref(c), _ptr(k_rows), _ptr(v_rows), dt, stride, _ptr(row_start), n, _ptr(dev_err),
+                _stream(stream)))
+
+
+def hs2_kv_write(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor, dev_err=None,
+                 stream=None) -> None:
+    """Rows of a ragged batch into the cache, quantised to its type: rows [row_start[b],
+    row_start[b+1]) are sequence b's last positions (seq_len already counts them). ``k_rows``
+    / ``v_rows``: float32 or bfloat16 [n_rows][Hkv][d], any token stride; the cache's
+    k_scale / v_scale are inputs."""
+    _kv_rows(load().hs2_kv_write, kv, k_rows, v_rows, row_start, dev_err, stream)
+
+
+def hs2_kv_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype = torch.float32, out=None,
+                dev_err=None, stream=None):
+    """The values of the rows hs2_kv_write with this ``row_start`` would write, as (k_rows,
+    v_rows) of ``dtype`` [n_rows][Hkv][d] (v_rows None for a key-only cache). Rows outside
+    every sequence are left as they are in ``out``."""
+    c = kv.c()
+    if out is None:
+        out = tuple(torch.empty((n_rows, c.Hkv, c.d), dtype=dtype, device=kv.k.device) if x is not None else None
+                    for x in (kv.k, kv.v))
+    elif out[0].shape[0] != n_rows or out[0].dtype != dtype:
+        raise HS2Error("out must hold n_rows rows of the dtype")
+    _kv_rows(load().hs2_kv_read, kv, out[0], out[1], row_start, dev_err, stream)
+    return out
+
+
+def hs2_fa_chunk_workspace(n_rows: int, Hq: int, kv: KV, max_n: int, max_t: int, w: int = 0) -> int:
+    c = kv.c()
+    return int(load().hs2_fa_chunk_workspace(n_rows, Hq, ctypes.byref(c), max_n, max_t, w))
+
+
+def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float, max_n: int,
+                 max_t: int | None = None, w: int = 0, sink: torch.Tensor | None = None,
+                 o_dtype: torch.dtype = torch.float32, out=None, workspace=None, dev_err=None, stream=None):
+    """Causal attention of a ragged batch of query chunks over the cache; returns (o, lse).
+
+    ``q`` [n_rows][Hq][d] (bf16; float32 with an F32 cache): rows [row_start[b],
+    row_start[b+1]) are sequence b's last positions. ``max_n`` bounds the rows of a sequence,
+    ``max_t`` its keys (default: the table's capacity). ``w`` > 0: a sliding window of that
+    many keys; ``sink``: float32 [Hq] logits of one more key with a zero value. ``o_dtype``
+    float32 or bfloat16; lse is float32 [n_rows][Hq]."""
+    lib = load()
+    c = kv.c()
+    n, Hq, d = q.shape
+    if max_t is None:
+        max_t = c.max_pages * c.page_size
+    if q.dtype != (torch.float32 if c.dtype == F32 else torch.bfloat16) or not q.is_contiguous() or d != c.d:
+        raise HS2Error("q must be contiguous [n_rows][Hq][d], bfloat16 (float32 with an F32 cache)")
+    if sink is not None and (sink.dtype != torch.float32 or not sink.is_contiguous() or sink.numel() != Hq):
+        raise HS2Error("sink must be float32 [Hq]")
+    if o_dtype not in _ROW_DTYPES:
+        raise HS2Error("o_dtype must be float32 or bfloat16")
+    if out is None:
+        out = (torch.empty((n, Hq, d), dtype=o_dtype, device=q.device),
+               torch.empty((n, Hq), dtype=torch.float32, device=q.device))
+    o, lse = out
+    if o.dtype != o_dtype or tuple(o.shape) != (n, Hq, d) or not o.is_contiguous() or (
+            lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, Hq) or not lse.is_contiguous())):
+        raise HS2Error("out must be contiguous (o [n_rows][Hq][d] of o_dtype, lse float32 [n_rows][Hq] or None)")
+    _i32(row_start, "row_start", c.batch + 1)
+    _here(stream, q, row_start, sink, o, lse, workspace, dev_err, *_kv_tensors(kv))
+    ws = _scratch(int(lib.hs2_fa_chunk_workspace(n, Hq, ctypes.byref(c), max_n, max_t, w)), q.device, workspace, stream)
+    _check(lib.hs2_fa_chunk(_ptr(q), _ptr(row_start), n, max_n, Hq, ctypes.byref(c), max_t, w, float(scale),
+                            _ptr(sink), _ptr(o), _ROW_DTYPES[o_dtype], _ptr(lse), _ptr(ws),
+                            ws.numel() * ws.element_size(), _ptr(dev_err), _stream(stream)))
+    return o, lse
+
+
+@dataclass
+class Pages:
+    """The books of a page pool: references per page and the stack of free pages."""
+
+    ref: torch.Tensor  # int32 [num_pages], table entries that hold the page (0: free)
+    free_list: torch.Tensor  # int32 [num_pages], of which the first n_free are free pages
+    n_free: torch.Tensor  # int32 [1]
+
+    @classmethod
+    def make(cls, num_pages: int, device="cuda") -> "Pages":
+        """A pool with every page free; the lowest are taken first."""
+        return cls(ref=torch.zeros(num_pages, dtype=torch.int32, device=device),
+                   free_list=torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
+                   n_free=torch.full((1,), num_pages, dtype=torch.int32, device=device))
+
+    def c(self) -> hs2_pages:
+        n = int(self.ref.shape[0])
+        for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
+            _i32(t, name, size)
+        return hs2_pages(_ptr(self.ref), _ptr(self.free_list), _ptr(self.n_free), n)
+
+
+def _pages_tensors(p: Pages):
+    return p.ref, p.free_list, p.n_free
+
+
+def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, n_new: torch.Tensor, dev_err=None,
+                   stream=None) -> None:
+    """seq_len += n_new, with free pages for the positions that need them, in place."""
+    c = pages.c()
+    _i32(block_table, "block_table", -1, -1)
+    b, mp = block_table.shape
+    _i32(seq_len, "seq_len", b)
+    _i32(n_new, "n_new", b)
+    _here(stream, block_table, seq_len, n_new, dev_err, *_pages_tensors(pages))
+    _check(load().hs2_pages_grow(ctypes.byref(c), _ptr(block_table), _ptr(seq_len), _ptr(n_new), b, mp, _ptr(dev_err),
+                                 _stream(stream)))
+
+
+def hs2_pages_free(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, drop: torch.Tensor, dev_err=None,
+                   stream=None) -> None:
+    """The pages of every sequence with drop[b] != 0 lose a reference; those left with none
+    return to the free list."""
+    c = pages.c()
+    _i32(block_table, "block_table", -1, -1)
+    b, mp = block_table.shape
+    _i32(seq_len, "seq_len", b)
+    _i32(drop, "drop", b)
+    _here(stream, block_table, seq_len, drop, dev_err, *_pages_tensors(pages))
+    _check(load().hs2_pages_free(ctypes.byref(c), _ptr(block_table), _ptr(seq_len), _ptr(drop), b, mp, _ptr(dev_err),
+                                 _stream(stream)))
+
+
+def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None, stream=None):
+    """Branches of the caches' sequences: branch c continues sequence src[c] (-1: none), with
+    its full pages shared and the last, partly filled one copied. ``kvs``: the caches of one
+    block table. Returns (child_table, child_len)."""
+    c = pages.c()
+    cs = (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
+    _i32(src, "src", -1)
+    n, mp = int(src.shape[0]), int(kvs[0].block_table.shape[1])
+    if out is None:
+        out = (torch.empty((n, mp), dtype=torch.int32, device=src.device),
+               torch.empty((n,), dtype=torch.int32, device=src.device))
+    table, length = _i32(out[0], "child_table", n, mp), _i32(out[1], "child_len", n)
+    _here(stream, src, table, length, dev_err, *_pages_tensors(pages), *[t for kv in kvs for t in _kv_tensors(kv)])
+    _check(load().hs2_pages_fork(ctypes.byref(c), len(kvs), cs, _ptr(src), n, _ptr(table), _ptr(length),
+                                 _ptr(dev_err), _stream(stream)))
+    return table, length
+
+
+def hs2_pages_compact_workspace(pages: Pages) -> int:
+    c = pages.c()
+    return int(load().hs2_pages_compact_workspace(ctypes.byref(c)))
+
+
+def hs2_pages_compact(pages: Pages, kvs, workspace=None, dev_err=None, stream=None) -> None:
+    """The pool's referenced pages to its front, in place in every cache of ``kvs`` (which
+    share one block table holding every sequence), with tables and books updated."""
+    c = pages.c()
+    cs = (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
+    _here(stream, dev_err, workspace, *_pages_tensors(pages), *[t for kv in kvs for t in _kv_tensors(kv)])
+    ws = _scratch(int(load().hs2_pages_compact_workspace(ctypes.byref(c))), pages.ref.device, workspace, stream)
+    _check(load().hs2_pages_compact(ctypes.byref(c), len(kvs), cs, _ptr(ws), ws.numel() * ws.element_size(),
+                                    _ptr(dev_err), _stream(stream)))
