@@ -314,7 +314,10 @@ hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype r
  * power of two up to 32.
  * Keys in pages whose table entry is bad are left out (HS2_DEV_BAD_PAGE; a row with no key
  * left and no sink gets o = 0, lse = -inf). A sequence whose n_b > max_n, t_b > max_t,
- * n_b > t_b, or rows beyond n_rows, sets HS2_DEV_BAD_LENGTH and its rows are not written.
+ * n_b > t_b, or rows beyond n_rows, sets HS2_DEV_BAD_LENGTH and its rows are not written
+ * (a descending row_start: none or only some rows are).
+ * A V row that is not finite makes the rows of a chunk undefined that see any key of its
+ * 128-key tile, as a weight of zero does not cancel it; values behind seq_len do not matter.
  * workspace: at least hs2_fa_chunk_workspace(...) bytes, 256-byte aligned, contents ignored;
  * calls that run at the same time need workspaces of their own.                         */
 size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w);

@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "../../include/hs2.h"
@@ -45,6 +46,86 @@ hs2_status kv_rows(const hs2_kv* kv, const void* k_rows, const void* v_rows, hs2
   a.dev_err = dev_err;
   const cudaError_t e = hs2::launch_kv_rows(a, kv->d, kv->dtype, write, row_dtype == HS2_F32, (cudaStream_t)stream);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  return n;
+}
+
+// Workspace of hs2_fa_chunk: the plan of the wide kernel, its parts, and the expanded pages of
+// a quantised cache.
+struct ChunkLayout {
+  bool wide;
+  hs2::ChunkPlan plan;  // pointers as offsets until bind()
+  size_t off[10];
+  int exp_seqs, exp_pages_seq;
+  size_t off_ek, off_ev, off_params, total;
+  long long tiles;  // an upper bound of the tiles in all
+};
+
+ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+  ChunkLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  L.wide = kv->dtype != HS2_F32;
+  if (L.wide && n_rows > 0 && max_t > 0) {
+    const int G = Hq / kv->Hkv;
+    hs2::ChunkPlan& p = L.plan;
+    p.ctas = sm_count();
+    p.tile_rows = 128;
+    p.min_rows = 0;
+    p.max_rows = 0x7fffffff;
+    p.min_tiles = 4;
+    const long long units = (long long)kv->Hkv * ((long long)n_rows * G / 128 + std::min(kv->batch, n_rows));
+    p.max_units = (int)std::min<long long>(units, 1 << 30);
+    L.tiles = units * (max_t / 128 + 1);
+    L.off[0] = take(16);
+    L.off[1] = take(4 * (size_t)p.ctas);
+    L.off[2] = take(4 * (size_t)p.max_units);
+    L.off[3] = take(48 * (size_t)p.max_units);
+    L.off[4] = take(2 * (size_t)p.ctas * p.tile_rows * 8);
+    L.off[5] = take(2 * (size_t)p.ctas * p.tile_rows * kv->d * 4);
+    p.expand = low_precision(kv);
+    if (p.expand) {
+      L.exp_seqs = std::min(kv->batch, n_rows);
+      L.exp_pages_seq = cdiv(max_t, 64);
+      if (w > 0) L.exp_pages_seq = std::min<long long>(L.exp_pages_seq, ((long long)max_n + w) / 64 + 2);
+      p.max_exp_pages = L.exp_seqs * L.exp_pages_seq;
+      L.off[6] = take(4 * (size_t)L.exp_seqs);
+      L.off[7] = take(4 * (size_t)L.exp_seqs);
+      L.off[8] = take(4 * (size_t)L.exp_seqs);
+      L.off[9] = take(4);
+      const size_t rows = (size_t)L.exp_seqs * L.exp_pages_seq * kv->Hkv * 64;
+      L.off_ek = take(rows * kv->d * 2);
+      L.off_ev = take(rows * kv->d * 2);
+      L.off_params = take(rows / 64 * 8);
+    }
+  }
+  L.total = std::max<size_t>(off, 256);
+  return L;
+}
+
+void bind(ChunkLayout& L, char* ws) {
+  hs2::ChunkPlan& p = L.plan;
+  p.head = (int32_t*)(ws + L.off[0]);
+  p.cta_first = (int32_t*)(ws + L.off[1]);
+  p.arrive = (int32_t*)(ws + L.off[2]);
+  p.units = (int32_t*)(ws + L.off[3]);
+  p.part_ml = (float*)(ws + L.off[4]);
+  p.part_o = (float*)(ws + L.off[5]);
+  p.exp_seq = (int32_t*)(ws + L.off[6]);
+  p.exp_base = (int32_t*)(ws + L.off[7]);
+  p.exp_page = (int32_t*)(ws + L.off[8]);
+  p.exp_head = (int32_t*)(ws + L.off[9]);
 }
 
 bool valid_pages(const hs2_pages* p) { return p && p->ref && p->free_list && p->n_free && p->num_pages >= 1; }
@@ -112,7 +193,8 @@ size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, i
   if (!kv || kv->batch < 1 || kv->Hkv < 1 || Hq < 1 || n_rows < 0 || max_n < 0 || max_t < 0 || w < 0 ||
       (kv->d != 64 && kv->d != 128))
     return 0;
-  return 256;
+  if (Hq % kv->Hkv != 0 || !pow2_le32(Hq / kv->Hkv)) return 0;
+  return chunk_layout(n_rows, Hq, kv, max_n, max_t, w).total;
 }
 
 hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
@@ -126,8 +208,9 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   if (n_rows == 0 || max_n == 0) return HS2_OK;
   if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
   if (Hq > 65535 || (kv->max_pages > (1 << 24))) return HS2_ERR_UNSUPPORTED;
-  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < hs2_fa_chunk_workspace(n_rows, Hq, kv, max_n, max_t, w))
-    return HS2_ERR_ARG;
+  ChunkLayout L = chunk_layout(n_rows, Hq, kv, max_n, max_t, w);
+  if (L.tiles > 1LL << 30 || kv->Hkv > 65535) return HS2_ERR_UNSUPPORTED;  // 32-bit tile counts, grid y
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return HS2_ERR_ARG;
   hs2::ChunkArgs a{};
   a.q = q;
   a.row_start = row_start;
@@ -155,7 +238,29 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   a.o_bf16 = o_dtype == HS2_BF16;
   a.lse = lse;
   a.dev_err = dev_err;
-  const cudaError_t e = hs2::launch_chunk_cc(a, kv->d, kv->dtype, (cudaStream_t)stream);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (!L.wide) {
+    const cudaError_t e = hs2::launch_chunk_cc(a, kv->d, kv->dtype, s);
+    return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+  }
+  char* ws = (char*)workspace;
+  bind(L, ws);
+  const hs2::ChunkPlan& p = L.plan;
+  const uint64_t rows = (uint64_t)(p.expand ? p.max_exp_pages : kv->num_pages) * kv->Hkv * 64;
+  CUtensorMap tq, tk, tv;
+  if (!encode_3d_bf16(&tq, q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, a.G, 128 / a.G) ||
+      !encode_2d_bf16(&tk, p.expand ? ws + L.off_ek : kv->k, kv->d, rows, 64) ||
+      !encode_2d_bf16(&tv, p.expand ? ws + L.off_ev : kv->v, kv->d, rows, 64))
+    return HS2_ERR_ARG;
+  cudaError_t e = hs2::launch_chunk_plan(a, &p, 1, s);
+  if (e != cudaSuccess) return cuda_fail(e);
+  float2* params = p.expand ? (float2*)(ws + L.off_params) : nullptr;
+  if (p.expand) {
+    e = hs2::launch_chunk_expand(a, p, kv->d, kv->dtype, ws + L.off_ek, ws + L.off_ev, params, L.exp_seqs,
+                                 L.exp_pages_seq, s);
+    if (e != cudaSuccess) return cuda_fail(e);
+  }
+  e = hs2::launch_chunk_wide(tq, tk, tv, a, p, params, kv->d, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 

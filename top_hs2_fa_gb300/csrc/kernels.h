@@ -126,6 +126,29 @@ struct ChunkArgs {
   int32_t* dev_err;
 };
 
+// The plan of a persistent chunk-attention kernel (device memory, written by the planning
+// kernel of the same call). rows: the packed rows of a unit; sequences with rows in
+// (min_rows, max_rows] are the kernel's.
+struct ChunkPlan {
+  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] units
+  int32_t* cta_first;  // [ctas] the unit at each CTA's range start
+  int32_t* arrive;     // [max_units] CTAs that have left their part of a unit
+  int32_t* units;      // [max_units] ChunkUnit
+  int max_units, ctas;
+  int tile_rows;            // rows of a unit: 128 or the narrow kernel's width
+  int min_rows, max_rows;   // of a sequence, times G
+  int min_tiles;            // the shortest range worth a CTA
+  float* part_ml;           // [2 ctas][tile_rows][2] m and l (base 2) of the parts
+  float* part_o;            // [2 ctas][D][tile_rows] unnormalised outputs
+  // sequences whose pages are expanded to bf16 first (wide kernel on FP8 / FP4), by ordinal
+  int32_t* exp_seq;   // [batch] sequence; exp_head[0]: how many
+  int32_t* exp_base;  // [batch] its first expanded page
+  int32_t* exp_page;  // [batch] its first page expanded
+  int32_t* exp_head;
+  int max_exp_pages;
+  int expand;
+};
+
 // The books of a page pool and what a call does with them.
 constexpr int kMaxPageCaches = kMaxAppendCaches;
 struct PageSlab {  // one array of a cache: page p, KV head g at base + (p * Hkv + g) * slab_bytes
@@ -278,6 +301,11 @@ struct SelectArgs {
 cudaError_t launch_fa_decode_mma(const AttnArgs& a, int Bq, cudaStream_t s);
 cudaError_t launch_kv_rows(const RowsArgs& a, int d, int dtype, bool write, bool row_f32, cudaStream_t s);
 cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s);
+cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, int dtype, void* ek, void* ev,
+                                float2* params, int max_seqs, int max_pages_seq, cudaStream_t s);
+cudaError_t launch_chunk_wide(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a,
+                              const ChunkPlan& p, const float2* params, int d, cudaStream_t s);
 cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t s);
 cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t s);
 cudaError_t launch_pages_fork(const PagesArgs& a, const PageSlabs& sl, cudaStream_t s);
