@@ -57,15 +57,21 @@ int sm_count() {
   return n;
 }
 
-// Workspace of hs2_fa_chunk: the plan of the wide kernel, its parts, and the expanded pages of
-// a quantised cache.
+// Which kernel takes a sequence, by the rows (tokens times G) that share its KV heads' keys. The
+// narrow kernel reads the cache's codes and converts each once per 64 rows; the wide one runs
+// at the tensor pipe's rate, but FP8 / FP4 pages are expanded to bf16 for it first.
+int narrow_rows(hs2_dtype t) { return t == HS2_BF16 ? 64 : 512; }
+
+// Workspace of hs2_fa_chunk: the plans of the two kernels with their parts, and the expanded
+// pages of a quantised cache.
 struct ChunkLayout {
-  bool wide;
-  hs2::ChunkPlan plan;  // pointers as offsets until bind()
-  size_t off[10];
+  int n_plans;
+  hs2::ChunkPlan plan[2];  // narrow and / or wide; pointers after bind()
+  bool narrow[2];
+  size_t off[2][6], off_exp[4];
   int exp_seqs, exp_pages_seq;
   size_t off_ek, off_ev, off_params, total;
-  long long tiles;  // an upper bound of the tiles in all
+  long long tiles;  // an upper bound of a plan's tiles
 };
 
 ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
@@ -76,38 +82,48 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
     off = align256(off + bytes);
     return at;
   };
-  L.wide = kv->dtype != HS2_F32;
-  if (L.wide && n_rows > 0 && max_t > 0) {
-    const int G = Hq / kv->Hkv;
-    hs2::ChunkPlan& p = L.plan;
-    p.ctas = sm_count();
-    p.tile_rows = 128;
-    p.min_rows = 0;
-    p.max_rows = 0x7fffffff;
-    p.min_tiles = 4;
-    const long long units = (long long)kv->Hkv * ((long long)n_rows * G / 128 + std::min(kv->batch, n_rows));
-    p.max_units = (int)std::min<long long>(units, 1 << 30);
-    L.tiles = units * (max_t / 128 + 1);
-    L.off[0] = take(16);
-    L.off[1] = take(4 * (size_t)p.ctas);
-    L.off[2] = take(4 * (size_t)p.max_units);
-    L.off[3] = take(48 * (size_t)p.max_units);
-    L.off[4] = take(2 * (size_t)p.ctas * p.tile_rows * 8);
-    L.off[5] = take(2 * (size_t)p.ctas * p.tile_rows * kv->d * 4);
-    p.expand = low_precision(kv);
-    if (p.expand) {
-      L.exp_seqs = std::min(kv->batch, n_rows);
-      L.exp_pages_seq = cdiv(max_t, 64);
-      if (w > 0) L.exp_pages_seq = std::min<long long>(L.exp_pages_seq, ((long long)max_n + w) / 64 + 2);
-      p.max_exp_pages = L.exp_seqs * L.exp_pages_seq;
-      L.off[6] = take(4 * (size_t)L.exp_seqs);
-      L.off[7] = take(4 * (size_t)L.exp_seqs);
-      L.off[8] = take(4 * (size_t)L.exp_seqs);
-      L.off[9] = take(4);
-      const size_t rows = (size_t)L.exp_seqs * L.exp_pages_seq * kv->Hkv * 64;
-      L.off_ek = take(rows * kv->d * 2);
-      L.off_ev = take(rows * kv->d * 2);
-      L.off_params = take(rows / 64 * 8);
+  if (kv->dtype != HS2_F32 && n_rows > 0 && max_n > 0 && max_t > 0) {
+    const int G = Hq / kv->Hkv, cut = narrow_rows(kv->dtype);
+    const long long top = (long long)std::min(max_n, n_rows) * G;  // rows of the largest sequence
+    auto add = [&](bool narrow, int tile_rows, int lo, int hi, int min_tiles) {
+      hs2::ChunkPlan& p = L.plan[L.n_plans];
+      L.narrow[L.n_plans] = narrow;
+      p.ctas = sm_count();
+      p.tile_rows = tile_rows;
+      p.min_rows = lo;
+      p.max_rows = hi;
+      p.min_tiles = min_tiles;
+      const long long units = (long long)kv->Hkv * ((long long)n_rows * G / tile_rows + std::min(kv->batch, n_rows));
+      p.max_units = (int)std::min<long long>(units, 1 << 30);
+      L.tiles = std::max(L.tiles, units * (max_t / 128 + 2));
+      size_t* o = L.off[L.n_plans++];
+      o[0] = take(16);
+      o[1] = take(4 * (size_t)p.ctas);
+      o[2] = take(4 * (size_t)p.max_units);
+      o[3] = take(48 * (size_t)p.max_units);
+      o[4] = take(2 * (size_t)p.ctas * tile_rows * 8);
+      o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
+      return &p;
+    };
+    const long long few = std::min<long long>(top, cut);
+    add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut, 2);
+    if (top > cut) {
+      hs2::ChunkPlan* p = add(false, 128, cut, 0x7fffffff, 4);
+      p->expand = low_precision(kv);
+      if (p->expand) {
+        L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut + 1));
+        L.exp_pages_seq = cdiv(max_t, 64);
+        if (w > 0) L.exp_pages_seq = (int)std::min<long long>(L.exp_pages_seq, ((long long)max_n + w) / 64 + 2);
+        const long long pages = (long long)L.exp_seqs * L.exp_pages_seq;
+        if (pages * kv->Hkv * 64 > 0x7fffffff) L.tiles = 1LL << 40;  // beyond a tensor map's rows
+        p->max_exp_pages = (int)std::min<long long>(pages, 0x7fffffff);
+        for (int i = 0; i < 3; ++i) L.off_exp[i] = take(4 * (size_t)L.exp_seqs);
+        L.off_exp[3] = take(4);
+        const size_t rows = (size_t)pages * kv->Hkv * 64;
+        L.off_ek = take(rows * kv->d * 2);
+        L.off_ev = take(rows * kv->d * 2);
+        L.off_params = take(rows / 64 * 8);
+      }
     }
   }
   L.total = std::max<size_t>(off, 256);
@@ -115,17 +131,21 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
 }
 
 void bind(ChunkLayout& L, char* ws) {
-  hs2::ChunkPlan& p = L.plan;
-  p.head = (int32_t*)(ws + L.off[0]);
-  p.cta_first = (int32_t*)(ws + L.off[1]);
-  p.arrive = (int32_t*)(ws + L.off[2]);
-  p.units = (int32_t*)(ws + L.off[3]);
-  p.part_ml = (float*)(ws + L.off[4]);
-  p.part_o = (float*)(ws + L.off[5]);
-  p.exp_seq = (int32_t*)(ws + L.off[6]);
-  p.exp_base = (int32_t*)(ws + L.off[7]);
-  p.exp_page = (int32_t*)(ws + L.off[8]);
-  p.exp_head = (int32_t*)(ws + L.off[9]);
+  for (int i = 0; i < L.n_plans; ++i) {
+    hs2::ChunkPlan& p = L.plan[i];
+    p.head = (int32_t*)(ws + L.off[i][0]);
+    p.cta_first = (int32_t*)(ws + L.off[i][1]);
+    p.arrive = (int32_t*)(ws + L.off[i][2]);
+    p.units = (int32_t*)(ws + L.off[i][3]);
+    p.part_ml = (float*)(ws + L.off[i][4]);
+    p.part_o = (float*)(ws + L.off[i][5]);
+    if (p.expand) {
+      p.exp_seq = (int32_t*)(ws + L.off_exp[0]);
+      p.exp_base = (int32_t*)(ws + L.off_exp[1]);
+      p.exp_page = (int32_t*)(ws + L.off_exp[2]);
+      p.exp_head = (int32_t*)(ws + L.off_exp[3]);
+    }
+  }
 }
 
 bool valid_pages(const hs2_pages* p) { return p && p->ref && p->free_list && p->n_free && p->num_pages >= 1; }
@@ -209,7 +229,9 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
   if (Hq > 65535 || (kv->max_pages > (1 << 24))) return HS2_ERR_UNSUPPORTED;
   ChunkLayout L = chunk_layout(n_rows, Hq, kv, max_n, max_t, w);
-  if (L.tiles > 1LL << 30 || kv->Hkv > 65535) return HS2_ERR_UNSUPPORTED;  // 32-bit tile counts, grid y
+  // 32-bit tile counts and pool rows; grid y
+  if (L.tiles > 1LL << 30 || (long long)kv->num_pages * kv->Hkv * 64 > 0x7fffffff - 64 || kv->Hkv > 65535)
+    return HS2_ERR_UNSUPPORTED;
   if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < L.total) return HS2_ERR_ARG;
   hs2::ChunkArgs a{};
   a.q = q;
@@ -231,7 +253,7 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   a.seq_len = kv->seq_len;
   a.num_pages = kv->num_pages;
   a.max_pages = kv->max_pages;
-  a.w = w;
+  a.w = w >= max_t ? 0 : w;  // a window that hides nothing
   a.scale_log2 = scale * 1.4426950408889634f;
   a.sink = sink;
   a.o = o;
@@ -239,28 +261,42 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   a.lse = lse;
   a.dev_err = dev_err;
   cudaStream_t s = (cudaStream_t)stream;
-  if (!L.wide) {
-    const cudaError_t e = hs2::launch_chunk_cc(a, kv->d, kv->dtype, s);
+  if (kv->dtype == HS2_F32) {
+    const cudaError_t e = hs2::launch_chunk_cc(a, kv->d, s);
     return e == cudaSuccess ? HS2_OK : cuda_fail(e);
   }
   char* ws = (char*)workspace;
   bind(L, ws);
-  const hs2::ChunkPlan& p = L.plan;
-  const uint64_t rows = (uint64_t)(p.expand ? p.max_exp_pages : kv->num_pages) * kv->Hkv * 64;
-  CUtensorMap tq, tk, tv;
-  if (!encode_3d_bf16(&tq, q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, a.G, 128 / a.G) ||
-      !encode_2d_bf16(&tk, p.expand ? ws + L.off_ek : kv->k, kv->d, rows, 64) ||
-      !encode_2d_bf16(&tv, p.expand ? ws + L.off_ev : kv->v, kv->d, rows, 64))
-    return HS2_ERR_ARG;
-  cudaError_t e = hs2::launch_chunk_plan(a, &p, 1, s);
-  if (e != cudaSuccess) return cuda_fail(e);
-  float2* params = p.expand ? (float2*)(ws + L.off_params) : nullptr;
-  if (p.expand) {
-    e = hs2::launch_chunk_expand(a, p, kv->d, kv->dtype, ws + L.off_ek, ws + L.off_ev, params, L.exp_seqs,
-                                 L.exp_pages_seq, s);
-    if (e != cudaSuccess) return cuda_fail(e);
+  // every tensor map before the first launch, so that an error launches nothing
+  CUtensorMap map[2][3];
+  const uint64_t pool_rows = (uint64_t)kv->num_pages * kv->Hkv * 64;
+  for (int i = 0; i < L.n_plans; ++i) {
+    const hs2::ChunkPlan& p = L.plan[i];
+    bool ok;
+    if (L.narrow[i] && low_precision(kv)) {
+      const uint32_t row = kv->dtype == HS2_FP8_E4M3 ? kv->d : kv->d / 2;
+      ok = encode_2d_bytes(&map[i][1], kv->k, row, pool_rows, 64) && encode_2d_bytes(&map[i][2], kv->v, row, pool_rows, 64);
+    } else {
+      const uint64_t rows = p.expand ? (uint64_t)p.max_exp_pages * kv->Hkv * 64 : pool_rows;
+      ok = encode_2d_bf16(&map[i][1], p.expand ? ws + L.off_ek : kv->k, kv->d, rows, 64) &&
+           encode_2d_bf16(&map[i][2], p.expand ? ws + L.off_ev : kv->v, kv->d, rows, 64);
+    }
+    if (!L.narrow[i]) ok = ok && encode_3d_bf16(&map[i][0], q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, a.G, 128 / a.G);
+    if (!ok) return HS2_ERR_ARG;
   }
-  e = hs2::launch_chunk_wide(tq, tk, tv, a, p, params, kv->d, s);
+  cudaError_t e = hs2::launch_chunk_plan(a, L.plan, L.n_plans, s);
+  for (int i = 0; i < L.n_plans && e == cudaSuccess; ++i) {
+    const hs2::ChunkPlan& p = L.plan[i];
+    if (L.narrow[i]) {
+      e = hs2::launch_chunk_narrow(map[i][1], map[i][2], a, p, kv->d, kv->dtype, s);
+      continue;
+    }
+    float2* params = p.expand ? (float2*)(ws + L.off_params) : nullptr;
+    if (p.expand)
+      e = hs2::launch_chunk_expand(a, p, kv->d, kv->dtype, ws + L.off_ek, ws + L.off_ev, params, L.exp_seqs,
+                                   L.exp_pages_seq, s);
+    if (e == cudaSuccess) e = hs2::launch_chunk_wide(map[i][0], map[i][1], map[i][2], a, p, params, kv->d, s);
+  }
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 

@@ -1,9 +1,8 @@
-// chunk_cc.cu — attention of a ragged batch of query chunks on the CUDA cores.
+// chunk_cc.cu — attention of a ragged batch of query chunks over a float32 cache.
 //
 // x(s) = scale q . k(s) over the row's visible keys, one pass with the running maximum and
-// sum: every key costs a warp one 32-lane dot product.
-#include <cuda_fp16.h>
-
+// sum: every key costs a warp one 32-lane dot product. On the CUDA cores, because the tensor
+// cores have no fp32 product and a float32 cache is kept for its exactness (1e-4, not 2e-2).
 #include "common.cuh"
 #include "kernels.h"
 #include "ragged.cuh"
@@ -15,44 +14,21 @@ namespace {
 constexpr int kCcWarps = 8;
 constexpr int kCcKeys = 4;  // keys per warp step: their loads and reductions overlap
 
-// V consecutive channels of a pool row as floats.
-template <int FMT, int V>
-HS2_DEVI void load_row(const uint8_t* pool, const float* scale, const uint8_t* sf, size_t line, int D, int ch,
-                       float (&x)[V]) {
-  if constexpr (FMT == HS2_F32) {
-    const float* p = reinterpret_cast<const float*>(pool) + line * D + ch;
+// V consecutive floats of a row.
+template <int V>
+HS2_DEVI void load_row(const void* rows, size_t line, int D, int ch, float (&x)[V]) {
+  const float* p = reinterpret_cast<const float*>(rows) + line * D + ch;
 #pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      const float2 v = *reinterpret_cast<const float2*>(p + i);
-      x[i] = v.x, x[i + 1] = v.y;
-    }
-  } else if constexpr (FMT == HS2_BF16) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(pool) + (line * D + ch) / 2;
-#pragma unroll
-    for (int i = 0; i < V; i += 2) x[i] = bf16_lo(p[i / 2]), x[i + 1] = bf16_hi(p[i / 2]);
-  } else {
-    const float S = scale[line / kPage];
-#pragma unroll
-    for (int i = 0; i < V; i += 2) {
-      uint32_t h;
-      if constexpr (FMT == HS2_FP8_E4M3) {
-        h = fp8x2_to_f16x2(*reinterpret_cast<const uint16_t*>(pool + line * D + ch + i));
-      } else {
-        uint32_t u1, u2, u3;
-        fp4x8_to_f16x8(pool[(line * D + ch + i) / 2], h, u1, u2, u3);
-        const uint32_t s = sf[(line * D + ch) / 16];
-        h = hmul2(h, e4m3_pair(s, s));
-      }
-      const float2 f = __half22float2(*reinterpret_cast<__half2*>(&h));
-      x[i] = f.x * S, x[i + 1] = f.y * S;
-    }
+  for (int i = 0; i < V; i += 2) {
+    const float2 v = *reinterpret_cast<const float2*>(p + i);
+    x[i] = v.x, x[i + 1] = v.y;
   }
 }
 
 }  // namespace
 
 // grid (rows, query heads), 8 warps over the row's keys, merged through shared memory.
-template <int D, int FMT>
+template <int D>
 __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs a) {
   constexpr int V = D / 32;
   __shared__ float sm_m[kCcWarps], sm_l[kCcWarps], sm_o[kCcWarps][D];
@@ -69,8 +45,7 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
   }
   const int32_t* bt = a.bt + (size_t)pl.b * a.max_pages;
   float q[V];
-  load_row<FMT == HS2_F32 ? HS2_F32 : HS2_BF16, V>(reinterpret_cast<const uint8_t*>(a.q), nullptr, nullptr,
-                                                   (size_t)r * a.Hq + h, D, V * lane, q);
+  load_row<V>(a.q, (size_t)r * a.Hq + h, D, V * lane, q);
   const int lo = a.w > 0 ? max(0, pl.pos - a.w + 1) : 0;
   float m = -INFINITY, l = 0.f, o[V];
 #pragma unroll
@@ -91,8 +66,8 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
       }
       const size_t line = ((size_t)phys * a.Hkv + g) * kPage + s % kPage;
       float k[V], dot = 0.f;
-      load_row<FMT, V>(reinterpret_cast<const uint8_t*>(a.k), a.k_scale, a.k_sf, line, D, V * lane, k);
-      load_row<FMT, V>(reinterpret_cast<const uint8_t*>(a.v), a.v_scale, a.v_sf, line, D, V * lane, vv[j]);
+      load_row<V>(a.k, line, D, V * lane, k);
+      load_row<V>(a.v, line, D, V * lane, vv[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) dot = fmaf(q[i], k[i], dot);
       x[j] = warp_sum(dot) * a.scale_log2;
@@ -136,21 +111,11 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
   if (a.lse && threadIdx.x == 0) a.lse[at] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
 }
 
-template <int D>
-static cudaError_t launch_cc(const ChunkArgs& a, int dtype, cudaStream_t s) {
+cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s) {
   const dim3 grid(a.n_rows, a.Hq);
-  switch (dtype) {
-    case HS2_F32: chunk_cc_kernel<D, HS2_F32><<<grid, kCcWarps * 32, 0, s>>>(a); break;
-    case HS2_BF16: chunk_cc_kernel<D, HS2_BF16><<<grid, kCcWarps * 32, 0, s>>>(a); break;
-    case HS2_FP8_E4M3: chunk_cc_kernel<D, HS2_FP8_E4M3><<<grid, kCcWarps * 32, 0, s>>>(a); break;
-    case HS2_FP4_E2M1: chunk_cc_kernel<D, HS2_FP4_E2M1><<<grid, kCcWarps * 32, 0, s>>>(a); break;
-    default: return cudaErrorInvalidValue;
-  }
+  if (d == 128) chunk_cc_kernel<128><<<grid, kCcWarps * 32, 0, s>>>(a);
+  else chunk_cc_kernel<64><<<grid, kCcWarps * 32, 0, s>>>(a);
   return cudaGetLastError();
-}
-
-cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, int dtype, cudaStream_t s) {
-  return d == 128 ? launch_cc<128>(a, dtype, s) : launch_cc<64>(a, dtype, s);
 }
 
 }  // namespace hs2

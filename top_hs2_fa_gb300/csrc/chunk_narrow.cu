@@ -1,0 +1,850 @@
+// chunk_narrow.cu — attention of few query rows per KV head (draft tokens, single tokens) on
+// tcgen05, straight from the cache's codes.
+//
+// Bound by the cache's bytes: up to 64 rows share every key, so the keys take the MMAs' M side
+// and the rows N = 16, 32 or 64 of it: S^T[128 keys][N] = K Q^T and O^T[d][N] += V^T P^T cost
+// tensor time in proportion to N, and a thread of the softmax owns one key. Codes are
+// converted once per key whatever N is (a scan that keeps the rows on the MMA's other side pays the
+// conversions' instructions per 8 rows). Per 128-key tile, pipelined over rings:
+//   warp 0       producer: TMA of the tile's two pages (codes, group scales)
+//   warps 4-7    K: codes -> f16 (code * group scale, exact) -> tensor memory, S's A operand
+//   warps 8-11   V: codes -> f16 -> shared memory, O's A operand (MN-major); rows that are not
+//                there are zeros
+//   warp 1       MMA issuer
+//   warps 12-15  softmax: p = 2^(x c + nm), nm = 6 - m per row with the reference m moving only
+//                when a weight would exceed 2^14 (f16 P keeps weights down to 2^-30 of the
+//                largest); the normaliser is summed in fp32 from unrounded weights, per thread
+//   warp 2       Q of the next unit: f16 after an exact power of two that fits its range
+// A bf16 cache skips the conversions: its TMA tiles are the operands (bf16 Q, P).
+// The page's K scale multiplies the logits; V's enters the weights relative to a unit that O is
+// kept in. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the softmax
+// warps leave their loops together (they meet at hardware barriers).
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "chunk_plan.cuh"
+#include "tc.cuh"
+
+namespace hs2 {
+
+namespace {
+
+constexpr int kNThreads = 512;
+constexpr float kBias = 6.f;     // log2 of the weight of a key at the reference max
+constexpr float kTop = 14.f;     // log2 of the largest weight before the reference moves
+constexpr float kUnset = 1e30f;  // nm of a row that has seen no key
+
+template <int D, int FMT, int N>
+struct NarrowSmem {
+  static constexpr bool QUANT = FMT != HS2_BF16;
+  static constexpr int RB = FMT == HS2_FP4_E2M1 ? D / 2 : FMT == HS2_FP8_E4M3 ? D : 2 * D;  // bytes of a row
+  static constexpr int SF = FMT == HS2_FP4_E2M1 ? D / 16 : 0;                               // group scales of a row
+  static constexpr int CODES = 128 * RB;
+  static constexpr int STAGE = 2 * CODES + 2 * 128 * SF;
+  static constexpr int STAGES = FMT == HS2_BF16 ? 2 : FMT == HS2_FP8_E4M3 ? (D == 128 && N == 64 ? 2 : 3) : 5;
+  static constexpr int VTILE = 128 * D * 2;
+  static constexpr int NB = D / 64;
+  uint8_t ring[STAGES][(STAGE + 1023) / 1024 * 1024];
+  uint8_t v[QUANT ? 2 : 1][QUANT ? VTILE : 1024];
+  uint8_t p[2][128 * 128];  // also the merge's factors
+  uint8_t q[2][NB * N * 128];
+  alignas(16) float nm[N], alpha[N], fin[N], warp_l[4][N], warp_m[4][N];
+  float qmul[2];
+  uint64_t ring_full[STAGES], ring_empty[STAGES];
+  uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full[2], q_empty[2],
+      o_empty[2];
+  uint32_t tmem_base;
+  int abort, last;
+};
+
+template <typename S>
+HS2_DEVI bool halted(S& sm) { return *(volatile int*)&sm.abort != 0; }
+template <typename S>
+HS2_DEVI void halt(S& sm, int32_t* dev_err) {
+  flag_error(dev_err, HS2_DEV_TIMEOUT);
+  atomicExch(&sm.abort, 1);
+}
+
+// Barrier 1 of the 128 softmax threads: whether any of them passes true.
+HS2_DEVI bool any_of_128(bool v) {
+  int r;
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, 1, 128, q;\n\tselp.b32 %0, 1, 0, p;}"
+      : "=r"(r)
+      : "r"((int)v)
+      : "memory");
+  return r != 0;
+}
+
+HS2_DEVI float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+HS2_DEVI void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   tc::smem_u32(smem)),
+               "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+               : "memory");
+}
+
+// N columns of a lane quadrant into registers (16, or 32).
+template <int C>
+HS2_DEVI void tmem_cols(uint32_t addr, float (&x)[C]) {
+  if constexpr (C == 32) {
+    tc::tmem_ld32(addr, x);
+  } else {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+  }
+}
+template <int C>
+HS2_DEVI void tmem_put(uint32_t addr, const float (&x)[C]) {
+  if constexpr (C == 32) {
+    tc::tmem_st32(addr, x);
+  } else {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(addr),
+        "r"(__float_as_uint(x[0])), "r"(__float_as_uint(x[1])), "r"(__float_as_uint(x[2])), "r"(__float_as_uint(x[3])),
+        "r"(__float_as_uint(x[4])), "r"(__float_as_uint(x[5])), "r"(__float_as_uint(x[6])), "r"(__float_as_uint(x[7])),
+        "r"(__float_as_uint(x[8])), "r"(__float_as_uint(x[9])), "r"(__float_as_uint(x[10])), "r"(__float_as_uint(x[11])),
+        "r"(__float_as_uint(x[12])), "r"(__float_as_uint(x[13])), "r"(__float_as_uint(x[14])), "r"(__float_as_uint(x[15]))
+        : "memory");
+  }
+}
+
+// 16-byte unit c of a row of RB bytes in a TMA tile swizzled by the row's width.
+template <int RB>
+HS2_DEVI int code_unit(int row, int c) {
+  const int x = RB == 128 ? (row & 7) : RB == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1);
+  return row * RB + ((c ^ x) << 4);
+}
+
+// 32 (FP4) or 16 (FP8) consecutive channels, one 16-byte unit of codes, as f16 pairs.
+template <int FMT>
+HS2_DEVI void unit_to_f16(const uint4& w, uint32_t sf2, uint32_t* h) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  if constexpr (FMT == HS2_FP4_E2M1) {
+    const uint32_t s0 = e4m3_pair(sf2, sf2), s1 = e4m3_pair(sf2 >> 8, sf2 >> 8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fp4x8_to_f16x8(x[i], h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[4 * i + j] = hmul2(h[4 * i + j], i < 2 ? s0 : s1);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) fp8x4_to_f16x4(x[i], h[2 * i], h[2 * i + 1]);
+  }
+}
+
+// Sums of 32 per-lane values over the warp's lanes: lane i gets the sum of column `i`.
+HS2_DEVI float transpose_sum32(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      if (i < s) {
+        const float give = up ? v[i] : v[i + s], keep = up ? v[i + s] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+      }
+    }
+  }
+  return v[0];
+}
+
+// kind::f16 instruction descriptor: M = 128, N, fp32 accumulators, f16 or bf16 operands.
+constexpr uint32_t narrow_idesc(bool bf16, int N, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) |
+         ((uint32_t)(N >> 3) << 17) | (8u << 24);
+}
+
+}  // namespace
+
+template <int D, int FMT, int N>
+__global__ void __launch_bounds__(kNThreads, 1)
+    chunk_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const ChunkArgs a, const ChunkPlan p) {
+  using Sm = NarrowSmem<D, FMT, N>;
+  constexpr bool QUANT = Sm::QUANT, BF = !QUANT;
+  constexpr int ST = Sm::STAGES, NB = Sm::NB, CODES = Sm::CODES, SF = Sm::SF, RB = Sm::RB;
+  constexpr int C = N < 32 ? N : 32;  // columns of a softmax step
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  Sm& sm = *reinterpret_cast<Sm*>(dsmem + ((1024 - (tc::smem_u32(dsmem) & 1023)) & 1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < ST; ++s) {
+      tc::mbar_init(&sm.ring_full[s], 1);
+      tc::mbar_init(&sm.ring_empty[s], QUANT ? 256 : 2);  // K and V warps; bf16: the two MMAs
+    }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&sm.k_full[s], 128);
+      tc::mbar_init(&sm.k_empty[s], 1);
+      tc::mbar_init(&sm.v_full[s], 128);
+      tc::mbar_init(&sm.s_full[s], 1);
+      tc::mbar_init(&sm.s_empty[s], 128);
+      tc::mbar_init(&sm.p_full[s], 128);
+      tc::mbar_init(&sm.pv_done[s], 1);
+      tc::mbar_init(&sm.q_full[s], 32);
+      tc::mbar_init(&sm.q_empty[s], 2);  // the last S of the unit, and the softmax's read of qmul
+      tc::mbar_init(&sm.o_empty[s], 128);
+    }
+    sm.abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) tc::tmem_alloc(&sm.tmem_base, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  griddep_wait();
+  const uint32_t tK = sm.tmem_base, tS = tK + 128, tO = tK + 256;  // each two buffers
+  const ChunkRange rg = chunk_range(p, blockIdx.x);
+  const int per = p.head[1];
+  // the two pages of a unit's tile j: the physical page, or -1
+  auto page_at = [&](const ChunkUnit& u, int lp) -> int {
+    if (lp >= u.npages) return -1;
+    const int phys = a.bt[(size_t)u.b * a.max_pages + lp];
+    return phys >= 0 && phys < a.num_pages ? phys : -1;
+  };
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ producer
+    int issued = 0;
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
+      const ChunkUnit u = load_unit(p, un);
+      const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
+      at = u.prefix + j1;
+      for (int c0 = j0; ok && c0 < j1; c0 += 16) {
+        // the table entries of 16 tiles, one per lane
+        const int lp = u.page0 + 2 * c0 + lane;
+        const int mine = page_at(u, lp);
+        if (mine < 0 && lp < u.npages && lp < u.page0 + 2 * j1) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        const int c1 = min(j1, c0 + 16);
+        for (int j = c0; j < c1; ++j) {
+          const int st = issued % ST;
+          const int ph0 = __shfl_sync(0xffffffffu, mine, 2 * (j - c0)), ph1 = __shfl_sync(0xffffffffu, mine, 2 * (j - c0) + 1);
+          if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_empty[st], ((issued / ST) & 1) ^ 1))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            uint8_t* s = sm.ring[st];
+            uint64_t* bar = &sm.ring_full[st];
+            if constexpr (QUANT) {
+              const int pages = (ph0 >= 0) + (ph1 >= 0);
+              if (pages) tc::mbar_arrive_expect_tx(bar, pages * (CODES + 128 * SF));
+              else tc::mbar_arrive(bar);
+              for (int h = 0; h < 2; ++h) {
+                const int ph = h ? ph1 : ph0;
+                if (ph < 0) continue;
+                const int row = (ph * a.Hkv + u.g) * kPage;
+                tc::tma_load_2d(s + h * (CODES / 2), &tm_k, 0, row, bar);
+                tc::tma_load_2d(s + CODES + h * (CODES / 2), &tm_v, 0, row, bar);
+                if constexpr (SF > 0) {
+                  bulk_load(s + 2 * CODES + h * 64 * SF, a.k_sf + (size_t)row * SF, 64 * SF, bar);
+                  bulk_load(s + 2 * CODES + 128 * SF + h * 64 * SF, a.v_sf + (size_t)row * SF, 64 * SF, bar);
+                }
+              }
+            } else {
+              const int oob = a.num_pages * a.Hkv * kPage;  // the row past the pool: zeros
+              tc::mbar_arrive_expect_tx(bar, 2 * CODES);
+              for (int h = 0; h < 2; ++h) {
+                const int ph = h ? ph1 : ph0;
+                const int row = ph >= 0 ? (ph * a.Hkv + u.g) * kPage : oob;
+                for (int c = 0; c < NB; ++c) {
+                  tc::tma_load_2d(s + c * 16384 + h * 8192, &tm_k, 64 * c, row, bar);
+                  tc::tma_load_2d(s + CODES + c * 16384 + h * 8192, &tm_v, 64 * c, row, bar);
+                }
+              }
+            }
+          }
+          ++issued;
+        }
+      }
+    }
+    if (!ok && lane == 0) halt(sm, a.dev_err);
+    if (lane == 0)
+      for (int i = max(0, issued - ST); i < issued; ++i) (void)tc::mbar_wait(&sm.ring_full[i % ST], (i / ST) & 1);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t idS = narrow_idesc(BF, N, false, false), idO = narrow_idesc(BF, N, true, true);
+      int pv = 0, si = 0;
+      bool ok = true;
+      int s_at = rg.begin, s_un = rg.first_unit, s_seg = 0, s_prefix = 0, s_end = 0;
+      auto enter = [&]() {  // the S cursor's unit: its first tile's place on the line, and where it ends here
+        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)s_un + 6);
+        s_prefix = pt.y;
+        s_end = min(rg.end, pt.y + pt.x);
+      };
+      if (s_at < rg.end) enter();
+      auto issue_s = [&]() -> bool {
+        const int b = si & 1, qb = s_seg & 1, st = si % ST;
+        if ((s_at == rg.begin || s_at == s_prefix) && !tc::mbar_wait(&sm.q_full[qb], (s_seg >> 1) & 1)) return false;
+        if (!tc::mbar_wait(&sm.s_empty[b], ((si >> 1) & 1) ^ 1)) return false;
+        if (QUANT) {
+          if (!tc::mbar_wait(&sm.k_full[b], (si >> 1) & 1)) return false;
+        } else {
+          if (!tc::mbar_wait(&sm.ring_full[st], (si / ST) & 1)) return false;
+        }
+        tc::tc_fence_after();
+        const uint32_t q0 = tc::smem_u32(sm.q[qb]), k0 = tc::smem_u32(sm.ring[st]);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t qd = tc::sdesc_sw128(q0 + (ks >> 2) * (N * 128u) + (ks & 3) * 32u);
+          if (QUANT) tc::mma_bf16_ts(tS + b * 64, tK + b * 64 + ks * 8, qd, idS, ks > 0 ? 1u : 0u);
+          else tc::mma_bf16(tS + b * 64, tc::sdesc_sw128(k0 + (ks >> 2) * 16384u + (ks & 3) * 32u), qd, idS, ks > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&sm.s_full[b]);
+        if (QUANT) tc::mma_commit(&sm.k_empty[b]);
+        else tc::mma_commit(&sm.ring_empty[st]);
+        ++si;
+        if (++s_at == s_end) {
+          tc::mma_commit(&sm.q_empty[qb]);
+          ++s_seg;
+          ++s_un;
+          if (s_at < rg.end) enter();
+        }
+        return true;
+      };
+      if (rg.begin < rg.end) ok = issue_s();
+      int seg = 0;
+      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
+        const int j0 = at - pt.y, j1 = min(pt.x, rg.end - pt.y);
+        at = pt.y + j1;
+        const uint32_t o = tO + (seg & 1) * 64;
+        if (!tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1)) { ok = false; break; }
+        for (int j = j0; j < j1; ++j) {
+          if (s_at < rg.end && !issue_s()) { ok = false; break; }
+          const int b = pv & 1, st = pv % ST;
+          if (!tc::mbar_wait(&sm.v_full[b], (pv >> 1) & 1) || !tc::mbar_wait(&sm.p_full[b], (pv >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          tc::tc_fence_after();
+          const uint32_t v0 = QUANT ? tc::smem_u32(sm.v[b]) : tc::smem_u32(sm.ring[st] + CODES), p0 = tc::smem_u32(sm.p[b]);
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)  // 16 keys each. D = 64: the upper 64 rows of M are not read back
+            tc::mma_bf16(o, tc::sdesc_sw128_mn(v0 + ks * 2048u, 16384u, 1024u),
+                         tc::sdesc_sw128_mn(p0 + ks * 2048u, 16384u, 1024u), idO, (j > j0 || ks > 0) ? 1u : 0u);
+          tc::mma_commit(&sm.pv_done[b]);
+          if (!QUANT) tc::mma_commit(&sm.ring_empty[st]);
+          ++pv;
+        }
+      }
+      if (!ok) halt(sm, a.dev_err);
+      if (pv > 0) (void)tc::mbar_wait(&sm.pv_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1);
+      if (si > pv) (void)tc::mbar_wait(&sm.s_full[(si - 1) & 1], ((si - 1) >> 1) & 1);
+    }
+  } else if (warp == 2) {
+    // ------------------------------------------------------------------ Q
+    int seg = 0;
+    for (int at = rg.begin, un = rg.first_unit; at < rg.end; ++un, ++seg) {
+      const ChunkUnit u = load_unit(p, un);
+      at = min(rg.end, u.prefix + u.ntiles);
+      const int qb = seg & 1;
+      const int rows = u.ntok * a.G;
+      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)u.row * a.Hq + (size_t)u.g * a.G) * D;
+      // 16-byte unit i: row i / (D / 8) (token-major, then head), channels 8 (i % (D / 8))
+      auto fetch = [&](int i) -> uint4 {
+        const int r = i / (D / 8), k = i % (D / 8);
+        if (r >= rows) return make_uint4(0, 0, 0, 0);
+        return __ldg(reinterpret_cast<const uint4*>(q + ((size_t)(r / a.G) * a.Hq + r % a.G) * D) + k);
+      };
+      constexpr int UNITS = N * D / 8;
+      float mul = 1.f;
+      if (QUANT) {
+        // the largest finite exponent among the unit's queries moves to 14
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int i = lane; i < UNITS; i += 32) {
+          const uint4 w = fetch(i);
+          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t lo = (x[j] >> 7) & 0xFFu, hi = (x[j] >> 23) & 0xFFu;
+            if (lo != 255u) top = max(top, lo);
+            if (hi != 255u) top = max(top, hi);
+          }
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        const int ex = max((int)top - 127, -100);
+        mul = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);  // 2^(14 - ex)
+      }
+      if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty[qb], ((seg >> 1) & 1) ^ 1))) {
+        if (lane == 0) halt(sm, a.dev_err);
+        break;
+      }
+#pragma unroll 4
+      for (int i = lane; i < UNITS; i += 32) {
+        const int r = i / (D / 8), k = i % (D / 8);
+        uint4 w = fetch(i);
+        if (QUANT) {
+          uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * mul, bf16_hi(x[j]) * mul);
+        }
+        *reinterpret_cast<uint4*>(sm.q[qb] + (k >> 3) * (N * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = w;
+      }
+      if (lane == 0) sm.qmul[qb] = 1.f / mul;
+      tc::fence_async_smem();
+      tc::mbar_arrive(&sm.q_full[qb]);
+    }
+  } else if (warp >= 4 && warp < 12) {
+    // ------------------------------------------------------------------ K and V operands
+    const bool is_v = warp >= 8;
+    const int qd = warp & 3, key = qd * 32 + lane;
+    if (QUANT || is_v) {
+      int it = 0;
+      bool ok = true;
+      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
+        const ChunkUnit u = load_unit(p, un);
+        const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
+        at = u.prefix + j1;
+        int next = is_v ? page_at(u, u.page0 + 2 * j0 + (qd >> 1)) : 0;
+        for (int j = j0; j < j1; ++j, ++it) {
+          const int st = it % ST, b = it & 1;
+          const int phys = next;
+          if (is_v && j + 1 < j1) next = page_at(u, u.page0 + 2 * (j + 1) + (qd >> 1));
+          if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1))) { ok = false; break; }
+          const int pos = (u.page0 + 2 * j) * kPage + key;
+          if constexpr (QUANT) {
+            const uint8_t* codes = sm.ring[st] + (is_v ? CODES : 0) + (qd >> 1) * (CODES / 2);
+            const uint8_t* sfp = sm.ring[st] + 2 * CODES + (is_v ? 128 * SF : 0) + key * SF;
+            const int row = key & 63;
+            constexpr int UN = RB / 16;           // 16-byte units of codes in a row
+            constexpr int PER = D / UN / 2;       // f16 pairs of a unit
+            uint4 w[UN];
+#pragma unroll
+            for (int c = 0; c < UN; ++c) w[c] = *reinterpret_cast<const uint4*>(codes + code_unit<RB>(row, c));
+            uint32_t sfw[2] = {0u, 0u};
+            if constexpr (SF == 8) {
+              const uint2 s8 = *reinterpret_cast<const uint2*>(sfp);
+              sfw[0] = s8.x, sfw[1] = s8.y;
+            } else if constexpr (SF == 4) {
+              sfw[0] = *reinterpret_cast<const uint32_t*>(sfp);
+            }
+            if (is_v) {
+              const bool live = phys >= 0 && pos < u.t;
+              if (!live) {
+#pragma unroll
+                for (int c = 0; c < UN; ++c) w[c] = make_uint4(0, 0, 0, 0);
+                sfw[0] = sfw[1] = 0u;
+              }
+              // the buffer is read by the P.V of two tiles ago
+              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
+#pragma unroll
+              for (int c = 0; c < UN; ++c) {
+                uint32_t h[PER];
+                unit_to_f16<FMT>(w[c], sfw[c >> 1] >> (16 * (c & 1)), h);
+#pragma unroll
+                for (int i = 0; i < PER / 4; ++i) {
+                  const int unit = c * (PER / 4) + i;  // of 8 channels
+                  *reinterpret_cast<uint4*>(sm.v[b] + (unit >> 3) * 16384 + key * 128 + (((unit & 7) ^ (key & 7)) << 4)) =
+                      make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                }
+              }
+              tc::fence_async_smem();
+              tc::mbar_arrive(&sm.ring_empty[st]);
+              tc::mbar_arrive(&sm.v_full[b]);
+            } else {
+              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.k_empty[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
+              tc::tc_fence_after();
+#pragma unroll
+              for (int hb = 0; hb < D / 64; ++hb) {  // 64 channels, 32 columns
+                uint32_t h[32];
+                constexpr int CU = UN / (D / 64);
+#pragma unroll
+                for (int c = 0; c < CU; ++c) {
+                  const int cc = hb * CU + c;
+                  unit_to_f16<FMT>(w[cc], sfw[cc >> 1] >> (16 * (cc & 1)), h + c * PER);
+                }
+                tc::tmem_st32u(tK + ((uint32_t)(qd * 32) << 16) + b * 64 + hb * 32, h);
+              }
+              tc::tc_fence_before();
+              tc::mbar_arrive(&sm.ring_empty[st]);
+              tc::mbar_arrive(&sm.k_full[b]);
+            }
+          } else {
+            // bf16: the tile is the operand; rows behind the sequence may hold anything
+            if (pos >= u.t && pos < u.npages * kPage && phys >= 0) {
+#pragma unroll
+              for (int i = 0; i < D / 8; ++i)
+                *reinterpret_cast<uint4*>(sm.ring[st] + CODES + (i >> 3) * 16384 + key * 128 + ((i & 7) << 4)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
+            tc::mbar_arrive(&sm.v_full[b]);
+          }
+        }
+      }
+      if (!ok && lane == 0) halt(sm, a.dev_err);
+    }
+  } else if (warp >= 12) {
+    // ------------------------------------------------------------------ softmax
+    const int qd = warp & 3, key = qd * 32 + lane, tid = key;
+    const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
+    int it = 0, seg = 0;
+    bool run = true;
+    struct Par {
+      float k, v0, v1;  // own page's K scale (0 and !there), both pages' V scales
+      bool there;
+    };
+    for (int at = rg.begin, un = rg.first_unit; run && at < rg.end; ++un, ++seg) {
+      const ChunkUnit u = load_unit(p, un);
+      const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
+      at = u.prefix + j1;
+      const int pos_last = u.pos0 + u.ntok - 1;
+      const uint32_t o = tO + (seg & 1) * 64;
+      float l[N];
+#pragma unroll
+      for (int n = 0; n < N; ++n) l[n] = 0.f;
+      float unit = BF ? 1.f : 0.f;
+      if (tid < N) sm.nm[tid] = kUnset;
+      int ph0 = page_at(u, u.page0 + 2 * j0), ph1 = page_at(u, u.page0 + 2 * j0 + 1);
+      auto scales = [&](int f0, int f1) -> Par {
+        const int own = qd >> 1 ? f1 : f0;
+        Par r;
+        r.there = own >= 0;
+        if (QUANT) {
+          r.k = own >= 0 ? a.k_scale[(size_t)own * a.Hkv + u.g] : 0.f;
+          r.v0 = f0 >= 0 ? a.v_scale[(size_t)f0 * a.Hkv + u.g] : 0.f;
+          r.v1 = f1 >= 0 ? a.v_scale[(size_t)f1 * a.Hkv + u.g] : 0.f;
+        } else {
+          r.k = r.v0 = r.v1 = 1.f;
+        }
+        return r;
+      };
+      Par nx = scales(ph0, ph1);
+      if (j0 + 1 < j1) ph0 = page_at(u, u.page0 + 2 * j0 + 2), ph1 = page_at(u, u.page0 + 2 * j0 + 3);
+      bool good = tc::mbar_wait(&sm.q_full[seg & 1], (seg >> 1) & 1);
+      const float cq = a.scale_log2 * (good ? *(volatile float*)&sm.qmul[seg & 1] : 1.f);
+      (void)any_of_128(false);  // nm is set, qmul has been read
+      if (tid == 0) tc::mbar_arrive(&sm.q_empty[seg & 1]);
+      for (int j = j0; j < j1; ++j, ++it) {
+        const int b = it & 1;
+        const Par par = nx;
+        if (j + 1 < j1) nx = scales(ph0, ph1);
+        if (j + 2 < j1) ph0 = page_at(u, u.page0 + 2 * j + 4), ph1 = page_at(u, u.page0 + 2 * j + 5);
+        good = good && tc::mbar_wait(&sm.s_full[b], (it >> 1) & 1);
+        good = __all_sync(0xffffffffu, good);
+        tc::tc_fence_after();
+        const int pos = (u.page0 + 2 * j) * kPage + key;
+        const float c = cq * par.k;
+        const bool edge = (u.page0 + 2 * j) * kPage + 127 > u.pos0 || (a.w > 0 && (u.page0 + 2 * j) * kPage <= pos_last - a.w);
+        // columns (rows of the unit) that see this key: [lo, hi)
+        const int ago = pos - u.pos0;  // tokens before this one do not
+        int lo = 0, hi = N;
+        if (edge) {
+          lo = ago <= 0 ? 0 : min(ago, 64) * a.G;
+          if (a.w > 0) hi = ago + a.w <= 0 ? 0 : min(ago + a.w, 64) * a.G;
+        }
+        if (!par.there) hi = 0;
+        // exponents of one step's columns, -inf where the key is hidden
+        auto exponents = [&](int n0, float (&x)[C]) {
+          tmem_cols<C>(tS + lane_off + b * 64 + n0, x);
+#pragma unroll
+          for (int n = 0; n < C; n += 4) {
+            const float4 m = *reinterpret_cast<const float4*>(sm.nm + n0 + n);
+            x[n] = fmaf(x[n], c, m.x), x[n + 1] = fmaf(x[n + 1], c, m.y);
+            x[n + 2] = fmaf(x[n + 2], c, m.z), x[n + 3] = fmaf(x[n + 3], c, m.w);
+          }
+          if (edge || !par.there) {
+#pragma unroll
+            for (int n = 0; n < C; ++n)
+              if (n0 + n < lo || n0 + n >= hi) x[n] = -INFINITY;
+          }
+        };
+        float x[C];
+        bool need = false;
+#pragma unroll
+        for (int n0 = 0; n0 < N; n0 += C) {
+          exponents(n0, x);
+          float top = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int n = 2; n < C; n += 2) top = fmax3(top, x[n], x[n + 1]);
+          need |= top > kTop;
+        }
+        const float vtop = fmaxf(fabsf(par.v0), fabsf(par.v1));
+        need |= QUANT && vtop > 2.f * unit;
+        bool moved = false;
+        if (any_of_128(need || !good || halted(sm))) {
+          moved = true;
+          if (any_of_128(!good || halted(sm))) {
+            run = false;
+            break;
+          }
+          // ---- some row's reference max, or V's unit, moves
+#pragma unroll
+          for (int n0 = 0; n0 < N; n0 += C) {
+            exponents(n0, x);
+#pragma unroll
+            for (int n = 0; n < C; ++n) {
+              float t;
+              asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(t) : "f"(x[n]));
+              if (lane == n) sm.warp_m[qd][n0 + n] = t;
+            }
+          }
+          (void)any_of_128(false);
+          float f = 1.f;
+          if (QUANT && vtop > 2.f * unit) {
+            f = unit / vtop;
+            unit = vtop;
+          }
+          if (tid < N) {
+            const float t = fmaxf(fmaxf(sm.warp_m[0][tid], sm.warp_m[1][tid]), fmaxf(sm.warp_m[2][tid], sm.warp_m[3][tid]));
+            float al = 1.f;
+            if (t > kTop) {  // t = x c + nm: the new nm is 6 - x c
+              const float old = sm.nm[tid];
+              // an unset row: x c is lost in the sum; its first reference comes from a second look
+              if (old == kUnset) {
+                sm.nm[tid] = 0.f;
+                al = 0.f;
+              } else {
+                const float to = old - t + kBias;
+                sm.nm[tid] = to;
+                al = ex2_approx(to - old);
+              }
+            }
+            sm.alpha[tid] = al;
+          }
+          (void)any_of_128(false);
+          // rows seen for the first time: their largest logit with nm = 0
+          bool fresh = false;
+          if (tid < N) fresh = sm.alpha[tid] == 0.f && sm.nm[tid] == 0.f;
+          if (any_of_128(fresh)) {
+#pragma unroll
+            for (int n0 = 0; n0 < N; n0 += C) {
+              exponents(n0, x);
+#pragma unroll
+              for (int n = 0; n < C; ++n) {
+                float t;
+                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(t) : "f"(x[n]));
+                if (lane == n) sm.warp_m[qd][n0 + n] = t;
+              }
+            }
+            (void)any_of_128(false);
+            if (fresh) {
+              const float t = fmaxf(fmaxf(sm.warp_m[0][tid], sm.warp_m[1][tid]), fmaxf(sm.warp_m[2][tid], sm.warp_m[3][tid]));
+              sm.nm[tid] = t > -INFINITY ? kBias - t : kUnset;
+            }
+            (void)any_of_128(false);
+          }
+#pragma unroll
+          for (int n = 0; n < N; ++n) l[n] *= sm.alpha[n];
+          if (j > j0) {
+            good = good && tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
+            good = __all_sync(0xffffffffu, good);
+            tc::tc_fence_after();
+#pragma unroll 1
+            for (int n0 = 0; n0 < N; n0 += C) {
+              float ov[C];
+              tmem_cols<C>(o + lane_off + n0, ov);
+#pragma unroll
+              for (int n = 0; n < C; ++n) ov[n] *= sm.alpha[n0 + n] * f;
+              tmem_put<C>(o + lane_off + n0, ov);
+            }
+          }
+          (void)any_of_128(false);  // alpha has been read
+        }
+        // ---- weights
+        if (it >= 2) good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1));
+        const float vs = qd >> 1 ? par.v1 : par.v0;
+        const float rel = BF ? 1.f : unit > 0.f ? vs / unit : 0.f;
+#pragma unroll
+        for (int n0 = 0; n0 < N; n0 += C) {
+          if (N > C || moved) exponents(n0, x);  // one step of columns is still in registers
+#pragma unroll
+          for (int n = 0; n < C; n += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float p0 = ex2_approx(x[n + 2 * i]), p1 = ex2_approx(x[n + 2 * i + 1]);
+              l[n0 + n + 2 * i] += p0;
+              l[n0 + n + 2 * i + 1] += p1;
+              w[i] = BF ? pack_bf16(p0, p1) : pack_f16(p0 * rel, p1 * rel);
+            }
+            *reinterpret_cast<uint4*>(sm.p[b] + key * 128 + ((((n0 + n) >> 3) ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(&sm.s_empty[b]);
+        tc::fence_async_smem();
+        tc::mbar_arrive(&sm.p_full[b]);
+      }
+      if (!run) break;
+      // ---- the unit's (or this part's) output
+      good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1));
+      if (any_of_128(!good || halted(sm))) {
+        run = false;
+        break;
+      }
+      tc::tc_fence_after();
+      // the normaliser of every row, over the 128 keys' threads
+#pragma unroll
+      for (int n0 = 0; n0 < N; n0 += C) {
+        if constexpr (C == 32) {
+          float t[32];
+#pragma unroll
+          for (int n = 0; n < 32; ++n) t[n] = l[n0 + n];
+          sm.warp_l[qd][n0 + lane] = transpose_sum32(t);
+        } else {
+          float t[32];
+#pragma unroll
+          for (int n = 0; n < 32; ++n) t[n] = n < C ? l[n] : 0.f;
+          const float s = transpose_sum32(t);
+          if (lane < C) sm.warp_l[qd][lane] = s;
+        }
+      }
+      (void)any_of_128(false);
+      const bool whole = j0 == 0 && j1 == u.ntiles;
+      const int rows = u.ntok * a.G;
+      auto out_row = [&](int n) -> size_t { return (size_t)(u.row + n / a.G) * a.Hq + (size_t)u.g * a.G + n % a.G; };
+      // factor of row n's output, and its lse, from its max and sum
+      auto finish = [&](int n, float M, float L) -> float {
+        const float b2 = sink_b2(a.sink, u.g * a.G + n % a.G);
+        const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
+        const float den = L * sc + exp2_rel(b2, M2);
+        if (a.lse && n < rows) a.lse[out_row(n)] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+        return den > 0.f ? sc / den : 0.f;
+      };
+      auto put = [&](int n, float v) {
+        if (n < rows && tid < D) {
+          const size_t at_o = out_row(n) * D + tid;
+          if (a.o_bf16) reinterpret_cast<__nv_bfloat16*>(a.o)[at_o] = __float2bfloat16(v);
+          else reinterpret_cast<float*>(a.o)[at_o] = v;
+        }
+      };
+      float M = -INFINITY, L = 0.f;
+      if (tid < N) {
+        M = sm.nm[tid] == kUnset ? -INFINITY : -sm.nm[tid];
+        L = sm.warp_l[0][tid] + sm.warp_l[1][tid] + sm.warp_l[2][tid] + sm.warp_l[3][tid];
+      }
+      if (whole) {
+        if (tid < N) sm.fin[tid] = finish(tid, M, L) * unit;
+        (void)any_of_128(false);
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += C) {
+          float ov[C];
+          tmem_cols<C>(o + lane_off + n0, ov);
+#pragma unroll
+          for (int n = 0; n < C; ++n) put(n0 + n, ov[n] * sm.fin[n0 + n]);
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(&sm.o_empty[seg & 1]);
+      } else {
+        const int slot = part_slot(u, per, blockIdx.x);
+        if (tid < N) reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * N + tid] = make_float2(M, L);
+        float* po = p.part_o + (size_t)slot * N * D;
+#pragma unroll 1
+        for (int n0 = 0; n0 < N; n0 += C) {
+          float ov[C];
+          tmem_cols<C>(o + lane_off + n0, ov);
+          if (tid < D)
+#pragma unroll
+            for (int n = 0; n < C; ++n) po[(size_t)(n0 + n) * D + tid] = ov[n] * unit;
+        }
+        tc::tc_fence_before();
+        tc::mbar_arrive(&sm.o_empty[seg & 1]);
+        // the last CTA to leave its part merges them all, in CTA order
+        const int c0 = u.prefix / per, c1 = (u.prefix + u.ntiles - 1) / per, parts = c1 - c0 + 1;
+        __threadfence();
+        (void)any_of_128(false);
+        if (tid == 0) sm.last = atomicAdd(&p.arrive[un], 1) == c1 - c0;
+        (void)any_of_128(false);
+        if (*(volatile int*)&sm.last) {
+          __threadfence();
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+          float Mx = -INFINITY, Lx = 0.f;
+          if (tid < N) {
+            for (int k = 0; k < parts; ++k) Mx = fmaxf(Mx, __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid).x);
+            for (int k = 0; k < parts; ++k) {
+              const float2 y = __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid);
+              Lx += exp2_rel(y.x, Mx) * y.y;
+            }
+            sm.fin[tid] = finish(tid, Mx, Lx);
+          }
+          float* fac = reinterpret_cast<float*>(sm.p);  // [parts of a round][N]: nobody writes or reads P now
+          constexpr int ROUND = 32768 / 4 / N;
+#pragma unroll 1
+          for (int n0 = 0; n0 < N; n0 += C) {
+            float acc[C];
+#pragma unroll
+            for (int n = 0; n < C; ++n) acc[n] = 0.f;
+            for (int k0 = 0; k0 < parts; k0 += ROUND) {
+              const int kn = min(ROUND, parts - k0);
+              (void)any_of_128(false);
+              if (tid < N)
+                for (int k = 0; k < kn; ++k)
+                  fac[k * N + tid] = exp2_rel(__ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + k) * N + tid).x, Mx);
+              (void)any_of_128(false);
+              if (tid < D)
+                for (int k = 0; k < kn; ++k) {
+                  const float* src = p.part_o + ((size_t)part_slot(u, per, c0 + k0 + k) * N + n0) * D + tid;
+#pragma unroll
+                  for (int n = 0; n < C; ++n) acc[n] += fac[k * N + n0 + n] * __ldcg(src + (size_t)n * D);
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < C; ++n) put(n0 + n, acc[n] * sm.fin[n0 + n]);
+          }
+        }
+      }
+      (void)any_of_128(false);  // the arrays are rewritten by the next unit
+    }
+    if (!run && lane == 0) halt(sm, a.dev_err);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tc::tmem_dealloc(sm.tmem_base, 512);
+}
+
+template <int D, int FMT, int N>
+static cudaError_t launch_n(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+                            cudaStream_t s) {
+  const size_t sm = sizeof(NarrowSmem<D, FMT, N>) + 1024;
+  static_assert(sizeof(NarrowSmem<D, FMT, N>) + 1024 <= 227 * 1024, "shared memory of a CTA");
+  auto kern = chunk_narrow_kernel<D, FMT, N>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(p.ctas), dim3(kNThreads), sm, s, tk, tv, a, p);
+}
+
+template <int D, int FMT>
+static cudaError_t launch_fmt(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+                              cudaStream_t s) {
+  switch (p.tile_rows) {
+    case 16: return launch_n<D, FMT, 16>(tk, tv, a, p, s);
+    case 32: return launch_n<D, FMT, 32>(tk, tv, a, p, s);
+    case 64: return launch_n<D, FMT, 64>(tk, tv, a, p, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_chunk_narrow(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+                                int d, int dtype, cudaStream_t s) {
+  if (d == 128) {
+    return dtype == HS2_FP4_E2M1   ? launch_fmt<128, HS2_FP4_E2M1>(tk, tv, a, p, s)
+           : dtype == HS2_FP8_E4M3 ? launch_fmt<128, HS2_FP8_E4M3>(tk, tv, a, p, s)
+                                   : launch_fmt<128, HS2_BF16>(tk, tv, a, p, s);
+  }
+  return dtype == HS2_FP4_E2M1   ? launch_fmt<64, HS2_FP4_E2M1>(tk, tv, a, p, s)
+         : dtype == HS2_FP8_E4M3 ? launch_fmt<64, HS2_FP8_E4M3>(tk, tv, a, p, s)
+                                 : launch_fmt<64, HS2_BF16>(tk, tv, a, p, s);
+}
+
+}  // namespace hs2

@@ -300,10 +300,12 @@ struct SelectArgs {
 
 cudaError_t launch_fa_decode_mma(const AttnArgs& a, int Bq, cudaStream_t s);
 cudaError_t launch_kv_rows(const RowsArgs& a, int d, int dtype, bool write, bool row_f32, cudaStream_t s);
-cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, int dtype, cudaStream_t s);
+cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s);
 cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s);
 cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, int dtype, void* ek, void* ev,
                                 float2* params, int max_seqs, int max_pages_seq, cudaStream_t s);
+cudaError_t launch_chunk_narrow(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+                                int d, int dtype, cudaStream_t s);
 cudaError_t launch_chunk_wide(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a,
                               const ChunkPlan& p, const float2* params, int d, cudaStream_t s);
 cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t s);
