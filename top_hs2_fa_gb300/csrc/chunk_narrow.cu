@@ -10,15 +10,17 @@
 //   warps 4-7    K: codes -> f16 (code * group scale, exact) -> tensor memory, S's A operand
 //   warps 8-11   V: codes -> f16 -> shared memory, O's A operand (MN-major); rows that are not
 //                there are zeros
-//   warp 1       MMA issuer
-//   warps 12-15  softmax: p = 2^(x c + nm), nm = 6 - m per row with the reference m moving only
-//                when a weight would exceed 2^14 (f16 P keeps weights down to 2^-30 of the
-//                largest); the normaliser is summed in fp32 from unrounded weights, per thread
+//   warps 1, 3   MMA issuers, of S and of O: their waits overlap the other's instructions
+//   warps 12-19  softmax, four warps for every other tile, each four with references, sums and
+//                an O of their own (joined when the unit ends): p = 2^(x c + nm), nm = 6 - m per
+//                row with the reference m moving only when a weight would exceed 2^14 (f16 P
+//                keeps weights down to 2^-30 of the largest); the normaliser is summed in fp32
+//                from unrounded weights, per thread
 //   warp 2       Q of the next unit: f16 after an exact power of two that fits its range
 // A bf16 cache skips the conversions: its TMA tiles are the operands (bf16 Q, P).
 // The page's K scale multiplies the logits; V's enters the weights relative to a unit that O is
-// kept in. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the softmax
-// warps leave their loops together (they meet at hardware barriers).
+// kept in. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four
+// softmax warps of a tile leave their loop together (they meet at a hardware barrier).
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -29,10 +31,17 @@ namespace hs2 {
 
 namespace {
 
-constexpr int kNThreads = 512;
+constexpr int kNThreads = 640;
 constexpr float kBias = 6.f;     // log2 of the weight of a key at the reference max
 constexpr float kTop = 14.f;     // log2 of the largest weight before the reference moves
 constexpr float kUnset = 1e30f;  // nm of a row that has seen no key
+constexpr int kInfo = 16;        // tiles whose pages' scales are kept: more than the pipeline holds
+
+struct __align__(16) TileInfo {
+  float k[2], v[2];  // the two pages' slab scales
+  int there[2];      // whether the page is there
+  int pad[2];
+};
 
 template <int D, int FMT, int N>
 struct NarrowSmem {
@@ -41,18 +50,23 @@ struct NarrowSmem {
   static constexpr int SF = FMT == HS2_FP4_E2M1 ? D / 16 : 0;                               // group scales of a row
   static constexpr int CODES = 128 * RB;
   static constexpr int STAGE = 2 * CODES + 2 * 128 * SF;
-  static constexpr int STAGES = FMT == HS2_BF16 ? 2 : FMT == HS2_FP8_E4M3 ? (D == 128 && N == 64 ? 2 : 3) : 5;
+  static constexpr int STAGES = FMT == HS2_BF16 ? 2 : FMT == HS2_FP8_E4M3 ? (D == 128 && N == 64 ? 2 : 3) : D == 128 && N == 64 ? 4 : 5;
   static constexpr int VTILE = 128 * D * 2;
   static constexpr int NB = D / 64;
   uint8_t ring[STAGES][(STAGE + 1023) / 1024 * 1024];
   uint8_t v[QUANT ? 2 : 1][QUANT ? VTILE : 1024];
   uint8_t p[2][128 * 128];  // also the merge's factors
   uint8_t q[2][NB * N * 128];
-  alignas(16) float nm[N], alpha[N], fin[N], warp_l[4][N], warp_m[4][N];
+  // per softmax group (even and odd tiles): nm, the last change's factors, the four warps' maxima
+  alignas(16) float nm[2][N], alpha[2][N], warp_m[2][4][N];
+  // per unit, by its parity: each group's maxima, the sums of its four warps, its V unit (0 tiles: -1)
+  alignas(16) float out_m[2][2][N], out_l[2][2][4][N], out_unit[2][2];
+  alignas(16) float fin[N];
+  TileInfo info[kInfo];
   float qmul[2];
+  uint64_t info_full[kInfo];
   uint64_t ring_full[STAGES], ring_empty[STAGES];
-  uint64_t k_full[2], k_empty[2], v_full[2], s_full[2], s_empty[2], p_full[2], pv_done[2], q_full[2], q_empty[2],
-      o_empty[2];
+  uint64_t k_full[2], s_full[2], s_empty[2], pv_ready[2], pv_done[2], q_full[2], q_empty[2], o_empty[2], out_ready[2], all;
   uint32_t tmem_base;
   int abort, last;
 };
@@ -65,21 +79,55 @@ HS2_DEVI void halt(S& sm, int32_t* dev_err) {
   atomicExch(&sm.abort, 1);
 }
 
-// Barrier 1 of the 128 softmax threads: whether any of them passes true.
-HS2_DEVI bool any_of_128(bool v) {
+// Barrier `id` of the 128 threads of a softmax group: whether any of them passes true.
+HS2_DEVI bool any_of_128(int id, bool v) {
   int r;
   asm volatile(
-      "{.reg .pred p, q; setp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, 1, 128, q;\n\tselp.b32 %0, 1, 0, p;}"
+      "{.reg .pred p, q; setp.ne.b32 q, %1, 0;\n\tbar.red.or.pred p, %2, 128, q;\n\tselp.b32 %0, 1, 0, p;}"
       : "=r"(r)
-      : "r"((int)v)
+      : "r"((int)v), "r"(id)
       : "memory");
   return r != 0;
 }
+// Registers per thread of the five 128-thread groups: 40 + 2 * 72 + 2 * 144 = 472 of the 5 * 96
+// that the block is launched with.
+constexpr int kRegsMisc = 40, kRegsCodes = 72, kRegsSoftmax = 144;
+template <int R>
+HS2_DEVI void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+HS2_DEVI void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 HS2_DEVI float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
+}
+
+// Pairs of floats in one instruction.
+struct F2 {
+  float x, y;
+};
+HS2_DEVI F2 fma2(F2 a, F2 b, F2 c) {
+  F2 d;
+  asm("{.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+HS2_DEVI F2 add2(F2 a, F2 b) {
+  F2 d;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+HS2_DEVI F2 mul2(F2 a, F2 b) {
+  F2 d;
+  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 
 HS2_DEVI void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -191,16 +239,17 @@ __global__ void __launch_bounds__(kNThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.k_full[s], 128);
-      tc::mbar_init(&sm.k_empty[s], 1);
-      tc::mbar_init(&sm.v_full[s], 128);
       tc::mbar_init(&sm.s_full[s], 1);
       tc::mbar_init(&sm.s_empty[s], 128);
-      tc::mbar_init(&sm.p_full[s], 128);
+      tc::mbar_init(&sm.pv_ready[s], 256);  // V's and P's threads
       tc::mbar_init(&sm.pv_done[s], 1);
       tc::mbar_init(&sm.q_full[s], 32);
-      tc::mbar_init(&sm.q_empty[s], 2);  // the last S of the unit, and the softmax's read of qmul
-      tc::mbar_init(&sm.o_empty[s], 128);
+      tc::mbar_init(&sm.q_empty[s], 3);  // the last S of the unit, and the two groups' reads of qmul
+      tc::mbar_init(&sm.o_empty[s], 256);
+      tc::mbar_init(&sm.out_ready[s], 256);
     }
+    for (int s = 0; s < kInfo; ++s) tc::mbar_init(&sm.info_full[s], 1);
+    tc::mbar_init(&sm.all, 256);
     sm.abort = 0;
     tc::fence_mbar_init();
   }
@@ -209,37 +258,52 @@ __global__ void __launch_bounds__(kNThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
-  const uint32_t tK = sm.tmem_base, tS = tK + 128, tO = tK + 256;  // each two buffers
+  const uint32_t tK = sm.tmem_base, tS = tK + 128, tO = tK + 256;  // two buffers; O: two groups by two units
   const ChunkRange rg = chunk_range(p, blockIdx.x);
   const int per = p.head[1];
-  // the two pages of a unit's tile j: the physical page, or -1
-  auto page_at = [&](const ChunkUnit& u, int lp) -> int {
-    if (lp >= u.npages) return -1;
-    const int phys = a.bt[(size_t)u.b * a.max_pages + lp];
-    return phys >= 0 && phys < a.num_pages ? phys : -1;
-  };
-
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
+    regs_down<kRegsMisc>();
+    // Lane i has the table entry and the scales of page i of a block of 32 (16 tiles); the next
+    // block's are fetched while this one is issued.
     int issued = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      for (int c0 = j0; ok && c0 < j1; c0 += 16) {
-        // the table entries of 16 tiles, one per lane
+      const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
+      const int page_end = min(u.npages, u.page0 + 2 * j1);
+      auto entry = [&](int c0) -> int {  // raw table entry of this lane's page of the block at tile c0
         const int lp = u.page0 + 2 * c0 + lane;
-        const int mine = page_at(u, lp);
-        if (mine < 0 && lp < u.npages && lp < u.page0 + 2 * j1) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        return lp < page_end ? bt[lp] : -1;
+      };
+      auto valid = [&](int e) { return e >= 0 && e < a.num_pages; };
+      int raw = entry(j0), raw_next = -1;
+      float ks = 1.f, vs = 1.f, ks_next = 1.f, vs_next = 1.f;
+      if (QUANT && valid(raw)) ks = a.k_scale[(size_t)raw * a.Hkv + u.g], vs = a.v_scale[(size_t)raw * a.Hkv + u.g];
+      for (int c0 = j0; ok && c0 < j1; c0 += 16) {
+        const int mine = valid(raw) ? raw : -1;
+        if (mine < 0 && u.page0 + 2 * c0 + lane < page_end) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        raw_next = entry(c0 + 16);
         const int c1 = min(j1, c0 + 16);
         for (int j = c0; j < c1; ++j) {
-          const int st = issued % ST;
-          const int ph0 = __shfl_sync(0xffffffffu, mine, 2 * (j - c0)), ph1 = __shfl_sync(0xffffffffu, mine, 2 * (j - c0) + 1);
+          if (QUANT && j == c0 + 8 && valid(raw_next)) {
+            ks_next = a.k_scale[(size_t)raw_next * a.Hkv + u.g];
+            vs_next = a.v_scale[(size_t)raw_next * a.Hkv + u.g];
+          }
+          const int st = issued % ST, l0 = 2 * (j - c0);
+          const int ph0 = __shfl_sync(0xffffffffu, mine, l0), ph1 = __shfl_sync(0xffffffffu, mine, l0 + 1);
           if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_empty[st], ((issued / ST) & 1) ^ 1))) {
             ok = false;
             break;
           }
+          if ((lane >> 1) == j - c0) {
+            TileInfo& f = sm.info[issued % kInfo];
+            f.k[lane & 1] = ks, f.v[lane & 1] = vs, f.there[lane & 1] = mine >= 0;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.info_full[issued % kInfo]);
           if (lane == 0) {
             uint8_t* s = sm.ring[st];
             uint64_t* bar = &sm.ring_full[st];
@@ -273,85 +337,78 @@ __global__ void __launch_bounds__(kNThreads, 1)
           }
           ++issued;
         }
+        raw = raw_next, ks = ks_next, vs = vs_next;
       }
     }
     if (!ok && lane == 0) halt(sm, a.dev_err);
     if (lane == 0)
       for (int i = max(0, issued - ST); i < issued; ++i) (void)tc::mbar_wait(&sm.ring_full[i % ST], (i / ST) & 1);
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------------ S = K Q^T
+    regs_down<kRegsMisc>();
     if (lane == 0) {
-      constexpr uint32_t idS = narrow_idesc(BF, N, false, false), idO = narrow_idesc(BF, N, true, true);
-      int pv = 0, si = 0;
+      constexpr uint32_t idS = narrow_idesc(BF, N, false, false);
+      int it = 0, seg = 0;
       bool ok = true;
-      int s_at = rg.begin, s_un = rg.first_unit, s_seg = 0, s_prefix = 0, s_end = 0;
-      auto enter = [&]() {  // the S cursor's unit: its first tile's place on the line, and where it ends here
-        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)s_un + 6);
-        s_prefix = pt.y;
-        s_end = min(rg.end, pt.y + pt.x);
-      };
-      if (s_at < rg.end) enter();
-      auto issue_s = [&]() -> bool {
-        const int b = si & 1, qb = s_seg & 1, st = si % ST;
-        if ((s_at == rg.begin || s_at == s_prefix) && !tc::mbar_wait(&sm.q_full[qb], (s_seg >> 1) & 1)) return false;
-        if (!tc::mbar_wait(&sm.s_empty[b], ((si >> 1) & 1) ^ 1)) return false;
-        if (QUANT) {
-          if (!tc::mbar_wait(&sm.k_full[b], (si >> 1) & 1)) return false;
-        } else {
-          if (!tc::mbar_wait(&sm.ring_full[st], (si / ST) & 1)) return false;
-        }
-        tc::tc_fence_after();
-        const uint32_t q0 = tc::smem_u32(sm.q[qb]), k0 = tc::smem_u32(sm.ring[st]);
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint64_t qd = tc::sdesc_sw128(q0 + (ks >> 2) * (N * 128u) + (ks & 3) * 32u);
-          if (QUANT) tc::mma_bf16_ts(tS + b * 64, tK + b * 64 + ks * 8, qd, idS, ks > 0 ? 1u : 0u);
-          else tc::mma_bf16(tS + b * 64, tc::sdesc_sw128(k0 + (ks >> 2) * 16384u + (ks & 3) * 32u), qd, idS, ks > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(&sm.s_full[b]);
-        if (QUANT) tc::mma_commit(&sm.k_empty[b]);
-        else tc::mma_commit(&sm.ring_empty[st]);
-        ++si;
-        if (++s_at == s_end) {
-          tc::mma_commit(&sm.q_empty[qb]);
-          ++s_seg;
-          ++s_un;
-          if (s_at < rg.end) enter();
-        }
-        return true;
-      };
-      if (rg.begin < rg.end) ok = issue_s();
-      int seg = 0;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
         const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
-        const int j0 = at - pt.y, j1 = min(pt.x, rg.end - pt.y);
-        at = pt.y + j1;
-        const uint32_t o = tO + (seg & 1) * 64;
-        if (!tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1)) { ok = false; break; }
-        for (int j = j0; j < j1; ++j) {
-          if (s_at < rg.end && !issue_s()) { ok = false; break; }
-          const int b = pv & 1, st = pv % ST;
-          if (!tc::mbar_wait(&sm.v_full[b], (pv >> 1) & 1) || !tc::mbar_wait(&sm.p_full[b], (pv >> 1) & 1)) {
-            ok = false;
-            break;
+        const int end = min(rg.end, pt.y + pt.x);
+        const int qb = seg & 1;
+        const uint32_t q0 = tc::smem_u32(sm.q[qb]);
+        ok = tc::mbar_wait(&sm.q_full[qb], (seg >> 1) & 1);
+        for (; ok && at < end; ++at, ++it) {
+          const int b = it & 1, st = it % ST;
+          ok = tc::mbar_wait(&sm.s_empty[b], ((it >> 1) & 1) ^ 1) &&
+               (QUANT ? tc::mbar_wait(&sm.k_full[b], (it >> 1) & 1) : tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1));
+          if (!ok) break;
+          tc::tc_fence_after();
+          const uint32_t k0 = tc::smem_u32(sm.ring[st]);
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t qd = tc::sdesc_sw128(q0 + (ks >> 2) * (N * 128u) + (ks & 3) * 32u);
+            if (QUANT) tc::mma_bf16_ts(tS + b * 64, tK + b * 64 + ks * 8, qd, idS, ks > 0 ? 1u : 0u);
+            else tc::mma_bf16(tS + b * 64, tc::sdesc_sw128(k0 + (ks >> 2) * 16384u + (ks & 3) * 32u), qd, idS, ks > 0 ? 1u : 0u);
           }
+          tc::mma_commit(&sm.s_full[b]);
+          if (!QUANT) tc::mma_commit(&sm.ring_empty[st]);
+        }
+        if (ok) tc::mma_commit(&sm.q_empty[qb]);
+      }
+      if (!ok) halt(sm, a.dev_err);
+      if (it > 0) (void)tc::mbar_wait(&sm.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
+    }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ O^T += V^T P^T
+    regs_down<kRegsMisc>();
+    if (lane == 0) {
+      constexpr uint32_t idO = narrow_idesc(BF, N, true, true);
+      int it = 0, seg = 0;
+      bool ok = true;
+      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
+        const int end = min(rg.end, pt.y + pt.x);
+        ok = tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
+        for (int j = 0; ok && at < end; ++at, ++it, ++j) {
+          const int b = it & 1, st = it % ST;
+          const uint32_t o = tO + ((seg & 1) * 2 + b) * 64;
+          ok = tc::mbar_wait(&sm.pv_ready[b], (it >> 1) & 1);
+          if (!ok) break;
           tc::tc_fence_after();
           const uint32_t v0 = QUANT ? tc::smem_u32(sm.v[b]) : tc::smem_u32(sm.ring[st] + CODES), p0 = tc::smem_u32(sm.p[b]);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // 16 keys each. D = 64: the upper 64 rows of M are not read back
             tc::mma_bf16(o, tc::sdesc_sw128_mn(v0 + ks * 2048u, 16384u, 1024u),
-                         tc::sdesc_sw128_mn(p0 + ks * 2048u, 16384u, 1024u), idO, (j > j0 || ks > 0) ? 1u : 0u);
+                         tc::sdesc_sw128_mn(p0 + ks * 2048u, 16384u, 1024u), idO, (j > 1 || ks > 0) ? 1u : 0u);
           tc::mma_commit(&sm.pv_done[b]);
           if (!QUANT) tc::mma_commit(&sm.ring_empty[st]);
-          ++pv;
         }
       }
       if (!ok) halt(sm, a.dev_err);
-      if (pv > 0) (void)tc::mbar_wait(&sm.pv_done[(pv - 1) & 1], ((pv - 1) >> 1) & 1);
-      if (si > pv) (void)tc::mbar_wait(&sm.s_full[(si - 1) & 1], ((si - 1) >> 1) & 1);
+      if (it > 0) (void)tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
     }
   } else if (warp == 2) {
     // ------------------------------------------------------------------ Q
+    regs_down<kRegsMisc>();
     int seg = 0;
     for (int at = rg.begin, un = rg.first_unit; at < rg.end; ++un, ++seg) {
       const ChunkUnit u = load_unit(p, un);
@@ -406,6 +463,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
     }
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ K and V operands
+    regs_down<kRegsCodes>();
     const bool is_v = warp >= 8;
     const int qd = warp & 3, key = qd * 32 + lane;
     if (QUANT || is_v) {
@@ -415,13 +473,11 @@ __global__ void __launch_bounds__(kNThreads, 1)
         const ChunkUnit u = load_unit(p, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
-        int next = is_v ? page_at(u, u.page0 + 2 * j0 + (qd >> 1)) : 0;
         for (int j = j0; j < j1; ++j, ++it) {
           const int st = it % ST, b = it & 1;
-          const int phys = next;
-          if (is_v && j + 1 < j1) next = page_at(u, u.page0 + 2 * (j + 1) + (qd >> 1));
           if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1))) { ok = false; break; }
           const int pos = (u.page0 + 2 * j) * kPage + key;
+          const bool there = is_v && sm.info[it % kInfo].there[qd >> 1] != 0;
           if constexpr (QUANT) {
             const uint8_t* codes = sm.ring[st] + (is_v ? CODES : 0) + (qd >> 1) * (CODES / 2);
             const uint8_t* sfp = sm.ring[st] + 2 * CODES + (is_v ? 128 * SF : 0) + key * SF;
@@ -439,11 +495,16 @@ __global__ void __launch_bounds__(kNThreads, 1)
               sfw[0] = *reinterpret_cast<const uint32_t*>(sfp);
             }
             if (is_v) {
-              const bool live = phys >= 0 && pos < u.t;
+              const bool live = there && pos < u.t;
               if (!live) {
 #pragma unroll
                 for (int c = 0; c < UN; ++c) w[c] = make_uint4(0, 0, 0, 0);
                 sfw[0] = sfw[1] = 0u;
+              }
+              // the rows of the tile before are handed over here, when their stores have long landed
+              if (it > 0) {
+                tc::fence_async_smem();
+                tc::mbar_arrive(&sm.pv_ready[b ^ 1]);
               }
               // the buffer is read by the P.V of two tiles ago
               if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
@@ -458,11 +519,10 @@ __global__ void __launch_bounds__(kNThreads, 1)
                       make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
                 }
               }
-              tc::fence_async_smem();
               tc::mbar_arrive(&sm.ring_empty[st]);
-              tc::mbar_arrive(&sm.v_full[b]);
             } else {
-              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.k_empty[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
+              // the buffer is read by the S of two tiles ago
+              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
               tc::tc_fence_after();
 #pragma unroll
               for (int hb = 0; hb < D / 64; ++hb) {  // 64 channels, 32 columns
@@ -473,122 +533,98 @@ __global__ void __launch_bounds__(kNThreads, 1)
                   const int cc = hb * CU + c;
                   unit_to_f16<FMT>(w[cc], sfw[cc >> 1] >> (16 * (cc & 1)), h + c * PER);
                 }
+                if (hb == 0) tc::mbar_arrive(&sm.ring_empty[st]);
                 tc::tmem_st32u(tK + ((uint32_t)(qd * 32) << 16) + b * 64 + hb * 32, h);
               }
               tc::tc_fence_before();
-              tc::mbar_arrive(&sm.ring_empty[st]);
               tc::mbar_arrive(&sm.k_full[b]);
             }
           } else {
             // bf16: the tile is the operand; rows behind the sequence may hold anything
-            if (pos >= u.t && pos < u.npages * kPage && phys >= 0) {
+            if (there && pos >= u.t) {
 #pragma unroll
               for (int i = 0; i < D / 8; ++i)
                 *reinterpret_cast<uint4*>(sm.ring[st] + CODES + (i >> 3) * 16384 + key * 128 + ((i & 7) << 4)) =
                     make_uint4(0, 0, 0, 0);
             }
             tc::fence_async_smem();
-            tc::mbar_arrive(&sm.v_full[b]);
+            tc::mbar_arrive(&sm.pv_ready[b]);
           }
         }
+      }
+      if (QUANT && is_v && ok && it > 0) {  // the last tile's rows
+        tc::fence_async_smem();
+        tc::mbar_arrive(&sm.pv_ready[(it - 1) & 1]);
       }
       if (!ok && lane == 0) halt(sm, a.dev_err);
     }
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ softmax
+    regs_up<kRegsSoftmax>();
+    const int grp = (warp - 12) >> 2, bar = 1 + grp;
     const int qd = warp & 3, key = qd * 32 + lane, tid = key;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
-    int it = 0, seg = 0;
-    bool run = true;
-    struct Par {
-      float k, v0, v1;  // own page's K scale (0 and !there), both pages' V scales
-      bool there;
+    float* const nm = sm.nm[grp];
+    float* const alpha = sm.alpha[grp];
+    int meetings = 0;
+    auto meet = [&]() -> bool {  // both groups; bounded
+      tc::mbar_arrive(&sm.all);
+      return __all_sync(0xffffffffu, tc::mbar_wait(&sm.all, meetings++ & 1));
     };
+    int it0 = 0, seg = 0;  // tiles of the units before
+    bool run = true;
     for (int at = rg.begin, un = rg.first_unit; run && at < rg.end; ++un, ++seg) {
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      const int pos_last = u.pos0 + u.ntok - 1;
-      const uint32_t o = tO + (seg & 1) * 64;
+      const int pos_last = u.pos0 + u.ntok - 1, sp = seg & 1;
+      const uint32_t o = tO + (sp * 2 + grp) * 64;
+      const int jf = j0 + ((it0 + grp) & 1);  // this group's first tile: tile j of the line's number it0 + j - j0
       float l[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) l[n] = 0.f;
       float unit = BF ? 1.f : 0.f;
-      if (tid < N) sm.nm[tid] = kUnset;
-      int ph0 = page_at(u, u.page0 + 2 * j0), ph1 = page_at(u, u.page0 + 2 * j0 + 1);
-      auto scales = [&](int f0, int f1) -> Par {
-        const int own = qd >> 1 ? f1 : f0;
-        Par r;
-        r.there = own >= 0;
-        if (QUANT) {
-          r.k = own >= 0 ? a.k_scale[(size_t)own * a.Hkv + u.g] : 0.f;
-          r.v0 = f0 >= 0 ? a.v_scale[(size_t)f0 * a.Hkv + u.g] : 0.f;
-          r.v1 = f1 >= 0 ? a.v_scale[(size_t)f1 * a.Hkv + u.g] : 0.f;
-        } else {
-          r.k = r.v0 = r.v1 = 1.f;
-        }
-        return r;
-      };
-      Par nx = scales(ph0, ph1);
-      if (j0 + 1 < j1) ph0 = page_at(u, u.page0 + 2 * j0 + 2), ph1 = page_at(u, u.page0 + 2 * j0 + 3);
-      bool good = tc::mbar_wait(&sm.q_full[seg & 1], (seg >> 1) & 1);
-      const float cq = a.scale_log2 * (good ? *(volatile float*)&sm.qmul[seg & 1] : 1.f);
-      (void)any_of_128(false);  // nm is set, qmul has been read
-      if (tid == 0) tc::mbar_arrive(&sm.q_empty[seg & 1]);
-      for (int j = j0; j < j1; ++j, ++it) {
-        const int b = it & 1;
-        const Par par = nx;
-        if (j + 1 < j1) nx = scales(ph0, ph1);
-        if (j + 2 < j1) ph0 = page_at(u, u.page0 + 2 * j + 4), ph1 = page_at(u, u.page0 + 2 * j + 5);
-        good = good && tc::mbar_wait(&sm.s_full[b], (it >> 1) & 1);
+      if (tid < N) nm[tid] = kUnset;
+      bool good = tc::mbar_wait(&sm.q_full[sp], (seg >> 1) & 1);
+      const float cq = a.scale_log2 * (good ? *(volatile float*)&sm.qmul[sp] : 1.f);
+      (void)any_of_128(bar, false);  // nm is set, qmul has been read
+      if (tid == 0) tc::mbar_arrive(&sm.q_empty[sp]);
+      for (int j = jf; j < j1; j += 2) {
+        const int it = it0 + j - j0, b = grp;
+        good = good && tc::mbar_wait(&sm.info_full[it % kInfo], (it / kInfo) & 1) &&
+               tc::mbar_wait(&sm.s_full[b], (it >> 1) & 1) &&
+               (it < 2 || tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1));  // P's buffer
         good = __all_sync(0xffffffffu, good);
         tc::tc_fence_after();
         const int pos = (u.page0 + 2 * j) * kPage + key;
-        const float c = cq * par.k;
+        const TileInfo& f = sm.info[it % kInfo];
+        const float v0 = f.v[0], v1 = f.v[1], c = cq * f.k[qd >> 1];
+        const bool there = f.there[qd >> 1] != 0;
         const bool edge = (u.page0 + 2 * j) * kPage + 127 > u.pos0 || (a.w > 0 && (u.page0 + 2 * j) * kPage <= pos_last - a.w);
-        // columns (rows of the unit) that see this key: [lo, hi)
-        const int ago = pos - u.pos0;  // tokens before this one do not
-        int lo = 0, hi = N;
-        if (edge) {
-          lo = ago <= 0 ? 0 : min(ago, 64) * a.G;
-          if (a.w > 0) hi = ago + a.w <= 0 ? 0 : min(ago + a.w, 64) * a.G;
-        }
-        if (!par.there) hi = 0;
         // exponents of one step's columns, -inf where the key is hidden
         auto exponents = [&](int n0, float (&x)[C]) {
           tmem_cols<C>(tS + lane_off + b * 64 + n0, x);
 #pragma unroll
           for (int n = 0; n < C; n += 4) {
-            const float4 m = *reinterpret_cast<const float4*>(sm.nm + n0 + n);
-            x[n] = fmaf(x[n], c, m.x), x[n + 1] = fmaf(x[n + 1], c, m.y);
-            x[n + 2] = fmaf(x[n + 2], c, m.z), x[n + 3] = fmaf(x[n + 3], c, m.w);
+            const float4 m = *reinterpret_cast<const float4*>(nm + n0 + n);
+            const F2 a0 = fma2({x[n], x[n + 1]}, {c, c}, {m.x, m.y}), a1 = fma2({x[n + 2], x[n + 3]}, {c, c}, {m.z, m.w});
+            x[n] = a0.x, x[n + 1] = a0.y, x[n + 2] = a1.x, x[n + 3] = a1.y;
           }
-          if (edge || !par.there) {
+          if (edge || !there) {
+            // columns (rows of the unit) that see this key: [lo, hi)
+            const int ago = pos - u.pos0;  // tokens before this one do not
+            const int lo = ago <= 0 ? 0 : min(ago, 64) * a.G;
+            int hi = N;
+            if (a.w > 0) hi = ago + a.w <= 0 ? 0 : min(ago + a.w, 64) * a.G;
+            if (!there) hi = 0;
 #pragma unroll
             for (int n = 0; n < C; ++n)
               if (n0 + n < lo || n0 + n >= hi) x[n] = -INFINITY;
           }
         };
+        // the group's maxima over the 128 keys, to warp_m
         float x[C];
-        bool need = false;
-#pragma unroll
-        for (int n0 = 0; n0 < N; n0 += C) {
-          exponents(n0, x);
-          float top = fmaxf(x[0], x[1]);
-#pragma unroll
-          for (int n = 2; n < C; n += 2) top = fmax3(top, x[n], x[n + 1]);
-          need |= top > kTop;
-        }
-        const float vtop = fmaxf(fabsf(par.v0), fabsf(par.v1));
-        need |= QUANT && vtop > 2.f * unit;
-        bool moved = false;
-        if (any_of_128(need || !good || halted(sm))) {
-          moved = true;
-          if (any_of_128(!good || halted(sm))) {
-            run = false;
-            break;
-          }
-          // ---- some row's reference max, or V's unit, moves
+        auto maxima = [&]() {
 #pragma unroll
           for (int n0 = 0; n0 < N; n0 += C) {
             exponents(n0, x);
@@ -596,74 +632,82 @@ __global__ void __launch_bounds__(kNThreads, 1)
             for (int n = 0; n < C; ++n) {
               float t;
               asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(t) : "f"(x[n]));
-              if (lane == n) sm.warp_m[qd][n0 + n] = t;
+              if (lane == n) sm.warp_m[grp][qd][n0 + n] = t;
             }
           }
-          (void)any_of_128(false);
-          float f = 1.f;
+          (void)any_of_128(bar, false);
+        };
+        auto top_of = [&](int n) {
+          return fmaxf(fmaxf(sm.warp_m[grp][0][n], sm.warp_m[grp][1][n]), fmaxf(sm.warp_m[grp][2][n], sm.warp_m[grp][3][n]));
+        };
+        bool need = false;
+#pragma unroll
+        for (int n0 = 0; n0 < N; n0 += C) {
+          exponents(n0, x);
+          float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
+#pragma unroll
+          for (int n = 4; n < C; n += 4) t0 = fmax3(t0, x[n], x[n + 1]), t1 = fmax3(t1, x[n + 2], x[n + 3]);
+          need |= fmaxf(t0, t1) > kTop;
+        }
+        const float vtop = fmaxf(fabsf(v0), fabsf(v1));
+        need |= QUANT && vtop > 2.f * unit;
+        bool moved = false;
+        if (any_of_128(bar, need || !good || halted(sm))) {
+          moved = true;
+          if (any_of_128(bar, !good || halted(sm))) {
+            run = false;
+            break;
+          }
+          // ---- some row's reference max, or V's unit, moves
+          maxima();
+          float fall = 1.f;
           if (QUANT && vtop > 2.f * unit) {
-            f = unit / vtop;
+            fall = unit / vtop;
             unit = vtop;
           }
+          bool fresh = false;
           if (tid < N) {
-            const float t = fmaxf(fmaxf(sm.warp_m[0][tid], sm.warp_m[1][tid]), fmaxf(sm.warp_m[2][tid], sm.warp_m[3][tid]));
+            const float t = top_of(tid);
             float al = 1.f;
             if (t > kTop) {  // t = x c + nm: the new nm is 6 - x c
-              const float old = sm.nm[tid];
-              // an unset row: x c is lost in the sum; its first reference comes from a second look
-              if (old == kUnset) {
-                sm.nm[tid] = 0.f;
+              const float old = nm[tid];
+              if (old == kUnset) {  // x c is lost in the sum: the first reference comes from a second look
+                fresh = true;
+                nm[tid] = 0.f;
                 al = 0.f;
               } else {
                 const float to = old - t + kBias;
-                sm.nm[tid] = to;
+                nm[tid] = to;
                 al = ex2_approx(to - old);
               }
             }
-            sm.alpha[tid] = al;
+            alpha[tid] = al;
           }
-          (void)any_of_128(false);
-          // rows seen for the first time: their largest logit with nm = 0
-          bool fresh = false;
-          if (tid < N) fresh = sm.alpha[tid] == 0.f && sm.nm[tid] == 0.f;
-          if (any_of_128(fresh)) {
-#pragma unroll
-            for (int n0 = 0; n0 < N; n0 += C) {
-              exponents(n0, x);
-#pragma unroll
-              for (int n = 0; n < C; ++n) {
-                float t;
-                asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(t) : "f"(x[n]));
-                if (lane == n) sm.warp_m[qd][n0 + n] = t;
-              }
-            }
-            (void)any_of_128(false);
+          if (any_of_128(bar, fresh)) {
+            maxima();
             if (fresh) {
-              const float t = fmaxf(fmaxf(sm.warp_m[0][tid], sm.warp_m[1][tid]), fmaxf(sm.warp_m[2][tid], sm.warp_m[3][tid]));
-              sm.nm[tid] = t > -INFINITY ? kBias - t : kUnset;
+              const float t = top_of(tid);
+              nm[tid] = t > -INFINITY ? kBias - t : kUnset;
             }
-            (void)any_of_128(false);
+            (void)any_of_128(bar, false);
           }
 #pragma unroll
-          for (int n = 0; n < N; ++n) l[n] *= sm.alpha[n];
-          if (j > j0) {
-            good = good && tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
-            good = __all_sync(0xffffffffu, good);
-            tc::tc_fence_after();
+          for (int n = 0; n < N; ++n) l[n] *= alpha[n];
+          if (j > jf) {
+            // O holds this group's tiles up to the last but this: P's buffer was waited for above
 #pragma unroll 1
             for (int n0 = 0; n0 < N; n0 += C) {
               float ov[C];
               tmem_cols<C>(o + lane_off + n0, ov);
 #pragma unroll
-              for (int n = 0; n < C; ++n) ov[n] *= sm.alpha[n0 + n] * f;
+              for (int n = 0; n < C; ++n) ov[n] *= alpha[n0 + n] * fall;
               tmem_put<C>(o + lane_off + n0, ov);
             }
           }
-          (void)any_of_128(false);  // alpha has been read
+          (void)any_of_128(bar, false);  // alpha has been read
         }
         // ---- weights
-        if (it >= 2) good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1));
-        const float vs = qd >> 1 ? par.v1 : par.v0;
+        const float vs = qd >> 1 ? v1 : v0;
         const float rel = BF ? 1.f : unit > 0.f ? vs / unit : 0.f;
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += C) {
@@ -673,10 +717,11 @@ __global__ void __launch_bounds__(kNThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float p0 = ex2_approx(x[n + 2 * i]), p1 = ex2_approx(x[n + 2 * i + 1]);
-              l[n0 + n + 2 * i] += p0;
-              l[n0 + n + 2 * i + 1] += p1;
-              w[i] = BF ? pack_bf16(p0, p1) : pack_f16(p0 * rel, p1 * rel);
+              F2 pr{ex2_approx(x[n + 2 * i]), ex2_approx(x[n + 2 * i + 1])};
+              const F2 sum = add2({l[n0 + n + 2 * i], l[n0 + n + 2 * i + 1]}, pr);
+              l[n0 + n + 2 * i] = sum.x, l[n0 + n + 2 * i + 1] = sum.y;
+              if (!BF) pr = mul2(pr, {rel, rel});
+              w[i] = BF ? pack_bf16(pr.x, pr.y) : pack_f16(pr.x, pr.y);
             }
             *reinterpret_cast<uint4*>(sm.p[b] + key * 128 + ((((n0 + n) >> 3) ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -684,35 +729,38 @@ __global__ void __launch_bounds__(kNThreads, 1)
         tc::tc_fence_before();
         tc::mbar_arrive(&sm.s_empty[b]);
         tc::fence_async_smem();
-        tc::mbar_arrive(&sm.p_full[b]);
+        tc::mbar_arrive(&sm.pv_ready[b]);
       }
       if (!run) break;
-      // ---- the unit's (or this part's) output
-      good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1));
-      if (any_of_128(!good || halted(sm))) {
+      // ---- the unit's (or this part's) output: both groups' sums meet, each group writes half the rows
+      const int nt = j1 - j0, last = it0 + nt - 1;
+      const bool has0 = nt > 1 || (it0 & 1) == 0, has1 = nt > 1 || (it0 & 1) == 1;
+      it0 += nt;
+      if (has0) good = good && tc::mbar_wait(&sm.pv_done[0], ((last - (last & 1)) >> 1) & 1);
+      if (has1) good = good && tc::mbar_wait(&sm.pv_done[1], ((last - 1 + (last & 1)) >> 1) & 1);
+      good = __all_sync(0xffffffffu, good && !halted(sm));
+      // the normaliser of every row, over the 32 keys of a warp
+#pragma unroll
+      for (int n0 = 0; n0 < N; n0 += C) {
+        float t[32];
+#pragma unroll
+        for (int n = 0; n < 32; ++n) t[n] = n < C ? l[n0 + n] : 0.f;
+        const float s = transpose_sum32(t);
+        if (lane < C) sm.out_l[sp][grp][qd][n0 + lane] = s;
+      }
+      if (tid < N) sm.out_m[sp][grp][tid] = nm[tid] == kUnset ? -INFINITY : -nm[tid];
+      if (tid == 0) sm.out_unit[sp][grp] = unit;
+      tc::mbar_arrive(&sm.out_ready[sp]);
+      good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.out_ready[sp], (seg >> 1) & 1));
+      if (any_of_128(bar, !good)) {
         run = false;
         break;
       }
       tc::tc_fence_after();
-      // the normaliser of every row, over the 128 keys' threads
-#pragma unroll
-      for (int n0 = 0; n0 < N; n0 += C) {
-        if constexpr (C == 32) {
-          float t[32];
-#pragma unroll
-          for (int n = 0; n < 32; ++n) t[n] = l[n0 + n];
-          sm.warp_l[qd][n0 + lane] = transpose_sum32(t);
-        } else {
-          float t[32];
-#pragma unroll
-          for (int n = 0; n < 32; ++n) t[n] = n < C ? l[n] : 0.f;
-          const float s = transpose_sum32(t);
-          if (lane < C) sm.warp_l[qd][lane] = s;
-        }
-      }
-      (void)any_of_128(false);
       const bool whole = j0 == 0 && j1 == u.ntiles;
       const int rows = u.ntok * a.G;
+      constexpr int H = N / 2;  // rows of this group: [nb, nb + H)
+      const int nb = grp * H;
       auto out_row = [&](int n) -> size_t { return (size_t)(u.row + n / a.G) * a.Hq + (size_t)u.g * a.G + n % a.G; };
       // factor of row n's output, and its lse, from its max and sum
       auto finish = [&](int n, float M, float L) -> float {
@@ -729,82 +777,103 @@ __global__ void __launch_bounds__(kNThreads, 1)
           else reinterpret_cast<float*>(a.o)[at_o] = v;
         }
       };
+      // this thread's row (tid < H): both groups' max and sum; the groups' factors to alpha and fin
       float M = -INFINITY, L = 0.f;
-      if (tid < N) {
-        M = sm.nm[tid] == kUnset ? -INFINITY : -sm.nm[tid];
-        L = sm.warp_l[0][tid] + sm.warp_l[1][tid] + sm.warp_l[2][tid] + sm.warp_l[3][tid];
+      if (tid < H) {
+        const int n = nb + tid;
+        const float m0 = sm.out_m[sp][0][n], m1 = sm.out_m[sp][1][n];
+        M = fmaxf(m0, m1);
+        const float e0 = exp2_rel(m0, M), e1 = exp2_rel(m1, M);
+        L = e0 * (sm.out_l[sp][0][0][n] + sm.out_l[sp][0][1][n] + sm.out_l[sp][0][2][n] + sm.out_l[sp][0][3][n]) +
+            e1 * (sm.out_l[sp][1][0][n] + sm.out_l[sp][1][1][n] + sm.out_l[sp][1][2][n] + sm.out_l[sp][1][3][n]);
+        const float f = whole ? finish(n, M, L) : 1.f;
+        sm.warp_m[grp][0][tid] = e0 * sm.out_unit[sp][0] * f;
+        sm.warp_m[grp][1][tid] = e1 * sm.out_unit[sp][1] * f;
       }
-      if (whole) {
-        if (tid < N) sm.fin[tid] = finish(tid, M, L) * unit;
-        (void)any_of_128(false);
-#pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += C) {
-          float ov[C];
-          tmem_cols<C>(o + lane_off + n0, ov);
+      (void)any_of_128(bar, false);
+      // a group without tiles in this part left nothing in its O
+      auto joined = [&](float (&v)[H]) {
 #pragma unroll
-          for (int n = 0; n < C; ++n) put(n0 + n, ov[n] * sm.fin[n0 + n]);
+        for (int n = 0; n < H; ++n) v[n] = 0.f;
+        float t[H > 32 ? 32 : H];
+        static_assert(H <= 32, "one step of columns");
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          if (!(g2 ? has1 : has0)) continue;
+          if constexpr (H == 8) {
+            float t16[16];
+            tmem_cols<16>(tO + (sp * 2 + g2) * 64 + lane_off, t16);
+#pragma unroll
+            for (int n = 0; n < 8; ++n) t[n] = grp ? t16[8 + n] : t16[n];
+          } else {
+            tmem_cols<H>(tO + (sp * 2 + g2) * 64 + lane_off + nb, t);
+          }
+#pragma unroll
+          for (int n = 0; n < H; ++n) v[n] = fmaf(sm.warp_m[grp][g2][n], t[n], v[n]);
         }
+      };
+      {
+        float v[H];
+        joined(v);
         tc::tc_fence_before();
-        tc::mbar_arrive(&sm.o_empty[seg & 1]);
-      } else {
-        const int slot = part_slot(u, per, blockIdx.x);
-        if (tid < N) reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * N + tid] = make_float2(M, L);
-        float* po = p.part_o + (size_t)slot * N * D;
-#pragma unroll 1
-        for (int n0 = 0; n0 < N; n0 += C) {
-          float ov[C];
-          tmem_cols<C>(o + lane_off + n0, ov);
+        tc::mbar_arrive(&sm.o_empty[sp]);
+        if (whole) {
+#pragma unroll
+          for (int n = 0; n < H; ++n) put(nb + n, v[n]);
+        } else {
+          const int slot = part_slot(u, per, blockIdx.x);
+          if (tid < H) reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * N + nb + tid] = make_float2(M, L);
+          float* po = p.part_o + ((size_t)slot * N + nb) * D + tid;
           if (tid < D)
 #pragma unroll
-            for (int n = 0; n < C; ++n) po[(size_t)(n0 + n) * D + tid] = ov[n] * unit;
+            for (int n = 0; n < H; ++n) po[(size_t)n * D] = v[n];
         }
-        tc::tc_fence_before();
-        tc::mbar_arrive(&sm.o_empty[seg & 1]);
+      }
+      if (!whole) {
         // the last CTA to leave its part merges them all, in CTA order
         const int c0 = u.prefix / per, c1 = (u.prefix + u.ntiles - 1) / per, parts = c1 - c0 + 1;
         __threadfence();
-        (void)any_of_128(false);
-        if (tid == 0) sm.last = atomicAdd(&p.arrive[un], 1) == c1 - c0;
-        (void)any_of_128(false);
+        if (!meet()) { run = false; break; }
+        if (grp == 0 && tid == 0) sm.last = atomicAdd(&p.arrive[un], 1) == c1 - c0;
+        if (!meet()) { run = false; break; }
         if (*(volatile int*)&sm.last) {
           __threadfence();
-          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + nb;
           float Mx = -INFINITY, Lx = 0.f;
-          if (tid < N) {
+          if (tid < H) {
             for (int k = 0; k < parts; ++k) Mx = fmaxf(Mx, __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid).x);
             for (int k = 0; k < parts; ++k) {
               const float2 y = __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid);
               Lx += exp2_rel(y.x, Mx) * y.y;
             }
-            sm.fin[tid] = finish(tid, Mx, Lx);
+            sm.fin[nb + tid] = finish(nb + tid, Mx, Lx);
           }
-          float* fac = reinterpret_cast<float*>(sm.p);  // [parts of a round][N]: nobody writes or reads P now
-          constexpr int ROUND = 32768 / 4 / N;
-#pragma unroll 1
-          for (int n0 = 0; n0 < N; n0 += C) {
-            float acc[C];
+          // factors of the parts, a round of them at a time; nobody writes or reads P now
+          float* fac = reinterpret_cast<float*>(sm.p[grp]);
+          constexpr int ROUND = 16384 / 4 / H;
+          float acc[H];
 #pragma unroll
-            for (int n = 0; n < C; ++n) acc[n] = 0.f;
-            for (int k0 = 0; k0 < parts; k0 += ROUND) {
-              const int kn = min(ROUND, parts - k0);
-              (void)any_of_128(false);
-              if (tid < N)
-                for (int k = 0; k < kn; ++k)
-                  fac[k * N + tid] = exp2_rel(__ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + k) * N + tid).x, Mx);
-              (void)any_of_128(false);
-              if (tid < D)
-                for (int k = 0; k < kn; ++k) {
-                  const float* src = p.part_o + ((size_t)part_slot(u, per, c0 + k0 + k) * N + n0) * D + tid;
+          for (int n = 0; n < H; ++n) acc[n] = 0.f;
+          for (int k0 = 0; k0 < parts; k0 += ROUND) {
+            const int kn = min(ROUND, parts - k0);
+            (void)any_of_128(bar, false);
+            if (tid < H)
+              for (int k = 0; k < kn; ++k)
+                fac[k * H + tid] = exp2_rel(__ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + k) * N + tid).x, Mx);
+            (void)any_of_128(bar, false);
+            if (tid < D)
+              for (int k = 0; k < kn; ++k) {
+                const float* src = p.part_o + ((size_t)part_slot(u, per, c0 + k0 + k) * N + nb) * D + tid;
 #pragma unroll
-                  for (int n = 0; n < C; ++n) acc[n] += fac[k * N + n0 + n] * __ldcg(src + (size_t)n * D);
-                }
-            }
-#pragma unroll
-            for (int n = 0; n < C; ++n) put(n0 + n, acc[n] * sm.fin[n0 + n]);
+                for (int n = 0; n < H; ++n) acc[n] += fac[k * H + n] * __ldcg(src + (size_t)n * D);
+              }
           }
+#pragma unroll
+          for (int n = 0; n < H; ++n) put(nb + n, acc[n] * sm.fin[nb + n]);
         }
+        if (!meet()) { run = false; break; }  // sm.last is rewritten by the next part
       }
-      (void)any_of_128(false);  // the arrays are rewritten by the next unit
+      (void)any_of_128(bar, false);  // the group's arrays are rewritten by the next unit
     }
     if (!run && lane == 0) halt(sm, a.dev_err);
   }
