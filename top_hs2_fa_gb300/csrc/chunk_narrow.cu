@@ -346,66 +346,65 @@ __global__ void __launch_bounds__(kNThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------------ S = K Q^T
     regs_down<kRegsMisc>();
-    if (lane == 0) {
-      constexpr uint32_t idS = narrow_idesc(BF, N, false, false);
-      int it = 0, seg = 0;
-      bool ok = true;
-      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
-        const int end = min(rg.end, pt.y + pt.x);
-        const int qb = seg & 1;
-        const uint32_t q0 = tc::smem_u32(sm.q[qb]);
-        ok = tc::mbar_wait(&sm.q_full[qb], (seg >> 1) & 1);
-        for (; ok && at < end; ++at, ++it) {
-          const int b = it & 1, st = it % ST;
-          ok = tc::mbar_wait(&sm.s_empty[b], ((it >> 1) & 1) ^ 1) &&
-               (QUANT ? tc::mbar_wait(&sm.k_full[b], (it >> 1) & 1) : tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1));
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t k0 = tc::smem_u32(sm.ring[st]);
+    constexpr uint32_t idS = narrow_idesc(BF, N, false, false);
+    const uint32_t el = tc::elect_one();
+    int it = 0, seg = 0;
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
+      const int end = min(rg.end, pt.y + pt.x);
+      const int qb = seg & 1;
+      const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sm.q[qb]));
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full[qb], (seg >> 1) & 1));
+      for (; ok && at < end; ++at, ++it) {
+        const int b = it & 1, st = it % ST;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.s_empty[b], ((it >> 1) & 1) ^ 1) &&
+                                         (QUANT ? tc::mbar_wait(&sm.k_full[b], (it >> 1) & 1)
+                                                : tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1)));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sm.ring[st]));
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) {
-            const uint64_t qd = tc::sdesc_sw128(q0 + (ks >> 2) * (N * 128u) + (ks & 3) * 32u);
-            if (QUANT) tc::mma_bf16_ts(tS + b * 64, tK + b * 64 + ks * 8, qd, idS, ks > 0 ? 1u : 0u);
-            else tc::mma_bf16(tS + b * 64, tc::sdesc_sw128(k0 + (ks >> 2) * 16384u + (ks & 3) * 32u), qd, idS, ks > 0 ? 1u : 0u);
-          }
-          tc::mma_commit(&sm.s_full[b]);
-          if (!QUANT) tc::mma_commit(&sm.ring_empty[st]);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t qo = ((ks >> 2) * (N * 128u) + (ks & 3) * 32u) >> 4, ko = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
+          if (QUANT) tc::mma_f16_ts_warp(tS + b * 64, tK + b * 64 + ks * 8, qd + qo, idS, ks > 0 ? 1u : 0u, el);
+          else tc::mma_f16_warp(tS + b * 64, kd + ko, qd + qo, idS, ks > 0 ? 1u : 0u, el);
         }
-        if (ok) tc::mma_commit(&sm.q_empty[qb]);
+        tc::mma_commit_warp(&sm.s_full[b], el);
+        if (!QUANT) tc::mma_commit_warp(&sm.ring_empty[st], el);
       }
-      if (!ok) halt(sm, a.dev_err);
-      if (it > 0) (void)tc::mbar_wait(&sm.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
+      if (ok) tc::mma_commit_warp(&sm.q_empty[qb], el);
     }
+    if (!ok && lane == 0) halt(sm, a.dev_err);
+    if (it > 0) (void)tc::mbar_wait(&sm.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
   } else if (warp == 3) {
     // ------------------------------------------------------------------ O^T += V^T P^T
     regs_down<kRegsMisc>();
-    if (lane == 0) {
-      constexpr uint32_t idO = narrow_idesc(BF, N, true, true);
-      int it = 0, seg = 0;
-      bool ok = true;
-      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
-        const int end = min(rg.end, pt.y + pt.x);
-        ok = tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1);
-        for (int j = 0; ok && at < end; ++at, ++it, ++j) {
-          const int b = it & 1, st = it % ST;
-          const uint32_t o = tO + ((seg & 1) * 2 + b) * 64;
-          ok = tc::mbar_wait(&sm.pv_ready[b], (it >> 1) & 1);
-          if (!ok) break;
-          tc::tc_fence_after();
-          const uint32_t v0 = QUANT ? tc::smem_u32(sm.v[b]) : tc::smem_u32(sm.ring[st] + CODES), p0 = tc::smem_u32(sm.p[b]);
+    constexpr uint32_t idO = narrow_idesc(BF, N, true, true);
+    const uint32_t el = tc::elect_one();
+    int it = 0, seg = 0;
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
+      const int end = min(rg.end, pt.y + pt.x);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1));
+      for (int j = 0; ok && at < end; ++at, ++it, ++j) {
+        const int b = it & 1, st = it % ST;
+        const uint32_t o = tO + ((seg & 1) * 2 + b) * 64;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_ready[b], (it >> 1) & 1));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t vd = tc::sdesc_sw128_mn(QUANT ? tc::smem_u32(sm.v[b]) : tc::smem_u32(sm.ring[st] + CODES), 16384u, 1024u);
+        const uint64_t pd = tc::sdesc_sw128_mn(tc::smem_u32(sm.p[b]), 16384u, 1024u);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)  // 16 keys each. D = 64: the upper 64 rows of M are not read back
-            tc::mma_bf16(o, tc::sdesc_sw128_mn(v0 + ks * 2048u, 16384u, 1024u),
-                         tc::sdesc_sw128_mn(p0 + ks * 2048u, 16384u, 1024u), idO, (j > 1 || ks > 0) ? 1u : 0u);
-          tc::mma_commit(&sm.pv_done[b]);
-          if (!QUANT) tc::mma_commit(&sm.ring_empty[st]);
-        }
+        for (int ks = 0; ks < 8; ++ks)  // 16 keys each. D = 64: the upper 64 rows of M are not read back
+          tc::mma_f16_warp(o, vd + ks * 128, pd + ks * 128, idO, (j > 1 || ks > 0) ? 1u : 0u, el);
+        tc::mma_commit_warp(&sm.pv_done[b], el);
+        if (!QUANT) tc::mma_commit_warp(&sm.ring_empty[st], el);
       }
-      if (!ok) halt(sm, a.dev_err);
-      if (it > 0) (void)tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
     }
+    if (!ok && lane == 0) halt(sm, a.dev_err);
+    if (it > 0) (void)tc::mbar_wait(&sm.pv_done[(it - 1) & 1], ((it - 1) >> 1) & 1);
   } else if (warp == 2) {
     // ------------------------------------------------------------------ Q
     regs_down<kRegsMisc>();
@@ -706,6 +705,10 @@ __global__ void __launch_bounds__(kNThreads, 1)
           }
           (void)any_of_128(bar, false);  // alpha has been read
         }
+        if (N == C && !moved) {
+          tc::tc_fence_before();
+          tc::mbar_arrive(&sm.s_empty[b]);
+        }
         // ---- weights
         const float vs = qd >> 1 ? v1 : v0;
         const float rel = BF ? 1.f : unit > 0.f ? vs / unit : 0.f;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
           }
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(&sm.s_empty[b]);
+        if (N != C || moved) tc::mbar_arrive(&sm.s_empty[b]);
         tc::fence_async_smem();
         tc::mbar_arrive(&sm.pv_ready[b]);
       }

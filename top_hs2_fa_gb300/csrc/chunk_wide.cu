@@ -7,8 +7,9 @@
 // tiles (chunk_plan.cuh); the pipeline runs on across units.
 //   warp 0      TMA producer of Q (two buffers, one per unit) and the K tiles
 //   warp 10     TMA producer of the V tiles
-//   warp 1      MMA issuer: S_j = Q K_j^T into one of two TMEM buffers, then O += P_j V_j with
-//               P_j read from tensor memory; S_{j+1} is issued before P_j is waited for
+//   warp 1      issues S_j = Q K_j^T into one of two TMEM buffers
+//   warp 11     issues O += P_j V_j with P_j read from tensor memory; two issuers, so that one's
+//               waits overlap the other's instructions
 //   warps 2-9   softmax, two threads per row (warps w and w + 4 share a lane quadrant, each has
 //               64 of the tile's 128 columns, i.e. one page): row max over both halves, p =
 //               2^(x c - m) with the reference m moving only when it is exceeded by 2^8, P
@@ -28,8 +29,8 @@ namespace hs2 {
 namespace {
 
 constexpr int kWRows = 128;
-constexpr int kWThreads = 352;
-constexpr int kWVWarp = 10;
+constexpr int kWThreads = 384;
+constexpr int kWVWarp = 10, kWPVWarp = 11;
 constexpr uint32_t kWTmem = 512;
 constexpr float kWRescale = 8.f;
 constexpr int kWStages = 2;  // K slots and V slots
@@ -160,72 +161,64 @@ __global__ void __launch_bounds__(kWThreads, 1)
       for (int i = max(0, q_issued - 2); i < q_issued; ++i) (void)tc::mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128);
-      constexpr uint32_t idO = tc::idesc_bf16_f32_bmn(128, D);
-      int pv_issued = 0, s_issued = 0;
-      bool ok = true;
-      // the next tile to issue S for: (segment, tile), ahead of the P.V cursor by one
-      int s_at = rg.begin, s_un = rg.first_unit, s_seg = 0;
-      ChunkUnit su{};
-      if (s_at < rg.end) su = load_unit(p, s_un);
-      auto issue_s = [&]() -> bool {
-        const int j = s_at - su.prefix, j1 = min(su.ntiles, rg.end - su.prefix);
-        const bool first = s_at == rg.begin || j == 0;
-        const int qb = s_seg & 1, st = s_issued & 1, kv = s_issued % kWStages;
-        if (first && !tc::mbar_wait(&sm.q_full[qb], (s_seg >> 1) & 1)) return false;
-        if (!tc::mbar_wait(&sm.k_full[kv], (s_issued / kWStages) & 1)) return false;
+    // ------------------------------------------------------------------ S = Q K^T
+    constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128);
+    const uint32_t el = tc::elect_one();
+    int it = 0, seg = 0;
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
+      const int end = min(rg.end, pt.y + pt.x);
+      const int qb = seg & 1;
+      const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sm.q[qb]));
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full[qb], (seg >> 1) & 1));
+      for (; ok && at < end; ++at, ++it) {
+        const int st = it & 1, kv = it % kWStages;
+        // S_j's buffer holds P_{j-2} until its P.V is done
+        ok = __all_sync(0xffffffffu, (it < 2 || tc::mbar_wait(&sm.p_empty[st], ((it - 2) >> 1) & 1)) &&
+                                         tc::mbar_wait(&sm.k_full[kv], (it / kWStages) & 1));
+        if (!ok) break;
         tc::tc_fence_after();
-        const uint32_t q0 = tc::smem_u32(sm.q[qb]), k0 = tc::smem_u32(sm.k[kv]);
+        const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sm.k[kv]));
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * 16384u + (ks & 3) * 32u;
-          tc::mma_bf16(tS + st * 128, tc::sdesc_sw128(q0 + off), tc::sdesc_sw128(k0 + off), idS, ks > 0 ? 1u : 0u);
+          const uint32_t off = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
+          tc::mma_f16_warp(tS + st * 128, qd + off, kd + off, idS, ks > 0 ? 1u : 0u, el);
         }
-        tc::mma_commit(&sm.s_full[st]);
-        tc::mma_commit(&sm.k_empty[kv]);
-        ++s_issued;
-        ++s_at;
-        if (j + 1 == j1) {
-          tc::mma_commit(&sm.q_empty[qb]);
-          ++s_seg;
-          if (s_at < rg.end) su = load_unit(p, ++s_un);
-        }
-        return true;
-      };
-      if (rg.begin < rg.end) ok = issue_s();
-      int seg = 0;
-      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-        const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
-        const int j0 = at - pt.y, j1 = min(pt.x, rg.end - pt.y);
-        at = pt.y + j1;
-        const uint32_t o = tO + (seg & 1) * 128;
-        if (!tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1)) { ok = false; break; }
-        for (int j = j0; j < j1; ++j) {
-          if (s_at < rg.end && !issue_s()) { ok = false; break; }
-          const int st = pv_issued & 1, kv = pv_issued % kWStages;
-          if (!tc::mbar_wait(&sm.p_full[st], (pv_issued >> 1) & 1) ||
-              !tc::mbar_wait(&sm.v_full[kv], (pv_issued / kWStages) & 1)) {
-            ok = false;
-            break;
-          }
-          tc::tc_fence_after();
-          const uint32_t v0 = tc::smem_u32(sm.v[kv]);
-#pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            tc::mma_bf16_ts(o, tS + st * 128 + ks * 8, tc::sdesc_sw128_mn(v0 + ks * 2048u, 16384u, 1024u), idO,
-                            (j > j0 || ks > 0) ? 1u : 0u);
-          tc::mma_commit(&sm.v_empty[kv]);
-          tc::mma_commit(&sm.p_empty[st]);
-          ++pv_issued;
-        }
+        tc::mma_commit_warp(&sm.s_full[st], el);
+        tc::mma_commit_warp(&sm.k_empty[kv], el);
       }
-      if (!ok) stop(sm, a.dev_err);
-      if (pv_issued > 0) (void)tc::mbar_wait(&sm.p_empty[(pv_issued - 1) & 1], ((pv_issued - 1) >> 1) & 1);
-      // an S issued ahead of a P that never came
-      if (s_issued > pv_issued) (void)tc::mbar_wait(&sm.s_full[(s_issued - 1) & 1], ((s_issued - 1) >> 1) & 1);
+      if (ok) tc::mma_commit_warp(&sm.q_empty[qb], el);
     }
+    if (!ok && lane == 0) stop(sm, a.dev_err);
+    if (it > 0) (void)tc::mbar_wait(&sm.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
+  } else if (warp == kWPVWarp) {
+    // ------------------------------------------------------------------ O += P V
+    constexpr uint32_t idO = tc::idesc_bf16_f32_bmn(128, D);
+    const uint32_t el = tc::elect_one();
+    int it = 0, seg = 0;
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
+      const int end = min(rg.end, pt.y + pt.x);
+      const uint32_t o = tO + (seg & 1) * 128;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1));
+      for (int j = 0; ok && at < end; ++at, ++it, ++j) {
+        const int st = it & 1, kv = it % kWStages;
+        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.v_full[kv], (it / kWStages) & 1) &&
+                                         tc::mbar_wait(&sm.p_full[st], (it >> 1) & 1));
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint64_t vd = tc::sdesc_sw128_mn(tc::smem_u32(sm.v[kv]), 16384u, 1024u);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_f16_ts_warp(o, tS + st * 128 + ks * 8, vd + ks * 128, idO, (j > 0 || ks > 0) ? 1u : 0u, el);
+        tc::mma_commit_warp(&sm.v_empty[kv], el);
+        tc::mma_commit_warp(&sm.p_empty[st], el);
+      }
+    }
+    if (!ok && lane == 0) stop(sm, a.dev_err);
+    if (it > 0) (void)tc::mbar_wait(&sm.p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
   } else {
     // ------------------------------------------------------------------ softmax warps
     const int qd = warp & 3;

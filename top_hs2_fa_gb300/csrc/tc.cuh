@@ -104,6 +104,39 @@ HS2_DEVI void mma_commit(uint64_t* bar) {
                : "memory");
 }
 
+// The same, issued by a whole converged warp of which the elected lane (elect_one) executes
+// the instruction: descriptors stay in uniform registers, so an issue costs a few cycles. From
+// a branch that one lane alone has taken every operand is moved across first: 8 MMAs of M = 128,
+// N = 32, K = 16 took 484 cycles to issue that way, 93 this way.
+HS2_DEVI uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{.reg .pred p; elect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;}" : "=r"(r));
+  return r;
+}
+HS2_DEVI void mma_f16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                           uint32_t elected) {
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+HS2_DEVI void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                              uint32_t elected) {
+  asm volatile(
+      "{.reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+      : "memory");
+}
+HS2_DEVI void mma_commit_warp(uint64_t* bar, uint32_t elected) {
+  asm volatile(
+      "{.reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];}" ::"r"(smem_u32(bar)),
+      "r"(elected)
+      : "memory");
+}
+
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, both K-major, shape M x N.
 HS2_DEVI constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4)                      // D format: f32
