@@ -32,6 +32,8 @@ template <int D>
 __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs a) {
   constexpr int V = D / 32;
   __shared__ float sm_m[kCcWarps], sm_l[kCcWarps], sm_o[kCcWarps][D];
+  griddep_launch_dependents();
+  griddep_wait();
   const int r = blockIdx.x, h = blockIdx.y, g = h / a.G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n1[1];
@@ -113,9 +115,7 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
 
 cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s) {
   const dim3 grid(a.n_rows, a.Hq);
-  if (d == 128) chunk_cc_kernel<128><<<grid, kCcWarps * 32, 0, s>>>(a);
-  else chunk_cc_kernel<64><<<grid, kCcWarps * 32, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(d == 128 ? chunk_cc_kernel<128> : chunk_cc_kernel<64>, grid, dim3(kCcWarps * 32), 0, s, a);
 }
 
 }  // namespace hs2

@@ -841,36 +841,53 @@ __global__ void __launch_bounds__(kNThreads, 1)
         if (!meet()) { run = false; break; }
         if (*(volatile int*)&sm.last) {
           __threadfence();
+          // a round of parts at a time: their maxima and sums by all threads, each row's new
+          // reference and the parts' factors by its thread, then the outputs
+          float2* const fac = reinterpret_cast<float2*>(sm.p[grp]);  // [part][H]: nobody writes or reads P now
+          constexpr int ROUND = 16384 / 8 / H;
           const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + nb;
-          float Mx = -INFINITY, Lx = 0.f;
-          if (tid < H) {
-            for (int k = 0; k < parts; ++k) Mx = fmaxf(Mx, __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid).x);
-            for (int k = 0; k < parts; ++k) {
-              const float2 y = __ldcg(ml + (size_t)part_slot(u, per, c0 + k) * N + tid);
-              Lx += exp2_rel(y.x, Mx) * y.y;
-            }
-            sm.fin[nb + tid] = finish(nb + tid, Mx, Lx);
-          }
-          // factors of the parts, a round of them at a time; nobody writes or reads P now
-          float* fac = reinterpret_cast<float*>(sm.p[grp]);
-          constexpr int ROUND = 16384 / 4 / H;
-          float acc[H];
+          float Mx = -INFINITY, Lx = 0.f, acc[H];
 #pragma unroll
           for (int n = 0; n < H; ++n) acc[n] = 0.f;
           for (int k0 = 0; k0 < parts; k0 += ROUND) {
             const int kn = min(ROUND, parts - k0);
             (void)any_of_128(bar, false);
-            if (tid < H)
-              for (int k = 0; k < kn; ++k)
-                fac[k * H + tid] = exp2_rel(__ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + k) * N + tid).x, Mx);
+            for (int x = tid; x < kn * H; x += 128)
+              fac[x] = __ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + x / H) * N + x % H);
             (void)any_of_128(bar, false);
-            if (tid < D)
+            if (tid < H) {
+              float top = Mx;
+              for (int k = 0; k < kn; ++k) top = fmaxf(top, fac[k * H + tid].x);
+              const float keep = exp2_rel(Mx, top);
+              Mx = top;
+              Lx *= keep;
               for (int k = 0; k < kn; ++k) {
-                const float* src = p.part_o + ((size_t)part_slot(u, per, c0 + k0 + k) * N + nb) * D + tid;
-#pragma unroll
-                for (int n = 0; n < H; ++n) acc[n] += fac[k * H + n] * __ldcg(src + (size_t)n * D);
+                const float2 y = fac[k * H + tid];
+                const float e = exp2_rel(y.x, top);
+                Lx += e * y.y;
+                fac[k * H + tid].x = e;
               }
+              sm.warp_m[grp][2][tid] = keep;
+            }
+            (void)any_of_128(bar, false);
+            if (k0 > 0)
+#pragma unroll
+              for (int n = 0; n < H; ++n) acc[n] *= sm.warp_m[grp][2][n];
+            if (tid < D) {
+              const float* src = p.part_o + (size_t)nb * D + tid;
+#pragma unroll 2
+              for (int k = 0; k < kn; ++k) {
+                const float* po = src + (size_t)part_slot(u, per, c0 + k0 + k) * N * D;
+                float t[H];
+#pragma unroll
+                for (int n = 0; n < H; ++n) t[n] = __ldcg(po + (size_t)n * D);
+#pragma unroll
+                for (int n = 0; n < H; ++n) acc[n] = fmaf(fac[k * H + n].x, t[n], acc[n]);
+              }
+            }
           }
+          if (tid < H) sm.fin[nb + tid] = finish(nb + tid, Mx, Lx);
+          (void)any_of_128(bar, false);
 #pragma unroll
           for (int n = 0; n < H; ++n) put(nb + n, acc[n] * sm.fin[nb + n]);
         }

@@ -2,6 +2,7 @@
 // pages to bf16 for the wide kernel.
 #include <cuda_fp16.h>
 
+#include "block_scan.cuh"
 #include "chunk_plan.cuh"
 
 namespace hs2 {
@@ -9,33 +10,6 @@ namespace hs2 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
-
-HS2_DEVI int plan_prefix(int v, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-    const int own = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += y;
-    }
-    warp_sums[lane] = s - own;
-    if (lane == 31) warp_sums[32] = s;
-  }
-  __syncthreads();
-  total = warp_sums[32];
-  return warp_sums[warp] + x - v;
-}
 
 // The first key a token at position p sees.
 HS2_DEVI int first_key(int p, int w) { return w > 0 ? max(0, p - w + 1) : 0; }
@@ -46,6 +20,8 @@ HS2_DEVI int first_key(int p, int w) { return w > 0 ? max(0, p - w + 1) : 0; }
 // per unit writes its record and a prefix sum over the units' tiles places it on the line.
 __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArgs a, const ChunkPlan p0,
                                                                   const ChunkPlan p1) {
+  griddep_launch_dependents();  // the attention kernel may set itself up meanwhile
+  griddep_wait();
   const ChunkPlan& p = blockIdx.x ? p1 : p0;
   __shared__ int sums[33], ubase[kPlanThreads + 1], s_row[kPlanThreads], s_n[kPlanThreads], s_t[kPlanThreads],
       s_exp[kPlanThreads];
@@ -79,7 +55,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     if (rows <= p.min_rows || rows > p.max_rows) n = 0;
     const int per_head = (n + tok - 1) / tok;
     int here, pages = 0, pg = 0;
-    const int ub = plan_prefix(per_head * a.Hkv, sums, here);
+    const int ub = block_prefix(per_head * a.Hkv, sums, here);
     ubase[threadIdx.x] = ub;
     if (threadIdx.x == 0) ubase[kPlanThreads] = here;
     s_row[threadIdx.x] = r0;
@@ -88,10 +64,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     if (p.expand) {
       const int e0 = n > 0 ? first_key(t - n, a.w) / kPage : 0;
       const int np = n > 0 ? (t + kPage - 1) / kPage - e0 : 0;
-      pg = exp_pages + plan_prefix(np, sums, pages);
+      pg = exp_pages + block_prefix(np, sums, pages);
       exp_pages += pages;
       int seqs;
-      const int at = n_exp + plan_prefix(n > 0, sums, seqs);
+      const int at = n_exp + block_prefix(n > 0, sums, seqs);
       n_exp += seqs;
       if (n > 0) {
         p.exp_seq[at] = b;
@@ -128,7 +104,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         cost = x.ntiles;
       }
       int tiles;
-      x.prefix = total_tiles + plan_prefix(cost, sums, tiles);
+      x.prefix = total_tiles + block_prefix(cost, sums, tiles);
       total_tiles += tiles;
       if (u < here) {  // within max_units: the valid sequences' rows are disjoint and within n_rows
         int4* d = reinterpret_cast<int4*>(p.units) + 3 * (size_t)(units + u);
@@ -153,12 +129,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     const int ntiles = y.z, prefix = y.w;
     for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
   }
-  griddep_launch_dependents();
 }
 
 cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s) {
-  chunk_plan_kernel<<<n_plans, kPlanThreads, 0, s>>>(a, plans[0], plans[n_plans - 1]);
-  return cudaGetLastError();
+  return launch_pdl(chunk_plan_kernel, dim3(n_plans), dim3(kPlanThreads), 0, s, a, plans[0], plans[n_plans - 1]);
 }
 
 // ---------------------------------------------------------------------------- expansion
@@ -171,6 +145,7 @@ cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_
 template <int D, int FMT>
 __global__ void __launch_bounds__(256) chunk_expand_kernel(const ChunkArgs a, const ChunkPlan p, uint4* ek, uint4* ev,
                                                            float2* params) {
+  griddep_launch_dependents();
   griddep_wait();
   const int i = blockIdx.z, g = blockIdx.y;
   if (i >= p.exp_head[0]) return;

@@ -6,10 +6,12 @@
 // in which atomics land, so tables, counts and stack are the same on every run.
 //
 // Bound by latency: the books of a pool of 10^4..10^5 pages are a few hundred KB, so a call
-// is one or two short launches with few dependent rounds of loads. Only the copies (a forked
+// is one or two short launches with few dependent rounds of loads, and every launch overlaps
+// the end of the one before it (programmatic dependent launch). Only the copies (a forked
 // sequence's partial page, the pages that compaction moves) are bandwidth.
 #include <cooperative_groups.h>
 
+#include "block_scan.cuh"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -23,27 +25,6 @@ constexpr int kPagesThreads = 1024;
 constexpr int kPagesCluster = 8;  // CTAs of the clusters that scan all pages
 constexpr int kGone = -1;         // ref of a page whose last reference the running free call took
 
-// Exclusive prefix sum over the block (all threads call it); `total` is the block's sum.
-HS2_DEVI int block_prefix(int v, int* warp_sums, int& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  __syncthreads();  // the sums of an earlier call have been read
-  if (lane == 31) warp_sums[warp] = x;
-  __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int k = 0; k < (int)(blockDim.x >> 5); ++k) {
-    if (k < warp) before += warp_sums[k];
-    total += warp_sums[k];
-  }
-  return before + x - v;
-}
-
 HS2_DEVI int pages_of(int t) { return (t + kPage - 1) / kPage; }
 HS2_DEVI bool good_len(int t, int max_pages) { return t >= 0 && t <= max_pages * kPage; }
 
@@ -51,27 +32,28 @@ HS2_DEVI bool good_len(int t, int max_pages) { return t >= 0 && t <= max_pages *
 
 // ---------------------------------------------------------------------------- grow
 // One block. Sequences in chunks of 1024: a prefix sum of the pages each needs, then a warp
-// per sequence writes its entries.
+// per sequence writes its entries. A batch of one chunk is summed once.
 __global__ void __launch_bounds__(kPagesThreads) pages_grow_kernel(const PagesArgs a) {
-  __shared__ int sums[32], base[kPagesThreads], need_s[kPagesThreads], from[kPagesThreads];
+  __shared__ int sums[33], base[kPagesThreads], need_s[kPagesThreads], from[kPagesThreads];
+  griddep_launch_dependents();
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nf = *a.n_free;
-  auto need_of = [&](int b, int& first, bool flag) -> int {
-    first = 0;
+  int old = 0, add = 0;  // this thread's sequence of the chunk
+  auto need_of = [&](int b, bool flag) -> int {
     if (b >= a.batch) return -1;
-    const int old = a.seq_len[b], add = a.n_new[b];
+    old = a.seq_len[b], add = a.n_new[b];
     if (add < 0 || !good_len(old, a.max_pages) || add > a.max_pages * kPage - old) {
       if (flag) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
       return -1;
     }
-    first = pages_of(old);
-    return pages_of(old + add) - first;
+    return pages_of(old + add) - pages_of(old);
   };
   long long all = 0;
-  int first, total;
+  int need = -1, at = 0, total = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kPagesThreads) {
-    const int need = need_of(b0 + threadIdx.x, first, true);
-    (void)block_prefix(max(need, 0), sums, total);
+    need = need_of(b0 + threadIdx.x, true);
+    at = block_prefix(max(need, 0), sums, total);
     all += total;
   }
   if (nf < 0 || nf > a.num_pages || all > nf) {
@@ -80,11 +62,14 @@ __global__ void __launch_bounds__(kPagesThreads) pages_grow_kernel(const PagesAr
   }
   int taken = 0;
   for (int b0 = 0; b0 < a.batch; b0 += kPagesThreads) {
-    const int need = need_of(b0 + threadIdx.x, first, false);
-    const int at = block_prefix(max(need, 0), sums, total);
+    if (a.batch > kPagesThreads) {
+      need = need_of(b0 + threadIdx.x, false);
+      at = block_prefix(max(need, 0), sums, total);
+    }
     base[threadIdx.x] = taken + at;
     need_s[threadIdx.x] = need;
-    from[threadIdx.x] = first;
+    from[threadIdx.x] = pages_of(old);
+    if (need >= 0) a.seq_len[b0 + threadIdx.x] = old + add;
     __syncthreads();
     const int nb = min(kPagesThreads, a.batch - b0);
     for (int i = warp; i < nb; i += kPagesThreads / 32)
@@ -94,7 +79,6 @@ __global__ void __launch_bounds__(kPagesThreads) pages_grow_kernel(const PagesAr
         if (page >= 0 && page < a.num_pages) a.ref[page] = 1;
         else flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
       }
-    if (need >= 0) a.seq_len[b0 + threadIdx.x] += a.n_new[b0 + threadIdx.x];
     taken += total;
     __syncthreads();
   }
@@ -102,52 +86,68 @@ __global__ void __launch_bounds__(kPagesThreads) pages_grow_kernel(const PagesAr
 }
 
 cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t s) {
-  pages_grow_kernel<<<1, kPagesThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(pages_grow_kernel, dim3(1), dim3(kPagesThreads), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------- free
 // One cluster. References go down by compare-and-swap, so that a page without one is seen; a
 // page that loses its last is marked. Then each block counts and pushes its slice of the
-// marked pages, in page order.
+// marked pages, in page order. A warp takes 128 entries of a row at a time, four a lane, so
+// that their atomics are in flight together (a row per warp, 32 at a time, took 30 us for 64
+// sequences of 160 pages, this 10).
 __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
     pages_free_kernel(const PagesArgs a) {
-  __shared__ int sums[32], found;
+  constexpr int E = 4;
+  __shared__ int sums[33], found;
   cg::cluster_group cl = cg::this_cluster();
+  griddep_launch_dependents();
+  griddep_wait();
   const int rank = (int)cl.block_rank();
   const int nf = *a.n_free;
   const int warp = rank * (kPagesThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  for (int b = warp; b < a.batch; b += kPagesCluster * (kPagesThreads / 32)) {
+  const int per_row = (a.max_pages + 32 * E - 1) / (32 * E);
+  for (long long item = warp; item < (long long)a.batch * per_row; item += kPagesCluster * (kPagesThreads / 32)) {
+    const int b = (int)(item / per_row), j0 = (int)(item % per_row) * 32 * E + lane;
     if (a.drop[b] == 0) continue;
     const int t = a.seq_len[b];
     if (!good_len(t, a.max_pages)) {
-      if (lane == 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
+      if (lane == 0 && item % per_row == 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
       continue;
     }
-    for (int j = lane; j < pages_of(t); j += 32) {
-      const int page = a.bt[(size_t)b * a.max_pages + j];
-      bool ok = page >= 0 && page < a.num_pages;
-      if (ok) {
-        int cur = atomicAdd(&a.ref[page], 0);
-        while (true) {
-          if (cur <= 0) {
-            ok = false;
-            break;
-          }
-          const int seen = atomicCAS(&a.ref[page], cur, cur == 1 ? kGone : cur - 1);
-          if (seen == cur) break;
-          cur = seen;
-        }
+    const int np = pages_of(t);
+    int page[E], cur[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      const int j = j0 + 32 * e;
+      page[e] = j < np ? a.bt[(size_t)b * a.max_pages + j] : -1;
+      if (j < np && (page[e] < 0 || page[e] >= a.num_pages)) {
+        flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        page[e] = -1;
       }
-      if (!ok) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+    }
+    // most pages have one reference
+#pragma unroll
+    for (int e = 0; e < E; ++e) cur[e] = page[e] >= 0 ? atomicCAS(&a.ref[page[e]], 1, kGone) : 1;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      int c = cur[e];
+      if (c == 1) continue;
+      while (true) {
+        if (c <= 0) {
+          flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+          break;
+        }
+        const int seen = atomicCAS(&a.ref[page[e]], c, c == 1 ? kGone : c - 1);
+        if (seen == c) break;
+        c = seen;
+      }
     }
   }
   cl.sync();
-  const int per = ((a.num_pages + kPagesCluster - 1) / kPagesCluster + 3) & ~3;
+  const int per = (a.num_pages + kPagesCluster - 1) / kPagesCluster;
   const int p0 = min(a.num_pages, rank * per), p1 = min(a.num_pages, p0 + per);
-  int mine = 0;
+  int mine = 0, total;
   for (int p = p0 + threadIdx.x; p < p1; p += kPagesThreads) mine += __ldcg(&a.ref[p]) == kGone;
-  int total;
   (void)block_prefix(mine, sums, total);
   if (threadIdx.x == 0) found = total;
   cl.sync();
@@ -157,31 +157,33 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     if (k < rank) at += f;
     all += f;
   }
-  cl.sync();  // every block has read the counts
-  for (int c0 = p0; c0 < p1; c0 += kPagesThreads) {
+  for (int c0 = p0; c0 < p1 && total > 0; c0 += kPagesThreads) {
     const int p = c0 + threadIdx.x;
     const bool gone = p < p1 && __ldcg(&a.ref[p]) == kGone;
-    const int i = at + block_prefix(gone, sums, total);
+    int here;
+    const int i = at + block_prefix(gone, sums, here);
     if (gone) {
       a.ref[p] = 0;
       if (i >= 0 && i < a.num_pages) a.free_list[i] = p;
       else flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
     }
-    at += total;
+    at += here;
   }
   if (rank == 0 && threadIdx.x == 0) *a.n_free = min(nf + all, a.num_pages);
+  cl.sync();  // no block leaves while its count may be read
 }
 
 cudaError_t launch_pages_free(const PagesArgs& a, cudaStream_t s) {
-  pages_free_kernel<<<kPagesCluster, kPagesThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(pages_free_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, s, a);
 }
 
 // ---------------------------------------------------------------------------- fork
 // First launch, one block: lengths, and the page of its own that a branch's partial page takes
 // (at its entry of the branch's table, -1 where it takes none).
 __global__ void __launch_bounds__(kPagesThreads) pages_fork_plan_kernel(const PagesArgs a) {
-  __shared__ int sums[32];
+  __shared__ int sums[33];
+  griddep_launch_dependents();
+  griddep_wait();
   const int nf = *a.n_free;
   auto len_of = [&](int c, bool flag) -> int {
     if (c >= a.n_child) return 0;
@@ -198,10 +200,10 @@ __global__ void __launch_bounds__(kPagesThreads) pages_fork_plan_kernel(const Pa
     }
     return t;
   };
-  int all = 0, total;
+  int all = 0, total = 0, len = 0, at = 0;
   for (int c0 = 0; c0 < a.n_child; c0 += kPagesThreads) {
-    const int t = len_of(c0 + threadIdx.x, true);
-    (void)block_prefix(t % kPage != 0, sums, total);
+    len = len_of(c0 + threadIdx.x, true);
+    at = block_prefix(len % kPage != 0, sums, total);
     all += total;
   }
   const bool fits = nf >= 0 && nf <= a.num_pages && all <= nf;
@@ -209,9 +211,12 @@ __global__ void __launch_bounds__(kPagesThreads) pages_fork_plan_kernel(const Pa
   int taken = 0;
   for (int c0 = 0; c0 < a.n_child; c0 += kPagesThreads) {
     const int c = c0 + threadIdx.x;
-    const int t = fits ? len_of(c, false) : 0;
+    if (a.n_child > kPagesThreads) {  // else the sum above was this chunk's
+      len = len_of(c, false);
+      at = block_prefix(len % kPage != 0, sums, total);
+    }
+    const int t = fits ? len : 0, i = taken + at;
     const bool own = t % kPage != 0;
-    const int i = taken + block_prefix(own, sums, total);
     if (c < a.n_child) {
       a.child_len[c] = t;
       if (own) {
@@ -224,13 +229,13 @@ __global__ void __launch_bounds__(kPagesThreads) pages_fork_plan_kernel(const Pa
     }
     taken += total;
   }
-  if (threadIdx.x == 0 && taken > 0) *a.n_free = nf - taken;
-  griddep_launch_dependents();
+  if (threadIdx.x == 0 && fits && taken > 0) *a.n_free = nf - taken;
 }
 
 // Second launch, grid (branches, slabs of a page): the rest of the branch's table (slab 0) and
 // the filled rows of the source's last page.
 __global__ void __launch_bounds__(256) pages_fork_copy_kernel(const PagesArgs a, const PageSlabs sl) {
+  griddep_launch_dependents();
   griddep_wait();
   const int c = blockIdx.x, p = a.src[c], t = a.child_len[c];
   const int full = t / kPage, rest = t % kPage;
@@ -280,8 +285,7 @@ __global__ void __launch_bounds__(256) pages_fork_copy_kernel(const PagesArgs a,
 }
 
 cudaError_t launch_pages_fork(const PagesArgs& a, const PageSlabs& sl, cudaStream_t s) {
-  pages_fork_plan_kernel<<<1, kPagesThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(pages_fork_plan_kernel, dim3(1), dim3(kPagesThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   int slabs = 0;
   for (int k = 0; k < sl.n; ++k) slabs += sl.Hkv[k];
@@ -289,78 +293,114 @@ cudaError_t launch_pages_fork(const PagesArgs& a, const PageSlabs& sl, cudaStrea
 }
 
 // ---------------------------------------------------------------------------- compact
-// First launch, one cluster: every block takes a slice of the pages; holes (free pages below
-// L) and movers (referenced pages from L on) get their ranks from the blocks' counts, the
-// i-th mover goes to the i-th hole, and the books and the block table follow.
+// First launch, one cluster: every block takes a slice of the pages. From the blocks' counts of
+// referenced pages come L and the ranks of its holes (free pages below L) and movers
+// (referenced pages from L on); the i-th mover goes to the i-th hole. The lists, a mover's
+// rank by page, and the free list are written; references and tables follow with the copies.
 __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
     pages_compact_plan_kernel(const PagesArgs a) {
-  __shared__ int sums[32], count[2];
+  __shared__ int sums[33], live_s, hole_s, mover_s;
   cg::cluster_group cl = cg::this_cluster();
+  griddep_launch_dependents();
+  griddep_wait();
   const int rank = (int)cl.block_rank();
   const int per = (a.num_pages + kPagesCluster - 1) / kPagesCluster;
   const int p0 = min(a.num_pages, rank * per), p1 = min(a.num_pages, p0 + per);
   const int half = a.num_pages / 2;
   int32_t* src = a.moves + 4;
   int32_t* dst = src + half;
-  int32_t* map = dst + half;
+  int32_t* rank_of = dst + half;
   int mine = 0, total;
   for (int p = p0 + threadIdx.x; p < p1; p += kPagesThreads) mine += a.ref[p] > 0;
   (void)block_prefix(mine, sums, total);
-  if (threadIdx.x == 0) count[0] = total;
+  if (threadIdx.x == 0) live_s = total;
   cl.sync();
   int L = 0;
-  for (int k = 0; k < kPagesCluster; ++k) L += *cl.map_shared_rank(&count[0], k);
-  // holes and movers of this slice: a slice's pages below L, then those from L on
+  for (int k = 0; k < kPagesCluster; ++k) L += *cl.map_shared_rank(&live_s, k);
+  // the slice's pages below L, then those from L on
   const int cut = min(max(L, p0), p1);
-  int holes = 0, movers = 0;
-  for (int p = p0 + threadIdx.x; p < p1; p += kPagesThreads) {
-    const bool live = a.ref[p] > 0;
-    holes += !live && p < cut;
-    movers += live && p >= cut;
+  int below = 0;
+  if (cut == p1) {
+    below = total;
+  } else if (cut > p0) {
+    mine = 0;
+    for (int p = p0 + threadIdx.x; p < cut; p += kPagesThreads) mine += a.ref[p] > 0;
+    (void)block_prefix(mine, sums, below);
   }
-  int nh, nm;
-  (void)block_prefix(holes, sums, nh);
-  (void)block_prefix(movers, sums, nm);
-  cl.sync();  // count[0] has been read
-  if (threadIdx.x == 0) count[0] = nh, count[1] = nm;
+  if (threadIdx.x == 0) hole_s = cut - p0 - below, mover_s = total - below;
   cl.sync();
   int hole_at = 0, mover_at = 0, n_moves = 0;
   for (int k = 0; k < kPagesCluster; ++k) {
-    const int h = *cl.map_shared_rank(&count[0], k), m = *cl.map_shared_rank(&count[1], k);
+    const int h = *cl.map_shared_rank(&hole_s, k), m = *cl.map_shared_rank(&mover_s, k);
     if (k < rank) hole_at += h, mover_at += m;
     n_moves += m;
   }
   for (int c0 = p0; c0 < p1; c0 += kPagesThreads) {
     const int p = c0 + threadIdx.x;
-    const bool live = p < p1 && a.ref[p] > 0;
-    const bool hole = p < p1 && !live && p < L, mover = live && p >= L;
-    const int hi = hole_at + block_prefix(hole, sums, total);
-    hole_at += total;
-    const int mi = mover_at + block_prefix(mover, sums, total);
-    mover_at += total;
-    if (hole) dst[hi] = p;
-    if (mover) src[mi] = p;
-    if (p < p1 && p >= L) {
-      if (!live) map[p] = -1;
-      a.free_list[a.num_pages - 1 - p] = p;
-    }
-    if (p < p1 && p < L) a.free_list[a.num_pages - 1 - p] = -1;
+    const bool in = p < p1, live = in && a.ref[p] > 0, low = p < L;
+    int here;
+    // of one chunk the holes lie below L and the movers do not: one sum with the two in halves
+    const int r = block_prefix(in && low && !live ? 1 : live && !low ? 1 << 16 : 0, sums, here);
+    const int hi = hole_at + (r & 0xffff), mi = mover_at + (r >> 16);
+    hole_at += here & 0xffff;
+    mover_at += here >> 16;
+    if (in && low && !live) dst[hi] = p;
+    if (live && !low) src[mi] = p;
+    if (in && !low) rank_of[p] = live ? mi : -1;
+    if (in) a.free_list[a.num_pages - 1 - p] = low ? -1 : p;
   }
-  cl.sync();
-  const int tid = rank * kPagesThreads + threadIdx.x;
-  for (int i = tid; i < n_moves; i += kPagesCluster * kPagesThreads) {
-    const int from = __ldcg(src + i), to = __ldcg(dst + i);
-    map[from] = to;
-    a.ref[to] = a.ref[from];
-    a.ref[from] = 0;
-  }
-  if (tid == 0) {
+  if (rank == 0 && threadIdx.x == 0) {
     a.moves[0] = n_moves;
+    a.moves[1] = L;
     *a.n_free = a.num_pages - L;
   }
-  cl.sync();
-  const int warp = tid >> 5, lane = tid & 31;
-  for (int b = warp; b < a.batch; b += kPagesCluster * (kPagesThreads / 32)) {
+  cl.sync();  // no block leaves while its counts may be read
+}
+
+// Second launch: the moved pages' arrays in pieces of 8 KB, their references, and the tables.
+// Sources are >= L and destinations < L, so no page is both and the copies need no order.
+constexpr int kMovePiece = 8192;
+__global__ void __launch_bounds__(256) pages_move_kernel(const PagesArgs a, const PageSlabs sl) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int half = a.num_pages / 2;
+  const int n_moves = a.moves[0], L = a.moves[1];
+  const int32_t* src = a.moves + 4;
+  const int32_t* dst = src + half;
+  const int32_t* rank_of = dst + half;
+  int pieces = 0;
+  for (int k = 0; k < sl.n; ++k) pieces += (int)((sl.s[k].slab_bytes * sl.Hkv[k] + kMovePiece - 1) / kMovePiece);
+  for (long long x = blockIdx.x; x < (long long)n_moves * pieces; x += gridDim.x) {
+    const int m = (int)(x / pieces);
+    int piece = (int)(x % pieces), k = 0;
+    const int of = src[m], to = dst[m];
+    long long bytes = sl.s[0].slab_bytes * sl.Hkv[0];
+    while (piece >= (int)((bytes + kMovePiece - 1) / kMovePiece)) {
+      piece -= (int)((bytes + kMovePiece - 1) / kMovePiece);
+      ++k;
+      bytes = sl.s[k].slab_bytes * sl.Hkv[k];
+    }
+    const long long o = (long long)piece * kMovePiece;
+    const int len = (int)min((long long)kMovePiece, bytes - o);
+    const uint8_t* f = sl.s[k].base + of * bytes + o;
+    uint8_t* d = sl.s[k].base + to * bytes + o;
+    if (len == kMovePiece && (((uintptr_t)f | (uintptr_t)d) & 15) == 0) {
+      uint4 v[kMovePiece / 16 / 256];
+#pragma unroll
+      for (int i = 0; i < kMovePiece / 16 / 256; ++i) v[i] = reinterpret_cast<const uint4*>(f)[threadIdx.x + 256 * i];
+#pragma unroll
+      for (int i = 0; i < kMovePiece / 16 / 256; ++i) reinterpret_cast<uint4*>(d)[threadIdx.x + 256 * i] = v[i];
+    } else {
+      for (int i = threadIdx.x; i < len / 4; i += 256)
+        reinterpret_cast<uint32_t*>(d)[i] = reinterpret_cast<const uint32_t*>(f)[i];
+    }
+    if (piece == 0 && k == 0 && threadIdx.x == 0) {
+      a.ref[to] = a.ref[of];
+      a.ref[of] = 0;
+    }
+  }
+  const int warp = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  for (int b = warp; b < a.batch; b += gridDim.x * 8) {
     const int t = a.seq_len[b];
     if (!good_len(t, a.max_pages)) {
       if (lane == 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
@@ -372,43 +412,16 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
       if (page < 0 || page >= a.num_pages) {
         flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
       } else if (page >= L) {
-        const int to = __ldcg(map + page);
-        if (to < 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-        else *e = to;
-      }
-    }
-  }
-  griddep_launch_dependents();
-}
-
-// Second launch: the moved pages' arrays. Sources are >= L and destinations < L, so no page is
-// both and the copies need no order.
-__global__ void __launch_bounds__(256) pages_move_kernel(const PagesArgs a, const PageSlabs sl) {
-  griddep_wait();
-  const int half = a.num_pages / 2;
-  const int n_moves = a.moves[0];
-  const int32_t* src = a.moves + 4;
-  const int32_t* dst = src + half;
-  for (int m = blockIdx.x; m < n_moves; m += gridDim.x) {
-    const int of = src[m], to = dst[m];
-    for (int k = 0; k < sl.n; ++k) {
-      const long long bytes = sl.s[k].slab_bytes * sl.Hkv[k];
-      const uint8_t* f = sl.s[k].base + of * bytes;
-      uint8_t* d = sl.s[k].base + to * bytes;
-      if (bytes % 16 == 0 && ((uintptr_t)f & 15) == 0) {
-        for (long long i = threadIdx.x; i < bytes / 16; i += blockDim.x)
-          reinterpret_cast<uint4*>(d)[i] = reinterpret_cast<const uint4*>(f)[i];
-      } else {
-        for (long long i = threadIdx.x; i < bytes / 4; i += blockDim.x)
-          reinterpret_cast<uint32_t*>(d)[i] = reinterpret_cast<const uint32_t*>(f)[i];
+        const int r = rank_of[page];
+        if (r < 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        else *e = dst[r];
       }
     }
   }
 }
 
 cudaError_t launch_pages_compact(const PagesArgs& a, const PageSlabs& sl, cudaStream_t s) {
-  pages_compact_plan_kernel<<<kPagesCluster, kPagesThreads, 0, s>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(pages_compact_plan_kernel, dim3(kPagesCluster), dim3(kPagesThreads), 0, s, a);
   if (e != cudaSuccess) return e;
   return launch_pdl(pages_move_kernel, dim3(152 * 8), dim3(256), 0, s, a, sl);
 }

@@ -146,8 +146,20 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+class _Handle:
+    """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
+    and a tensor whose storage has moved makes a new one."""
+
+    _c = None  # (struct, pointers of the tensors it was made from)
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        if name != "_c":
+            object.__setattr__(self, "_c", None)
+
+
 @dataclass
-class KV:
+class KV(_Handle):
     """Device tensors of one group's paged KV cache."""
 
     k: torch.Tensor  # [num_pages][Hkv][64][d], float32, bfloat16 or uint8 (FP8 E4M3 codes);
@@ -160,6 +172,12 @@ class KV:
     v_sf: torch.Tensor | None = None
 
     def c(self) -> hs2_kv:
+        ptrs = [None if t is None else t.data_ptr() for t in _kv_tensors(self)]
+        if self._c is None or self._c[1] != ptrs:
+            self._c = (self._make(), ptrs)
+        return self._c[0]
+
+    def _make(self) -> hs2_kv:
         d = int(self.k.shape[3])
         if self.k.dtype == torch.uint8 and self.k_sf is not None:
             dt, d = FP4_E2M1, 2 * d
@@ -387,59 +405,70 @@ def hs2_selftest_wait_timeout(timeout_us: int, dev_err: torch.Tensor, stream=Non
 
 
 # ---------------------------------------------------------------------------- paged-cache operators
-def _scratch(nbytes: int, device, ws, stream):
-    """The caller's workspace, or one of this call's own that stays alive until `stream` is done."""
-    t = _workspace(nbytes, device, ws)
-    if ws is None and stream is not None:
-        t.record_stream(stream)
-    return t
-
-
 _ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
-
-
-def _i32(t: torch.Tensor, name: str, *shape) -> torch.Tensor:
-    """An int32 contiguous tensor of the given shape (-1: any), or an error."""
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape) or any(
-            a not in (-1, b) for a, b in zip(shape, t.shape)):
-        raise HS2Error(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
-    return t
-
-
-def _here(stream, *tensors) -> None:
-    """Every tensor on one device, and that the current one (the library launches there)."""
-    dev = {t.device for t in tensors if t is not None}
-    if len(dev) > 1:
-        raise HS2Error("tensors on several devices")
-    d = next(iter(dev))
-    if d.type != "cuda" or d.index != torch.cuda.current_device() or (stream is not None and stream.device != d):
-        raise HS2Error("the tensors must be on the current CUDA device (and the stream's)")
 
 
 def _kv_tensors(kv: KV):
     return kv.k, kv.v, kv.block_table, kv.seq_len, kv.k_scale, kv.v_scale, kv.k_sf, kv.v_sf
 
 
+def _pages_tensors(p: "Pages"):
+    return p.ref, p.free_list, p.n_free
+
+
+def _i32(t: torch.Tensor, name: str, *shape) -> None:
+    """t is an int32 contiguous tensor of that shape, or an error."""
+    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise HS2Error(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
+
+
+def _table(t: torch.Tensor, name: str):
+    """(rows, columns) of an int32 contiguous table, or an error."""
+    if t.dtype is not torch.int32 or t.dim() != 2 or not t.is_contiguous():
+        raise HS2Error(f"{name} must be a contiguous int32 matrix")
+    return t.shape
+
+
+def _launch_stream(stream, tensors) -> int:
+    """The stream to launch on, once every tensor is on the current device (and the stream's)."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise HS2Error("tensors on several devices")
+    if dev < 0 or dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
+        raise HS2Error("the tensors must be on the current CUDA device (and the stream's)")
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of this call's own; it stays alive until `stream` is done with it."""
+    t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _rows(t: torch.Tensor, kv: hs2_kv, n_rows: int, name: str):
     """Row dtype code and token stride of [n_rows][Hkv][d] rows, heads next to each other."""
-    if t.dtype not in _ROW_DTYPES or tuple(t.shape) != (n_rows, kv.Hkv, kv.d) or t.stride(2) != 1 or (
-            kv.Hkv > 1 and t.stride(1) != kv.d):
+    stride = t.stride()
+    if t.dtype not in _ROW_DTYPES or tuple(t.shape) != (n_rows, kv.Hkv, kv.d) or stride[2] != 1 or (
+            kv.Hkv > 1 and stride[1] != kv.d):
         raise HS2Error(f"{name} must be float32 or bfloat16 [n_rows][Hkv][d] with contiguous tokens")
-    return _ROW_DTYPES[t.dtype], int(t.stride(0)) if n_rows > 1 else kv.Hkv * kv.d
+    return _ROW_DTYPES[t.dtype], stride[0] if n_rows > 1 else kv.Hkv * kv.d
 
 
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
     c = kv.c()
-    n = int(k_rows.shape[0])
-    _here(stream, k_rows, v_rows, row_start, dev_err, *_kv_tensors(kv))
+    n = k_rows.shape[0]
     dt, stride = _rows(k_rows, c, n, "k_rows")
     if (v_rows is None) != (kv.v is None):
         raise HS2Error("v_rows goes with a cache that has V")
     if v_rows is not None and _rows(v_rows, c, n, "v_rows") != (dt, stride):
         raise HS2Error("v_rows must have k_rows' dtype and token stride")
     _i32(row_start, "row_start", c.batch + 1)
-    _check(call(ctypes.byref(c), _ptr(k_rows), _ptr(v_rows), dt, stride, _ptr(row_start), n, _ptr(dev_err),
-                _stream(stream)))
+    st = _launch_stream(stream, (k_rows, v_rows, row_start, dev_err, *_kv_tensors(kv)))
+    _check(call(ctypes.byref(c), k_rows.data_ptr(), _ptr(v_rows), dt, stride, row_start.data_ptr(), n, _ptr(dev_err),
+                st))
 
 
 def hs2_kv_write(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor, dev_err=None,
@@ -456,10 +485,10 @@ def hs2_kv_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype
     """The values of the rows hs2_kv_write with this ``row_start`` would write, as (k_rows,
     v_rows) of ``dtype`` [n_rows][Hkv][d] (v_rows None for a key-only cache). Rows outside
     every sequence are left as they are in ``out``."""
-    c = kv.c()
     if out is None:
-        out = tuple(torch.empty((n_rows, c.Hkv, c.d), dtype=dtype, device=kv.k.device) if x is not None else None
-                    for x in (kv.k, kv.v))
+        c = kv.c()
+        k = torch.empty((n_rows, c.Hkv, c.d), dtype=dtype, device=kv.k.device)
+        out = (k, None if kv.v is None else torch.empty_like(k))
     elif out[0].shape[0] != n_rows or out[0].dtype != dtype:
         raise HS2Error("out must hold n_rows rows of the dtype")
     _kv_rows(load().hs2_kv_read, kv, out[0], out[1], row_start, dev_err, stream)
@@ -467,8 +496,7 @@ def hs2_kv_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype
 
 
 def hs2_fa_chunk_workspace(n_rows: int, Hq: int, kv: KV, max_n: int, max_t: int, w: int = 0) -> int:
-    c = kv.c()
-    return int(load().hs2_fa_chunk_workspace(n_rows, Hq, ctypes.byref(c), max_n, max_t, w))
+    return load().hs2_fa_chunk_workspace(n_rows, Hq, ctypes.byref(kv.c()), max_n, max_t, w)
 
 
 def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float, max_n: int,
@@ -486,30 +514,34 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
     n, Hq, d = q.shape
     if max_t is None:
         max_t = c.max_pages * c.page_size
-    if q.dtype != (torch.float32 if c.dtype == F32 else torch.bfloat16) or not q.is_contiguous() or d != c.d:
+    if q.dtype is not (torch.float32 if c.dtype == F32 else torch.bfloat16) or d != c.d or not q.is_contiguous():
         raise HS2Error("q must be contiguous [n_rows][Hq][d], bfloat16 (float32 with an F32 cache)")
-    if sink is not None and (sink.dtype != torch.float32 or not sink.is_contiguous() or sink.numel() != Hq):
+    if sink is not None and (sink.dtype is not torch.float32 or not sink.is_contiguous() or sink.numel() != Hq):
         raise HS2Error("sink must be float32 [Hq]")
     if o_dtype not in _ROW_DTYPES:
         raise HS2Error("o_dtype must be float32 or bfloat16")
-    if out is None:
-        out = (torch.empty((n, Hq, d), dtype=o_dtype, device=q.device),
-               torch.empty((n, Hq), dtype=torch.float32, device=q.device))
-    o, lse = out
-    if o.dtype != o_dtype or tuple(o.shape) != (n, Hq, d) or not o.is_contiguous() or (
-            lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (n, Hq) or not lse.is_contiguous())):
-        raise HS2Error("out must be contiguous (o [n_rows][Hq][d] of o_dtype, lse float32 [n_rows][Hq] or None)")
     _i32(row_start, "row_start", c.batch + 1)
-    _here(stream, q, row_start, sink, o, lse, workspace, dev_err, *_kv_tensors(kv))
-    ws = _scratch(int(lib.hs2_fa_chunk_workspace(n, Hq, ctypes.byref(c), max_n, max_t, w)), q.device, workspace, stream)
-    _check(lib.hs2_fa_chunk(_ptr(q), _ptr(row_start), n, max_n, Hq, ctypes.byref(c), max_t, w, float(scale),
-                            _ptr(sink), _ptr(o), _ROW_DTYPES[o_dtype], _ptr(lse), _ptr(ws),
-                            ws.numel() * ws.element_size(), _ptr(dev_err), _stream(stream)))
+    if out is None:
+        o = torch.empty((n, Hq, d), dtype=o_dtype, device=q.device)
+        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+    else:
+        o, lse = out
+        if o.dtype is not o_dtype or tuple(o.shape) != (n, Hq, d) or not o.is_contiguous() or (
+                lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (n, Hq)
+                                     or not lse.is_contiguous())):
+            raise HS2Error("out must be contiguous (o [n_rows][Hq][d] of o_dtype, lse float32 [n_rows][Hq] or None)")
+    st = _launch_stream(stream, (q, row_start, sink, o, lse, workspace, dev_err, *_kv_tensors(kv)))
+    ws = workspace
+    if ws is None:
+        ws = _scratch(lib.hs2_fa_chunk_workspace(n, Hq, ctypes.byref(c), max_n, max_t, w), q.device, stream)
+    _check(lib.hs2_fa_chunk(q.data_ptr(), row_start.data_ptr(), n, max_n, Hq, ctypes.byref(c), max_t, w, scale,
+                            _ptr(sink), o.data_ptr(), _ROW_DTYPES[o_dtype], _ptr(lse), ws.data_ptr(), ws.nbytes,
+                            _ptr(dev_err), st))
     return o, lse
 
 
 @dataclass
-class Pages:
+class Pages(_Handle):
     """The books of a page pool: references per page and the stack of free pages."""
 
     ref: torch.Tensor  # int32 [num_pages], table entries that hold the page (0: free)
@@ -524,72 +556,79 @@ class Pages:
                    n_free=torch.full((1,), num_pages, dtype=torch.int32, device=device))
 
     def c(self) -> hs2_pages:
-        n = int(self.ref.shape[0])
-        for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
-            _i32(t, name, size)
-        return hs2_pages(_ptr(self.ref), _ptr(self.free_list), _ptr(self.n_free), n)
-
-
-def _pages_tensors(p: Pages):
-    return p.ref, p.free_list, p.n_free
+        ptrs = [t.data_ptr() for t in _pages_tensors(self)]
+        if self._c is None or self._c[1] != ptrs:
+            n = int(self.ref.shape[0])
+            for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
+                _i32(t, name, size)
+            self._c = (hs2_pages(*ptrs, n), ptrs)
+        return self._c[0]
 
 
 def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, n_new: torch.Tensor, dev_err=None,
                    stream=None) -> None:
     """seq_len += n_new, with free pages for the positions that need them, in place."""
-    c = pages.c()
-    _i32(block_table, "block_table", -1, -1)
-    b, mp = block_table.shape
+    b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(n_new, "n_new", b)
-    _here(stream, block_table, seq_len, n_new, dev_err, *_pages_tensors(pages))
-    _check(load().hs2_pages_grow(ctypes.byref(c), _ptr(block_table), _ptr(seq_len), _ptr(n_new), b, mp, _ptr(dev_err),
-                                 _stream(stream)))
+    st = _launch_stream(stream, (block_table, seq_len, n_new, dev_err, *_pages_tensors(pages)))
+    _check(load().hs2_pages_grow(ctypes.byref(pages.c()), block_table.data_ptr(), seq_len.data_ptr(),
+                                 n_new.data_ptr(), b, mp, _ptr(dev_err), st))
 
 
 def hs2_pages_free(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, drop: torch.Tensor, dev_err=None,
                    stream=None) -> None:
     """The pages of every sequence with drop[b] != 0 lose a reference; those left with none
     return to the free list."""
-    c = pages.c()
-    _i32(block_table, "block_table", -1, -1)
-    b, mp = block_table.shape
+    b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(drop, "drop", b)
-    _here(stream, block_table, seq_len, drop, dev_err, *_pages_tensors(pages))
-    _check(load().hs2_pages_free(ctypes.byref(c), _ptr(block_table), _ptr(seq_len), _ptr(drop), b, mp, _ptr(dev_err),
-                                 _stream(stream)))
+    st = _launch_stream(stream, (block_table, seq_len, drop, dev_err, *_pages_tensors(pages)))
+    _check(load().hs2_pages_free(ctypes.byref(pages.c()), block_table.data_ptr(), seq_len.data_ptr(),
+                                 drop.data_ptr(), b, mp, _ptr(dev_err), st))
+
+
+def _kv_array(kvs):
+    """The caches' C structs as an array."""
+    if not kvs:
+        raise HS2Error("at least one cache")
+    return ctypes.byref(kvs[0].c()) if len(kvs) == 1 else (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
 
 
 def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None, stream=None):
     """Branches of the caches' sequences: branch c continues sequence src[c] (-1: none), with
     its full pages shared and the last, partly filled one copied. ``kvs``: the caches of one
     block table. Returns (child_table, child_len)."""
-    c = pages.c()
-    cs = (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
-    _i32(src, "src", -1)
-    n, mp = int(src.shape[0]), int(kvs[0].block_table.shape[1])
+    cs = _kv_array(kvs)
+    n, mp = src.numel(), kvs[0].block_table.shape[1]
+    _i32(src, "src", n)
     if out is None:
         out = (torch.empty((n, mp), dtype=torch.int32, device=src.device),
                torch.empty((n,), dtype=torch.int32, device=src.device))
-    table, length = _i32(out[0], "child_table", n, mp), _i32(out[1], "child_len", n)
-    _here(stream, src, table, length, dev_err, *_pages_tensors(pages), *[t for kv in kvs for t in _kv_tensors(kv)])
-    _check(load().hs2_pages_fork(ctypes.byref(c), len(kvs), cs, _ptr(src), n, _ptr(table), _ptr(length),
-                                 _ptr(dev_err), _stream(stream)))
-    return table, length
+    else:
+        _i32(out[0], "child_table", n, mp)
+        _i32(out[1], "child_len", n)
+    ts = [src, *out, dev_err, *_pages_tensors(pages)]
+    for kv in kvs:
+        ts += _kv_tensors(kv)
+    st = _launch_stream(stream, ts)
+    _check(load().hs2_pages_fork(ctypes.byref(pages.c()), len(kvs), cs, src.data_ptr(), n, out[0].data_ptr(),
+                                 out[1].data_ptr(), _ptr(dev_err), st))
+    return out
 
 
 def hs2_pages_compact_workspace(pages: Pages) -> int:
-    c = pages.c()
-    return int(load().hs2_pages_compact_workspace(ctypes.byref(c)))
+    return load().hs2_pages_compact_workspace(ctypes.byref(pages.c()))
 
 
 def hs2_pages_compact(pages: Pages, kvs, workspace=None, dev_err=None, stream=None) -> None:
     """The pool's referenced pages to its front, in place in every cache of ``kvs`` (which
     share one block table holding every sequence), with tables and books updated."""
+    cs = _kv_array(kvs)
+    ts = [pages.ref, pages.free_list, pages.n_free, workspace, dev_err]
+    for kv in kvs:
+        ts += _kv_tensors(kv)
+    st = _launch_stream(stream, ts)
     c = pages.c()
-    cs = (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
-    _here(stream, dev_err, workspace, *_pages_tensors(pages), *[t for kv in kvs for t in _kv_tensors(kv)])
-    ws = _scratch(int(load().hs2_pages_compact_workspace(ctypes.byref(c))), pages.ref.device, workspace, stream)
-    _check(load().hs2_pages_compact(ctypes.byref(c), len(kvs), cs, _ptr(ws), ws.numel() * ws.element_size(),
-                                    _ptr(dev_err), _stream(stream)))
+    ws = workspace if workspace is not None else _scratch(hs2_pages_compact_workspace(pages), pages.ref.device, stream)
+    _check(load().hs2_pages_compact(ctypes.byref(c), len(kvs), cs, ws.data_ptr(), ws.nbytes, _ptr(dev_err), st))
