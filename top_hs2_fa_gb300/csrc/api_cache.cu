@@ -90,6 +90,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       L.narrow[L.n_plans] = narrow;
       p.ctas = sm_count();
       p.tile_rows = tile_rows;
+      p.halves = narrow ? 1 : 2;
       p.min_rows = lo;
       p.max_rows = hi;
       p.min_tiles = min_tiles;
@@ -99,7 +100,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       size_t* o = L.off[L.n_plans++];
       o[0] = take(16);
       o[1] = take(4 * (size_t)p.ctas);
-      o[2] = take(4 * (size_t)p.max_units);
+      o[2] = take(4 * (size_t)p.max_units * p.halves);
       o[3] = take(48 * (size_t)p.max_units);
       o[4] = take(2 * (size_t)p.ctas * tile_rows * 8);
       o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
@@ -108,7 +109,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
     const long long few = std::min<long long>(top, cut);
     add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut, 2);
     if (top > cut) {
-      hs2::ChunkPlan* p = add(false, 128, cut, 0x7fffffff, 4);
+      hs2::ChunkPlan* p = add(false, 256, cut, 0x7fffffff, 4);
       p->expand = low_precision(kv);
       if (p->expand) {
         L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut + 1));

@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 
 #include "chunk_plan.cuh"
+#include "f32x2.cuh"
 #include "tc.cuh"
 
 namespace hs2 {
@@ -101,33 +102,6 @@ HS2_DEVI float fmax3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-
-// Pairs of floats in one instruction.
-struct F2 {
-  float x, y;
-};
-HS2_DEVI F2 fma2(F2 a, F2 b, F2 c) {
-  F2 d;
-  asm("{.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-HS2_DEVI F2 add2(F2 a, F2 b) {
-  F2 d;
-  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-HS2_DEVI F2 mul2(F2 a, F2 b) {
-  F2 d;
-  asm("{.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
 }
 
 HS2_DEVI void bulk_load(void* smem, const void* src, uint32_t bytes, uint64_t* bar) {

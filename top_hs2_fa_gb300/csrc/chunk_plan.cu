@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         int4* d = reinterpret_cast<int4*>(p.units) + 3 * (size_t)(units + u);
         const int4* s = reinterpret_cast<const int4*>(&x);
         d[0] = s[0], d[1] = s[1], d[2] = s[2];
-        p.arrive[units + u] = 0;
+        if (p.halves == 2) reinterpret_cast<int2*>(p.arrive)[units + u] = make_int2(0, 0);
+        else p.arrive[units + u] = 0;
       }
     }
     units += here;

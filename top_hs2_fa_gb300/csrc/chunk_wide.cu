@@ -1,53 +1,51 @@
-// chunk_wide.cu — attention of query chunks on tcgen05: units of up to 128 rows.
+// chunk_wide.cu — attention of query chunks on tcgen05: units of up to 256 rows.
 //
 // Bound by the tensor pipe: 4 D flops per (row, key) against 4 D / rows bytes of K and V. A
 // unit's rows are a KV head's query heads of consecutive tokens, token-major, so that a chunk
 // of 128 / G tokens fills the 128 rows of an MMA whatever G is, and one K/V tile serves all
-// the heads that share it. Persistent CTAs (one per SM) walk equal ranges of the units' key
-// tiles (chunk_plan.cuh); the pipeline runs on across units.
-//   warp 0      TMA producer of Q (two buffers, one per unit) and the K tiles
-//   warp 10     TMA producer of the V tiles
-//   warp 1      issues S_j = Q K_j^T into one of two TMEM buffers
-//   warp 11     issues O += P_j V_j with P_j read from tensor memory; two issuers, so that one's
-//               waits overlap the other's instructions
-//   warps 2-9   softmax, two threads per row (warps w and w + 4 share a lane quadrant, each has
-//               64 of the tile's 128 columns, i.e. one page): row max over both halves, p =
-//               2^(x c - m) with the reference m moving only when it is exceeded by 2^8, P
-//               rounded to bf16 over the tile's own S columns, the normaliser summed in fp32
-//               from the unrounded weights
+// the heads that share it. A unit is two such halves, a and b, that take turns on the tensor
+// pipe: while one half's softmax runs, the other's products do (one half with two S buffers left
+// the pipe waiting for the softmax of the only tile: 1.02 ms against 0.70 for 2048 tokens over
+// 32768 FP4 keys). Persistent CTAs (one per SM) walk equal ranges of the units' key tiles
+// (chunk_plan.cuh).
+//   warp 0      TMA producer of Q and the K tiles; warp 1 of the V tiles
+//   warps 2, 3  issue half a's and half b's MMAs: O += P_j V_j with P_j read from tensor memory,
+//               then S_{j+1} = Q K^T over it
+//   warps 4-7, 8-11  softmax of half a, b: a thread has a whole row. p = 2^(x c - m) with the
+//               reference m moving only when it is exceeded by 2^8, P rounded to bf16 over the
+//               tile's own S columns, the normaliser summed in fp32 from unrounded weights
 // FP8 / FP4 caches come as expanded bf16 pages: their page factors scale the logits (c) and the
-// weights (2^lv) per half-tile, at no cost per element.
-// TMEM: S0 [0,128), S1 [128,256), O [256,384) and [384,512) in turn, so that a unit's output is
-// read while the next one accumulates. Every wait is bounded.
+// weights (2^lv) per page, at no cost per element.
+// TMEM: S of a [0,128), of b [128,256), O of a [256,384), of b [384,512). Every wait is bounded.
 #include <cuda.h>
 
 #include "chunk_plan.cuh"
+#include "f32x2.cuh"
 #include "tc.cuh"
 
 namespace hs2 {
 
 namespace {
 
-constexpr int kWRows = 128;
+constexpr int kWRows = 128;      // rows of a half
 constexpr int kWThreads = 384;
-constexpr int kWVWarp = 10, kWPVWarp = 11;
 constexpr uint32_t kWTmem = 512;
 constexpr float kWRescale = 8.f;
 constexpr int kWStages = 2;  // K slots and V slots
+// Registers per thread of the three 128-thread groups, of the 3 * 168 of the launch.
+constexpr int kWRegsMisc = 64, kWRegsSoftmax = 216;
 
 template <int D>
 struct WideSmem {
   static constexpr uint32_t kTile = 128 * D * 2;
-  uint8_t q[2][kTile];
+  uint8_t q[2][kTile];  // by half
   uint8_t k[kWStages][kTile];
   uint8_t v[kWStages][kTile];
-  float xch[2][kWRows];
-  uint64_t q_full[2], q_empty[2], k_full[kWStages], k_empty[kWStages], v_full[kWStages], v_empty[kWStages], s_full[2],
-      p_full[2], p_empty[2], o_empty[2];
-  uint64_t x_full[4], x_empty[4];
-  uint64_t all;  // a meeting of the softmax threads
+  uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], v_full[kWStages], v_empty[kWStages];
+  // by half
+  uint64_t s_full[2], p_full[2], pv_done[2], all[2];
   uint32_t tmem_base;
-  int abort, last;
+  int abort, last[2];
 };
 
 template <typename S>
@@ -63,6 +61,10 @@ HS2_DEVI float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+template <int R>
+HS2_DEVI void wide_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R>
+HS2_DEVI void wide_regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
 
 }  // namespace
 
@@ -78,25 +80,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
   Sm& sm = *reinterpret_cast<Sm*>(dsmem + ((1024 - (tc::smem_u32(dsmem) & 1023)) & 1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2; ++s) {
-      tc::mbar_init(&sm.q_full[s], 1);
-      tc::mbar_init(&sm.q_empty[s], 1);
-      tc::mbar_init(&sm.s_full[s], 1);
-      tc::mbar_init(&sm.p_full[s], 256);
-      tc::mbar_init(&sm.p_empty[s], 1);
-      tc::mbar_init(&sm.o_empty[s], 256);
-    }
+    tc::mbar_init(&sm.q_full, 1);
+    tc::mbar_init(&sm.q_empty, 2);  // the last S of either half
     for (int s = 0; s < kWStages; ++s) {
       tc::mbar_init(&sm.k_full[s], 1);
-      tc::mbar_init(&sm.k_empty[s], 1);
+      tc::mbar_init(&sm.k_empty[s], 2);  // S, P.V of either half
       tc::mbar_init(&sm.v_full[s], 1);
-      tc::mbar_init(&sm.v_empty[s], 1);
+      tc::mbar_init(&sm.v_empty[s], 2);
     }
-    for (int q = 0; q < 4; ++q) {
-      tc::mbar_init(&sm.x_full[q], 64);
-      tc::mbar_init(&sm.x_empty[q], 64);
+    for (int h = 0; h < 2; ++h) {
+      tc::mbar_init(&sm.s_full[h], 1);
+      tc::mbar_init(&sm.p_full[h], 128);
+      tc::mbar_init(&sm.pv_done[h], 1);
+      tc::mbar_init(&sm.all[h], 128);
     }
-    tc::mbar_init(&sm.all, 256);
     sm.abort = 0;
     tc::fence_mbar_init();
   }
@@ -108,33 +105,34 @@ __global__ void __launch_bounds__(kWThreads, 1)
   const uint32_t tS = sm.tmem_base, tO = tS + 256;
   const ChunkRange rg = chunk_range(p, blockIdx.x);
   const int per = p.head[1];
+  const int half_tok = kWRows / a.G;  // tokens of a half
 
-  if (warp == 0 || warp == kWVWarp) {
+  if (warp < 2) {
     // ------------------------------------------------------------------ TMA producers
+    wide_regs_down<kWRegsMisc>();
     if (lane == 0) {
       const bool is_k = warp == 0;
       uint64_t* full = is_k ? sm.k_full : sm.v_full;
       uint64_t* empty = is_k ? sm.k_empty : sm.v_empty;
       const CUtensorMap* tm = is_k ? &tm_k : &tm_v;
       const int oob = (EXP ? p.max_exp_pages : a.num_pages) * a.Hkv * kPage;  // the row past the pool: zeros
-      int issued = 0, seg = 0, q_issued = 0;
+      int issued = 0, seg = 0;
       bool ok = true;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
         const ChunkUnit u = load_unit(p, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
         if (is_k) {
-          const int qb = seg & 1;
-          if (!tc::mbar_wait(&sm.q_empty[qb], ((seg >> 1) & 1) ^ 1)) { ok = false; break; }
-          tc::mbar_arrive_expect_tx(&sm.q_full[qb], kTile);
-          for (int c = 0; c < NB; ++c)
-            tc::tma_load_3d(sm.q[qb] + c * 16384, &tm_q, 64 * c, u.g * a.G, u.row, &sm.q_full[qb]);
-          q_issued = seg + 1;
+          if (!tc::mbar_wait(&sm.q_empty, (seg & 1) ^ 1)) { ok = false; break; }
+          const int halves = u.ntok > half_tok ? 2 : 1;
+          tc::mbar_arrive_expect_tx(&sm.q_full, halves * kTile);
+          for (int h = 0; h < halves; ++h)
+            for (int c = 0; c < NB; ++c)
+              tc::tma_load_3d(sm.q[h] + c * 16384, &tm_q, 64 * c, u.g * a.G, u.row + h * half_tok, &sm.q_full);
         }
         const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
         for (int j = j0; j < j1; ++j) {
           const int st = issued % kWStages;
-          if (stopped(sm) || !tc::mbar_wait(&empty[st], ((issued / kWStages) & 1) ^ 1)) { ok = false; break; }
           int rows[2];
           for (int h = 0; h < 2; ++h) {
             const int lp = u.page0 + 2 * j + h;
@@ -149,6 +147,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
               }
             }
           }
+          if (stopped(sm) || !tc::mbar_wait(&empty[st], ((issued / kWStages) & 1) ^ 1)) { ok = false; break; }
           tc::mbar_arrive_expect_tx(&full[st], kTile);
           uint8_t* dst = is_k ? sm.k[st] : sm.v[st];
           for (int h = 0; h < 2; ++h)
@@ -158,206 +157,202 @@ __global__ void __launch_bounds__(kWThreads, 1)
       }
       if (!ok) stop(sm, a.dev_err);
       for (int i = max(0, issued - kWStages); i < issued; ++i) (void)tc::mbar_wait(&full[i % kWStages], (i / kWStages) & 1);
-      for (int i = max(0, q_issued - 2); i < q_issued; ++i) (void)tc::mbar_wait(&sm.q_full[i & 1], (i >> 1) & 1);
+      if (is_k && seg > 0) (void)tc::mbar_wait(&sm.q_full, (seg - 1) & 1);
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ S = Q K^T
-    constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128);
+  } else if (warp < 4) {
+    // ------------------------------------------------------------------ MMA issuers
+    wide_regs_down<kWRegsMisc>();
+    constexpr uint32_t idS = tc::idesc_bf16_f32(128, 128), idO = tc::idesc_bf16_f32_bmn(128, D);
+    const int h = warp - 2;
     const uint32_t el = tc::elect_one();
-    int it = 0, seg = 0;
+    const uint32_t s = tS + h * 128, o = tO + h * 128;
+    const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sm.q[h]));
+    int it = 0, seg = 0, mine = 0;  // tiles and units of the CTA, and the tiles of this half
     bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
-      const int end = min(rg.end, pt.y + pt.x);
-      const int qb = seg & 1;
-      const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sm.q[qb]));
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.q_full[qb], (seg >> 1) & 1));
-      for (; ok && at < end; ++at, ++it) {
-        const int st = it & 1, kv = it % kWStages;
-        // S_j's buffer holds P_{j-2} until its P.V is done
-        ok = __all_sync(0xffffffffu, (it < 2 || tc::mbar_wait(&sm.p_empty[st], ((it - 2) >> 1) & 1)) &&
-                                         tc::mbar_wait(&sm.k_full[kv], (it / kWStages) & 1));
-        if (!ok) break;
-        tc::tc_fence_after();
-        const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sm.k[kv]));
+      const ChunkUnit u = load_unit(p, un);
+      const int end = min(rg.end, u.prefix + u.ntiles);
+      const bool here = h == 0 || u.ntok > half_tok;
+      ok = all(tc::mbar_wait(&sm.q_full, seg & 1));
+      // S of tile i of the CTA
+      auto scores = [&](int i) -> bool {
+        const int kv = i % kWStages;
+        if (!all(tc::mbar_wait(&sm.k_full[kv], (i / kWStages) & 1))) return false;
+        if (here) {
+          tc::tc_fence_after();
+          const uint64_t kd = tc::sdesc_sw128(tc::smem_u32(sm.k[kv]));
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t off = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
-          tc::mma_f16_warp(tS + st * 128, qd + off, kd + off, idS, ks > 0 ? 1u : 0u, el);
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint32_t off = ((ks >> 2) * 16384u + (ks & 3) * 32u) >> 4;
+            tc::mma_f16_warp(s, qd + off, kd + off, idS, ks > 0 ? 1u : 0u, el);
+          }
+          tc::mma_commit_warp(&sm.s_full[h], el);
+          tc::mma_commit_warp(&sm.k_empty[kv], el);
+        } else if (el) {
+          tc::mbar_arrive(&sm.k_empty[kv]);
         }
-        tc::mma_commit_warp(&sm.s_full[st], el);
-        tc::mma_commit_warp(&sm.k_empty[kv], el);
-      }
-      if (ok) tc::mma_commit_warp(&sm.q_empty[qb], el);
-    }
-    if (!ok && lane == 0) stop(sm, a.dev_err);
-    if (it > 0) (void)tc::mbar_wait(&sm.s_full[(it - 1) & 1], ((it - 1) >> 1) & 1);
-  } else if (warp == kWPVWarp) {
-    // ------------------------------------------------------------------ O += P V
-    constexpr uint32_t idO = tc::idesc_bf16_f32_bmn(128, D);
-    const uint32_t el = tc::elect_one();
-    int it = 0, seg = 0;
-    bool ok = true;
-    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
-      const int end = min(rg.end, pt.y + pt.x);
-      const uint32_t o = tO + (seg & 1) * 128;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1));
+        return true;
+      };
+      ok = ok && scores(it);
+      // (the first P of a unit comes from the threads that have read the last unit out of O)
       for (int j = 0; ok && at < end; ++at, ++it, ++j) {
-        const int st = it & 1, kv = it % kWStages;
-        ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.v_full[kv], (it / kWStages) & 1) &&
-                                         tc::mbar_wait(&sm.p_full[st], (it >> 1) & 1));
+        const int kv = it % kWStages;
+        ok = all(tc::mbar_wait(&sm.v_full[kv], (it / kWStages) & 1) &&
+                 (!here || tc::mbar_wait(&sm.p_full[h], mine & 1)));
         if (!ok) break;
-        tc::tc_fence_after();
-        const uint64_t vd = tc::sdesc_sw128_mn(tc::smem_u32(sm.v[kv]), 16384u, 1024u);
+        if (here) {
+          tc::tc_fence_after();
+          const uint64_t vd = tc::sdesc_sw128_mn(tc::smem_u32(sm.v[kv]), 16384u, 1024u);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_f16_ts_warp(o, tS + st * 128 + ks * 8, vd + ks * 128, idO, (j > 0 || ks > 0) ? 1u : 0u, el);
-        tc::mma_commit_warp(&sm.v_empty[kv], el);
-        tc::mma_commit_warp(&sm.p_empty[st], el);
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_f16_ts_warp(o, s + ks * 8, vd + ks * 128, idO, (j > 0 || ks > 0) ? 1u : 0u, el);
+          tc::mma_commit_warp(&sm.v_empty[kv], el);
+          tc::mma_commit_warp(&sm.pv_done[h], el);
+          ++mine;
+        } else if (el) {
+          tc::mbar_arrive(&sm.v_empty[kv]);
+        }
+        if (at + 1 < end) ok = scores(it + 1);
+      }
+      if (ok) {
+        if (here) tc::mma_commit_warp(&sm.q_empty, el);
+        else if (el) tc::mbar_arrive(&sm.q_empty);
       }
     }
     if (!ok && lane == 0) stop(sm, a.dev_err);
-    if (it > 0) (void)tc::mbar_wait(&sm.p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1);
+    if (mine > 0) (void)tc::mbar_wait(&sm.pv_done[h], (mine - 1) & 1);
+    if (!ok) (void)tc::mbar_wait(&sm.s_full[h], mine & 1, 1000000ull);  // an S whose P never came
   } else {
     // ------------------------------------------------------------------ softmax warps
-    const int qd = warp & 3;
-    const int half = (warp - 2) >> 2;
-    const int r = qd * 32 + lane;
+    wide_regs_up<kWRegsSoftmax>();
+    const int h = (warp - 4) >> 2;
+    const int qd = warp & 3, r = qd * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
-    int rounds = 0;  // of swap
-    auto swap = [&](float v, float& other) -> bool {
-      if (rounds > 0 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.x_empty[qd], (rounds - 1) & 1))) return false;
-      sm.xch[half][r] = v;
-      tc::mbar_arrive(&sm.x_full[qd]);
-      if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.x_full[qd], rounds & 1))) return false;
-      other = sm.xch[half ^ 1][r];
-      tc::mbar_arrive(&sm.x_empty[qd]);
-      ++rounds;
-      return true;
-    };
+    const uint32_t s = tS + h * 128 + lane_off, o = tO + h * 128 + lane_off;
     int meetings = 0;
-    auto meet = [&]() -> bool {  // bounded, unlike a hardware barrier
-      tc::mbar_arrive(&sm.all);
-      return __all_sync(0xffffffffu, tc::mbar_wait(&sm.all, meetings++ & 1));
+    auto meet = [&]() -> bool {  // of the half's threads; bounded, unlike a hardware barrier
+      tc::mbar_arrive(&sm.all[h]);
+      return __all_sync(0xffffffffu, tc::mbar_wait(&sm.all[h], meetings++ & 1));
     };
     bool ok = true;
-    int it = 0, seg = 0;
-    const int tr = r / a.G;  // the row's token of the unit
-    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
+    int it = 0, mine = 0;  // tiles of the CTA, and of them this half's
+    const int tr = h * half_tok + r / a.G;  // the row's token of the unit
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      const int pos = u.pos0 + tr, pos_last = u.pos0 + u.ntok - 1;
-      const uint32_t o = tO + (seg & 1) * 128;
+      if (h == 1 && u.ntok <= half_tok) {  // no second half
+        it += j1 - j0;
+        continue;
+      }
+      const int pos = u.pos0 + tr, pos_first = u.pos0 + h * half_tok, pos_last = u.pos0 + u.ntok - 1;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
       float m_used = -INFINITY, l = 0.f;
-      // this half's page of tile j: (factor of the logits or -1 where it is not there, log2 of V's)
-      auto page_params = [&](int j) -> float2 {
-        const int lp = u.page0 + 2 * j + half;
-        if (lp >= u.npages) return make_float2(-1.f, 0.f);
+      // page `lp` of the sequence: (factor of the logits or -1 where it is not there, log2 of V's);
+      // of a bf16 cache the raw table entry, looked at a tile later when it has arrived
+      auto page_params = [&](int lp) -> float2 {
+        if (lp >= u.npages) return make_float2(EXP ? -1.f : __int_as_float(-1), 0.f);
         if (EXP) return params[(size_t)(u.slot_page + lp) * a.Hkv + u.g];
-        const int phys = bt[lp];
-        return make_float2(phys >= 0 && phys < a.num_pages ? 1.f : -1.f, 0.f);
+        return make_float2(__int_as_float(bt[lp]), 0.f);
       };
-      float2 pp = page_params(j0);
-      for (int j = j0; j < j1; ++j, ++it) {
-        const int sb = it & 1;
-        const float2 par = pp;
-        if (j + 1 < j1) pp = page_params(j + 1);
-        if (!__all_sync(0xffffffffu, !stopped(sm) && tc::mbar_wait(&sm.s_full[sb], (it >> 1) & 1))) { ok = false; break; }
+      float2 n0 = page_params(u.page0 + 2 * j0), n1 = page_params(u.page0 + 2 * j0 + 1);
+      for (int j = j0; j < j1; ++j, ++it, ++mine) {
+        float2 par[2] = {n0, n1};
+        if (!EXP)
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int phys = __float_as_int(par[q].x);
+            par[q].x = phys >= 0 && phys < a.num_pages ? 1.f : -1.f;
+          }
+        if (j + 1 < j1) n0 = page_params(u.page0 + 2 * j + 2), n1 = page_params(u.page0 + 2 * j + 3);
+        if (!__all_sync(0xffffffffu, !stopped(sm) && tc::mbar_wait(&sm.s_full[h], mine & 1))) { ok = false; break; }
         tc::tc_fence_after();
-        float x[64];
+        float x[128];
         {
-          uint32_t raw[2][32];
+          uint32_t raw[4][32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) tc::tmem_ld32_async(tS + lane_off + sb * 128 + half * 64 + c * 32, raw[c]);
-          tc::tmem_wait_ld(raw[1]);
-          tc::tmem_regs_ready(raw[0]);
+          for (int c = 0; c < 4; ++c) tc::tmem_ld32_async(s + c * 32, raw[c]);
+          tc::tmem_wait_ld(raw[3]);
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int c = 0; c < 3; ++c) tc::tmem_regs_ready(raw[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e) x[c * 32 + e] = __uint_as_float(raw[c][e]);
         }
-        const int kb = (u.page0 + 2 * j + half) * kPage;  // this half's first key
-        if (par.x < 0.f) {
-#pragma unroll
-          for (int e = 0; e < 64; ++e) x[e] = -INFINITY;
-        } else if (kb + 63 > u.pos0 || (a.w > 0 && kb <= pos_last - a.w)) {
+        const int kb = (u.page0 + 2 * j) * kPage;  // the tile's first key
+        if (kb + 127 > pos_first || (a.w > 0 && kb <= pos_last - a.w) || par[0].x < 0.f || par[1].x < 0.f) {
           const int hi = pos - kb, lo = a.w > 0 ? hi - a.w : -1;
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e > hi || e <= lo) x[e] = -INFINITY;
+          for (int e = 0; e < 128; ++e)
+            if (e > hi || e <= lo || par[e >> 6].x < 0.f) x[e] = -INFINITY;
         }
-        const float c = par.x * a.scale_log2;
-        float mt = fmaxf(x[0], x[1]);
+        // a page that is not there has no weights: any positive factor will do
+        const float c0 = fabsf(par[0].x) * a.scale_log2, c1 = fabsf(par[1].x) * a.scale_log2;
+        float t[4];
 #pragma unroll
-        for (int e = 2; e < 64; e += 2) mt = max3(mt, x[e], x[e + 1]);
-        mt *= fabsf(c);
-        float mo;
-        if (!swap(mt, mo)) { ok = false; break; }
-        const float m_new = max3(m_used, mt, mo);
+        for (int q = 0; q < 4; ++q) {
+          t[q] = fmaxf(x[32 * q], x[32 * q + 1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 2) t[q] = max3(t[q], x[32 * q + e], x[32 * q + e + 1]);
+        }
+        const float m_new = max3(m_used, fmaxf(t[0], t[1]) * c0, fmaxf(t[2], t[3]) * c1);
         const bool need = m_new > m_used + kWRescale || (m_used == -INFINITY && m_new > -INFINITY);
         const float alpha = (need && m_used > -INFINITY) ? tc::ex2(m_used - m_new) : 1.f;
         if (need) m_used = m_new;
         l *= alpha;
         if (j > j0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1))) { ok = false; break; }
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[h], (mine - 1) & 1))) { ok = false; break; }
           tc::tc_fence_after();
 #pragma unroll 1
-          for (int k = 0; k < D / 64; ++k) {  // this half's share of the D columns
+          for (int k = 0; k < D / 32; ++k) {
             float ov[32];
-            const uint32_t col = half * (D / 2) + k * 32;
-            tc::tmem_ld32(o + lane_off + col, ov);
+            tc::tmem_ld32(o + k * 32, ov);
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] *= alpha;
-            tc::tmem_st32(o + lane_off + col, ov);
+            tc::tmem_st32(o + k * 32, ov);
           }
         }
         // p = 2^(x c - m) (a row with nothing visible yet: all zero), times the page's V factor
-        const float shift = m_used == -INFINITY ? 0.f : par.y - m_used;
-        float sum0 = 0.f, sum1 = 0.f;
-        uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const float p0 = tc::ex2(fmaf(x[e], c, shift)), p1 = tc::ex2(fmaf(x[e + 1], c, shift));
-          sum0 += p0;
-          sum1 += p1;
-          w[e >> 1] = pack_bf16(p0, p1);
-        }
-        if (par.x < 0.f) {  // no page: c is negative and -inf * c is not a weight
+        for (int q = 0; q < 2; ++q) {
+          const float c = q ? c1 : c0;
+          const float shift = m_used == -INFINITY ? 0.f : par[q].y - m_used;
+          F2 sum{0.f, 0.f};
+          uint32_t w[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) w[e] = 0u;
-          sum0 = sum1 = 0.f;
+          for (int e = 0; e < 64; e += 2) {
+            F2 y = fma2({x[64 * q + e], x[64 * q + e + 1]}, {c, c}, {shift, shift});
+            y.x = tc::ex2(y.x), y.y = tc::ex2(y.y);
+            sum = add2(sum, y);
+            w[e >> 1] = pack_bf16(y.x, y.y);
+          }
+          l += EXP ? (sum.x + sum.y) * tc::ex2(-par[q].y) : sum.x + sum.y;
+          tc::tmem_st32u(s + q * 32, w);
         }
-        l += EXP ? (sum0 + sum1) * tc::ex2(-par.y) : sum0 + sum1;
-        tc::tmem_st32u(tS + lane_off + sb * 128 + half * 32, w);
-        if (!EXP && kb < u.t && kb + kPage > u.t) {
-          // the sequence ends inside this page: what lies behind it in the pool may be anything,
-          // and 0 times a NaN is a NaN
+        if (!EXP && kb < u.t && kb + 128 > u.t) {
+          // the sequence ends inside this tile: what lies behind it in the pool may be anything,
+          // and 0 times a NaN is a NaN. Either half clears it before its own P.V
           if (!__all_sync(0xffffffffu, tc::mbar_wait(&sm.v_full[it % kWStages], (it / kWStages) & 1))) { ok = false; break; }
-          uint8_t* v = sm.v[it % kWStages] + half * 8192;
-          const int dead = kb + kPage - u.t;
-          for (int e = qd * 32 + lane; e < dead * 8 * NB; e += 128) {
+          const int from = u.t - kb, dead = 128 - from;
+          for (int e = r; e < dead * 8 * NB; e += 128) {
             const int blk = e / (dead * 8), z = e % (dead * 8);
-            *reinterpret_cast<uint4*>(v + blk * 16384 + (u.t - kb) * 128 + 16 * z) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(sm.v[it % kWStages] + blk * 16384 + from * 128 + 16 * z) = make_uint4(0, 0, 0, 0);
           }
           tc::fence_async_smem();
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(&sm.p_full[sb]);
+        tc::mbar_arrive(&sm.p_full[h]);
       }
       if (!ok) break;
       // ---- the unit's (or this part's) output
-      if (!__all_sync(0xffffffffu, !stopped(sm) && tc::mbar_wait(&sm.p_empty[(it - 1) & 1], ((it - 1) >> 1) & 1))) { ok = false; break; }
-      float lo;
-      if (!swap(l, lo)) { ok = false; break; }
+      if (!__all_sync(0xffffffffu, !stopped(sm) && tc::mbar_wait(&sm.pv_done[h], (mine - 1) & 1))) { ok = false; break; }
       tc::tc_fence_after();
       const bool whole = j0 == 0 && j1 == u.ntiles;
       const bool live = tr < u.ntok;
       const int head = u.g * a.G + r % a.G;
       const size_t row = (size_t)(u.row + tr) * a.Hq + head;
-      const float lsum = half ? lo + l : l + lo;
       // normalised values of 32 columns to o
       auto store = [&](const float (&ov)[32], float f, int col) {
         if (a.o_bf16) {
@@ -378,67 +373,63 @@ __global__ void __launch_bounds__(kWThreads, 1)
         const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
         const float den = L * sc + exp2_rel(b2, M2);
         f = den > 0.f ? sc / den : 0.f;
-        if (a.lse && half == 0 && live) a.lse[row] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+        if (a.lse && live) a.lse[row] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
       };
       if (whole) {
         float f;
-        finish(m_used, lsum, f);
+        finish(m_used, l, f);
 #pragma unroll 1
-        for (int k = 0; k < D / 64; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
           float ov[32];
-          tc::tmem_ld32(o + lane_off + half * (D / 2) + k * 32, ov);
-          if (live) store(ov, f, half * (D / 2) + k * 32);
+          tc::tmem_ld32(o + k * 32, ov);
+          if (live) store(ov, f, k * 32);
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(&sm.o_empty[seg & 1]);
       } else {
-        const int slot = part_slot(u, per, blockIdx.x);
-        float4* po = reinterpret_cast<float4*>(p.part_o) + (size_t)slot * (D / 4) * kWRows;
-        if (half == 0) reinterpret_cast<float2*>(p.part_ml)[(size_t)slot * kWRows + r] = make_float2(m_used, lsum);
+        // parts are kept by slot and half: [slot][half][D / 4][128 rows] float4
+        auto ml_of = [&](int c) { return reinterpret_cast<float2*>(p.part_ml) + ((size_t)part_slot(u, per, c) * 2 + h) * kWRows + r; };
+        auto o_of = [&](int c) { return reinterpret_cast<float4*>(p.part_o) + ((size_t)part_slot(u, per, c) * 2 + h) * (D / 4) * kWRows + r; };
+        *ml_of(blockIdx.x) = make_float2(m_used, l);
+        float4* po = o_of(blockIdx.x);
 #pragma unroll 1
-        for (int k = 0; k < D / 64; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
           float ov[32];
-          tc::tmem_ld32(o + lane_off + half * (D / 2) + k * 32, ov);
+          tc::tmem_ld32(o + k * 32, ov);
 #pragma unroll
-          for (int e = 0; e < 32; e += 4)
-            po[(half * (D / 8) + k * 8 + e / 4) * kWRows + r] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+          for (int e = 0; e < 32; e += 4) po[(k * 8 + e / 4) * kWRows] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
         }
         tc::tc_fence_before();
-        tc::mbar_arrive(&sm.o_empty[seg & 1]);
         // the last CTA to leave its part merges them all, in CTA order
-        const int c0 = u.prefix / per, c1 = (u.prefix + u.ntiles - 1) / per;
+        const int cf = u.prefix / per, cl = (u.prefix + u.ntiles - 1) / per;
         __threadfence();
         if (!meet()) { ok = false; break; }
-        if (threadIdx.x == 64) sm.last = atomicAdd(&p.arrive[un], 1) == c1 - c0;
+        if (r == 0) sm.last[h] = atomicAdd(&p.arrive[2 * un + h], 1) == cl - cf;
         if (!meet()) { ok = false; break; }
-        if (*(volatile int*)&sm.last) {
+        if (*(volatile int*)&sm.last[h]) {
           __threadfence();
-          auto slot_of = [&](int c) { return part_slot(u, per, c); };
           float M = -INFINITY, L = 0.f;
-          for (int c = c0; c <= c1; ++c)
-            M = fmaxf(M, __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_of(c) * kWRows + r).x);
-          for (int c = c0; c <= c1; ++c) {
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot_of(c) * kWRows + r);
+          for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(ml_of(c)).x);
+          for (int c = cf; c <= cl; ++c) {
+            const float2 ml = __ldcg(ml_of(c));
             L += exp2_rel(ml.x, M) * ml.y;
           }
           float f;
           finish(M, L, f);
 #pragma unroll 1
-          for (int k = 0; k < D / 64; ++k) {
+          for (int k = 0; k < D / 32; ++k) {
             float ov[32];
 #pragma unroll
             for (int e = 0; e < 32; ++e) ov[e] = 0.f;
-            for (int c = c0; c <= c1; ++c) {
-              const size_t sl = slot_of(c);
-              const float g = exp2_rel(__ldcg(reinterpret_cast<const float2*>(p.part_ml) + sl * kWRows + r).x, M);
-              const float4* src = reinterpret_cast<const float4*>(p.part_o) + sl * (D / 4) * kWRows;
+            for (int c = cf; c <= cl; ++c) {
+              const float g = exp2_rel(__ldcg(ml_of(c)).x, M);
+              const float4* src = o_of(c);
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const float4 v = __ldcg(src + (half * (D / 8) + k * 8 + e / 4) * kWRows + r);
+                const float4 v = __ldcg(src + (k * 8 + e / 4) * kWRows);
                 ov[e] += g * v.x, ov[e + 1] += g * v.y, ov[e + 2] += g * v.z, ov[e + 3] += g * v.w;
               }
             }
-            if (live) store(ov, f, half * (D / 2) + k * 32);
+            if (live) store(ov, f, k * 32);
           }
         }
         if (!meet()) { ok = false; break; }  // sm.last is rewritten by the next part

@@ -132,14 +132,15 @@ struct ChunkArgs {
 struct ChunkPlan {
   int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] units
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
-  int32_t* arrive;     // [max_units] CTAs that have left their part of a unit
+  int32_t* arrive;     // [max_units][halves] CTAs that have left their part of a unit
   int32_t* units;      // [max_units] ChunkUnit
   int max_units, ctas;
-  int tile_rows;            // rows of a unit: 128 or the narrow kernel's width
+  int tile_rows;            // rows of a unit: 256 or the narrow kernel's width
+  int halves;               // a unit's independent outputs: 2 (wide) or 1
   int min_rows, max_rows;   // of a sequence, times G
   int min_tiles;            // the shortest range worth a CTA
   float* part_ml;           // [2 ctas][tile_rows][2] m and l (base 2) of the parts
-  float* part_o;            // [2 ctas][D][tile_rows] unnormalised outputs
+  float* part_o;            // [2 ctas][tile_rows x D] unnormalised outputs, in the kernel's order
   // sequences whose pages are expanded to bf16 first (wide kernel on FP8 / FP4), by ordinal
   int32_t* exp_seq;   // [batch] sequence; exp_head[0]: how many
   int32_t* exp_base;  // [batch] its first expanded page
