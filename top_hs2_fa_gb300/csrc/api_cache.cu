@@ -54,7 +54,7 @@ int sm_count() {
     (void)cudaGetLastError();
     return 152;
   }
-  return n;
+  return std::min(n, 256);  // the merge holds a unit's parts, one per CTA, in shared memory
 }
 
 // Which kernel takes a sequence, by the rows (tokens times G) that share its KV heads' keys. The
@@ -90,7 +90,6 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       L.narrow[L.n_plans] = narrow;
       p.ctas = sm_count();
       p.tile_rows = tile_rows;
-      p.halves = narrow ? 1 : 2;
       p.min_rows = lo;
       p.max_rows = hi;
       p.min_tiles = min_tiles;
@@ -100,7 +99,6 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       size_t* o = L.off[L.n_plans++];
       o[0] = take(16);
       o[1] = take(4 * (size_t)p.ctas);
-      o[2] = take(4 * (size_t)p.max_units * p.halves);
       o[3] = take(48 * (size_t)p.max_units);
       o[4] = take(2 * (size_t)p.ctas * tile_rows * 8);
       o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
@@ -136,7 +134,6 @@ void bind(ChunkLayout& L, char* ws) {
     hs2::ChunkPlan& p = L.plan[i];
     p.head = (int32_t*)(ws + L.off[i][0]);
     p.cta_first = (int32_t*)(ws + L.off[i][1]);
-    p.arrive = (int32_t*)(ws + L.off[i][2]);
     p.units = (int32_t*)(ws + L.off[i][3]);
     p.part_ml = (float*)(ws + L.off[i][4]);
     p.part_o = (float*)(ws + L.off[i][5]);
@@ -244,6 +241,7 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
   a.Hq = Hq;
   a.Hkv = kv->Hkv;
   a.G = Hq / kv->Hkv;
+  while ((1 << a.log2G) < a.G) ++a.log2G;
   a.k = kv->k;
   a.v = kv->v;
   a.k_scale = kv->k_scale;
@@ -282,14 +280,15 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
       ok = encode_2d_bf16(&map[i][1], p.expand ? ws + L.off_ek : kv->k, kv->d, rows, 64) &&
            encode_2d_bf16(&map[i][2], p.expand ? ws + L.off_ev : kv->v, kv->d, rows, 64);
     }
-    if (!L.narrow[i]) ok = ok && encode_3d_bf16(&map[i][0], q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, a.G, 128 / a.G);
+    ok = ok && encode_3d_bf16(&map[i][0], q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, a.G,
+                              (L.narrow[i] ? p.tile_rows : 128) / a.G);
     if (!ok) return HS2_ERR_ARG;
   }
   cudaError_t e = hs2::launch_chunk_plan(a, L.plan, L.n_plans, s);
   for (int i = 0; i < L.n_plans && e == cudaSuccess; ++i) {
     const hs2::ChunkPlan& p = L.plan[i];
     if (L.narrow[i]) {
-      e = hs2::launch_chunk_narrow(map[i][1], map[i][2], a, p, kv->d, kv->dtype, s);
+      e = hs2::launch_chunk_narrow(map[i][0], map[i][1], map[i][2], a, p, kv->d, kv->dtype, s);
       continue;
     }
     float2* params = p.expand ? (float2*)(ws + L.off_params) : nullptr;
@@ -298,6 +297,7 @@ hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int
                                    L.exp_pages_seq, s);
     if (e == cudaSuccess) e = hs2::launch_chunk_wide(map[i][0], map[i][1], map[i][2], a, p, params, kv->d, s);
   }
+  if (e == cudaSuccess) e = hs2::launch_chunk_merge(a, L.plan, L.n_plans, kv->d, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 

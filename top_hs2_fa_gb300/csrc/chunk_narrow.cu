@@ -16,7 +16,8 @@
 //                row with the reference m moving only when a weight would exceed 2^14 (f16 P
 //                keeps weights down to 2^-30 of the largest); the normaliser is summed in fp32
 //                from unrounded weights, per thread
-//   warp 2       Q of the next unit: f16 after an exact power of two that fits its range
+//   warp 2       Q of the next unit by TMA, then to f16 in place, with an exact power of two
+//                where its values would leave f16's range
 // A bf16 cache skips the conversions: its TMA tiles are the operands (bf16 Q, P).
 // The page's K scale multiplies the logits; V's enters the weights relative to a unit that O is
 // kept in. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four
@@ -62,14 +63,13 @@ struct NarrowSmem {
   alignas(16) float nm[2][N], alpha[2][N], warp_m[2][4][N];
   // per unit, by its parity: each group's maxima, the sums of its four warps, its V unit (0 tiles: -1)
   alignas(16) float out_m[2][2][N], out_l[2][2][4][N], out_unit[2][2];
-  alignas(16) float fin[N];
   TileInfo info[kInfo];
   float qmul[2];
   uint64_t info_full[kInfo];
   uint64_t ring_full[STAGES], ring_empty[STAGES];
-  uint64_t k_full[2], s_full[2], s_empty[2], pv_ready[2], pv_done[2], q_full[2], q_empty[2], o_empty[2], out_ready[2], all;
+  uint64_t k_full[2], s_full[2], s_empty[2], pv_ready[2], pv_done[2], q_full[2], q_empty[2], o_empty[2], out_ready[2], q_raw[2];
   uint32_t tmem_base;
-  int abort, last;
+  int abort;
 };
 
 template <typename S>
@@ -197,8 +197,8 @@ constexpr uint32_t narrow_idesc(bool bf16, int N, bool a_mn, bool b_mn) {
 
 template <int D, int FMT, int N>
 __global__ void __launch_bounds__(kNThreads, 1)
-    chunk_narrow_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const ChunkArgs a, const ChunkPlan p) {
+    chunk_narrow_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, 
+                        const __grid_constant__ CUtensorMap tm_v, const ChunkArgs a, const ChunkPlan p) {
   using Sm = NarrowSmem<D, FMT, N>;
   constexpr bool QUANT = Sm::QUANT, BF = !QUANT;
   constexpr int ST = Sm::STAGES, NB = Sm::NB, CODES = Sm::CODES, SF = Sm::SF, RB = Sm::RB;
@@ -217,13 +217,14 @@ __global__ void __launch_bounds__(kNThreads, 1)
       tc::mbar_init(&sm.s_empty[s], 128);
       tc::mbar_init(&sm.pv_ready[s], 256);  // V's and P's threads
       tc::mbar_init(&sm.pv_done[s], 1);
-      tc::mbar_init(&sm.q_full[s], 32);
+      tc::mbar_init(&sm.q_full[s], QUANT ? 32 : 1);
       tc::mbar_init(&sm.q_empty[s], 3);  // the last S of the unit, and the two groups' reads of qmul
       tc::mbar_init(&sm.o_empty[s], 256);
       tc::mbar_init(&sm.out_ready[s], 256);
     }
     for (int s = 0; s < kInfo; ++s) tc::mbar_init(&sm.info_full[s], 1);
-    tc::mbar_init(&sm.all, 256);
+    tc::mbar_init(&sm.q_raw[0], 1);
+    tc::mbar_init(&sm.q_raw[1], 1);
     sm.abort = 0;
     tc::fence_mbar_init();
   }
@@ -232,9 +233,9 @@ __global__ void __launch_bounds__(kNThreads, 1)
   __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
-  const uint32_t tK = sm.tmem_base, tS = tK + 128, tO = tK + 256;  // two buffers; O: two groups by two units
   const ChunkRange rg = chunk_range(p, blockIdx.x);
   const int per = p.head[1];
+  const uint32_t tK = sm.tmem_base, tS = tK + 128, tO = tK + 256;  // two buffers; O: two groups by two units
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
     regs_down<kRegsMisc>();
@@ -272,12 +273,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
             ok = false;
             break;
           }
-          if ((lane >> 1) == j - c0) {
-            TileInfo& f = sm.info[issued % kInfo];
-            f.k[lane & 1] = ks, f.v[lane & 1] = vs, f.there[lane & 1] = mine >= 0;
-          }
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.info_full[issued % kInfo]);
           if (lane == 0) {
             uint8_t* s = sm.ring[st];
             uint64_t* bar = &sm.ring_full[st];
@@ -309,6 +304,13 @@ __global__ void __launch_bounds__(kNThreads, 1)
               }
             }
           }
+          // (the scales have arrived meanwhile)
+          if ((lane >> 1) == j - c0) {
+            TileInfo& f = sm.info[issued % kInfo];
+            f.k[lane & 1] = ks, f.v[lane & 1] = vs, f.there[lane & 1] = mine >= 0;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&sm.info_full[issued % kInfo]);
           ++issued;
         }
         raw = raw_next, ks = ks_next, vs = vs_next;
@@ -359,7 +361,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
     int it = 0, seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
-      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);
+      const int2 pt = *reinterpret_cast<const int2*>(p.units + 12 * (size_t)un + 6);  // ntiles, prefix
       const int end = min(rg.end, pt.y + pt.x);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg & 1], ((seg >> 1) & 1) ^ 1));
       for (int j = 0; ok && at < end; ++at, ++it, ++j) {
@@ -383,57 +385,55 @@ __global__ void __launch_bounds__(kNThreads, 1)
     // ------------------------------------------------------------------ Q
     regs_down<kRegsMisc>();
     int seg = 0;
-    for (int at = rg.begin, un = rg.first_unit; at < rg.end; ++un, ++seg) {
+    bool ok = true;
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un, ++seg) {
       const ChunkUnit u = load_unit(p, un);
       at = min(rg.end, u.prefix + u.ntiles);
       const int qb = seg & 1;
-      const int rows = u.ntok * a.G;
-      const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(a.q) + ((size_t)u.row * a.Hq + (size_t)u.g * a.G) * D;
-      // 16-byte unit i: row i / (D / 8) (token-major, then head), channels 8 (i % (D / 8))
-      auto fetch = [&](int i) -> uint4 {
-        const int r = i / (D / 8), k = i % (D / 8);
-        if (r >= rows) return make_uint4(0, 0, 0, 0);
-        return __ldg(reinterpret_cast<const uint4*>(q + ((size_t)(r / a.G) * a.Hq + r % a.G) * D) + k);
-      };
-      constexpr int UNITS = N * D / 8;
-      float mul = 1.f;
-      if (QUANT) {
-        // the largest finite exponent among the unit's queries moves to 14
-        uint32_t top = 0;
-#pragma unroll 8
-        for (int i = lane; i < UNITS; i += 32) {
-          const uint4 w = fetch(i);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+      ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty[qb], ((seg >> 1) & 1) ^ 1));
+      if (!ok) break;
+      uint64_t* landed = QUANT ? &sm.q_raw[qb] : &sm.q_full[qb];
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(landed, NB * N * 128);
+        for (int c = 0; c < NB; ++c) tc::tma_load_3d(sm.q[qb] + c * N * 128, &tm_q, 64 * c, u.g * a.G, u.row, landed);
+      }
+      ok = __all_sync(0xffffffffu, tc::mbar_wait(landed, (seg >> 1) & 1));
+      if (!QUANT || !ok) continue;
+      // In place: 16-byte unit i of the tile, whatever its place in a row, is row (i / 8) % N. The
+      // largest exponent among the unit's own rows decides whether the values fit as they are.
+      constexpr int UNITS = NB * N * 8;
+      const int rows = u.ntok << a.log2G;
+      uint4* q = reinterpret_cast<uint4*>(sm.q[qb]);
+      uint32_t top = 0;
+#pragma unroll 4
+      for (int i = lane; i < UNITS; i += 32) {
+        const uint4 w = q[i];
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+        if ((i >> 3) % N < rows)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t lo = (x[j] >> 7) & 0xFFu, hi = (x[j] >> 23) & 0xFFu;
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t lo = (x[k] >> 7) & 0xFFu, hi = (x[k] >> 23) & 0xFFu;
             if (lo != 255u) top = max(top, lo);
             if (hi != 255u) top = max(top, hi);
           }
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        const int ex = max((int)top - 127, -100);
-        mul = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);  // 2^(14 - ex)
       }
-      if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty[qb], ((seg >> 1) & 1) ^ 1))) {
-        if (lane == 0) halt(sm, a.dev_err);
-        break;
-      }
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int ex = max((int)top - 127, -100);
+      // 1 for ordinary queries; else the largest exponent goes to 14
+      const float mul = ex >= -2 && ex <= 14 ? 1.f : __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll 4
       for (int i = lane; i < UNITS; i += 32) {
-        const int r = i / (D / 8), k = i % (D / 8);
-        uint4 w = fetch(i);
-        if (QUANT) {
-          uint32_t* x = reinterpret_cast<uint32_t*>(&w);
+        uint4 w = q[i];
+        uint32_t* x = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = pack_f16(bf16_lo(x[j]) * mul, bf16_hi(x[j]) * mul);
-        }
-        *reinterpret_cast<uint4*>(sm.q[qb] + (k >> 3) * (N * 128) + r * 128 + (((k & 7) ^ (r & 7)) << 4)) = w;
+        for (int k = 0; k < 4; ++k) x[k] = pack_f16(bf16_lo(x[k]) * mul, bf16_hi(x[k]) * mul);
+        q[i] = w;
       }
       if (lane == 0) sm.qmul[qb] = 1.f / mul;
       tc::fence_async_smem();
       tc::mbar_arrive(&sm.q_full[qb]);
     }
+    if (!ok && lane == 0) halt(sm, a.dev_err);
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ K and V operands
     regs_down<kRegsCodes>();
@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
           const int st = it % ST, b = it & 1;
           if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1))) { ok = false; break; }
           const int pos = (u.page0 + 2 * j) * kPage + key;
+          if (is_v && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.info_full[it % kInfo], (it / kInfo) & 1))) { ok = false; break; }
           const bool there = is_v && sm.info[it % kInfo].there[qd >> 1] != 0;
           if constexpr (QUANT) {
             const uint8_t* codes = sm.ring[st] + (is_v ? CODES : 0) + (qd >> 1) * (CODES / 2);
@@ -539,11 +540,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     float* const nm = sm.nm[grp];
     float* const alpha = sm.alpha[grp];
-    int meetings = 0;
-    auto meet = [&]() -> bool {  // both groups; bounded
-      tc::mbar_arrive(&sm.all);
-      return __all_sync(0xffffffffu, tc::mbar_wait(&sm.all, meetings++ & 1));
-    };
     int it0 = 0, seg = 0;  // tiles of the units before
     bool run = true;
     for (int at = rg.begin, un = rg.first_unit; run && at < rg.end; ++un, ++seg) {
@@ -559,7 +555,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
       float unit = BF ? 1.f : 0.f;
       if (tid < N) nm[tid] = kUnset;
       bool good = tc::mbar_wait(&sm.q_full[sp], (seg >> 1) & 1);
-      const float cq = a.scale_log2 * (good ? *(volatile float*)&sm.qmul[sp] : 1.f);
+      const float cq = a.scale_log2 * (QUANT && good ? *(volatile float*)&sm.qmul[sp] : 1.f);
       (void)any_of_128(bar, false);  // nm is set, qmul has been read
       if (tid == 0) tc::mbar_arrive(&sm.q_empty[sp]);
       for (int j = jf; j < j1; j += 2) {
@@ -586,9 +582,9 @@ __global__ void __launch_bounds__(kNThreads, 1)
           if (edge || !there) {
             // columns (rows of the unit) that see this key: [lo, hi)
             const int ago = pos - u.pos0;  // tokens before this one do not
-            const int lo = ago <= 0 ? 0 : min(ago, 64) * a.G;
+            const int lo = ago <= 0 ? 0 : min(ago, 64) << a.log2G;
             int hi = N;
-            if (a.w > 0) hi = ago + a.w <= 0 ? 0 : min(ago + a.w, 64) * a.G;
+            if (a.w > 0) hi = ago + a.w <= 0 ? 0 : min(ago + a.w, 64) << a.log2G;
             if (!there) hi = 0;
 #pragma unroll
             for (int n = 0; n < C; ++n)
@@ -632,7 +628,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
             break;
           }
           // ---- some row's reference max, or V's unit, moves
-          maxima();
+          if (j > jf) maxima();  // at the group's first tile every row is unset
           float fall = 1.f;
           if (QUANT && vtop > 2.f * unit) {
             fall = unit / vtop;
@@ -640,7 +636,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
           }
           bool fresh = false;
           if (tid < N) {
-            const float t = top_of(tid);
+            const float t = j > jf ? top_of(tid) : kUnset;
             float al = 1.f;
             if (t > kTop) {  // t = x c + nm: the new nm is 6 - x c
               const float old = nm[tid];
@@ -735,13 +731,13 @@ __global__ void __launch_bounds__(kNThreads, 1)
       }
       tc::tc_fence_after();
       const bool whole = j0 == 0 && j1 == u.ntiles;
-      const int rows = u.ntok * a.G;
+      const int rows = u.ntok << a.log2G;
       constexpr int H = N / 2;  // rows of this group: [nb, nb + H)
       const int nb = grp * H;
-      auto out_row = [&](int n) -> size_t { return (size_t)(u.row + n / a.G) * a.Hq + (size_t)u.g * a.G + n % a.G; };
+      auto out_row = [&](int n) -> size_t { return (size_t)(u.row + (n >> a.log2G)) * a.Hq + (size_t)u.g * a.G + (n & (a.G - 1)); };
       // factor of row n's output, and its lse, from its max and sum
       auto finish = [&](int n, float M, float L) -> float {
-        const float b2 = sink_b2(a.sink, u.g * a.G + n % a.G);
+        const float b2 = sink_b2(a.sink, u.g * a.G + (n & (a.G - 1)));
         const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
         const float den = L * sc + exp2_rel(b2, M2);
         if (a.lse && n < rows) a.lse[out_row(n)] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
@@ -806,67 +802,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
             for (int n = 0; n < H; ++n) po[(size_t)n * D] = v[n];
         }
       }
-      if (!whole) {
-        // the last CTA to leave its part merges them all, in CTA order
-        const int c0 = u.prefix / per, c1 = (u.prefix + u.ntiles - 1) / per, parts = c1 - c0 + 1;
-        __threadfence();
-        if (!meet()) { run = false; break; }
-        if (grp == 0 && tid == 0) sm.last = atomicAdd(&p.arrive[un], 1) == c1 - c0;
-        if (!meet()) { run = false; break; }
-        if (*(volatile int*)&sm.last) {
-          __threadfence();
-          // a round of parts at a time: their maxima and sums by all threads, each row's new
-          // reference and the parts' factors by its thread, then the outputs
-          float2* const fac = reinterpret_cast<float2*>(sm.p[grp]);  // [part][H]: nobody writes or reads P now
-          constexpr int ROUND = 16384 / 8 / H;
-          const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + nb;
-          float Mx = -INFINITY, Lx = 0.f, acc[H];
-#pragma unroll
-          for (int n = 0; n < H; ++n) acc[n] = 0.f;
-          for (int k0 = 0; k0 < parts; k0 += ROUND) {
-            const int kn = min(ROUND, parts - k0);
-            (void)any_of_128(bar, false);
-            for (int x = tid; x < kn * H; x += 128)
-              fac[x] = __ldcg(ml + (size_t)part_slot(u, per, c0 + k0 + x / H) * N + x % H);
-            (void)any_of_128(bar, false);
-            if (tid < H) {
-              float top = Mx;
-              for (int k = 0; k < kn; ++k) top = fmaxf(top, fac[k * H + tid].x);
-              const float keep = exp2_rel(Mx, top);
-              Mx = top;
-              Lx *= keep;
-              for (int k = 0; k < kn; ++k) {
-                const float2 y = fac[k * H + tid];
-                const float e = exp2_rel(y.x, top);
-                Lx += e * y.y;
-                fac[k * H + tid].x = e;
-              }
-              sm.warp_m[grp][2][tid] = keep;
-            }
-            (void)any_of_128(bar, false);
-            if (k0 > 0)
-#pragma unroll
-              for (int n = 0; n < H; ++n) acc[n] *= sm.warp_m[grp][2][n];
-            if (tid < D) {
-              const float* src = p.part_o + (size_t)nb * D + tid;
-#pragma unroll 2
-              for (int k = 0; k < kn; ++k) {
-                const float* po = src + (size_t)part_slot(u, per, c0 + k0 + k) * N * D;
-                float t[H];
-#pragma unroll
-                for (int n = 0; n < H; ++n) t[n] = __ldcg(po + (size_t)n * D);
-#pragma unroll
-                for (int n = 0; n < H; ++n) acc[n] = fmaf(fac[k * H + n].x, t[n], acc[n]);
-              }
-            }
-          }
-          if (tid < H) sm.fin[nb + tid] = finish(nb + tid, Mx, Lx);
-          (void)any_of_128(bar, false);
-#pragma unroll
-          for (int n = 0; n < H; ++n) put(nb + n, acc[n] * sm.fin[nb + n]);
-        }
-        if (!meet()) { run = false; break; }  // sm.last is rewritten by the next part
-      }
       (void)any_of_128(bar, false);  // the group's arrays are rewritten by the next unit
     }
     if (!run && lane == 0) halt(sm, a.dev_err);
@@ -877,37 +812,37 @@ __global__ void __launch_bounds__(kNThreads, 1)
 }
 
 template <int D, int FMT, int N>
-static cudaError_t launch_n(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+static cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
                             cudaStream_t s) {
   const size_t sm = sizeof(NarrowSmem<D, FMT, N>) + 1024;
   static_assert(sizeof(NarrowSmem<D, FMT, N>) + 1024 <= 227 * 1024, "shared memory of a CTA");
   auto kern = chunk_narrow_kernel<D, FMT, N>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(p.ctas), dim3(kNThreads), sm, s, tk, tv, a, p);
+  return launch_pdl(kern, dim3(p.ctas), dim3(kNThreads), sm, s, tq, tk, tv, a, p);
 }
 
 template <int D, int FMT>
-static cudaError_t launch_fmt(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+static cudaError_t launch_fmt(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
                               cudaStream_t s) {
   switch (p.tile_rows) {
-    case 16: return launch_n<D, FMT, 16>(tk, tv, a, p, s);
-    case 32: return launch_n<D, FMT, 32>(tk, tv, a, p, s);
-    case 64: return launch_n<D, FMT, 64>(tk, tv, a, p, s);
+    case 16: return launch_n<D, FMT, 16>(tq, tk, tv, a, p, s);
+    case 32: return launch_n<D, FMT, 32>(tq, tk, tv, a, p, s);
+    case 64: return launch_n<D, FMT, 64>(tq, tk, tv, a, p, s);
   }
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_chunk_narrow(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+cudaError_t launch_chunk_narrow(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
                                 int d, int dtype, cudaStream_t s) {
   if (d == 128) {
-    return dtype == HS2_FP4_E2M1   ? launch_fmt<128, HS2_FP4_E2M1>(tk, tv, a, p, s)
-           : dtype == HS2_FP8_E4M3 ? launch_fmt<128, HS2_FP8_E4M3>(tk, tv, a, p, s)
-                                   : launch_fmt<128, HS2_BF16>(tk, tv, a, p, s);
+    return dtype == HS2_FP4_E2M1   ? launch_fmt<128, HS2_FP4_E2M1>(tq, tk, tv, a, p, s)
+           : dtype == HS2_FP8_E4M3 ? launch_fmt<128, HS2_FP8_E4M3>(tq, tk, tv, a, p, s)
+                                   : launch_fmt<128, HS2_BF16>(tq, tk, tv, a, p, s);
   }
-  return dtype == HS2_FP4_E2M1   ? launch_fmt<64, HS2_FP4_E2M1>(tk, tv, a, p, s)
-         : dtype == HS2_FP8_E4M3 ? launch_fmt<64, HS2_FP8_E4M3>(tk, tv, a, p, s)
-                                 : launch_fmt<64, HS2_BF16>(tk, tv, a, p, s);
+  return dtype == HS2_FP4_E2M1   ? launch_fmt<64, HS2_FP4_E2M1>(tq, tk, tv, a, p, s)
+         : dtype == HS2_FP8_E4M3 ? launch_fmt<64, HS2_FP8_E4M3>(tq, tk, tv, a, p, s)
+                                 : launch_fmt<64, HS2_BF16>(tq, tk, tv, a, p, s);
 }
 
 }  // namespace hs2

@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
       s_exp[kPlanThreads];
   const int tok = p.tile_rows / a.G;
   int total_tiles = 0, units = 0, exp_pages = 0, n_exp = 0;
+  int my_tiles = 0, my_prefix = 0;  // of the last unit this thread wrote
   // rows of two sequences at once would overrun what the host sized for n_rows rows
   bool descends = false;
   for (int b = threadIdx.x; b < a.batch; b += kPlanThreads) descends |= a.row_start[b + 1] < a.row_start[b];
@@ -106,12 +107,11 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
       int tiles;
       x.prefix = total_tiles + block_prefix(cost, sums, tiles);
       total_tiles += tiles;
+      my_tiles = cost, my_prefix = x.prefix;
       if (u < here) {  // within max_units: the valid sequences' rows are disjoint and within n_rows
         int4* d = reinterpret_cast<int4*>(p.units) + 3 * (size_t)(units + u);
         const int4* s = reinterpret_cast<const int4*>(&x);
         d[0] = s[0], d[1] = s[1], d[2] = s[2];
-        if (p.halves == 2) reinterpret_cast<int2*>(p.arrive)[units + u] = make_int2(0, 0);
-        else p.arrive[units + u] = 0;
       }
     }
     units += here;
@@ -124,11 +124,18 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     p.head[2] = units;
     if (p.expand) p.exp_head[0] = n_exp;
   }
+  // the unit at each CTA's range start
+  auto starts = [&](int u, int ntiles, int prefix) {
+    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
+  };
+  if (a.batch <= kPlanThreads && units <= kPlanThreads) {  // they are in registers
+    if ((int)threadIdx.x < units) starts(threadIdx.x, my_tiles, my_prefix);
+    return;
+  }
   __syncthreads();  // the records are visible to the block
   for (int u = threadIdx.x; u < units; u += kPlanThreads) {
     const int4 y = reinterpret_cast<const int4*>(p.units)[3 * (size_t)u + 1];
-    const int ntiles = y.z, prefix = y.w;
-    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
+    starts(u, y.z, y.w);
   }
 }
 

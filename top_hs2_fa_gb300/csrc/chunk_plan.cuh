@@ -5,7 +5,7 @@
 // the 128-key tiles (two pages) that its rows see. The tiles of all units, one after another,
 // are a line of `total` tiles that the CTAs of a persistent kernel share out in equal ranges,
 // so lengths and batch sizes do not matter to the balance; a unit cut by a range border leaves
-// partial results, which the CTA that finishes last of its CTAs merges in CTA order.
+// partial results, which a last kernel merges in CTA order (chunk_merge.cu).
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
@@ -25,10 +25,10 @@ struct ChunkRange {
 
 HS2_DEVI ChunkRange chunk_range(const ChunkPlan& p, int cta) {
   ChunkRange r;
-  const int total = p.head[0], per = p.head[1];
+  const int total = p.head[0], per = p.head[1], first = p.cta_first[cta];  // one round of loads
   r.begin = min(total, cta * per);
   r.end = min(total, r.begin + per);
-  r.first_unit = r.begin < r.end ? p.cta_first[cta] : 0;
+  r.first_unit = r.begin < r.end ? first : 0;
   return r;
 }
 

@@ -43,9 +43,9 @@ struct WideSmem {
   uint8_t v[kWStages][kTile];
   uint64_t q_full, q_empty, k_full[kWStages], k_empty[kWStages], v_full[kWStages], v_empty[kWStages];
   // by half
-  uint64_t s_full[2], p_full[2], pv_done[2], all[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];
   uint32_t tmem_base;
-  int abort, last[2];
+  int abort;
 };
 
 template <typename S>
@@ -92,20 +92,20 @@ __global__ void __launch_bounds__(kWThreads, 1)
       tc::mbar_init(&sm.s_full[h], 1);
       tc::mbar_init(&sm.p_full[h], 128);
       tc::mbar_init(&sm.pv_done[h], 1);
-      tc::mbar_init(&sm.all[h], 128);
     }
     sm.abort = 0;
     tc::fence_mbar_init();
   }
+  griddep_wait();
+  const ChunkRange rg = chunk_range(p, blockIdx.x);
+  if (rg.begin >= rg.end) return;  // nothing for this CTA (the whole block leaves)
   if (warp == 1) tc::tmem_alloc(&sm.tmem_base, kWTmem);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  griddep_wait();
   const uint32_t tS = sm.tmem_base, tO = tS + 256;
-  const ChunkRange rg = chunk_range(p, blockIdx.x);
   const int per = p.head[1];
-  const int half_tok = kWRows / a.G;  // tokens of a half
+  const int half_tok = kWRows >> a.log2G;  // tokens of a half
 
   if (warp < 2) {
     // ------------------------------------------------------------------ TMA producers
@@ -230,14 +230,9 @@ __global__ void __launch_bounds__(kWThreads, 1)
     const int qd = warp & 3, r = qd * 32 + lane;
     const uint32_t lane_off = (uint32_t)(qd * 32) << 16;
     const uint32_t s = tS + h * 128 + lane_off, o = tO + h * 128 + lane_off;
-    int meetings = 0;
-    auto meet = [&]() -> bool {  // of the half's threads; bounded, unlike a hardware barrier
-      tc::mbar_arrive(&sm.all[h]);
-      return __all_sync(0xffffffffu, tc::mbar_wait(&sm.all[h], meetings++ & 1));
-    };
     bool ok = true;
     int it = 0, mine = 0;  // tiles of the CTA, and of them this half's
-    const int tr = h * half_tok + r / a.G;  // the row's token of the unit
+    const int tr = h * half_tok + (r >> a.log2G);  // the row's token of the unit
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
@@ -351,7 +346,7 @@ __global__ void __launch_bounds__(kWThreads, 1)
       tc::tc_fence_after();
       const bool whole = j0 == 0 && j1 == u.ntiles;
       const bool live = tr < u.ntok;
-      const int head = u.g * a.G + r % a.G;
+      const int head = u.g * a.G + (r & (a.G - 1));
       const size_t row = (size_t)(u.row + tr) * a.Hq + head;
       // normalised values of 32 columns to o
       auto store = [&](const float (&ov)[32], float f, int col) {
@@ -386,53 +381,18 @@ __global__ void __launch_bounds__(kWThreads, 1)
         }
         tc::tc_fence_before();
       } else {
-        // parts are kept by slot and half: [slot][half][D / 4][128 rows] float4
-        auto ml_of = [&](int c) { return reinterpret_cast<float2*>(p.part_ml) + ((size_t)part_slot(u, per, c) * 2 + h) * kWRows + r; };
-        auto o_of = [&](int c) { return reinterpret_cast<float4*>(p.part_o) + ((size_t)part_slot(u, per, c) * 2 + h) * (D / 4) * kWRows + r; };
-        *ml_of(blockIdx.x) = make_float2(m_used, l);
-        float4* po = o_of(blockIdx.x);
+        const size_t at_p = (size_t)part_slot(u, per, blockIdx.x) * 2 * kWRows + h * kWRows + r;
+        reinterpret_cast<float2*>(p.part_ml)[at_p] = make_float2(m_used, l);
+        float4* po = reinterpret_cast<float4*>(p.part_o + at_p * D);
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           float ov[32];
           tc::tmem_ld32(o + k * 32, ov);
+          if (live)
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) po[(k * 8 + e / 4) * kWRows] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            for (int e = 0; e < 32; e += 4) po[k * 8 + e / 4] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
         }
         tc::tc_fence_before();
-        // the last CTA to leave its part merges them all, in CTA order
-        const int cf = u.prefix / per, cl = (u.prefix + u.ntiles - 1) / per;
-        __threadfence();
-        if (!meet()) { ok = false; break; }
-        if (r == 0) sm.last[h] = atomicAdd(&p.arrive[2 * un + h], 1) == cl - cf;
-        if (!meet()) { ok = false; break; }
-        if (*(volatile int*)&sm.last[h]) {
-          __threadfence();
-          float M = -INFINITY, L = 0.f;
-          for (int c = cf; c <= cl; ++c) M = fmaxf(M, __ldcg(ml_of(c)).x);
-          for (int c = cf; c <= cl; ++c) {
-            const float2 ml = __ldcg(ml_of(c));
-            L += exp2_rel(ml.x, M) * ml.y;
-          }
-          float f;
-          finish(M, L, f);
-#pragma unroll 1
-          for (int k = 0; k < D / 32; ++k) {
-            float ov[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) ov[e] = 0.f;
-            for (int c = cf; c <= cl; ++c) {
-              const float g = exp2_rel(__ldcg(ml_of(c)).x, M);
-              const float4* src = o_of(c);
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 v = __ldcg(src + (k * 8 + e / 4) * kWRows);
-                ov[e] += g * v.x, ov[e + 1] += g * v.y, ov[e + 2] += g * v.z, ov[e + 3] += g * v.w;
-              }
-            }
-            if (live) store(ov, f, k * 32);
-          }
-        }
-        if (!meet()) { ok = false; break; }  // sm.last is rewritten by the next part
       }
     }
     if (!ok && !stopped(sm)) stop(sm, a.dev_err);

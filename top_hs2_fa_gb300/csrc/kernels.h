@@ -107,7 +107,7 @@ struct ChunkArgs {
   const void* q;  // [n_rows][Hq][D]
   const int32_t* row_start;  // [batch + 1]
   int n_rows, max_n, max_t, batch;
-  int Hq, Hkv, G;
+  int Hq, Hkv, G, log2G;
   const void* k;
   const void* v;
   const float* k_scale;
@@ -132,15 +132,13 @@ struct ChunkArgs {
 struct ChunkPlan {
   int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] units
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
-  int32_t* arrive;     // [max_units][halves] CTAs that have left their part of a unit
   int32_t* units;      // [max_units] ChunkUnit
   int max_units, ctas;
   int tile_rows;            // rows of a unit: 256 or the narrow kernel's width
-  int halves;               // a unit's independent outputs: 2 (wide) or 1
   int min_rows, max_rows;   // of a sequence, times G
   int min_tiles;            // the shortest range worth a CTA
-  float* part_ml;           // [2 ctas][tile_rows][2] m and l (base 2) of the parts
-  float* part_o;            // [2 ctas][tile_rows x D] unnormalised outputs, in the kernel's order
+  float* part_ml;           // [2 ctas][tile_rows][2] m (base 2) and l of the parts
+  float* part_o;            // [2 ctas][tile_rows][D] their unnormalised outputs
   // sequences whose pages are expanded to bf16 first (wide kernel on FP8 / FP4), by ordinal
   int32_t* exp_seq;   // [batch] sequence; exp_head[0]: how many
   int32_t* exp_base;  // [batch] its first expanded page
@@ -305,7 +303,8 @@ cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s);
 cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s);
 cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, int dtype, void* ek, void* ev,
                                 float2* params, int max_seqs, int max_pages_seq, cudaStream_t s);
-cudaError_t launch_chunk_narrow(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
+cudaError_t launch_chunk_merge(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, int d, cudaStream_t s);
+cudaError_t launch_chunk_narrow(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a, const ChunkPlan& p,
                                 int d, int dtype, cudaStream_t s);
 cudaError_t launch_chunk_wide(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const ChunkArgs& a,
                               const ChunkPlan& p, const float2* params, int d, cudaStream_t s);

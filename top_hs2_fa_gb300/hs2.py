@@ -150,7 +150,7 @@ class _Handle:
     """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
     and a tensor whose storage has moved makes a new one."""
 
-    _c = None  # (struct, pointers of the tensors it was made from)
+    _c = None  # (struct, pointers of the tensors it was made from, their device)
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -172,10 +172,15 @@ class KV(_Handle):
     v_sf: torch.Tensor | None = None
 
     def c(self) -> hs2_kv:
+        return self._cached()[0]
+
+    def _cached(self):
         ptrs = [None if t is None else t.data_ptr() for t in _kv_tensors(self)]
-        if self._c is None or self._c[1] != ptrs:
-            self._c = (self._make(), ptrs)
-        return self._c[0]
+        got = self._c
+        if got is None or got[1] != ptrs:
+            got = (self._make(), ptrs, _device_of(_kv_tensors(self)))
+            object.__setattr__(self, "_c", got)
+        return got
 
     def _make(self) -> hs2_kv:
         d = int(self.k.shape[3])
@@ -418,7 +423,7 @@ def _pages_tensors(p: "Pages"):
 
 def _i32(t: torch.Tensor, name: str, *shape) -> None:
     """t is an int32 contiguous tensor of that shape, or an error."""
-    if t.dtype is not torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
         raise HS2Error(f"{name} must be a contiguous int32 tensor of shape {list(shape)}")
 
 
@@ -429,9 +434,18 @@ def _table(t: torch.Tensor, name: str):
     return t.shape
 
 
-def _launch_stream(stream, tensors) -> int:
-    """The stream to launch on, once every tensor is on the current device (and the stream's)."""
+def _device_of(tensors) -> int:
+    """The one device of the tensors (None: left out), or an error."""
     dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise HS2Error("tensors on several devices")
+    return dev
+
+
+def _launch_stream(stream, dev: int, *tensors) -> int:
+    """The stream to launch on, once every tensor is on device `dev` and that is the current
+    device (and the stream's)."""
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise HS2Error("tensors on several devices")
@@ -448,27 +462,20 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     return t
 
 
-def _rows(t: torch.Tensor, kv: hs2_kv, n_rows: int, name: str):
-    """Row dtype code and token stride of [n_rows][Hkv][d] rows, heads next to each other."""
-    stride = t.stride()
-    if t.dtype not in _ROW_DTYPES or tuple(t.shape) != (n_rows, kv.Hkv, kv.d) or stride[2] != 1 or (
-            kv.Hkv > 1 and stride[1] != kv.d):
-        raise HS2Error(f"{name} must be float32 or bfloat16 [n_rows][Hkv][d] with contiguous tokens")
-    return _ROW_DTYPES[t.dtype], stride[0] if n_rows > 1 else kv.Hkv * kv.d
-
-
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
-    c = kv.c()
-    n = k_rows.shape[0]
-    dt, stride = _rows(k_rows, c, n, "k_rows")
+    c, _, dev = kv._cached()
+    shape, stride, dtype = k_rows.shape, k_rows.stride(), k_rows.dtype
+    n = shape[0]
+    if dtype not in _ROW_DTYPES or shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
+        raise HS2Error("rows must be float32 or bfloat16 [n_rows][Hkv][d] with contiguous tokens")
     if (v_rows is None) != (kv.v is None):
         raise HS2Error("v_rows goes with a cache that has V")
-    if v_rows is not None and _rows(v_rows, c, n, "v_rows") != (dt, stride):
-        raise HS2Error("v_rows must have k_rows' dtype and token stride")
+    if v_rows is not None and (v_rows.dtype is not dtype or v_rows.shape != shape or v_rows.stride() != stride):
+        raise HS2Error("v_rows must have k_rows' dtype, shape and strides")
     _i32(row_start, "row_start", c.batch + 1)
-    st = _launch_stream(stream, (k_rows, v_rows, row_start, dev_err, *_kv_tensors(kv)))
-    _check(call(ctypes.byref(c), k_rows.data_ptr(), _ptr(v_rows), dt, stride, row_start.data_ptr(), n, _ptr(dev_err),
-                st))
+    st = _launch_stream(stream, dev, k_rows, v_rows, row_start, dev_err)
+    _check(call(ctypes.byref(c), k_rows.data_ptr(), _ptr(v_rows), _ROW_DTYPES[dtype],
+                stride[0] if n > 1 else c.Hkv * c.d, row_start.data_ptr(), n, _ptr(dev_err), st))
 
 
 def hs2_kv_write(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor, dev_err=None,
@@ -510,7 +517,7 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
     many keys; ``sink``: float32 [Hq] logits of one more key with a zero value. ``o_dtype``
     float32 or bfloat16; lse is float32 [n_rows][Hq]."""
     lib = load()
-    c = kv.c()
+    c, _, dev = kv._cached()
     n, Hq, d = q.shape
     if max_t is None:
         max_t = c.max_pages * c.page_size
@@ -526,11 +533,11 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
         lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
     else:
         o, lse = out
-        if o.dtype is not o_dtype or tuple(o.shape) != (n, Hq, d) or not o.is_contiguous() or (
-                lse is not None and (lse.dtype is not torch.float32 or tuple(lse.shape) != (n, Hq)
+        if o.dtype is not o_dtype or o.shape != (n, Hq, d) or not o.is_contiguous() or (
+                lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, Hq)
                                      or not lse.is_contiguous())):
             raise HS2Error("out must be contiguous (o [n_rows][Hq][d] of o_dtype, lse float32 [n_rows][Hq] or None)")
-    st = _launch_stream(stream, (q, row_start, sink, o, lse, workspace, dev_err, *_kv_tensors(kv)))
+    st = _launch_stream(stream, dev, q, row_start, sink, o, lse, workspace, dev_err)
     ws = workspace
     if ws is None:
         ws = _scratch(lib.hs2_fa_chunk_workspace(n, Hq, ctypes.byref(c), max_n, max_t, w), q.device, stream)
@@ -556,13 +563,18 @@ class Pages(_Handle):
                    n_free=torch.full((1,), num_pages, dtype=torch.int32, device=device))
 
     def c(self) -> hs2_pages:
-        ptrs = [t.data_ptr() for t in _pages_tensors(self)]
-        if self._c is None or self._c[1] != ptrs:
+        return self._cached()[0]
+
+    def _cached(self):
+        ptrs = [self.ref.data_ptr(), self.free_list.data_ptr(), self.n_free.data_ptr()]
+        got = self._c
+        if got is None or got[1] != ptrs:
             n = int(self.ref.shape[0])
             for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
                 _i32(t, name, size)
-            self._c = (hs2_pages(*ptrs, n), ptrs)
-        return self._c[0]
+            got = (hs2_pages(*ptrs, n), ptrs, _device_of(_pages_tensors(self)))
+            object.__setattr__(self, "_c", got)
+        return got
 
 
 def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, n_new: torch.Tensor, dev_err=None,
@@ -571,8 +583,9 @@ def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(n_new, "n_new", b)
-    st = _launch_stream(stream, (block_table, seq_len, n_new, dev_err, *_pages_tensors(pages)))
-    _check(load().hs2_pages_grow(ctypes.byref(pages.c()), block_table.data_ptr(), seq_len.data_ptr(),
+    c, _, dev = pages._cached()
+    st = _launch_stream(stream, dev, block_table, seq_len, n_new, dev_err)
+    _check(load().hs2_pages_grow(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  n_new.data_ptr(), b, mp, _ptr(dev_err), st))
 
 
@@ -583,23 +596,28 @@ def hs2_pages_free(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(drop, "drop", b)
-    st = _launch_stream(stream, (block_table, seq_len, drop, dev_err, *_pages_tensors(pages)))
-    _check(load().hs2_pages_free(ctypes.byref(pages.c()), block_table.data_ptr(), seq_len.data_ptr(),
+    c, _, dev = pages._cached()
+    st = _launch_stream(stream, dev, block_table, seq_len, drop, dev_err)
+    _check(load().hs2_pages_free(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  drop.data_ptr(), b, mp, _ptr(dev_err), st))
 
 
-def _kv_array(kvs):
-    """The caches' C structs as an array."""
+def _kv_array(kvs, dev: int):
+    """The caches' C structs as an array, all on device `dev`."""
     if not kvs:
         raise HS2Error("at least one cache")
-    return ctypes.byref(kvs[0].c()) if len(kvs) == 1 else (hs2_kv * len(kvs))(*[kv.c() for kv in kvs])
+    got = [kv._cached() for kv in kvs]
+    if any(x[2] != dev for x in got):
+        raise HS2Error("tensors on several devices")
+    return ctypes.byref(got[0][0]) if len(got) == 1 else (hs2_kv * len(got))(*[x[0] for x in got])
 
 
 def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None, stream=None):
     """Branches of the caches' sequences: branch c continues sequence src[c] (-1: none), with
     its full pages shared and the last, partly filled one copied. ``kvs``: the caches of one
     block table. Returns (child_table, child_len)."""
-    cs = _kv_array(kvs)
+    c, _, dev = pages._cached()
+    cs = _kv_array(kvs, dev)
     n, mp = src.numel(), kvs[0].block_table.shape[1]
     _i32(src, "src", n)
     if out is None:
@@ -608,11 +626,8 @@ def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None,
     else:
         _i32(out[0], "child_table", n, mp)
         _i32(out[1], "child_len", n)
-    ts = [src, *out, dev_err, *_pages_tensors(pages)]
-    for kv in kvs:
-        ts += _kv_tensors(kv)
-    st = _launch_stream(stream, ts)
-    _check(load().hs2_pages_fork(ctypes.byref(pages.c()), len(kvs), cs, src.data_ptr(), n, out[0].data_ptr(),
+    st = _launch_stream(stream, dev, src, out[0], out[1], dev_err)
+    _check(load().hs2_pages_fork(ctypes.byref(c), len(kvs), cs, src.data_ptr(), n, out[0].data_ptr(),
                                  out[1].data_ptr(), _ptr(dev_err), st))
     return out
 
@@ -624,11 +639,8 @@ def hs2_pages_compact_workspace(pages: Pages) -> int:
 def hs2_pages_compact(pages: Pages, kvs, workspace=None, dev_err=None, stream=None) -> None:
     """The pool's referenced pages to its front, in place in every cache of ``kvs`` (which
     share one block table holding every sequence), with tables and books updated."""
-    cs = _kv_array(kvs)
-    ts = [pages.ref, pages.free_list, pages.n_free, workspace, dev_err]
-    for kv in kvs:
-        ts += _kv_tensors(kv)
-    st = _launch_stream(stream, ts)
-    c = pages.c()
+    c, _, dev = pages._cached()
+    cs = _kv_array(kvs, dev)
+    st = _launch_stream(stream, dev, workspace, dev_err)
     ws = workspace if workspace is not None else _scratch(hs2_pages_compact_workspace(pages), pages.ref.device, stream)
     _check(load().hs2_pages_compact(ctypes.byref(c), len(kvs), cs, ws.data_ptr(), ws.nbytes, _ptr(dev_err), st))
