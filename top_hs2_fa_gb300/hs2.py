@@ -146,11 +146,14 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+_data_ptr = torch.Tensor.data_ptr
+
+
 class _Handle:
     """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
     and a tensor whose storage has moved makes a new one."""
 
-    _c = None  # (struct, pointers of the tensors it was made from, their device)
+    _c = None  # (struct, device, tensors it was made from, their pointers)
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -175,10 +178,10 @@ class KV(_Handle):
         return self._cached()[0]
 
     def _cached(self):
-        ptrs = [None if t is None else t.data_ptr() for t in _kv_tensors(self)]
         got = self._c
-        if got is None or got[1] != ptrs:
-            got = (self._make(), ptrs, _device_of(_kv_tensors(self)))
+        if got is None or got[3] != tuple(map(_data_ptr, got[2])):
+            ts = tuple(t for t in _kv_tensors(self) if t is not None)
+            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)))
             object.__setattr__(self, "_c", got)
         return got
 
@@ -417,10 +420,6 @@ def _kv_tensors(kv: KV):
     return kv.k, kv.v, kv.block_table, kv.seq_len, kv.k_scale, kv.v_scale, kv.k_sf, kv.v_sf
 
 
-def _pages_tensors(p: "Pages"):
-    return p.ref, p.free_list, p.n_free
-
-
 def _i32(t: torch.Tensor, name: str, *shape) -> None:
     """t is an int32 contiguous tensor of that shape, or an error."""
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
@@ -463,7 +462,7 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
 
 
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
-    c, _, dev = kv._cached()
+    c, dev, _, _ = kv._cached()
     shape, stride, dtype = k_rows.shape, k_rows.stride(), k_rows.dtype
     n = shape[0]
     if dtype not in _ROW_DTYPES or shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
@@ -517,7 +516,7 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
     many keys; ``sink``: float32 [Hq] logits of one more key with a zero value. ``o_dtype``
     float32 or bfloat16; lse is float32 [n_rows][Hq]."""
     lib = load()
-    c, _, dev = kv._cached()
+    c, dev, _, _ = kv._cached()
     n, Hq, d = q.shape
     if max_t is None:
         max_t = c.max_pages * c.page_size
@@ -566,13 +565,14 @@ class Pages(_Handle):
         return self._cached()[0]
 
     def _cached(self):
-        ptrs = [self.ref.data_ptr(), self.free_list.data_ptr(), self.n_free.data_ptr()]
         got = self._c
-        if got is None or got[1] != ptrs:
+        if got is None or got[3] != tuple(map(_data_ptr, got[2])):
             n = int(self.ref.shape[0])
             for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
                 _i32(t, name, size)
-            got = (hs2_pages(*ptrs, n), ptrs, _device_of(_pages_tensors(self)))
+            ts = (self.ref, self.free_list, self.n_free)
+            ptrs = tuple(map(_data_ptr, ts))
+            got = (hs2_pages(*ptrs, n), _device_of(ts), ts, ptrs)
             object.__setattr__(self, "_c", got)
         return got
 
@@ -583,7 +583,7 @@ def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(n_new, "n_new", b)
-    c, _, dev = pages._cached()
+    c, dev, _, _ = pages._cached()
     st = _launch_stream(stream, dev, block_table, seq_len, n_new, dev_err)
     _check(load().hs2_pages_grow(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  n_new.data_ptr(), b, mp, _ptr(dev_err), st))
@@ -596,7 +596,7 @@ def hs2_pages_free(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(drop, "drop", b)
-    c, _, dev = pages._cached()
+    c, dev, _, _ = pages._cached()
     st = _launch_stream(stream, dev, block_table, seq_len, drop, dev_err)
     _check(load().hs2_pages_free(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  drop.data_ptr(), b, mp, _ptr(dev_err), st))
@@ -607,7 +607,7 @@ def _kv_array(kvs, dev: int):
     if not kvs:
         raise HS2Error("at least one cache")
     got = [kv._cached() for kv in kvs]
-    if any(x[2] != dev for x in got):
+    if any(x[1] != dev for x in got):
         raise HS2Error("tensors on several devices")
     return ctypes.byref(got[0][0]) if len(got) == 1 else (hs2_kv * len(got))(*[x[0] for x in got])
 
@@ -616,7 +616,7 @@ def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None,
     """Branches of the caches' sequences: branch c continues sequence src[c] (-1: none), with
     its full pages shared and the last, partly filled one copied. ``kvs``: the caches of one
     block table. Returns (child_table, child_len)."""
-    c, _, dev = pages._cached()
+    c, dev, _, _ = pages._cached()
     cs = _kv_array(kvs, dev)
     n, mp = src.numel(), kvs[0].block_table.shape[1]
     _i32(src, "src", n)
@@ -639,7 +639,7 @@ def hs2_pages_compact_workspace(pages: Pages) -> int:
 def hs2_pages_compact(pages: Pages, kvs, workspace=None, dev_err=None, stream=None) -> None:
     """The pool's referenced pages to its front, in place in every cache of ``kvs`` (which
     share one block table holding every sequence), with tables and books updated."""
-    c, _, dev = pages._cached()
+    c, dev, _, _ = pages._cached()
     cs = _kv_array(kvs, dev)
     st = _launch_stream(stream, dev, workspace, dev_err)
     ws = workspace if workspace is not None else _scratch(hs2_pages_compact_workspace(pages), pages.ref.device, stream)
