@@ -7,9 +7,14 @@
 // converted once per key whatever N is (a scan that keeps the rows on the MMA's other side pays the
 // conversions' instructions per 8 rows). Per 128-key tile, pipelined over rings:
 //   warp 0       producer: TMA of the tile's two pages (codes, group scales)
-//   warps 4-7    K: codes -> f16 (code * group scale, exact) -> tensor memory, S's A operand
-//   warps 8-11   V: codes -> f16 -> shared memory, O's A operand (MN-major); rows that are not
-//                there are zeros
+//   warps 4-7, 8-11  operands, a key a thread: K's codes -> f16 (code * group scale, exact) ->
+//                tensor memory, S's A operand; V's -> shared memory, O's A operand (MN-major),
+//                rows that are not there as zeros. Waits, fences and arrivals cost a warp more
+//                than the conversions (2200 cycles a tile, of which 500 convert). FP4: each group
+//                takes K and V of every other tile (303 us against 288 for drafts of 4 and 12
+//                tokens, 271 against 262 for single tokens). That holds a ring stage longer, and FP8's
+//                ring has three: there one group takes K, the other V (330 against 300 us for
+//                single tokens)
 //   warps 1, 3   MMA issuers, of S and of O: their waits overlap the other's instructions
 //   warps 12-19  softmax, four warps for every other tile, each four with references, sums and
 //                an O of their own (joined when the unit ends): p = 2^(x c + nm), nm = 6 - m per
@@ -203,13 +208,14 @@ __global__ void __launch_bounds__(kNThreads, 1)
   constexpr bool QUANT = Sm::QUANT, BF = !QUANT;
   constexpr int ST = Sm::STAGES, NB = Sm::NB, CODES = Sm::CODES, SF = Sm::SF, RB = Sm::RB;
   constexpr int C = N < 32 ? N : 32;  // columns of a softmax step
+  constexpr bool SPLIT = FMT == HS2_FP8_E4M3;  // K and V by a group each; else a group a tile
   extern __shared__ __align__(1024) uint8_t dsmem[];
   Sm& sm = *reinterpret_cast<Sm*>(dsmem + ((1024 - (tc::smem_u32(dsmem) & 1023)) & 1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int s = 0; s < ST; ++s) {
       tc::mbar_init(&sm.ring_full[s], 1);
-      tc::mbar_init(&sm.ring_empty[s], QUANT ? 256 : 2);  // K and V warps; bf16: the two MMAs
+      tc::mbar_init(&sm.ring_empty[s], SPLIT ? 256 : QUANT ? 128 : 2);  // the tile's group or groups; bf16: the two MMAs
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.k_full[s], 128);
@@ -437,101 +443,107 @@ __global__ void __launch_bounds__(kNThreads, 1)
   } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------------ K and V operands
     regs_down<kRegsCodes>();
-    const bool is_v = warp >= 8;
+    const int own = (warp - 4) >> 2;  // SPLIT: 0 for K, 1 for V; else the parity of this group's tiles
     const int qd = warp & 3, key = qd * 32 + lane;
-    if (QUANT || is_v) {
-      int it = 0;
-      bool ok = true;
-      for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, un);
-        const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
-        at = u.prefix + j1;
-        for (int j = j0; j < j1; ++j, ++it) {
-          const int st = it % ST, b = it & 1;
-          if (!__all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1))) { ok = false; break; }
-          const int pos = (u.page0 + 2 * j) * kPage + key;
-          if (is_v && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.info_full[it % kInfo], (it / kInfo) & 1))) { ok = false; break; }
-          const bool there = is_v && sm.info[it % kInfo].there[qd >> 1] != 0;
-          if constexpr (QUANT) {
-            const uint8_t* codes = sm.ring[st] + (is_v ? CODES : 0) + (qd >> 1) * (CODES / 2);
-            const uint8_t* sfp = sm.ring[st] + 2 * CODES + (is_v ? 128 * SF : 0) + key * SF;
-            const int row = key & 63;
-            constexpr int UN = RB / 16;           // 16-byte units of codes in a row
-            constexpr int PER = D / UN / 2;       // f16 pairs of a unit
-            uint4 w[UN];
+    int it = 0;
+    bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
+    for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
+      const ChunkUnit u = load_unit(p, un);
+      const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
+      at = u.prefix + j1;
+      for (int j = j0; j < j1; ++j, ++it) {
+        if (!SPLIT && (it & 1) != own) continue;
+        const int st = it % ST, b = it & 1;
+        ok = all(!halted(sm) && tc::mbar_wait(&sm.info_full[it % kInfo], (it / kInfo) & 1) &&
+                 tc::mbar_wait(&sm.ring_full[st], (it / ST) & 1));
+        if (!ok) break;
+        const bool live = sm.info[it % kInfo].there[qd >> 1] != 0 && (u.page0 + 2 * j) * kPage + key < u.t;
+        if constexpr (QUANT) {
+          constexpr int UN = RB / 16;      // 16-byte units of codes in a row
+          constexpr int PER = D / UN / 2;  // f16 pairs of a unit
+          uint4 w[UN];
+          uint32_t sfw[2] = {0u, 0u};
+          auto fetch = [&](int side) {  // this key's row: codes and group scales
+            const uint8_t* codes = sm.ring[st] + side * CODES + (qd >> 1) * (CODES / 2);
+            const uint8_t* sfp = sm.ring[st] + 2 * CODES + side * 128 * SF + key * SF;
 #pragma unroll
-            for (int c = 0; c < UN; ++c) w[c] = *reinterpret_cast<const uint4*>(codes + code_unit<RB>(row, c));
-            uint32_t sfw[2] = {0u, 0u};
+            for (int c = 0; c < UN; ++c) w[c] = *reinterpret_cast<const uint4*>(codes + code_unit<RB>(key & 63, c));
             if constexpr (SF == 8) {
               const uint2 s8 = *reinterpret_cast<const uint2*>(sfp);
               sfw[0] = s8.x, sfw[1] = s8.y;
             } else if constexpr (SF == 4) {
               sfw[0] = *reinterpret_cast<const uint32_t*>(sfp);
             }
-            if (is_v) {
-              const bool live = there && pos < u.t;
-              if (!live) {
+          };
+          if (!SPLIT || own == 0) {
+            fetch(0);
+            // K's buffer is read by the S of two tiles ago
+            ok = all(it < 2 || tc::mbar_wait(&sm.s_full[b], ((it - 2) >> 1) & 1));
+            if (!ok) break;
+            tc::tc_fence_after();
 #pragma unroll
-                for (int c = 0; c < UN; ++c) w[c] = make_uint4(0, 0, 0, 0);
-                sfw[0] = sfw[1] = 0u;
+            for (int hb = 0; hb < D / 64; ++hb) {  // 64 channels, 32 columns
+              uint32_t h[32];
+              constexpr int CU = UN / (D / 64);
+#pragma unroll
+              for (int c = 0; c < CU; ++c) {
+                const int cc = hb * CU + c;
+                unit_to_f16<FMT>(w[cc], sfw[cc >> 1] >> (16 * (cc & 1)), h + c * PER);
               }
-              // the rows of the tile before are handed over here, when their stores have long landed
-              if (it > 0) {
-                tc::fence_async_smem();
-                tc::mbar_arrive(&sm.pv_ready[b ^ 1]);
-              }
-              // the buffer is read by the P.V of two tiles ago
-              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
-#pragma unroll
-              for (int c = 0; c < UN; ++c) {
-                uint32_t h[PER];
-                unit_to_f16<FMT>(w[c], sfw[c >> 1] >> (16 * (c & 1)), h);
-#pragma unroll
-                for (int i = 0; i < PER / 4; ++i) {
-                  const int unit = c * (PER / 4) + i;  // of 8 channels
-                  *reinterpret_cast<uint4*>(sm.v[b] + (unit >> 3) * 16384 + key * 128 + (((unit & 7) ^ (key & 7)) << 4)) =
-                      make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                }
-              }
-              tc::mbar_arrive(&sm.ring_empty[st]);
-            } else {
-              // the buffer is read by the S of two tiles ago
-              if (it >= 2 && !__all_sync(0xffffffffu, tc::mbar_wait(&sm.s_full[b], ((it - 2) >> 1) & 1))) { ok = false; break; }
-              tc::tc_fence_after();
-#pragma unroll
-              for (int hb = 0; hb < D / 64; ++hb) {  // 64 channels, 32 columns
-                uint32_t h[32];
-                constexpr int CU = UN / (D / 64);
-#pragma unroll
-                for (int c = 0; c < CU; ++c) {
-                  const int cc = hb * CU + c;
-                  unit_to_f16<FMT>(w[cc], sfw[cc >> 1] >> (16 * (cc & 1)), h + c * PER);
-                }
-                if (hb == 0) tc::mbar_arrive(&sm.ring_empty[st]);
-                tc::tmem_st32u(tK + ((uint32_t)(qd * 32) << 16) + b * 64 + hb * 32, h);
-              }
-              tc::tc_fence_before();
-              tc::mbar_arrive(&sm.k_full[b]);
+              if (SPLIT && hb == 0) tc::mbar_arrive(&sm.ring_empty[st]);
+              tc::tmem_st32u(tK + ((uint32_t)(qd * 32) << 16) + b * 64 + hb * 32, h);
             }
-          } else {
-            // bf16: the tile is the operand; rows behind the sequence may hold anything
-            if (there && pos >= u.t) {
-#pragma unroll
-              for (int i = 0; i < D / 8; ++i)
-                *reinterpret_cast<uint4*>(sm.ring[st] + CODES + (i >> 3) * 16384 + key * 128 + ((i & 7) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
-            tc::mbar_arrive(&sm.pv_ready[b]);
+            if (!SPLIT) fetch(1);
+            tc::tc_fence_before();
+            tc::mbar_arrive(&sm.k_full[b]);
           }
+          if (SPLIT && own == 0) continue;
+          if (SPLIT) fetch(1);
+          if (!live) {  // a weight of 0 does not cancel what else may be there
+#pragma unroll
+            for (int c = 0; c < UN; ++c) w[c] = make_uint4(0, 0, 0, 0);
+            sfw[0] = sfw[1] = 0u;
+          }
+          if (!SPLIT) tc::mbar_arrive(&sm.ring_empty[st]);
+          // SPLIT: the tile before is handed over here, when its stores have long landed
+          if (SPLIT && it > 0) {
+            tc::fence_async_smem();
+            tc::mbar_arrive(&sm.pv_ready[b ^ 1]);
+          }
+          // V's buffer is read by the P.V of two tiles ago
+          ok = all(it < 2 || tc::mbar_wait(&sm.pv_done[b], ((it - 2) >> 1) & 1));
+          if (!ok) break;
+#pragma unroll
+          for (int c = 0; c < UN; ++c) {
+            uint32_t h[PER];
+            unit_to_f16<FMT>(w[c], sfw[c >> 1] >> (16 * (c & 1)), h);
+#pragma unroll
+            for (int i = 0; i < PER / 4; ++i) {
+              const int unit = c * (PER / 4) + i;  // of 8 channels
+              *reinterpret_cast<uint4*>(sm.v[b] + (unit >> 3) * 16384 + key * 128 + (((unit & 7) ^ (key & 7)) << 4)) =
+                  make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+            }
+          }
+          if (SPLIT) tc::mbar_arrive(&sm.ring_empty[st]);
+        } else if (!live) {
+          // bf16: the tile is the operand; rows behind the sequence may hold anything
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(sm.ring[st] + CODES + (i >> 3) * 16384 + key * 128 + ((i & 7) << 4)) =
+                make_uint4(0, 0, 0, 0);
+        }
+        if (!SPLIT) {
+          tc::fence_async_smem();
+          tc::mbar_arrive(&sm.pv_ready[b]);
         }
       }
-      if (QUANT && is_v && ok && it > 0) {  // the last tile's rows
-        tc::fence_async_smem();
-        tc::mbar_arrive(&sm.pv_ready[(it - 1) & 1]);
-      }
-      if (!ok && lane == 0) halt(sm, a.dev_err);
     }
+    if (SPLIT && own == 1 && ok && it > 0) {  // the last tile
+      tc::fence_async_smem();
+      tc::mbar_arrive(&sm.pv_ready[(it - 1) & 1]);
+    }
+    if (!ok && lane == 0) halt(sm, a.dev_err);
   } else if (warp >= 12) {
     // ------------------------------------------------------------------ softmax
     regs_up<kRegsSoftmax>();
