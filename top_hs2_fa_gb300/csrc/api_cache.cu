@@ -59,14 +59,18 @@ int sm_count() {
 
 // Which kernel takes a sequence, by the rows (tokens times G) that share its KV heads' keys. The
 // narrow kernel reads the cache's codes and converts each once per 64 rows; the wide one runs
-// at the tensor pipe's rate, but FP8 / FP4 pages are expanded to bf16 for it first.
-int narrow_rows(hs2_dtype t) { return t == HS2_BF16 ? 64 : 512; }
+// at the tensor pipe's rate, but FP8 / FP4 pages are expanded to bf16 for it first. FP4, d = 128,
+// 4 KV heads, narrow against wide: 8 sequences of 8K to 16K keys with 256 rows 143 against 134 us,
+// with 512 rows 247 against 166; one sequence of 32K keys with 256 rows 68 against 95, with 512
+// 98 against 95; FP8 the same within 4 %. A bf16 cache needs no expansion: single tokens of 8
+// rows take 25 against 29 us (8 sequences), 94 against 107 (256), 477 against 480 (64 long ones).
+int narrow_rows(hs2_dtype t) { return t == HS2_BF16 ? 64 : 256; }
 
 // Workspace of hs2_fa_chunk: the plans of the two kernels with their parts, and the expanded
 // pages of a quantised cache.
 struct ChunkLayout {
   int n_plans;
-  hs2::ChunkPlan plan[2];  // narrow and / or wide; pointers after bind()
+  hs2::ChunkPlan plan[2];  // narrow, wide, or both; pointers after bind()
   bool narrow[2];
   size_t off[2][6], off_exp[4];
   int exp_seqs, exp_pages_seq;
@@ -83,8 +87,11 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
     return at;
   };
   if (kv->dtype != HS2_F32 && n_rows > 0 && max_n > 0 && max_t > 0) {
-    const int G = Hq / kv->Hkv, cut = narrow_rows(kv->dtype);
+    const int G = Hq / kv->Hkv;
     const long long top = (long long)std::min(max_n, n_rows) * G;  // rows of the largest sequence
+    // a bf16 call that may hold a longer sequence takes the wide kernel for all: a second plan's
+    // launch costs more (8 sequences of 1 to 20 tokens 67 us with both, 40 with one; 64: 603, 590)
+    const int cut = kv->dtype == HS2_BF16 && top > narrow_rows(kv->dtype) ? 0 : narrow_rows(kv->dtype);
     auto add = [&](bool narrow, int tile_rows, int lo, int hi, int min_tiles) {
       hs2::ChunkPlan& p = L.plan[L.n_plans];
       L.narrow[L.n_plans] = narrow;
@@ -105,7 +112,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       return &p;
     };
     const long long few = std::min<long long>(top, cut);
-    add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut, 2);
+    if (few > 0) add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut, 2);
     if (top > cut) {
       hs2::ChunkPlan* p = add(false, 256, cut, 0x7fffffff, 4);
       p->expand = low_precision(kv);
