@@ -54,7 +54,7 @@ int sm_count() {
     (void)cudaGetLastError();
     return 152;
   }
-  return std::min(n, 256);  // the merge holds a unit's parts, one per CTA, in shared memory
+  return std::min(n, 512);  // the merge's blocks hold the list of cut units, one per CTA at most
 }
 
 // Which kernel takes a sequence, by the rows (tokens times G) that share its KV heads' keys. The
@@ -106,6 +106,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       size_t* o = L.off[L.n_plans++];
       o[0] = take(16);
       o[1] = take(4 * (size_t)p.ctas);
+      o[2] = take(4 * (size_t)p.ctas);
       o[3] = take(48 * (size_t)p.max_units);
       o[4] = take(2 * (size_t)p.ctas * tile_rows * 8);
       o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
@@ -141,6 +142,7 @@ void bind(ChunkLayout& L, char* ws) {
     hs2::ChunkPlan& p = L.plan[i];
     p.head = (int32_t*)(ws + L.off[i][0]);
     p.cta_first = (int32_t*)(ws + L.off[i][1]);
+    p.cuts = (int32_t*)(ws + L.off[i][2]);
     p.units = (int32_t*)(ws + L.off[i][3]);
     p.part_ml = (float*)(ws + L.off[i][4]);
     p.part_o = (float*)(ws + L.off[i][5]);

@@ -13,127 +13,126 @@ namespace hs2 {
 namespace {
 
 constexpr int kMergeWarps = 8;
-constexpr int kMergeParts = 256;  // CTAs of a unit at most (the host launches no more)
-
-template <int LPR>
-HS2_DEVI float lanes_max(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-template <int LPR>
-HS2_DEVI float lanes_sum(float v) {
-#pragma unroll
-  for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
+constexpr int kMergeBlocks = 4;  // per CTA of the attention kernels, and so per cut unit at least; all resident at once
 
 // Rows of a block: a warp has 32 / LPR rows at LPR lanes each, WPR warps share a row's parts.
 constexpr int merge_rows_of(int WPR, int LPR) { return kMergeWarps / WPR * (32 / LPR); }
+constexpr int kMergeShare = 4;  // warps of a row where blocks abound
 
-// Block c has the unit that starts in CTA c's range and ends behind it.
+// Every `step`th group of merge_rows_of() rows of unit u, from group y on.
 template <int D, int WPR, int LPR>
-HS2_DEVI void merge_rows(const ChunkArgs& a, const ChunkPlan& p, float (*fac)[kMergeParts], float4* sum_) {
-  constexpr int RPW = 32 / LPR, Q = D / (4 * LPR);  // rows of a warp; float4 of a lane
+HS2_DEVI void merge_rows(const ChunkArgs& a, const ChunkPlan& p, const ChunkUnit& u, int per, int y, int step, float4* sum_, float* sum_l) {
+  constexpr int RPW = 32 / LPR, Q = D / (4 * LPR), ROWS = merge_rows_of(WPR, LPR);  // rows of a warp; float4 of a lane
   float4(*sum)[WPR][D / 4] = reinterpret_cast<float4(*)[WPR][D / 4]>(sum_);
-  const int c = blockIdx.x;
-  const int total = p.head[0], per = p.head[1], next = c + 1 < p.ctas ? p.cta_first[c + 1] : 0;
-  if (c + 1 >= p.ctas || (long long)(c + 1) * per >= total) return;
-  const ChunkUnit u = load_unit(p, next);
-  if (u.prefix / per != c) return;  // whole, or cut at an earlier border
   const int live = u.ntok << a.log2G;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ln = lane % LPR;
-  const int rr = warp / WPR * RPW + lane / LPR, part = warp % WPR;  // row of the block; share of its parts
-  const int n = blockIdx.y * merge_rows_of(WPR, LPR) + rr;
-  if ((int)blockIdx.y * merge_rows_of(WPR, LPR) >= live) return;
-  const int parts = (u.prefix + u.ntiles - 1) / per - c + 1;
-  const bool have = n < live;
-  const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + n;
-  float M = -INFINITY, L = 0.f;
-  if (have)
-    for (int k = ln; k < parts; k += LPR) M = fmaxf(M, __ldcg(ml + (size_t)part_slot(u, per, c + k) * p.tile_rows).x);
-  M = lanes_max<LPR>(M);
-  if (have)
-    for (int k = ln; k < parts; k += LPR) {
-      const float2 y = __ldcg(ml + (size_t)part_slot(u, per, c + k) * p.tile_rows);
-      const float e = exp2_rel(y.x, M);
-      L += e * y.y;
-      if (part == 0) fac[rr][k] = e;
-    }
-  L = lanes_sum<LPR>(L);
-  __syncthreads();
-  float4 acc[Q];
+  const int rr = warp / WPR * RPW + lane / LPR, share = warp % WPR;  // row of the group; share of its parts
+  const int c = u.prefix / per, parts = (u.prefix + u.ntiles - 1) / per - c + 1;
+  for (; y * ROWS < live; y += step) {
+    const int n = y * ROWS + rr;
+    const bool have = n < live;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + n;
+    float M = -INFINITY, L = 0.f;
+    if (have)
+      for (int k = ln; k < parts; k += LPR) M = fmaxf(M, __ldcg(ml + (size_t)part_slot(u, per, c + k) * p.tile_rows).x);
 #pragma unroll
-  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (have) {
-#pragma unroll 4
-    for (int k = part; k < parts; k += WPR) {
-      const float4* src = reinterpret_cast<const float4*>(p.part_o + ((size_t)part_slot(u, per, c + k) * p.tile_rows + n) * D);
-      const float f = fac[rr][k];
+    for (int o = LPR / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float4 acc[Q];
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        const float4 v = __ldcg(src + q * LPR + ln);
-        acc[q].x = fmaf(f, v.x, acc[q].x), acc[q].y = fmaf(f, v.y, acc[q].y);
-        acc[q].z = fmaf(f, v.z, acc[q].z), acc[q].w = fmaf(f, v.w, acc[q].w);
+    for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (have) {
+#pragma unroll 2
+      for (int k = share; k < parts; k += WPR) {
+        const size_t at = (size_t)part_slot(u, per, c + k) * p.tile_rows;
+        const float2 x = __ldcg(ml + at);
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (at + n) * D);
+        float4 v[Q];
+#pragma unroll
+        for (int q = 0; q < Q; ++q) v[q] = __ldcg(src + q * LPR + ln);
+        const float f = exp2_rel(x.x, M);
+        L += f * x.y;
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+          acc[q].x = fmaf(f, v[q].x, acc[q].x), acc[q].y = fmaf(f, v[q].y, acc[q].y);
+          acc[q].z = fmaf(f, v[q].z, acc[q].z), acc[q].w = fmaf(f, v[q].w, acc[q].w);
+        }
       }
     }
-  }
-  if (WPR > 1) {
+    if constexpr (WPR > 1) {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) sum[rr][part][q * LPR + ln] = acc[q];
-    __syncthreads();
-  }
-  if (!have || part != 0) return;
-  const int head = (u.g << a.log2G) + (n & (a.G - 1));
-  const size_t at = (size_t)(u.row + (n >> a.log2G)) * a.Hq + head;
-  const float b2 = sink_b2(a.sink, head);
-  const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
-  const float den = L * sc + exp2_rel(b2, M2), f = den > 0.f ? sc / den : 0.f;
-  if (a.lse && ln == 0) a.lse[at] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+      for (int q = 0; q < Q; ++q) sum[rr][share][q * LPR + ln] = acc[q];
+      if (ln == 0) sum_l[rr * WPR + share] = L;
+      __syncthreads();
+      if (share == 0) {
 #pragma unroll
-  for (int q = 0; q < Q; ++q) {
-    float4 v = acc[q];
-    if (WPR > 1)
+        for (int i = 1; i < WPR; ++i) {
+          L += sum_l[rr * WPR + i];
 #pragma unroll
-      for (int i = 1; i < WPR; ++i) {
-        const float4 t = sum[rr][i][q * LPR + ln];
-        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+          for (int q = 0; q < Q; ++q) {
+            const float4 t = sum[rr][i][q * LPR + ln];
+            acc[q].x += t.x, acc[q].y += t.y, acc[q].z += t.z, acc[q].w += t.w;
+          }
+        }
       }
-    const size_t col = at * D + 4 * (q * LPR + ln);
-    if (a.o_bf16)
-      *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + col) = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
-    else
-      *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.o) + col) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+      __syncthreads();  // the next group's sums
+    }
+    if (!have || share != 0) continue;
+    const int head = (u.g << a.log2G) + (n & (a.G - 1));
+    const size_t at = (size_t)(u.row + (n >> a.log2G)) * a.Hq + head;
+    const float b2 = sink_b2(a.sink, head);
+    const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
+    const float den = L * sc + exp2_rel(b2, M2), f = den > 0.f ? sc / den : 0.f;
+    if (a.lse && ln == 0) a.lse[at] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 v = acc[q];
+      const size_t col = at * D + 4 * (q * LPR + ln);
+      if (a.o_bf16)
+        *reinterpret_cast<uint2*>(reinterpret_cast<__nv_bfloat16*>(a.o) + col) = make_uint2(pack_bf16(v.x * f, v.y * f), pack_bf16(v.z * f, v.w * f));
+      else
+        *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.o) + col) = make_float4(v.x * f, v.y * f, v.z * f, v.w * f);
+    }
   }
 }
 
-constexpr int kWideLanes = 8;  // the wide kernel's units: 256 rows, few parts
-constexpr int kNarrowWarps = 4;  // the narrow one's: up to 64 rows, many parts
-
 }  // namespace
 
-// grid (CTAs of the attention kernels, groups of a unit's rows, plans)
+// grid (kMergeBlocks per CTA of the attention kernels, plans). The cut units share the blocks:
+// with many units a block takes many rows of few parts, with few units few rows of many parts.
 template <int D>
-__global__ void __launch_bounds__(kMergeWarps * 32) chunk_merge_kernel(const ChunkArgs a, const ChunkPlan p0, const ChunkPlan p1) {
+__global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocks) chunk_merge_kernel(const ChunkArgs a, const ChunkPlan p0,
+                                                                                     const ChunkPlan p1) {
   constexpr int LPR = D / 4 < 32 ? D / 4 : 32;
-  __shared__ float fac[merge_rows_of(1, kWideLanes)][kMergeParts];
-  __shared__ float4 sum[merge_rows_of(kNarrowWarps, LPR) * kNarrowWarps * D / 4];
+  constexpr int MORE = merge_rows_of(1, LPR), FEW = merge_rows_of(kMergeShare, LPR);
+  __shared__ float4 sum[FEW * kMergeShare * D / 4];
+  __shared__ float sum_l[FEW * kMergeShare];
+  __shared__ int cut_s;
   griddep_launch_dependents();
   griddep_wait();
-  const ChunkPlan& p = blockIdx.z ? p1 : p0;
-  if (p.tile_rows > 64) merge_rows<D, 1, kWideLanes>(a, p, fac, sum);
-  else merge_rows<D, kNarrowWarps, LPR>(a, p, fac, sum);
+  const ChunkPlan& p = blockIdx.y ? p1 : p0;
+  // the whole list with its length, in one round of loads
+  const int per = p.head[1], cuts = p.head[2];
+  int mine[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int at = threadIdx.x + k * kMergeWarps * 32;
+    mine[k] = at < p.ctas ? p.cuts[at] : 0;
+  }
+  if (cuts <= 0) return;
+  const int blocks = gridDim.x / cuts, i = blockIdx.x / blocks, y = blockIdx.x - i * blocks;
+  if (i >= cuts) return;
+  if ((int)threadIdx.x == i % (kMergeWarps * 32)) cut_s = mine[i / (kMergeWarps * 32)];
+  __syncthreads();
+  const ChunkUnit u = load_unit(p, cut_s);
+  const int rows = ((u.ntok << a.log2G) + blocks - 1) / blocks;
+  if (rows > MORE) merge_rows<D, 1, 8>(a, p, u, per, y, blocks, sum, sum_l);
+  else if (rows > FEW) merge_rows<D, 1, LPR>(a, p, u, per, y, blocks, sum, sum_l);
+  else merge_rows<D, kMergeShare, LPR>(a, p, u, per, y, blocks, sum, sum_l);
 }
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, int d, cudaStream_t s) {
   const ChunkPlan &p0 = plans[0], &p1 = plans[n_plans - 1];
-  if (p0.ctas > kMergeParts || p1.ctas != p0.ctas) return cudaErrorInvalidValue;
-  int groups = 0;
-  for (int i = 0; i < n_plans; ++i) {
-    const int rows = plans[i].tile_rows > 64 ? merge_rows_of(1, kWideLanes) : merge_rows_of(kNarrowWarps, d == 128 ? 32 : 16);
-    groups = groups > plans[i].tile_rows / rows ? groups : plans[i].tile_rows / rows;
-  }
-  const dim3 grid(p0.ctas, groups, n_plans);
+  const dim3 grid(kMergeBlocks * p0.ctas, n_plans);  // every plan is cut among as many CTAs
   return launch_pdl(d == 128 ? chunk_merge_kernel<128> : chunk_merge_kernel<64>, grid, dim3(kMergeWarps * 32), 0, s, a, p0, p1);
 }
 

@@ -24,7 +24,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   griddep_wait();
   const ChunkPlan& p = blockIdx.x ? p1 : p0;
   __shared__ int sums[33], ubase[kPlanThreads + 1], s_row[kPlanThreads], s_n[kPlanThreads], s_t[kPlanThreads],
-      s_exp[kPlanThreads];
+      s_exp[kPlanThreads], n_cuts;
   const int tok = p.tile_rows / a.G;
   int total_tiles = 0, units = 0, exp_pages = 0, n_exp = 0;
   int my_tiles = 0, my_prefix = 0;  // of the last unit this thread wrote
@@ -118,24 +118,28 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __syncthreads();  // the chunk's arrays are rewritten
   }
   const int per = max(p.min_tiles, (total_tiles + p.ctas - 1) / p.ctas);
+  // the unit at each CTA's range start, and the list of units that a range border cuts (in any
+  // order: the merge treats each by itself)
+  auto place = [&](int u, int ntiles, int prefix) {
+    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
+    if (prefix / per != (prefix + ntiles - 1) / per) p.cuts[atomicAdd(&n_cuts, 1)] = u;
+  };
+  if (threadIdx.x == 0) n_cuts = 0;
+  __syncthreads();  // also: the records are visible to the block
+  if (a.batch <= kPlanThreads && units <= kPlanThreads) {  // they are in registers
+    if ((int)threadIdx.x < units) place(threadIdx.x, my_tiles, my_prefix);
+  } else {
+    for (int u = threadIdx.x; u < units; u += kPlanThreads) {
+      const int4 y = reinterpret_cast<const int4*>(p.units)[3 * (size_t)u + 1];
+      place(u, y.z, y.w);
+    }
+  }
+  __syncthreads();
   if (threadIdx.x == 0) {
     p.head[0] = total_tiles;
     p.head[1] = per;
-    p.head[2] = units;
+    p.head[2] = n_cuts;
     if (p.expand) p.exp_head[0] = n_exp;
-  }
-  // the unit at each CTA's range start
-  auto starts = [&](int u, int ntiles, int prefix) {
-    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
-  };
-  if (a.batch <= kPlanThreads && units <= kPlanThreads) {  // they are in registers
-    if ((int)threadIdx.x < units) starts(threadIdx.x, my_tiles, my_prefix);
-    return;
-  }
-  __syncthreads();  // the records are visible to the block
-  for (int u = threadIdx.x; u < units; u += kPlanThreads) {
-    const int4 y = reinterpret_cast<const int4*>(p.units)[3 * (size_t)u + 1];
-    starts(u, y.z, y.w);
   }
 }
 

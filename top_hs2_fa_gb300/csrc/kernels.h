@@ -130,8 +130,9 @@ struct ChunkArgs {
 // kernel of the same call). rows: the packed rows of a unit; sequences with rows in
 // (min_rows, max_rows] are the kernel's.
 struct ChunkPlan {
-  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] units
+  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
+  int32_t* cuts;       // [ctas] units that a range border cuts: one per border at most
   int32_t* units;      // [max_units] ChunkUnit
   int max_units, ctas;
   int tile_rows;            // rows of a unit: 256 or the narrow kernel's width
