@@ -57,14 +57,34 @@ int sm_count() {
   return std::min(n, 512);  // the merge's blocks hold the list of cut units, one per CTA at most
 }
 
-// Which kernel takes a sequence, by the rows (tokens times G) that share its KV heads' keys. The
-// narrow kernel reads the cache's codes and converts each once per 64 rows; the wide one runs
-// at the tensor pipe's rate, but FP8 / FP4 pages are expanded to bf16 for it first. FP4, d = 128,
-// 4 KV heads, narrow against wide: 8 sequences of 8K to 16K keys with 256 rows 143 against 134 us,
-// with 512 rows 247 against 166; one sequence of 32K keys with 256 rows 68 against 95, with 512
-// 98 against 95; FP8 the same within 4 %. A bf16 cache needs no expansion: single tokens of 8
-// rows take 25 against 29 us (8 sequences), 94 against 107 (256), 477 against 480 (64 long ones).
-int narrow_rows(hs2_dtype t) { return t == HS2_BF16 ? 64 : 256; }
+// Which kernels a call runs, by the rows (tokens times G) that share a KV head's keys.
+struct ChunkCuts {
+  int narrow;  // the narrow kernel takes sequences of up to this many rows, 0: none
+  bool wide;   // the wide kernel takes the rest
+};
+
+// The narrow kernel reads the cache's codes and converts each once per 64 rows. The wide one runs
+// at the tensor pipe's rate, 256 rows at a time, but FP8 / FP4 pages are expanded to bf16 for it. Each
+// plan costs about 20 us whatever it holds. `top` rows are the most a sequence can have. d = 128,
+// FP8 where nothing else is said; FP4 is within 4 %:
+//   bf16: no expansion. Single tokens of 8 rows take 25 us narrow, 29 wide (8 sequences), 94 and 107
+//     (256), 477 and 480 (64 long ones); 8 sequences of 8 to 160 rows 67 with both, 40 wide, 64 long
+//     ones 603 and 590.
+//   up to 256 rows: one sequence of 256 rows and 32K keys 68 narrow, 95 wide; at 512 rows 98 and 95;
+//     8 sequences of 8K to 16K keys with 256 rows 143 and 134, with 512 rows 247 and 166 (FP4).
+//   few rows times keys: 5 sequences of 32 to 352 rows over 1K to 6K keys 35 narrow, 39 wide, 55 both;
+//     one of 512 rows and 2K keys 31 and 35, and 16K keys 62 and 56.
+//   little to expand: 12 sequences of 32 to 22400 rows over 1K to 6K keys 132 wide, 161 both; 9 of up
+//     to 512 rows (110 MB expanded) 68 and 84; 16 of up to 800 rows and 16K keys (520 MB) 229 and
+//     212; 64 of up to 800 rows (8 GB) 2998 and 2191.
+ChunkCuts chunk_cuts(long long top, int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+  const int all = 0x7fffffff;
+  const long long keys = w > 0 ? std::min<long long>(max_t, (long long)max_n + w) : max_t;
+  if (kv->dtype == HS2_BF16) return top <= 64 ? ChunkCuts{all, false} : ChunkCuts{0, true};
+  if (top <= 256 || (long long)n_rows * Hq * keys <= 1LL << 24) return {all, false};
+  const long long expanded = kv->batch * keys * kv->Hkv * kv->d * 4;  // bytes, K and V
+  return {expanded <= 256LL << 20 ? 0 : 256, true};
+}
 
 // Workspace of hs2_fa_chunk: the plans of the two kernels with their parts, and the expanded
 // pages of a quantised cache.
@@ -89,9 +109,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
   if (kv->dtype != HS2_F32 && n_rows > 0 && max_n > 0 && max_t > 0) {
     const int G = Hq / kv->Hkv;
     const long long top = (long long)std::min(max_n, n_rows) * G;  // rows of the largest sequence
-    // a bf16 call that may hold a longer sequence takes the wide kernel for all: a second plan's
-    // launch costs more (8 sequences of 1 to 20 tokens 67 us with both, 40 with one; 64: 603, 590)
-    const int cut = kv->dtype == HS2_BF16 && top > narrow_rows(kv->dtype) ? 0 : narrow_rows(kv->dtype);
+    const ChunkCuts cut = chunk_cuts(top, n_rows, Hq, kv, max_n, max_t, w);
     auto add = [&](bool narrow, int tile_rows, int lo, int hi, int min_tiles) {
       hs2::ChunkPlan& p = L.plan[L.n_plans];
       L.narrow[L.n_plans] = narrow;
@@ -112,13 +130,15 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
       return &p;
     };
-    const long long few = std::min<long long>(top, cut);
-    if (few > 0) add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut, 2);
-    if (top > cut) {
-      hs2::ChunkPlan* p = add(false, 256, cut, 0x7fffffff, 4);
+    if (cut.narrow > 0) {
+      const long long few = std::min<long long>(top, cut.narrow);
+      add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut.narrow, 2);
+    }
+    if (cut.wide) {
+      hs2::ChunkPlan* p = add(false, 256, cut.narrow, 0x7fffffff, 4);
       p->expand = low_precision(kv);
       if (p->expand) {
-        L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut + 1));
+        L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut.narrow + 1));
         L.exp_pages_seq = cdiv(max_t, 64);
         if (w > 0) L.exp_pages_seq = (int)std::min<long long>(L.exp_pages_seq, ((long long)max_n + w) / 64 + 2);
         const long long pages = (long long)L.exp_seqs * L.exp_pages_seq;

@@ -159,58 +159,59 @@ __global__ void __launch_bounds__(256) chunk_expand_kernel(const ChunkArgs a, co
                                                            float2* params) {
   griddep_launch_dependents();
   griddep_wait();
-  const int i = blockIdx.z, g = blockIdx.y;
-  if (i >= p.exp_head[0]) return;
-  const int b = p.exp_seq[i], page = p.exp_page[i] + blockIdx.x, t = a.seq_len[b];
-  if (page >= (t + kPage - 1) / kPage) return;
-  const int slot = p.exp_base[i] + blockIdx.x;
-  if (slot >= p.max_exp_pages) return;  // never: the host sized the buffer for every sequence
-  const int phys = a.bt[(size_t)b * a.max_pages + page];
-  const bool there = phys >= 0 && phys < a.num_pages;
-  if (!there && threadIdx.x == 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-  const size_t line0 = ((size_t)(there ? phys : 0) * a.Hkv + g) * kPage;
-  const size_t out0 = ((size_t)slot * a.Hkv + g) * kPage;
-  float f[2], e[2];  // a slab scale S = f * 2^e-with-sign
+  const int g = blockIdx.y, n = p.exp_head[0];
+  for (int i = blockIdx.z; i < n; i += gridDim.z) {
+    const int b = p.exp_seq[i], page = p.exp_page[i] + blockIdx.x, t = a.seq_len[b];
+    if (page >= (t + kPage - 1) / kPage) continue;
+    const int slot = p.exp_base[i] + blockIdx.x;
+    if (slot >= p.max_exp_pages) continue;  // never: the host sized the buffer for every sequence
+    const int phys = a.bt[(size_t)b * a.max_pages + page];
+    const bool there = phys >= 0 && phys < a.num_pages;
+    if (!there && threadIdx.x == 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+    const size_t line0 = ((size_t)(there ? phys : 0) * a.Hkv + g) * kPage;
+    const size_t out0 = ((size_t)slot * a.Hkv + g) * kPage;
+    float f[2], e[2];  // a slab scale S = f * 2^e-with-sign
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const float S = there ? (side ? a.v_scale : a.k_scale)[line0 / kPage] : 0.f;
-    const uint32_t u = __float_as_uint(S);
-    const bool plain = (u & 0x7F800000u) != 0 && (u & 0x7F800000u) != 0x7F800000u;
-    f[side] = plain ? __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u) : 1.f;
-    e[side] = plain ? __uint_as_float(u & 0xFF800000u) : S;  // subnormal, zero, inf, NaN: as it is
-  }
-  if (threadIdx.x == 0) params[(size_t)slot * a.Hkv + g] = make_float2(there ? f[0] : -1.f, log2f(f[1]));
-  constexpr int UNITS = kPage * D / 8;  // 16-byte outputs per side
+    for (int side = 0; side < 2; ++side) {
+      const float S = there ? (side ? a.v_scale : a.k_scale)[line0 / kPage] : 0.f;
+      const uint32_t u = __float_as_uint(S);
+      const bool plain = (u & 0x7F800000u) != 0 && (u & 0x7F800000u) != 0x7F800000u;
+      f[side] = plain ? __uint_as_float((u & 0x007FFFFFu) | 0x3F800000u) : 1.f;
+      e[side] = plain ? __uint_as_float(u & 0xFF800000u) : S;  // subnormal, zero, inf, NaN: as it is
+    }
+    if (threadIdx.x == 0) params[(size_t)slot * a.Hkv + g] = make_float2(there ? f[0] : -1.f, log2f(f[1]));
+    constexpr int UNITS = kPage * D / 8;  // 16-byte outputs per side
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const uint8_t* pool = reinterpret_cast<const uint8_t*>(side ? a.v : a.k);
-    const uint8_t* sf = side ? a.v_sf : a.k_sf;
-    uint4* out = (side ? ev : ek) + out0 * (D / 8);
-    for (int x = threadIdx.x; x < UNITS; x += 256) {
-      const int row = x / (D / 8), u8 = x % (D / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (there && page * kPage + row < t) {
-        uint32_t h[4];
-        if constexpr (FMT == HS2_FP4_E2M1) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + (line0 + row) * (D / 2) + 4 * u8);
-          fp4x8_to_f16x8(w, h[0], h[1], h[2], h[3]);
-          const uint32_t s = sf[(line0 + row) * (D / 16) + u8 / 2], s2 = e4m3_pair(s, s);
+    for (int side = 0; side < 2; ++side) {
+      const uint8_t* pool = reinterpret_cast<const uint8_t*>(side ? a.v : a.k);
+      const uint8_t* sf = side ? a.v_sf : a.k_sf;
+      uint4* out = (side ? ev : ek) + out0 * (D / 8);
+      for (int x = threadIdx.x; x < UNITS; x += 256) {
+        const int row = x / (D / 8), u8 = x % (D / 8);
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (there && page * kPage + row < t) {
+          uint32_t h[4];
+          if constexpr (FMT == HS2_FP4_E2M1) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(pool + (line0 + row) * (D / 2) + 4 * u8);
+            fp4x8_to_f16x8(w, h[0], h[1], h[2], h[3]);
+            const uint32_t s = sf[(line0 + row) * (D / 16) + u8 / 2], s2 = e4m3_pair(s, s);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s2);
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(pool + (line0 + row) * D + 8 * u8);
-          fp8x4_to_f16x4(w.x, h[0], h[1]);
-          fp8x4_to_f16x4(w.y, h[2], h[3]);
+            for (int j = 0; j < 4; ++j) h[j] = hmul2(h[j], s2);
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(pool + (line0 + row) * D + 8 * u8);
+            fp8x4_to_f16x4(w.x, h[0], h[1]);
+            fp8x4_to_f16x4(w.y, h[2], h[3]);
+          }
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 q = __half22float2(*reinterpret_cast<__half2*>(&h[j]));
+            r[j] = pack_bf16(q.x * e[side], q.y * e[side]);
+          }
+          v = make_uint4(r[0], r[1], r[2], r[3]);
         }
-        uint32_t r[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 q = __half22float2(*reinterpret_cast<__half2*>(&h[j]));
-          r[j] = pack_bf16(q.x * e[side], q.y * e[side]);
-        }
-        v = make_uint4(r[0], r[1], r[2], r[3]);
+        out[x] = v;
       }
-      out[x] = v;
     }
   }
 }
@@ -221,7 +222,7 @@ cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, i
                                                 : chunk_expand_kernel<128, HS2_FP8_E4M3>)
                        : (dtype == HS2_FP4_E2M1 ? chunk_expand_kernel<64, HS2_FP4_E2M1>
                                                 : chunk_expand_kernel<64, HS2_FP8_E4M3>);
-  return launch_pdl(kern, dim3(max_pages_seq, a.Hkv, max_seqs), dim3(256), 0, s, a, p, (uint4*)ek, (uint4*)ev, params);
+  return launch_pdl(kern, dim3(max_pages_seq, a.Hkv, max_seqs < 65535 ? max_seqs : 65535), dim3(256), 0, s, a, p, (uint4*)ek, (uint4*)ev, params);
 }
 
 }  // namespace hs2
