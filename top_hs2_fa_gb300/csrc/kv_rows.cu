@@ -16,8 +16,9 @@
 // fma(a, S, -p), exactly, for S in [2^-60, 2^60]. FP8 likewise, the borders of E4M3 having at
 // most 5 bits; its exact way is quotient_to_odd.
 //
-// Bound by the rows' bytes; the instructions per value decide how near it comes. Comparing
-// every value took 13 a value: 46 us for 32768 rows of 2 x 4 x 128 values (86 MB).
+// Bound by the rows' bytes; the instructions per value decide how near it comes. 32768 rows of
+// 2 x 4 x 128 bf16 values to FP4 (86 MB) take 27 us; comparing every value against the borders
+// took 46. Their way back to floats (153 MB) takes 29 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -78,6 +79,12 @@ HS2_DEVI float quotient_to_odd(float x, float S, float inv) {
 HS2_DEVI uint32_t low_bits(float q) { return (__float_as_uint(q) + 8u) & 0x3FFFFu; }
 constexpr uint32_t kNear = 16;
 
+HS2_DEVI float max_nan3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // two floats to E2M1 codes, nearest even, saturating; a in the low nibble
 HS2_DEVI uint32_t e2m1_codes(float a, float b) {
   uint32_t r;
@@ -106,40 +113,10 @@ HS2_DEVI void load16(const void* rows, long long at, float (&x)[16]) {
   }
 }
 
-// One thread per (row, KV head, 16 channels) of K or V; a warp takes 32 / (D / 16) consecutive
-// rows of one head, so its codes and group scales fall next to each other in the page.
-template <int D, int FMT, bool ROW_F32>
-__global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  constexpr int GPR = D / 16, TOK = 32 / GPR;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r0 = (blockIdx.x * (kRowThreads / 32) + warp) * TOK;
-  const int tok = lane / GPR, grp = lane % GPR, r = r0 + tok;
-  const int g = blockIdx.y, side = blockIdx.z;
-  if (r0 >= a.n_rows) return;
-  const bool have = r < a.n_rows;
-  float x[16];
-  if (have) load16<ROW_F32>(side ? a.v_rows : a.k_rows, (long long)r * a.row_stride + g * D + 16 * grp, x);
-  int n[TOK], n_le = 0;
-  warp_rows_at_most<TOK>(a.row_start, a.batch, r0, n);
-#pragma unroll
-  for (int k = 0; k < TOK; ++k)
-    if (k == tok) n_le = n[k];
-  if (!have) return;
-  const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, r, n_le);
-  if (pl.b < 0) return;
-  if (pl.pos < 0) {
-    flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
-    return;
-  }
-  const int phys = a.bt[(size_t)pl.b * a.max_pages + pl.pos / kPage];
-  if (phys < 0 || phys >= a.num_pages) {
-    flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-    return;
-  }
-  const size_t slab = (size_t)phys * a.Hkv + g;
-  const size_t line = slab * kPage + pl.pos % kPage;  // row of the pool
+// One side's 16 channels to their place.
+template <int D, int FMT>
+HS2_DEVI void put16(const RowsArgs& a, int side, size_t slab, size_t line, int grp, const float (&x)[16]) {
+  constexpr int GPR = D / 16;
   uint8_t* pool = reinterpret_cast<uint8_t*>(side ? a.v : a.k);
   if constexpr (FMT == HS2_F32) {
     float4* dst = reinterpret_cast<float4*>(pool + (line * D + 16 * grp) * 4);
@@ -162,9 +139,9 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a)
       float q[16];
       uint32_t low = kNear;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        q[j] = x[j] * inv;
-        low = min(low, low_bits(q[j]));
+      for (int j = 0; j < 16; j += 2) {
+        q[j] = x[j] * inv, q[j + 1] = x[j + 1] * inv;
+        low = __vimin3_u32(low, low_bits(q[j]), low_bits(q[j + 1]));
       }
       if (low < kNear) {
 #pragma unroll
@@ -175,20 +152,21 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a)
       for (int i = 0; i < 4; ++i) w[i] = e4m3_codes(q[4 * i], q[4 * i + 1]) | (e4m3_codes(q[4 * i + 2], q[4 * i + 3]) << 16);
       *reinterpret_cast<uint4*>(pool + line * D + 16 * grp) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
-      uint32_t top = 0;  // the largest magnitude as bits: a NaN's exceed infinity's
+      float top = fabsf(x[0]);  // the largest magnitude, or NaN
 #pragma unroll
-      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x[j]) & 0x7FFFFFFFu);
-      const bool nan = top > 0x7F800000u;
-      const uint32_t s = nan ? 0x7Fu : group_scale(__uint_as_float(top), S);
+      for (int j = 1; j < 15; j += 2) top = max_nan3(top, fabsf(x[j]), fabsf(x[j + 1]));
+      top = max_nan3(top, fabsf(x[15]), 0.f);
+      const bool nan = top != top;
+      const uint32_t s = nan ? 0x7Fu : group_scale(top, S);
       const float sv = nan ? 0.f : e4m3_value(s);
       uint32_t w[2] = {0u, 0u};
       const float inv = sv > 0.f ? 1.f / (sv * S) : 0.f;
       float q[16];
       uint32_t low = kNear;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        q[j] = x[j] * inv;
-        low = min(low, low_bits(q[j]));
+      for (int j = 0; j < 16; j += 2) {
+        q[j] = x[j] * inv, q[j + 1] = x[j + 1] * inv;
+        low = __vimin3_u32(low, low_bits(q[j]), low_bits(q[j + 1]));
       }
       if (low >= kNear) {
 #pragma unroll
@@ -214,6 +192,46 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a)
       (side ? a.v_sf : a.k_sf)[line * GPR + grp] = (uint8_t)s;
     }
   }
+}
+
+// One thread per (row, KV head, 16 channels) of K or V, or of both (SIDES 2); a warp takes 32 / (D / 16) consecutive
+// rows of one head, so its codes and group scales fall next to each other in the page.
+template <int D, int FMT, bool ROW_F32, int SIDES>
+__global__ void __launch_bounds__(kRowThreads) kv_write_kernel(const RowsArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int GPR = D / 16, TOK = 32 / GPR;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = (blockIdx.x * (kRowThreads / 32) + warp) * TOK;
+  const int tok = lane / GPR, grp = lane % GPR, r = r0 + tok;
+  const int g = blockIdx.y, side = SIDES == 1 ? blockIdx.z : 0;
+  if (r0 >= a.n_rows) return;
+  const bool have = r < a.n_rows;
+  float x[16], y[16];
+  const long long at = (long long)r * a.row_stride + g * D + 16 * grp;
+  if (have) load16<ROW_F32>(side ? a.v_rows : a.k_rows, at, x);
+  if (SIDES == 2 && have) load16<ROW_F32>(a.v_rows, at, y);
+  int n[TOK], n_le = 0;
+  warp_rows_at_most<TOK>(a.row_start, a.batch, r0, n);
+#pragma unroll
+  for (int k = 0; k < TOK; ++k)
+    if (k == tok) n_le = n[k];
+  if (!have) return;
+  const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, r, n_le);
+  if (pl.b < 0) return;
+  if (pl.pos < 0) {
+    flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
+    return;
+  }
+  const int phys = a.bt[(size_t)pl.b * a.max_pages + pl.pos / kPage];
+  if (phys < 0 || phys >= a.num_pages) {
+    flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+    return;
+  }
+  const size_t slab = (size_t)phys * a.Hkv + g;
+  const size_t line = slab * kPage + pl.pos % kPage;  // row of the pool
+  put16<D, FMT>(a, side, slab, line, grp, x);
+  if (SIDES == 2) put16<D, FMT>(a, 1, slab, line, grp, y);
 }
 
 // Four channels per lane, so that every store of a warp is contiguous; a warp takes as many
@@ -287,11 +305,18 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
   }
 }
 
+// From so many rows times heads on a thread finds a row's place once for K and V: 32768 rows of
+// 4 heads written and read back 60 us with a thread a side and 56 with both, 4096 rows 13.5 and
+// 12.5; below, more threads hide more of the latency: 1024 rows 8.4 and 10.3.
+constexpr long long kTwoSides = 8192;
+
 template <int D, int FMT>
 cudaError_t launch_fmt(const RowsArgs& a, bool write, bool row_f32, cudaStream_t s) {
   const int per_cta = kRowThreads / (D / 16);
-  const dim3 grid((a.n_rows + per_cta - 1) / per_cta, a.Hkv, a.v ? 2 : 1);
-  auto kern = write ? (row_f32 ? kv_write_kernel<D, FMT, true> : kv_write_kernel<D, FMT, false>)
+  const bool two = write && a.v && (long long)a.n_rows * a.Hkv >= kTwoSides;
+  const dim3 grid((a.n_rows + per_cta - 1) / per_cta, a.Hkv, a.v && !two ? 2 : 1);
+  auto kern = write ? (two ? (row_f32 ? kv_write_kernel<D, FMT, true, 2> : kv_write_kernel<D, FMT, false, 2>)
+                           : (row_f32 ? kv_write_kernel<D, FMT, true, 1> : kv_write_kernel<D, FMT, false, 1>))
                     : (row_f32 ? kv_read_kernel<D, FMT, true> : kv_read_kernel<D, FMT, false>);
   return launch_pdl(kern, grid, dim3(kRowThreads), 0, s, a);
 }
