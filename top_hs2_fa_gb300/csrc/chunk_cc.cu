@@ -3,8 +3,7 @@
 // x(s) = scale q . k(s) over the row's visible keys, one pass with the running maximum and
 // sum: every key costs a warp one 32-lane dot product. On the CUDA cores, because the tensor
 // cores have no fp32 product and a float32 cache is kept for its exactness (1e-4, not 2e-2).
-#include "common.cuh"
-#include "kernels.h"
+#include "chunk_plan.cuh"
 #include "ragged.cuh"
 
 namespace hs2 {
@@ -83,7 +82,7 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
     for (int i = 0; i < V; ++i) o[i] *= alpha;
 #pragma unroll
     for (int j = 0; j < kCcKeys; ++j) {
-      const float p = exp2_rel(x[j], mn);
+      const float p = x[j] != x[j] ? x[j] : exp2_rel(x[j], mn);  // the maximum leaves NaN out
       l += p;
 #pragma unroll
       for (int i = 0; i < V; ++i) o[i] = fmaf(p, vv[j][i], o[i]);
@@ -107,10 +106,10 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
     O += f * sm_o[k][threadIdx.x];
   }
   const size_t at = (size_t)r * a.Hq + h;
-  const float out = L > 0.f ? O / L : 0.f;
+  const float out = chunk_factor(O, L);
   if (a.o_bf16) reinterpret_cast<__nv_bfloat16*>(a.o)[at * D + threadIdx.x] = __float2bfloat16(out);
   else reinterpret_cast<float*>(a.o)[at * D + threadIdx.x] = out;
-  if (a.lse && threadIdx.x == 0) a.lse[at] = L > 0.f ? (M + log2f(L)) / kLog2e : -INFINITY;
+  if (a.lse && threadIdx.x == 0) a.lse[at] = chunk_lse(L, M);
 }
 
 cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s) {

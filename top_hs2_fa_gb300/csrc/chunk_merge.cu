@@ -81,8 +81,8 @@ HS2_DEVI void merge_rows(const ChunkArgs& a, const ChunkPlan& p, const ChunkUnit
     const size_t at = (size_t)(u.row + (n >> a.log2G)) * a.Hq + head;
     const float b2 = sink_b2(a.sink, head);
     const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
-    const float den = L * sc + exp2_rel(b2, M2), f = den > 0.f ? sc / den : 0.f;
-    if (a.lse && ln == 0) a.lse[at] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+    const float den = L * sc + exp2_rel(b2, M2), f = chunk_factor(sc, den);
+    if (a.lse && ln == 0) a.lse[at] = chunk_lse(den, M2);
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
       const float4 v = acc[q];

@@ -752,8 +752,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
         const float b2 = sink_b2(a.sink, u.g * a.G + (n & (a.G - 1)));
         const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
         const float den = L * sc + exp2_rel(b2, M2);
-        if (a.lse && n < rows) a.lse[out_row(n)] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
-        return den > 0.f ? sc / den : 0.f;
+        if (a.lse && n < rows) a.lse[out_row(n)] = chunk_lse(den, M2);
+        return chunk_factor(sc, den);
       };
       auto put = [&](int n, float v) {
         if (n < rows && tid < D) {

@@ -42,6 +42,10 @@ HS2_DEVI ChunkUnit load_unit(const ChunkPlan& p, int u) {
   return x;
 }
 
+// A row's results from its denominator, relative to 2^M: 0 where no key is left, NaN passes on.
+HS2_DEVI float chunk_lse(float den, float M) { return den == 0.f ? -INFINITY : (M + log2f(den)) / kLog2e; }
+HS2_DEVI float chunk_factor(float num, float den) { return den == 0.f ? 0.f : num / den; }
+
 // Partial slots: a CTA leaves at most two, that of its first and that of its last unit.
 HS2_DEVI int part_slot(const ChunkUnit& u, int per, int cta) {
   const int c0 = u.prefix / per;

@@ -367,8 +367,8 @@ __global__ void __launch_bounds__(kWThreads, 1)
       auto finish = [&](float M, float L, float& f) {  // the output's factor; the row's lse
         const float M2 = fmaxf(M, b2), sc = exp2_rel(M, M2);
         const float den = L * sc + exp2_rel(b2, M2);
-        f = den > 0.f ? sc / den : 0.f;
-        if (a.lse && live) a.lse[row] = den > 0.f ? (M2 + log2f(den)) / kLog2e : -INFINITY;
+        f = chunk_factor(sc, den);
+        if (a.lse && live) a.lse[row] = chunk_lse(den, M2);
       };
       if (whole) {
         float f;

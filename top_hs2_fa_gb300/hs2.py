@@ -9,6 +9,7 @@ cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 
@@ -149,16 +150,30 @@ def _stream(stream) -> int:
 _data_ptr = torch.Tensor.data_ptr
 
 
+_shape = operator.attrgetter("shape")
+
+
 class _Handle:
     """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
-    and a tensor whose storage has moved makes a new one."""
+    and a tensor whose storage has moved or whose shape has changed makes a new one."""
 
-    _c = None  # (struct, device, tensors it was made from, their pointers)
+    _c = None  # (struct, device, tensors it was made from, their pointers, their shapes)
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
         if name != "_c":
             object.__setattr__(self, "_c", None)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
+
+    def _cached(self):
+        got = self._c
+        if got is None or got[3] != tuple(map(_data_ptr, got[2])) or got[4] != tuple(map(_shape, got[2])):
+            ts = self._tensors()
+            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)), tuple(map(_shape, ts)))
+            object.__setattr__(self, "_c", got)
+        return got
 
 
 @dataclass
@@ -174,18 +189,14 @@ class KV(_Handle):
     k_sf: torch.Tensor | None = None  # FP4: uint8 E4M3 [num_pages][Hkv][64][d/16]
     v_sf: torch.Tensor | None = None
 
-    def c(self) -> hs2_kv:
-        return self._cached()[0]
-
-    def _cached(self):
-        got = self._c
-        if got is None or got[3] != tuple(map(_data_ptr, got[2])):
-            ts = tuple(t for t in _kv_tensors(self) if t is not None)
-            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)))
-            object.__setattr__(self, "_c", got)
-        return got
+    def _tensors(self):
+        return tuple(t for t in (self.k, self.v, self.block_table, self.seq_len, self.k_scale, self.v_scale,
+                                 self.k_sf, self.v_sf) if t is not None)
 
     def _make(self) -> hs2_kv:
+        return self.c()
+
+    def c(self) -> hs2_kv:
         d = int(self.k.shape[3])
         if self.k.dtype == torch.uint8 and self.k_sf is not None:
             dt, d = FP4_E2M1, 2 * d
@@ -416,10 +427,6 @@ def hs2_selftest_wait_timeout(timeout_us: int, dev_err: torch.Tensor, stream=Non
 _ROW_DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 
-def _kv_tensors(kv: KV):
-    return kv.k, kv.v, kv.block_table, kv.seq_len, kv.k_scale, kv.v_scale, kv.k_sf, kv.v_sf
-
-
 def _i32(t: torch.Tensor, name: str, *shape) -> None:
     """t is an int32 contiguous tensor of that shape, or an error."""
     if t.dtype is not torch.int32 or t.shape != shape or not t.is_contiguous():
@@ -453,16 +460,25 @@ def _launch_stream(stream, dev: int, *tensors) -> int:
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """A workspace of this call's own; it stays alive until `stream` is done with it."""
-    t = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that a call on `stream` may write: memory of that stream's own, which what is
+    still running on the current stream does not use, kept until the current stream is done
+    with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
     return t
 
 
+def _scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """A workspace of this call's own."""
+    return _new(max(nbytes, 256), torch.uint8, device, stream)
+
+
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
-    c, dev, _, _ = kv._cached()
+    c, dev = kv._cached()[:2]
     shape, stride, dtype = k_rows.shape, k_rows.stride(), k_rows.dtype
     n = shape[0]
     if dtype not in _ROW_DTYPES or shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
@@ -493,8 +509,8 @@ def hs2_kv_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype
     every sequence are left as they are in ``out``."""
     if out is None:
         c = kv.c()
-        k = torch.empty((n_rows, c.Hkv, c.d), dtype=dtype, device=kv.k.device)
-        out = (k, None if kv.v is None else torch.empty_like(k))
+        k, v = (_new((n_rows, c.Hkv, c.d), dtype, kv.k.device, stream) if t is not None else None for t in (kv.k, kv.v))
+        out = (k, v)
     elif out[0].shape[0] != n_rows or out[0].dtype != dtype:
         raise HS2Error("out must hold n_rows rows of the dtype")
     _kv_rows(load().hs2_kv_read, kv, out[0], out[1], row_start, dev_err, stream)
@@ -516,7 +532,7 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
     many keys; ``sink``: float32 [Hq] logits of one more key with a zero value. ``o_dtype``
     float32 or bfloat16; lse is float32 [n_rows][Hq]."""
     lib = load()
-    c, dev, _, _ = kv._cached()
+    c, dev = kv._cached()[:2]
     n, Hq, d = q.shape
     if max_t is None:
         max_t = c.max_pages * c.page_size
@@ -528,8 +544,8 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
         raise HS2Error("o_dtype must be float32 or bfloat16")
     _i32(row_start, "row_start", c.batch + 1)
     if out is None:
-        o = torch.empty((n, Hq, d), dtype=o_dtype, device=q.device)
-        lse = torch.empty((n, Hq), dtype=torch.float32, device=q.device)
+        o = _new((n, Hq, d), o_dtype, q.device, stream)
+        lse = _new((n, Hq), torch.float32, q.device, stream)
     else:
         o, lse = out
         if o.dtype is not o_dtype or o.shape != (n, Hq, d) or not o.is_contiguous() or (
@@ -561,20 +577,17 @@ class Pages(_Handle):
                    free_list=torch.arange(num_pages - 1, -1, -1, dtype=torch.int32, device=device),
                    n_free=torch.full((1,), num_pages, dtype=torch.int32, device=device))
 
-    def c(self) -> hs2_pages:
-        return self._cached()[0]
+    def _tensors(self):
+        return self.ref, self.free_list, self.n_free
 
-    def _cached(self):
-        got = self._c
-        if got is None or got[3] != tuple(map(_data_ptr, got[2])):
-            n = int(self.ref.shape[0])
-            for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
-                _i32(t, name, size)
-            ts = (self.ref, self.free_list, self.n_free)
-            ptrs = tuple(map(_data_ptr, ts))
-            got = (hs2_pages(*ptrs, n), _device_of(ts), ts, ptrs)
-            object.__setattr__(self, "_c", got)
-        return got
+    def _make(self) -> hs2_pages:
+        return self.c()
+
+    def c(self) -> hs2_pages:
+        n = int(self.ref.shape[0])
+        for t, name, size in ((self.ref, "ref", n), (self.free_list, "free_list", n), (self.n_free, "n_free", 1)):
+            _i32(t, name, size)
+        return hs2_pages(self.ref.data_ptr(), self.free_list.data_ptr(), self.n_free.data_ptr(), n)
 
 
 def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tensor, n_new: torch.Tensor, dev_err=None,
@@ -583,7 +596,7 @@ def hs2_pages_grow(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(n_new, "n_new", b)
-    c, dev, _, _ = pages._cached()
+    c, dev = pages._cached()[:2]
     st = _launch_stream(stream, dev, block_table, seq_len, n_new, dev_err)
     _check(load().hs2_pages_grow(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  n_new.data_ptr(), b, mp, _ptr(dev_err), st))
@@ -596,7 +609,7 @@ def hs2_pages_free(pages: Pages, block_table: torch.Tensor, seq_len: torch.Tenso
     b, mp = _table(block_table, "block_table")
     _i32(seq_len, "seq_len", b)
     _i32(drop, "drop", b)
-    c, dev, _, _ = pages._cached()
+    c, dev = pages._cached()[:2]
     st = _launch_stream(stream, dev, block_table, seq_len, drop, dev_err)
     _check(load().hs2_pages_free(ctypes.byref(c), block_table.data_ptr(), seq_len.data_ptr(),
                                  drop.data_ptr(), b, mp, _ptr(dev_err), st))
@@ -616,13 +629,12 @@ def hs2_pages_fork(pages: Pages, kvs, src: torch.Tensor, out=None, dev_err=None,
     """Branches of the caches' sequences: branch c continues sequence src[c] (-1: none), with
     its full pages shared and the last, partly filled one copied. ``kvs``: the caches of one
     block table. Returns (child_table, child_len)."""
-    c, dev, _, _ = pages._cached()
+    c, dev = pages._cached()[:2]
     cs = _kv_array(kvs, dev)
     n, mp = src.numel(), kvs[0].block_table.shape[1]
     _i32(src, "src", n)
     if out is None:
-        out = (torch.empty((n, mp), dtype=torch.int32, device=src.device),
-               torch.empty((n,), dtype=torch.int32, device=src.device))
+        out = _new((n, mp), torch.int32, src.device, stream), _new((n,), torch.int32, src.device, stream)
     else:
         _i32(out[0], "child_table", n, mp)
         _i32(out[1], "child_len", n)
@@ -639,7 +651,7 @@ def hs2_pages_compact_workspace(pages: Pages) -> int:
 def hs2_pages_compact(pages: Pages, kvs, workspace=None, dev_err=None, stream=None) -> None:
     """The pool's referenced pages to its front, in place in every cache of ``kvs`` (which
     share one block table holding every sequence), with tables and books updated."""
-    c, dev, _, _ = pages._cached()
+    c, dev = pages._cached()[:2]
     cs = _kv_array(kvs, dev)
     st = _launch_stream(stream, dev, workspace, dev_err)
     ws = workspace if workspace is not None else _scratch(hs2_pages_compact_workspace(pages), pages.ref.device, stream)
