@@ -61,6 +61,13 @@ HS2_DEVI float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// A whole 32-byte sector from one thread (halves of sectors took 3 to 12 % longer where units are
+// cut, e.g. 49 against 43 us for 512 tokens over 2048 keys).
+HS2_DEVI void store8(float* p, const float* x) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
 template <int R>
 HS2_DEVI void wide_regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 template <int R>
@@ -383,14 +390,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
       } else {
         const size_t at_p = (size_t)part_slot(u, per, blockIdx.x) * 2 * kWRows + h * kWRows + r;
         reinterpret_cast<float2*>(p.part_ml)[at_p] = make_float2(m_used, l);
-        float4* po = reinterpret_cast<float4*>(p.part_o + at_p * D);
+        float* po = p.part_o + at_p * D;
 #pragma unroll 1
         for (int k = 0; k < D / 32; ++k) {
           float ov[32];
           tc::tmem_ld32(o + k * 32, ov);
           if (live)
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) po[k * 8 + e / 4] = make_float4(ov[e], ov[e + 1], ov[e + 2], ov[e + 3]);
+            for (int e = 0; e < 32; e += 8) store8(po + k * 32 + e, ov + e);
         }
         tc::tc_fence_before();
       }
