@@ -34,7 +34,8 @@
  *   into (HS2_DEV_*) when they meet an out-of-range block-table entry or index,
  *   or give up a bounded wait. Bad accesses are skipped, never performed. The
  *   caller zeroes it and reads it after synchronising.
- * - Outputs are float32 whatever the input dtype (fp32 accumulation).
+ * - Outputs are float32 whatever the input dtype (fp32 accumulation); hs2_fa_chunk and
+ *   hs2_kv_read take the output type as an argument.
  * - Index sets are written sorted ascending, padded with -1, with a count array.
  *   Among equal scores the lower position (or lower block id) wins.
  */
@@ -85,8 +86,9 @@ typedef enum { HS2_F32 = 0, HS2_BF16 = 1, HS2_FP8_E4M3 = 2, HS2_FP4_E2M1 = 3 } h
  *              [page_size][d/2] bytes, channel 2i in the low nibble of byte i (E2M1: sign,
  *              2 exponent bits with bias 1, 1 mantissa bit); channel c of a row stands for
  *              e2m1(code) * e4m3(sf[c / 16]) * scale[p][g].
- *              FP8 and FP4 caches are read by hs2_fa_select (decode) and hs2_sa_reuse
- *              (decode); queries are bf16; prefill and the KV append refuse them.
+ *              FP8 and FP4 caches are written and read back by hs2_kv_write / hs2_kv_read,
+ *              and read by hs2_fa_select (decode), hs2_sa_reuse (decode) and hs2_fa_chunk;
+ *              queries are bf16; the prefill selection and the KV append refuse them.
  * page_size must be 64; d must be 64 or 128.                                        */
 typedef struct {
   const void* k;
@@ -153,7 +155,7 @@ hs2_status hs2_fa_select_ex(const void* q, int B_or_n, int Hq, const hs2_kv* kv,
  *   K row t-1 of KV head g  <-  k_new[c][b][g][:]   (and V likewise from v_new[c]),
  * i.e. slot (t-1) % 64 of page block_table[b][(t-1) / 64]. One launch for all caches.
  * kvs: host array of n_caches descriptors (1 <= n_caches <= 8), bf16 or f32 pools; an FP8
- *   pool returns HS2_ERR_UNSUPPORTED (its per-page scale would have to change). A key-only
+ *   or FP4 pool returns HS2_ERR_UNSUPPORTED (hs2_kv_write quantises). A key-only
  *   cache (v = NULL, e.g. a CSA2 indexer-key cache) takes k_new only.
  * k_new, v_new: host arrays of n_caches device pointers, each [batch][Hkv][d] in the
  *   cache's dtype, 16-byte aligned; v_new may be NULL when every cache is key-only.
@@ -318,8 +320,12 @@ hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype r
  * (a descending row_start: none or only some rows are).
  * A V row that is not finite makes the rows of a chunk undefined that see any key of its
  * 128-key tile, as a weight of zero does not cancel it; values behind seq_len do not matter.
- * workspace: at least hs2_fa_chunk_workspace(...) bytes, 256-byte aligned, contents ignored;
- * calls that run at the same time need workspaces of their own.                         */
+ * A K row or query that is not finite gives NaN in the rows that see it.
+ * workspace: at least hs2_fa_chunk_workspace(...) bytes of the same arguments, 256-byte
+ * aligned, contents ignored; calls that run at the same time need workspaces of their own.
+ * Calls of many rows over an FP8 / FP4 cache keep bf16 copies of the pages there: up to
+ * batch * min(max_t, max_n + w) * Hkv * d * 4 bytes (w = 0: batch * max_t ...), so max_n and
+ * max_t are best kept close to what the batch holds.                                     */
 size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w);
 hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
                         int max_t, int w, float scale, const float* sink, void* o, hs2_dtype o_dtype, float* lse,

@@ -5,7 +5,8 @@
 //
 // A kernel of its own: where one sequence is spread over all CTAs a unit has 152 parts, which the
 // last CTA to arrive took 45 us to join by itself, and no counters need clearing. Bound by
-// latency: a handful of dependent loads, then the parts of all rows at once.
+// latency: a handful of dependent loads, then the parts of all rows at once. 152 cut units of 256
+// rows (40 MB of parts) take about 12 us, 152 of 64 rows about 7.
 #include "chunk_plan.cuh"
 
 namespace hs2 {

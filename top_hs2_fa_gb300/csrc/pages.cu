@@ -9,6 +9,9 @@
 // is one or two short launches with few dependent rounds of loads, and every launch overlaps
 // the end of the one before it (programmatic dependent launch). Only the copies (a forked
 // sequence's partial page, the pages that compaction moves) are bandwidth.
+// Measured: fork, grow and free of 64 branches of 16 sequences (4K to 16K keys, two caches) 35 us together,
+// of 8 branches 16.5; compaction that moves half of what is left of 64 sequences (540 MB read and
+// written) 101 us, 0.80 of the copy bandwidth.
 #include <cooperative_groups.h>
 
 #include "block_scan.cuh"
