@@ -9,7 +9,6 @@ cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
-import operator
 import os
 from dataclasses import dataclass
 
@@ -147,17 +146,14 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
-_data_ptr = torch.Tensor.data_ptr
-
-
-_shape = operator.attrgetter("shape")
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
 
 
 class _Handle:
     """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
-    and a tensor whose storage has moved or whose shape has changed makes a new one."""
+    and a tensor whose storage has moved or whose size has changed makes a new one."""
 
-    _c = None  # (struct, device, tensors it was made from, their pointers, their shapes)
+    _c = None  # (struct, device, tensors it was made from, their pointers, the first three's sizes)
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -169,9 +165,9 @@ class _Handle:
 
     def _cached(self):
         got = self._c
-        if got is None or got[3] != tuple(map(_data_ptr, got[2])) or got[4] != tuple(map(_shape, got[2])):
+        if got is None or got[3] != tuple(map(_data_ptr, got[2])) or got[4] != tuple(map(_numel, got[2][:3])):
             ts = self._tensors()
-            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)), tuple(map(_shape, ts)))
+            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)), tuple(map(_numel, ts[:3])))
             object.__setattr__(self, "_c", got)
         return got
 
@@ -190,7 +186,7 @@ class KV(_Handle):
     v_sf: torch.Tensor | None = None
 
     def _tensors(self):
-        return tuple(t for t in (self.k, self.v, self.block_table, self.seq_len, self.k_scale, self.v_scale,
+        return tuple(t for t in (self.k, self.block_table, self.seq_len, self.v, self.k_scale, self.v_scale,
                                  self.k_sf, self.v_sf) if t is not None)
 
     def _make(self) -> hs2_kv:
