@@ -8,17 +8,16 @@
 // with 6 s S >= A, code_j the E2M1 value nearest to x_j / (s S), ties to the even code, as exact
 // arithmetic has it. q = x * (1 / (s S)) in fp32 is within 4 units in the last place of the
 // quotient, so rounding q gives that code unless a border between codes (0.25 .. 5, numbers of at most
-// 3 significant bits) lies within them; such a q has the low 18 bits of its mantissa near
-// zero (near_short), which one value in 16000 has by chance. A thread that meets one computes
-// its 16 codes by comparison: code_j counts the borders b s S that |x_j| reaches, and a float
-// x reaches the real number b s S exactly when it reaches a float computed from it
-// (reach_float). A product a S with a of at most 7 bits is p + e, p = fl(a S), e =
-// fma(a, S, -p), exactly, for S in [2^-60, 2^60]. FP8 likewise, the borders of E4M3 having at
-// most 5 bits; its exact way is quotient_to_odd.
+// 3 significant bits) lies within them; such a q has the low bits of its mantissa near zero
+// (low_bits), which one value in 10^5 has by chance, and many have where rows and scales are short
+// numbers. A thread that meets one rounds its quotients to odd by their exact remainders, which
+// keeps what the rounding to a code has to see (quotients). FP8 likewise, the borders of E4M3
+// having at most 5 bits. S in [2^-60, 2^60] keeps all products away from under- and overflow.
 //
-// Bound by the rows' bytes; the instructions per value decide how near it comes. 32768 rows of
-// 2 x 4 x 128 bf16 values to FP4 (86 MB) take 27 us; comparing every value against the borders
-// took 46. Their way back to floats (153 MB) takes 29 us.
+// Bound by the instructions per value, mostly the integer pipe's; the rows' bytes come next. 32768
+// rows of 2 x 4 x 128 bf16 values to FP4 (86 MB) take 26 us with slab scales of many bits and
+// 39 with a power of two, where nearly every group meets a border (comparing every value against the
+// borders took 46). Their way back to floats (153 MB) takes 29 us.
 #include <cuda_fp16.h>
 
 #include "common.cuh"
@@ -43,12 +42,6 @@ HS2_DEVI uint32_t e4m3_codes(float a, float b) {
   return r;
 }
 
-// The smallest float that is >= the real number a * S (tie) or > it (not tie).
-HS2_DEVI float reach_float(float a, float S, bool tie) {
-  const float p = a * S, e = fmaf(a, S, -p);
-  return (e < 0.f || (e == 0.f && tie)) ? p : __uint_as_float(__float_as_uint(p) + 1);
-}
-
 // The smallest E4M3 code whose value s has 6 s S >= A (A finite or inf); 126 (448) where none has.
 HS2_DEVI uint32_t group_scale(float A, float S) {
   // the nearest code to about A / (6 S) is the one sought or the one before it
@@ -58,26 +51,37 @@ HS2_DEVI uint32_t group_scale(float A, float S) {
   return c + (short_of && c < 126u);
 }
 
-// x / S to E4M3 in exact arithmetic: the quotient rounded to odd (its last bit set where the
-// quotient is not exact) keeps what the second rounding, to 4 bits, needs to see.
-HS2_DEVI float quotient_to_odd(float x, float S, float inv) {
-  float q = x * inv;
-  if (!(fabsf(q) < 1024.f)) return q;  // saturates, or NaN
-  q = copysignf(fmaf(fmaf(-q, S, x), inv, q), x);
-  const float rest = fmaf(-q, S, x);
-  const uint32_t u = __float_as_uint(q);
-  if (rest != 0.f && !(u & 1u)) {
-    const bool away = (rest > 0.f) == !(u >> 31);  // the true magnitude is larger
-    if (away) return __uint_as_float(u + 1);
-    return (u & 0x7FFFFFFFu) ? __uint_as_float(u - 1) : q;
-  }
-  return q;
-}
-
-// Whether the low 18 bits of q's mantissa are within 8 units of zero: q is near a number of at
-// most 5 significant bits.
-HS2_DEVI uint32_t low_bits(float q) { return (__float_as_uint(q) + 8u) & 0x3FFFFu; }
+// Whether a quotient q is within 8 units in its last place of a number of so few significant bits
+// (a border between codes) is low_bits(q) < kNear.
+template <int BITS>
+HS2_DEVI uint32_t low_bits(float q) { return (__float_as_uint(q) + 8u) & ((1u << (24 - BITS)) - 1u); }
 constexpr uint32_t kNear = 16;
+
+// q[j]: what rounds to the code of x[j] / (d + e), where d + e is exact, |e| at most half a unit of
+// d, inv about 1 / d, and the borders between codes have BITS significant bits. The corrected
+// quotient is within a unit, and its remainder exact in sign (a multiple of 2^-126 where the
+// quotient is 2^-11 or more; smaller ones have code 0 anyway): a quotient that is not exact
+// moves to the odd neighbour on its side, so that it is no border and lies on the same side of
+// each as the true one.
+template <int BITS>
+HS2_DEVI void quotients(const float (&x)[16], float inv, float d, float e, float (&q)[16]) {
+  uint32_t low = kNear;
+#pragma unroll
+  for (int j = 0; j < 16; j += 2) {
+    q[j] = x[j] * inv, q[j + 1] = x[j + 1] * inv;
+    low = __vimin3_u32(low, low_bits<BITS>(q[j]), low_bits<BITS>(q[j + 1]));
+  }
+  if (low >= kNear) return;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    if (!(fabsf(q[j]) < 1024.f)) continue;  // saturates, or NaN
+    q[j] = copysignf(fmaf(fmaf(-q[j], e, fmaf(-q[j], d, x[j])), inv, q[j]), x[j]);  // (the sign of zeros)
+    const float rest = fmaf(-q[j], e, fmaf(-q[j], d, x[j]));
+    const uint32_t u = __float_as_uint(q[j]), some = rest != 0.f;
+    const uint32_t toward = ((u ^ __float_as_uint(rest)) >> 31) & some;  // the true quotient is smaller
+    q[j] = __uint_as_float((u - toward) | some);
+  }
+}
 
 HS2_DEVI float max_nan3(float a, float b, float c) {
   float r;
@@ -85,10 +89,13 @@ HS2_DEVI float max_nan3(float a, float b, float c) {
   return r;
 }
 
-// two floats to E2M1 codes, nearest even, saturating; a in the low nibble
-HS2_DEVI uint32_t e2m1_codes(float a, float b) {
+// eight floats to E2M1 codes, nearest even, saturating; x[0] in the low nibble
+HS2_DEVI uint32_t e2m1_codes(const float* x) {
   uint32_t r;
-  asm("{.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tcvt.u32.u8 %0, c;}" : "=r"(r) : "f"(b), "f"(a));
+  asm("{.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};}"
+      : "=r"(r)
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 
@@ -137,16 +144,7 @@ HS2_DEVI void put16(const RowsArgs& a, int side, size_t slab, size_t line, int g
     if constexpr (FMT == HS2_FP8_E4M3) {
       const float inv = 1.f / S;
       float q[16];
-      uint32_t low = kNear;
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        q[j] = x[j] * inv, q[j + 1] = x[j + 1] * inv;
-        low = __vimin3_u32(low, low_bits(q[j]), low_bits(q[j + 1]));
-      }
-      if (low < kNear) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) q[j] = quotient_to_odd(x[j], S, inv);
-      }
+      quotients<5>(x, inv, S, 0.f, q);
       uint32_t w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = e4m3_codes(q[4 * i], q[4 * i + 1]) | (e4m3_codes(q[4 * i + 2], q[4 * i + 3]) << 16);
@@ -159,35 +157,10 @@ HS2_DEVI void put16(const RowsArgs& a, int side, size_t slab, size_t line, int g
       const bool nan = top != top;
       const uint32_t s = nan ? 0x7Fu : group_scale(top, S);
       const float sv = nan ? 0.f : e4m3_value(s);
-      uint32_t w[2] = {0u, 0u};
-      const float inv = sv > 0.f ? 1.f / (sv * S) : 0.f;
+      const float d = sv * S, inv = sv > 0.f ? 1.f / d : 0.f;
       float q[16];
-      uint32_t low = kNear;
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        q[j] = x[j] * inv, q[j + 1] = x[j + 1] * inv;
-        low = __vimin3_u32(low, low_bits(q[j]), low_bits(q[j + 1]));
-      }
-      if (low >= kNear) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) w[j >> 3] |= e2m1_codes(q[j], q[j + 1]) << (4 * (j & 7));
-      } else {
-        const float t0 = reach_float(0.25f * sv, S, false), t1 = reach_float(0.75f * sv, S, true),
-                    t2 = reach_float(1.25f * sv, S, false), t3 = reach_float(1.75f * sv, S, true),
-                    t4 = reach_float(2.5f * sv, S, false), t5 = reach_float(3.5f * sv, S, true),
-                    t6 = reach_float(5.f * sv, S, false);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float m = fabsf(x[j]);
-          const bool b2 = m >= t3;
-          const bool b1 = m >= (b2 ? t5 : t1);
-          const bool b0 = m >= (b2 ? (b1 ? t6 : t4) : (b1 ? t2 : t0));
-          uint32_t c = (b2 ? 4u : 0u) | (b1 ? 2u : 0u) | (b0 ? 1u : 0u);
-          if (sv == 0.f) c = 0u;  // an all-zero group (or a NaN's)
-          c |= (__float_as_uint(x[j]) >> 28) & 8u;
-          w[j >> 3] |= c << (4 * (j & 7));
-        }
-      }
+      quotients<3>(x, inv, d, fmaf(sv, S, -d), q);
+      const uint32_t w[2] = {e2m1_codes(q), e2m1_codes(q + 8)};
       *reinterpret_cast<uint2*>(pool + line * (D / 2) + 8 * grp) = make_uint2(w[0], w[1]);
       (side ? a.v_sf : a.k_sf)[line * GPR + grp] = (uint8_t)s;
     }
@@ -306,7 +279,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_read_kernel(const RowsArgs a) 
 }
 
 // From so many rows times heads on a thread finds a row's place once for K and V: 32768 rows of
-// 4 heads written and read back 60 us with a thread a side and 56 with both, 4096 rows 13.5 and
+// 4 heads written and read back 60 us with a thread a side and 55 with both, 4096 rows 13.5 and
 // 12.5; below, more threads hide more of the latency: 1024 rows 8.4 and 10.3.
 constexpr long long kTwoSides = 8192;
 

@@ -6,6 +6,8 @@ A self-contained driver for ``ncu -k regex:<kernel>`` captures of one workload s
            ``--kv-fp8``: the KV stored as FP8 E4M3)
   prefill  causal FA + per-row selection, then SA layers over ``--n`` rows
   csa2     Full indexer + SA, Reindex indexer + SA (``--batch`` sequences of ``--t`` keys)
+  chunk    pages for ``--batch`` sequences of t-lo .. t-hi keys, their rows written to a
+           ``--kv`` cache, attention of the last ``--tokens`` of each
 
 e.g. ``python -m top_hs2_fa_gb300.profile_case --mode prefill --n 8192 --steps 1``.
 """
@@ -76,9 +78,34 @@ def run_csa2(a) -> float:
     return float(o.abs().mean())
 
 
+def run_chunk(a) -> float:
+    Hq, Hkv, d, B = 32, 4, 128, a.batch
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    lens = np.linspace(a.t_lo, a.t_hi, B).round().astype(np.int32)
+    pages = int((-(-lens // 64)).sum())
+    shape = (pages, Hkv, 64)
+    dt, width = (torch.bfloat16, d) if a.kv == "bf16" else (torch.uint8, d if a.kv == "fp8" else d // 2)
+    new = lambda w, dtype=torch.uint8: torch.zeros((*shape, w), dtype=dtype, device="cuda")  # noqa: E731
+    scale = lambda: None if a.kv == "bf16" else torch.full((pages, Hkv), 1 / 16, device="cuda")  # noqa: E731
+    sf = lambda: new(d // 16) if a.kv == "fp4" else None  # noqa: E731
+    kv = hs2.KV(k=new(width, dt), v=new(width, dt), block_table=torch.full((B, -(-int(lens.max()) // 64)), -1,
+                                                                           dtype=torch.int32, device="cuda"),
+                seq_len=torch.zeros(B, dtype=torch.int32, device="cuda"), k_scale=scale(), v_scale=scale(),
+                k_sf=sf(), v_sf=sf())
+    hs2.hs2_pages_grow(hs2.Pages.make(pages), kv.block_table, kv.seq_len, up(lens))
+    starts = up(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    rows = [torch.randn((int(lens.sum()), Hkv, d), generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(2)]
+    hs2.hs2_kv_write(kv, *rows, starts)
+    q = torch.randn((B * a.tokens, Hq, d), generator=gen, device="cuda", dtype=torch.bfloat16)
+    starts = torch.arange(0, B * a.tokens + 1, a.tokens, dtype=torch.int32, device="cuda")
+    for _ in range(a.steps):
+        o, lse = hs2.hs2_fa_chunk(q, starts, kv, d ** -0.5, a.tokens, max_t=int(lens.max()))
+    return float(o.abs().mean())
+
+
 def main() -> None:
     ap = argparse.ArgumentParser()
-    ap.add_argument("--mode", choices=("decode", "prefill", "csa2"), default="decode")
+    ap.add_argument("--mode", choices=("decode", "prefill", "csa2", "chunk"), default="decode")
     ap.add_argument("--batch", type=int, default=8)
     ap.add_argument("--t-lo", type=int, default=16384)
     ap.add_argument("--t-hi", type=int, default=32768)
@@ -86,10 +113,12 @@ def main() -> None:
     ap.add_argument("--t", type=int, default=131072, help="csa2 keys per sequence")
     ap.add_argument("--steps", type=int, default=3)
     ap.add_argument("--sa-layers", type=int, default=5)
+    ap.add_argument("--tokens", type=int, default=4, help="chunk: query tokens of a sequence")
+    ap.add_argument("--kv", choices=("bf16", "fp8", "fp4"), default="fp4", help="chunk: the cache's type")
     ap.add_argument("--kv-fp8", action="store_true", help="decode: FP8 E4M3 paged KV")
     a = ap.parse_args()
     build.build()
-    v = {"decode": run_decode, "prefill": run_prefill, "csa2": run_csa2}[a.mode](a)
+    v = {"decode": run_decode, "prefill": run_prefill, "csa2": run_csa2, "chunk": run_chunk}[a.mode](a)
     torch.cuda.synchronize()
     print("ok", v)
 
