@@ -92,7 +92,7 @@ struct ChunkLayout {
   int n_plans;
   hs2::ChunkPlan plan[2];  // narrow, wide, or both; pointers after bind()
   bool narrow[2];
-  size_t off[2][6], off_exp[4];
+  size_t off[2][7], off_exp[4];
   int exp_seqs, exp_pages_seq;
   size_t off_ek, off_ev, off_params, total;
   long long tiles;  // an upper bound of a plan's tiles
@@ -125,6 +125,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       o[0] = take(16);
       o[1] = take(4 * (size_t)p.ctas);
       o[2] = take(4 * (size_t)p.ctas);
+      o[6] = take(4 * (size_t)p.ctas);
       o[3] = take(48 * (size_t)p.max_units);
       o[4] = take(2 * (size_t)p.ctas * tile_rows * 8);
       o[5] = take(2 * (size_t)p.ctas * tile_rows * kv->d * 4);
@@ -163,6 +164,7 @@ void bind(ChunkLayout& L, char* ws) {
     p.head = (int32_t*)(ws + L.off[i][0]);
     p.cta_first = (int32_t*)(ws + L.off[i][1]);
     p.cuts = (int32_t*)(ws + L.off[i][2]);
+    p.cta_begin = (int32_t*)(ws + L.off[i][6]);
     p.units = (int32_t*)(ws + L.off[i][3]);
     p.part_ml = (float*)(ws + L.off[i][4]);
     p.part_o = (float*)(ws + L.off[i][5]);

@@ -25,14 +25,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   griddep_wait();
   const ChunkPlan& p = blockIdx.x ? p1 : p0;
   __shared__ int sums[33], ubase[kPlanThreads + 1], s_row[kPlanThreads], s_n[kPlanThreads], s_t[kPlanThreads],
-      s_exp[kPlanThreads], n_cuts;
+      s_exp[kPlanThreads], n_cuts, longest;
   const int tok = p.tile_rows / a.G;
   int total_tiles = 0, units = 0, exp_pages = 0, n_exp = 0;
   int my_tiles = 0, my_prefix = 0;  // of the last unit this thread wrote
+  if (threadIdx.x == 0) n_cuts = longest = 0;
   // rows of two sequences at once would overrun what the host sized for n_rows rows
   bool descends = false;
   for (int b = threadIdx.x; b < a.batch; b += kPlanThreads) descends |= a.row_start[b + 1] < a.row_start[b];
   if (__syncthreads_or(descends)) {
+    for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) p.cta_begin[c] = 0;
     if (threadIdx.x == 0) {
       flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
       p.head[0] = p.head[2] = 0;
@@ -106,6 +108,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         cost = x.ntiles;
       }
       int tiles;
+      const int top = __reduce_max_sync(0xffffffffu, cost);
+      if ((threadIdx.x & 31) == 0 && top > 0) atomicMax(&longest, top);
       x.prefix = total_tiles + block_prefix(cost, sums, tiles);
       total_tiles += tiles;
       my_tiles = cost, my_prefix = x.prefix;
@@ -119,14 +123,20 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     __syncthreads();  // the chunk's arrays are rewritten
   }
   const int per = max(p.min_tiles, (total_tiles + p.ctas - 1) / p.ctas);
-  // the unit at each CTA's range start, and the list of units that a range border cuts (in any
-  // order: the merge treats each by itself)
+  __syncthreads();  // the records are visible to the block
+  const bool snap = 2 * longest <= per;
+  // each CTA's range start and the unit there, and the list of units that a range border cuts (in
+  // any order: the merge treats each by itself)
   auto place = [&](int u, int ntiles, int prefix) {
-    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) p.cta_first[c] = u;
-    if (prefix / per != (prefix + ntiles - 1) / per) p.cuts[atomicAdd(&n_cuts, 1)] = u;
+    for (int c = (prefix + per - 1) / per; c < p.ctas && (long long)c * per < prefix + ntiles; ++c) {
+      const bool next = snap && 2 * (c * per - prefix) > ntiles;
+      p.cta_first[c] = u + next;
+      p.cta_begin[c] = next ? prefix + ntiles : snap ? prefix : c * per;
+    }
+    if (!snap && prefix / per != (prefix + ntiles - 1) / per) p.cuts[atomicAdd(&n_cuts, 1)] = u;
   };
-  if (threadIdx.x == 0) n_cuts = 0;
-  __syncthreads();  // also: the records are visible to the block
+  for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads)
+    if ((long long)c * per >= total_tiles) p.cta_begin[c] = total_tiles;
   if (a.batch <= kPlanThreads && units <= kPlanThreads) {  // they are in registers
     if ((int)threadIdx.x < units) place(threadIdx.x, my_tiles, my_prefix);
   } else {

@@ -5,7 +5,8 @@
 // the 128-key tiles (two pages) that its rows see. The tiles of all units, one after another,
 // are a line of `total` tiles that the CTAs of a persistent kernel share out in equal ranges,
 // so lengths and batch sizes do not matter to the balance; a unit cut by a range border leaves
-// partial results, which a last kernel merges in CTA order (chunk_merge.cu).
+// partial results, which a last kernel merges in CTA order (chunk_merge.cu). Where every unit is
+// short against a range (a sliding window), the borders move to the nearest unit's and cut none.
 #pragma once
 #include "common.cuh"
 #include "kernels.h"
@@ -25,9 +26,10 @@ struct ChunkRange {
 
 HS2_DEVI ChunkRange chunk_range(const ChunkPlan& p, int cta) {
   ChunkRange r;
-  const int total = p.head[0], per = p.head[1], first = p.cta_first[cta];  // one round of loads
-  r.begin = min(total, cta * per);
-  r.end = min(total, r.begin + per);
+  const int total = p.head[0], first = p.cta_first[cta], begin = p.cta_begin[cta];  // one round of loads
+  const int next = p.cta_begin[min(cta + 1, p.ctas - 1)];
+  r.begin = min(total, begin);
+  r.end = cta + 1 < p.ctas ? min(total, next) : total;
   r.first_unit = r.begin < r.end ? first : 0;
   return r;
 }

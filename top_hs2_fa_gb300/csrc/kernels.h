@@ -132,6 +132,7 @@ struct ChunkArgs {
 struct ChunkPlan {
   int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
+  int32_t* cta_begin;  // [ctas] the range start
   int32_t* cuts;       // [ctas] units that a range border cuts: one per border at most
   int32_t* units;      // [max_units] ChunkUnit
   int max_units, ctas;
