@@ -62,6 +62,9 @@ HS2_DEVI float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
+// Bits 0 .. n of a word (none for n < 0).
+HS2_DEVI uint32_t bits_upto(int n) { return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u; }
+
 // A whole 32-byte sector from one thread (halves of sectors took 3 to 12 % longer where units are
 // cut, e.g. 49 against 43 us for 512 tokens over 2048 keys).
 HS2_DEVI void store8(float* p, const float* x) {
@@ -288,8 +291,14 @@ __global__ void __launch_bounds__(kWThreads, 1)
         if (kb + 127 > pos_first || (a.w > 0 && kb <= pos_last - a.w) || par[0].x < 0.f || par[1].x < 0.f) {
           const int hi = pos - kb, lo = a.w > 0 ? hi - a.w : -1;
 #pragma unroll
-          for (int e = 0; e < 128; ++e)
-            if (e > hi || e <= lo || par[e >> 6].x < 0.f) x[e] = -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            // a bit per key, one test each (two comparisons each: 37 us against 33 for chunks of 333 to
+            // 1200 tokens with a window of 128, where every tile is masked)
+            const uint32_t seen = par[q >> 1].x < 0.f ? 0u : bits_upto(hi - 32 * q) & ~bits_upto(lo - 32 * q);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(seen & (1u << e))) x[32 * q + e] = -INFINITY;
+          }
         }
         // a page that is not there has no weights: any positive factor will do
         const float c0 = fabsf(par[0].x) * a.scale_log2, c1 = fabsf(par[1].x) * a.scale_log2;
