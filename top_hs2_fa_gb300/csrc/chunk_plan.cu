@@ -32,7 +32,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   if (threadIdx.x == 0) n_cuts = longest = 0;
   // rows of two sequences at once would overrun what the host sized for n_rows rows
   bool descends = false;
-  for (int b = threadIdx.x; b < a.batch; b += kPlanThreads) descends |= a.row_start[b + 1] < a.row_start[b];
+  int n = 0, t = 0, r0 = 0;  // this thread's sequence of the chunk
+  auto load = [&](int b) {
+    n = t = r0 = 0;
+    if (b >= a.batch) return;
+    r0 = a.row_start[b], t = a.seq_len[b];
+    const int r1 = a.row_start[b + 1];
+    descends |= r1 < r0;
+    n = r1 - r0;
+  };
+  for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) load(b0 + threadIdx.x);
   if (__syncthreads_or(descends)) {
     for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) p.cta_begin[c] = 0;
     if (threadIdx.x == 0) {
@@ -45,11 +54,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   }
   for (int b0 = 0; b0 < a.batch; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
-    int n = 0, t = 0, r0 = 0;
+    if (a.batch > kPlanThreads) load(b);
     if (b < a.batch) {
-      r0 = a.row_start[b];
-      n = a.row_start[b + 1] - r0;
-      t = a.seq_len[b];
       if (n != 0 && (r0 < 0 || n > a.max_n || t < n || t > a.max_t || r0 > a.n_rows - n)) {
         if (blockIdx.x == 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
         n = 0;
