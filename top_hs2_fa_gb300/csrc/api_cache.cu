@@ -110,14 +110,13 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
     const int G = Hq / kv->Hkv;
     const long long top = (long long)std::min(max_n, n_rows) * G;  // rows of the largest sequence
     const ChunkCuts cut = chunk_cuts(top, n_rows, Hq, kv, max_n, max_t, w);
-    auto add = [&](bool narrow, int tile_rows, int lo, int hi, int min_tiles) {
+    auto add = [&](bool narrow, int tile_rows, int lo, int hi) {
       hs2::ChunkPlan& p = L.plan[L.n_plans];
       L.narrow[L.n_plans] = narrow;
       p.ctas = sm_count();
       p.tile_rows = tile_rows;
       p.min_rows = lo;
       p.max_rows = hi;
-      p.min_tiles = min_tiles;
       const long long units = (long long)kv->Hkv * ((long long)n_rows * G / tile_rows + std::min(kv->batch, n_rows));
       p.max_units = (int)std::min<long long>(units, 1 << 30);
       L.tiles = std::max(L.tiles, units * (max_t / 128 + 2));
@@ -133,10 +132,10 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
     };
     if (cut.narrow > 0) {
       const long long few = std::min<long long>(top, cut.narrow);
-      add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut.narrow, 2);
+      add(true, few <= 16 ? 16 : few <= 32 ? 32 : 64, 0, cut.narrow);
     }
     if (cut.wide) {
-      hs2::ChunkPlan* p = add(false, 256, cut.narrow, 0x7fffffff, 4);
+      hs2::ChunkPlan* p = add(false, 256, cut.narrow, 0x7fffffff);
       p->expand = low_precision(kv);
       if (p->expand) {
         L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut.narrow + 1));
