@@ -321,8 +321,9 @@ hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype r
  * A V row that is not finite makes the rows of a chunk undefined that see any key of its
  * 128-key tile, as a weight of zero does not cancel it; values behind seq_len do not matter.
  * A K row or query that is not finite gives NaN in the rows that see it.
- * workspace: at least hs2_fa_chunk_workspace(...) bytes of the same arguments, 256-byte
- * aligned, contents ignored; calls that run at the same time need workspaces of their own.
+ * workspace: at least hs2_fa_chunk_workspace(...) bytes, 256-byte aligned, contents ignored;
+ * what it gives for some n_rows, max_n and max_t also suffices where any of them is smaller
+ * (same Hq, kv and w). Calls that run at the same time need workspaces of their own.
  * Calls of many rows over an FP8 / FP4 cache keep bf16 copies of the pages there: up to
  * batch * min(max_t, max_n + w) * Hkv * d * 4 bytes (w = 0: batch * max_t ...), so max_n and
  * max_t are best kept close to what the batch holds.                                     */

@@ -77,13 +77,14 @@ struct ChunkCuts {
 //   little to expand: 12 sequences of 32 to 22400 rows over 1K to 6K keys 132 wide, 161 both; 9 of up
 //     to 512 rows (110 MB expanded) 68 and 84; 16 of up to 800 rows and 16K keys (520 MB) 229 and
 //     212; 64 of up to 800 rows (8 GB) 2998 and 2191.
+constexpr long long kFewExpanded = 256LL << 20;
 ChunkCuts chunk_cuts(long long top, int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
   const int all = 0x7fffffff;
   const long long keys = w > 0 ? std::min<long long>(max_t, (long long)max_n + w) : max_t;
   if (kv->dtype == HS2_BF16) return top <= 64 ? ChunkCuts{all, false} : ChunkCuts{0, true};
   if (top <= 256 || (long long)n_rows * Hq * keys <= 1LL << 24) return {all, false};
   const long long expanded = kv->batch * keys * kv->Hkv * kv->d * 4;  // bytes, K and V
-  return {expanded <= 256LL << 20 ? 0 : 256, true};
+  return {expanded <= kFewExpanded ? 0 : 256, true};
 }
 
 // Workspace of hs2_fa_chunk: the plans of the two kernels with their parts, and the expanded
@@ -98,7 +99,14 @@ struct ChunkLayout {
   long long tiles;  // an upper bound of a plan's tiles
 };
 
-ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+// Most rows of a sequence, as the declared sizes have it.
+long long chunk_top(int n_rows, int Hq, const hs2_kv* kv, int max_n) {
+  return (long long)std::min(max_n, n_rows) * (Hq / kv->Hkv);
+}
+
+// `most_pages` bounds the expanded pages further.
+ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w, ChunkCuts cut,
+                         long long most_pages) {
   ChunkLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -108,8 +116,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
   };
   if (kv->dtype != HS2_F32 && n_rows > 0 && max_n > 0 && max_t > 0) {
     const int G = Hq / kv->Hkv;
-    const long long top = (long long)std::min(max_n, n_rows) * G;  // rows of the largest sequence
-    const ChunkCuts cut = chunk_cuts(top, n_rows, Hq, kv, max_n, max_t, w);
+    const long long top = chunk_top(n_rows, Hq, kv, max_n);
     auto add = [&](bool narrow, int tile_rows, int lo, int hi) {
       hs2::ChunkPlan& p = L.plan[L.n_plans];
       L.narrow[L.n_plans] = narrow;
@@ -141,7 +148,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
         L.exp_seqs = (int)std::min<long long>(kv->batch, (long long)n_rows * G / (cut.narrow + 1));
         L.exp_pages_seq = cdiv(max_t, 64);
         if (w > 0) L.exp_pages_seq = (int)std::min<long long>(L.exp_pages_seq, ((long long)max_n + w) / 64 + 2);
-        const long long pages = (long long)L.exp_seqs * L.exp_pages_seq;
+        const long long pages = std::min((long long)L.exp_seqs * L.exp_pages_seq, most_pages);
         if (pages * kv->Hkv * 64 > 0x7fffffff) L.tiles = 1LL << 40;  // beyond a tensor map's rows
         p->max_exp_pages = (int)std::min<long long>(pages, 0x7fffffff);
         for (int i = 0; i < 3; ++i) L.off_exp[i] = take(4 * (size_t)L.exp_seqs);
@@ -155,6 +162,29 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
   }
   L.total = std::max<size_t>(off, 256);
   return L;
+}
+
+ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+  const ChunkCuts cut = chunk_cuts(chunk_top(n_rows, Hq, kv, max_n), n_rows, Hq, kv, max_n, max_t, w);
+  return chunk_layout(n_rows, Hq, kv, max_n, max_t, w, cut, 1LL << 60);
+}
+
+// What this call and every call with fewer rows, tokens or keys needs, whichever kernels those run:
+// narrower units are more, and a call that splits its sequences may expand fewer pages than a
+// smaller one that does not.
+size_t chunk_bytes(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t, int w) {
+  const long long any = 1LL << 60;
+  const ChunkCuts cut = chunk_cuts(chunk_top(n_rows, Hq, kv, max_n), n_rows, Hq, kv, max_n, max_t, w);
+  size_t need = chunk_layout(n_rows, Hq, kv, max_n, max_t, w, cut, any).total;
+  for (int rows = 16; rows <= 64; rows *= 2) {
+    const int n = std::min(max_n, std::max(1, rows / (Hq / kv->Hkv)));
+    need = std::max(need, chunk_layout(n_rows, Hq, kv, n, max_t, w, {0x7fffffff, false}, any).total);
+  }
+  if (cut.wide) {
+    const long long few = kFewExpanded / (256LL * kv->Hkv * kv->d) + 2LL * kv->batch;
+    need = std::max(need, chunk_layout(n_rows, Hq, kv, max_n, max_t, w, {0, true}, few).total);
+  }
+  return need;
 }
 
 void bind(ChunkLayout& L, char* ws) {
@@ -242,7 +272,7 @@ size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, i
       (kv->d != 64 && kv->d != 128))
     return 0;
   if (Hq % kv->Hkv != 0 || !pow2_le32(Hq / kv->Hkv)) return 0;
-  return chunk_layout(n_rows, Hq, kv, max_n, max_t, w).total;
+  return chunk_bytes(n_rows, Hq, kv, max_n, max_t, w);
 }
 
 hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
