@@ -66,7 +66,7 @@ struct NarrowSmem {
   static constexpr int NB = D / 64;
   uint8_t ring[STAGES][(STAGE + 1023) / 1024 * 1024];
   uint8_t v[QUANT ? 2 : 1][QUANT ? VTILE : 1024];
-  uint8_t p[2][128 * 128];  // also the merge's factors
+  uint8_t p[2][128 * 128];
   uint8_t q[2][NB * N * 128];
   // per softmax group (even and odd tiles): nm, the last change's factors, the four warps' maxima
   alignas(16) float nm[2][N], alpha[2][N], warp_m[2][4][N];
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
           else reinterpret_cast<float*>(a.o)[at_o] = v;
         }
       };
-      // this thread's row (tid < H): both groups' max and sum; the groups' factors to alpha and fin
+      // this thread's row (tid < H): both groups' max and sum; the groups' factors to warp_m
       float M = -INFINITY, L = 0.f;
       if (tid < H) {
         const int n = nb + tid;
