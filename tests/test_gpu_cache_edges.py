@@ -130,3 +130,28 @@ def test_a_nan_key_reaches_the_rows_that_see_it(H, dtype, n):  # noqa: F811
     assert np.isnan(o[sees]).all() and np.isnan(lse[sees]).all()
     check((o[~sees], lse[~sees]), tuple(x[~sees] for x in clean), dtype)
     del rng
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("max_n,max_t", [(16, 200), (300, 512), (131072, 131072)])
+def test_descending_row_starts(H, dtype, max_n, max_t):  # noqa: F811
+    """Row starts that fall: flagged on every route, and nothing is written (float32: only rows of
+    sequences that the starts give some)."""
+    import torch
+
+    lens, counts = [200, 70, 90, 64], [10, 10, 10, 10]
+    rng, c, bt, rs, qraw, qval = case(64, dtype, lens, counts, 8, 1, 64, extra=300)
+    wide = np.full((4, max(max_t // 64, bt.shape[1])), 10 ** 9, np.int32)
+    wide[:, :bt.shape[1]] = bt
+    for starts in ([0, 10, 5, 20, 30], [0, 10, -2 ** 31, -5, 10], [0, 2 ** 31 - 1, -2 ** 31, 0, 10]):
+        o, lse, err = run(H, c, wide, lens, np.array(starts, np.int32), qraw, 0.1, max_n=max_n, max_t=max_t)
+        assert err & H.DEV_BAD_LENGTH
+        rows = slice(20 if dtype == "f32" else 0, None)
+        assert (o[rows] == 9).all() or dtype == "f32"
+        assert np.isfinite(o).all()
+    kv = T.device_cache(H, c, wide, lens)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k, _ = H.hs2_kv_read(kv, T.device(np.array([0, 10, 5, 20, 30], np.int32)), 30, dev_err=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) & H.DEV_BAD_LENGTH
+    del rng, qval, rs, k

@@ -36,9 +36,7 @@ HS2_DEVI RowPlace row_place(const int32_t* row_start, const int32_t* seq_len, in
     return p;
   }
   const int r0 = row_start[p.b], n = row_start[p.b + 1] - r0, t = seq_len[p.b];
-  if (r - r0 >= n) {  // a descending row_start
-    return p;
-  }
+  if (r < r0 || n <= 0 || (uint32_t)(r - r0) >= (uint32_t)n) return p;  // a descending row_start
   if (t >= n && t <= max_pages * kPage) p.pos = t - n + (r - r0);
   return p;
 }
