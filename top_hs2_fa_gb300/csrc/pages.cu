@@ -9,8 +9,8 @@
 // is one or two short launches with few dependent rounds of loads, and every launch overlaps
 // the end of the one before it (programmatic dependent launch). Only the copies (a forked
 // sequence's partial page, the pages that compaction moves) are bandwidth.
-// Measured: fork, grow and free of 64 branches of 16 sequences (4K to 16K keys, two caches) 35 us together,
-// of 8 branches 16.5; compaction that moves half of what is left of 64 sequences (540 MB read and
+// Measured: fork, grow and free of 64 branches of 16 sequences (4K to 16K keys, two caches) 19 us together,
+// of 8 branches 14; compaction that moves half of what is left of 64 sequences (540 MB read and
 // written) 101 us, 0.80 of the copy bandwidth.
 #include <cooperative_groups.h>
 
@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesCluster = 8;  // CTAs of the clusters that scan all pages
-constexpr int kGone = -1;         // ref of a page whose last reference the running free call took
+constexpr int kGone = -(1 << 30);  // ref of a page whose last reference the running free call took
 
 HS2_DEVI int pages_of(int t) { return (t + kPage - 1) / kPage; }
 HS2_DEVI bool good_len(int t, int max_pages) { return t >= 0 && t <= max_pages * kPage; }
@@ -93,11 +93,12 @@ cudaError_t launch_pages_grow(const PagesArgs& a, cudaStream_t s) {
 }
 
 // ---------------------------------------------------------------------------- free
-// One cluster. References go down by compare-and-swap, so that a page without one is seen; a
-// page that loses its last is marked. Then each block counts and pushes its slice of the
-// marked pages, in page order. A warp takes 128 entries of a row at a time, four a lane, so
-// that their atomics are in flight together (a row per warp, 32 at a time, took 30 us for 64
-// sequences of 160 pages, this 10).
+// One cluster. Every entry takes a reference down; the one that took a page's last marks the page by
+// an addition, and one that found none left (a bad table) gives it back: additions commute, so
+// the counts come out the same in any order. (By compare-and-swap the branches of a page retried
+// against each other: 24 us for 64 branches of 64 to 256 pages, four to a page, now 9.) Then each block
+// counts and pushes its slice of the marked pages, in page order. A warp takes 128 entries of a
+// row at a time, four a lane, so that their atomics are in flight together.
 __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
     pages_free_kernel(const PagesArgs a) {
   constexpr int E = 4;
@@ -118,7 +119,7 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
       continue;
     }
     const int np = pages_of(t);
-    int page[E], cur[E];
+    int page[E], was[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       const int j = j0 + 32 * e;
@@ -128,21 +129,15 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
         page[e] = -1;
       }
     }
-    // most pages have one reference
 #pragma unroll
-    for (int e = 0; e < E; ++e) cur[e] = page[e] >= 0 ? atomicCAS(&a.ref[page[e]], 1, kGone) : 1;
+    for (int e = 0; e < E; ++e) was[e] = page[e] >= 0 ? atomicSub(&a.ref[page[e]], 1) : 2;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      int c = cur[e];
-      if (c == 1) continue;
-      while (true) {
-        if (c <= 0) {
-          flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-          break;
-        }
-        const int seen = atomicCAS(&a.ref[page[e]], c, c == 1 ? kGone : c - 1);
-        if (seen == c) break;
-        c = seen;
+      if (was[e] == 1) {
+        atomicAdd(&a.ref[page[e]], kGone);
+      } else if (was[e] <= 0) {
+        atomicAdd(&a.ref[page[e]], 1);
+        flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
       }
     }
   }
