@@ -318,6 +318,10 @@ hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype r
  * left and no sink gets o = 0, lse = -inf). A sequence whose n_b > max_n, t_b > max_t,
  * n_b > t_b, or rows beyond n_rows, sets HS2_DEV_BAD_LENGTH and its rows are not written
  * (a descending row_start: none or only some rows are).
+ * The weights enter P.V rounded to 16 bits whatever o_dtype is (float32 caches: not rounded): to
+ * bfloat16, or, with few rows per KV head over an FP8 / FP4 cache, weight times V scale to float16
+ * relative to the row's largest, of which 2^-30 and less is lost. Their sum and lse are float32.
+ * V scales may differ from page to page; magnitudes in [2^-60, 2^60], or 0.
  * A V row that is not finite makes the rows of a chunk undefined that see any key of its
  * 128-key tile, as a weight of zero does not cancel it; values behind seq_len do not matter.
  * A K row or query that is not finite gives NaN in the rows that see it.

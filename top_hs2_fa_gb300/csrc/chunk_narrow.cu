@@ -18,9 +18,10 @@
 //   warps 1, 3   MMA issuers, of S and of O: their waits overlap the other's instructions
 //   warps 12-19  softmax, four warps for every other tile, each four with references, sums and
 //                an O of their own (joined when the unit ends): p = 2^(x c + nm), nm = 6 - m per
-//                row with the reference m moving only when a weight would exceed 2^14 (f16 P
-//                keeps weights down to 2^-30 of the largest); the normaliser is summed in fp32
-//                from unrounded weights, per thread
+//                row; P holds p S_v, S_v the V scale of the key's page, and the reference m moves
+//                only when |p S_v| of a key that the row sees would exceed 2^14 (f16 P keeps what
+//                is within 2^-30 of a row's largest, whatever other pages' scales are); the
+//                normaliser is summed in fp32 from unrounded p, per thread
 //   warp 2       Q of the next unit by TMA, then to f16 in place, with an exact power of two
 //                where its values would leave f16's range
 // A bf16 cache skips the conversions: its TMA tiles are the operands (bf16 Q, P).
@@ -28,8 +29,7 @@
 // of bf16 476 us (1.01 of the copy bandwidth), FP8 296 (0.81), FP4 261 (0.52); 4 tokens of FP4 279
 // (0.48). FP4 is bound by the instructions and waits around its operands, not by any one pipe:
 // conversions fill 23 % of a tile's time, the MMAs 26 %.
-// The page's K scale multiplies the logits; V's enters the weights relative to a unit that O is
-// kept in. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four
+// The page's K scale multiplies the logits; V's enters P. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four
 // softmax warps of a tile leave their loop together (they meet at a hardware barrier).
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -46,10 +46,13 @@ constexpr int kNThreads = 640;
 constexpr float kBias = 6.f;     // log2 of the weight of a key at the reference max
 constexpr float kTop = 14.f;     // log2 of the largest weight before the reference moves
 constexpr float kUnset = 1e30f;  // nm of a row that has seen no key
+// log2 |S_v| as the references take it. From below: p = 2^(14 - log2 |S_v|) at most, of which 2^24
+// keys have to add up within fp32, and a scale of zero has to leave p finite.
+constexpr float kLeastScale = -64.f, kMostScale = 127.f;
 constexpr int kInfo = 16;        // tiles whose pages' scales are kept: more than the pipeline holds
 
 struct __align__(16) TileInfo {
-  float k[2], v[2];  // the two pages' slab scales
+  float k[2], v[2];  // the two pages' slab scales (V's of a page that is not there: 0)
   int there[2];      // whether the page is there
   int pad[2];
 };
@@ -70,8 +73,8 @@ struct NarrowSmem {
   uint8_t q[2][NB * N * 128];
   // per softmax group (even and odd tiles): nm, the last change's factors, the four warps' maxima
   alignas(16) float nm[2][N], alpha[2][N], warp_m[2][4][N];
-  // per unit, by its parity: each group's maxima, the sums of its four warps, its V unit (0 tiles: -1)
-  alignas(16) float out_m[2][2][N], out_l[2][2][4][N], out_unit[2][2];
+  // per unit, by its parity: each group's maxima, the sums of its four warps
+  alignas(16) float out_m[2][2][N], out_l[2][2][4][N];
   TileInfo info[kInfo];
   float qmul[2];
   uint64_t info_full[kInfo];
@@ -317,7 +320,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
           // (the scales have arrived meanwhile)
           if ((lane >> 1) == j - c0) {
             TileInfo& f = sm.info[issued % kInfo];
-            f.k[lane & 1] = ks, f.v[lane & 1] = vs, f.there[lane & 1] = mine >= 0;
+            const bool here = mine >= 0;  // (else the scales may be those of an earlier page)
+            f.k[lane & 1] = here ? ks : 1.f, f.v[lane & 1] = here ? vs : 0.f, f.there[lane & 1] = here;
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&sm.info_full[issued % kInfo]);
@@ -568,7 +572,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
       float l[N];
 #pragma unroll
       for (int n = 0; n < N; ++n) l[n] = 0.f;
-      float unit = BF ? 1.f : 0.f;
       if (tid < N) nm[tid] = kUnset;
       bool good = tc::mbar_wait(&sm.q_full[sp], (seg >> 1) & 1);
       const float cq = a.scale_log2 * (QUANT && good ? *(volatile float*)&sm.qmul[sp] : 1.f);
@@ -583,7 +586,9 @@ __global__ void __launch_bounds__(kNThreads, 1)
         tc::tc_fence_after();
         const int pos = (u.page0 + 2 * j) * kPage + key;
         const TileInfo& f = sm.info[it % kInfo];
-        const float v0 = f.v[0], v1 = f.v[1], c = cq * f.k[qd >> 1];
+        const float vs = f.v[qd >> 1], c = cq * f.k[qd >> 1];
+        // (NaN: as the least)
+        const float lv = BF ? 0.f : fminf(fmaxf(log2f(fabsf(vs)), kLeastScale), kMostScale);
         const bool there = f.there[qd >> 1] != 0;
         const bool edge = (u.page0 + 2 * j) * kPage + 127 > u.pos0 || (a.w > 0 && (u.page0 + 2 * j) * kPage <= pos_last - a.w);
         // exponents of one step's columns, -inf where the key is hidden
@@ -607,7 +612,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
               if (n0 + n < lo || n0 + n >= hi) x[n] = -INFINITY;
           }
         };
-        // the group's maxima over the 128 keys, to warp_m
+        // the group's maxima over the 128 keys, with their V scales, to warp_m
         float x[C];
         auto maxima = [&]() {
 #pragma unroll
@@ -617,7 +622,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
             for (int n = 0; n < C; ++n) {
               float t;
               asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(t) : "f"(x[n]));
-              if (lane == n) sm.warp_m[grp][qd][n0 + n] = t;
+              if (lane == n) sm.warp_m[grp][qd][n0 + n] = t + lv;
             }
           }
           (void)any_of_128(bar, false);
@@ -632,10 +637,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
           float t0 = fmaxf(x[0], x[1]), t1 = fmaxf(x[2], x[3]);
 #pragma unroll
           for (int n = 4; n < C; n += 4) t0 = fmax3(t0, x[n], x[n + 1]), t1 = fmax3(t1, x[n + 2], x[n + 3]);
-          need |= fmaxf(t0, t1) > kTop;
+          need |= fmaxf(t0, t1) + lv > kTop;
         }
-        const float vtop = fmaxf(fabsf(v0), fabsf(v1));
-        need |= QUANT && vtop > 2.f * unit;
         bool moved = false;
         if (any_of_128(bar, need || !good || halted(sm))) {
           moved = true;
@@ -643,18 +646,13 @@ __global__ void __launch_bounds__(kNThreads, 1)
             run = false;
             break;
           }
-          // ---- some row's reference max, or V's unit, moves
+          // ---- some row's reference moves
           if (j > jf) maxima();  // at the group's first tile every row is unset
-          float fall = 1.f;
-          if (QUANT && vtop > 2.f * unit) {
-            fall = unit / vtop;
-            unit = vtop;
-          }
           bool fresh = false;
           if (tid < N) {
             const float t = j > jf ? top_of(tid) : kUnset;
             float al = 1.f;
-            if (t > kTop) {  // t = x c + nm: the new nm is 6 - x c
+            if (t > kTop) {  // t = x c + lv + nm: the new nm is 6 - (x c + lv)
               const float old = nm[tid];
               if (old == kUnset) {  // x c is lost in the sum: the first reference comes from a second look
                 fresh = true;
@@ -663,7 +661,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
               } else {
                 const float to = old - t + kBias;
                 nm[tid] = to;
-                al = ex2_approx(to - old);
+                al = exp2f(to - old);  // (subnormals count: with scales far apart l can be large beside it)
               }
             }
             alpha[tid] = al;
@@ -685,7 +683,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
               float ov[C];
               tmem_cols<C>(o + lane_off + n0, ov);
 #pragma unroll
-              for (int n = 0; n < C; ++n) ov[n] *= alpha[n0 + n] * fall;
+              for (int n = 0; n < C; ++n) ov[n] *= alpha[n0 + n];
               tmem_put<C>(o + lane_off + n0, ov);
             }
           }
@@ -696,8 +694,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
           tc::mbar_arrive(&sm.s_empty[b]);
         }
         // ---- weights
-        const float vs = qd >> 1 ? v1 : v0;
-        const float rel = BF ? 1.f : unit > 0.f ? vs / unit : 0.f;
 #pragma unroll
         for (int n0 = 0; n0 < N; n0 += C) {
           if (N > C || moved) exponents(n0, x);  // one step of columns is still in registers
@@ -709,7 +705,7 @@ __global__ void __launch_bounds__(kNThreads, 1)
               F2 pr{ex2_approx(x[n + 2 * i]), ex2_approx(x[n + 2 * i + 1])};
               const F2 sum = add2({l[n0 + n + 2 * i], l[n0 + n + 2 * i + 1]}, pr);
               l[n0 + n + 2 * i] = sum.x, l[n0 + n + 2 * i + 1] = sum.y;
-              if (!BF) pr = mul2(pr, {rel, rel});
+              if (!BF) pr = mul2(pr, {vs, vs});
               w[i] = BF ? pack_bf16(pr.x, pr.y) : pack_f16(pr.x, pr.y);
             }
             *reinterpret_cast<uint4*>(sm.p[b] + key * 128 + ((((n0 + n) >> 3) ^ (key & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -738,7 +734,6 @@ __global__ void __launch_bounds__(kNThreads, 1)
         if (lane < C) sm.out_l[sp][grp][qd][n0 + lane] = s;
       }
       if (tid < N) sm.out_m[sp][grp][tid] = nm[tid] == kUnset ? -INFINITY : -nm[tid];
-      if (tid == 0) sm.out_unit[sp][grp] = unit;
       tc::mbar_arrive(&sm.out_ready[sp]);
       good = __all_sync(0xffffffffu, good && tc::mbar_wait(&sm.out_ready[sp], (seg >> 1) & 1));
       if (any_of_128(bar, !good)) {
@@ -776,8 +771,8 @@ __global__ void __launch_bounds__(kNThreads, 1)
         L = e0 * (sm.out_l[sp][0][0][n] + sm.out_l[sp][0][1][n] + sm.out_l[sp][0][2][n] + sm.out_l[sp][0][3][n]) +
             e1 * (sm.out_l[sp][1][0][n] + sm.out_l[sp][1][1][n] + sm.out_l[sp][1][2][n] + sm.out_l[sp][1][3][n]);
         const float f = whole ? finish(n, M, L) : 1.f;
-        sm.warp_m[grp][0][tid] = e0 * sm.out_unit[sp][0] * f;
-        sm.warp_m[grp][1][tid] = e1 * sm.out_unit[sp][1] * f;
+        sm.warp_m[grp][0][tid] = e0 * f;
+        sm.warp_m[grp][1][tid] = e1 * f;
       }
       (void)any_of_128(bar, false);
       // a group without tiles in this part left nothing in its O
