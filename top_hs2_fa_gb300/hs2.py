@@ -9,6 +9,7 @@ cannot be loaded, every call raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 from dataclasses import dataclass
 
@@ -146,14 +147,16 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
-_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_data_ptr, _size, _contiguous = torch.Tensor.data_ptr, torch.Tensor.size, torch.Tensor.is_contiguous
+_dtype = operator.attrgetter("dtype")
 
 
 class _Handle:
     """Base of the handles whose C struct is kept between calls: setting an attribute drops it,
-    and a tensor whose storage has moved or whose size has changed makes a new one."""
+    and a tensor whose storage, shape, type or strides have changed makes a new one (or an error)."""
 
-    _c = None  # (struct, device, tensors it was made from, their pointers, the first three's sizes)
+    # (struct, device, tensors it was made from, their pointers, the first three's shapes and types)
+    _c = None
 
     def __setattr__(self, name, value):
         object.__setattr__(self, name, value)
@@ -165,9 +168,11 @@ class _Handle:
 
     def _cached(self):
         got = self._c
-        if got is None or got[3] != tuple(map(_data_ptr, got[2])) or got[4] != tuple(map(_numel, got[2][:3])):
+        if (got is None or got[3] != tuple(map(_data_ptr, got[2])) or got[4] != tuple(map(_size, got[2][:3]))
+                or got[5] != tuple(map(_dtype, got[2][:3])) or not all(map(_contiguous, got[2]))):
             ts = self._tensors()
-            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)), tuple(map(_numel, ts[:3])))
+            got = (self._make(), _device_of(ts), ts, tuple(map(_data_ptr, ts)), tuple(map(_size, ts[:3])),
+                   tuple(map(_dtype, ts[:3])))
             object.__setattr__(self, "_c", got)
         return got
 
