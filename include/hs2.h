@@ -279,7 +279,8 @@ hs2_status hs2_hier_reindex(hs2_idx_mode mode, const void* q_idx, const float* w
  * k_rows, v_rows: [n_rows][Hkv][d] of row_dtype (HS2_F32 or HS2_BF16), token r at
  *   r * row_stride elements (row_stride >= Hkv * d: slices of a fused projection's output
  *   fit), 16-byte aligned, row_stride * sizeof(element) a multiple of 16. v_rows is ignored
- *   for a key-only cache (kv->v = NULL).
+ *   for a key-only cache (kv->v = NULL); K and V rows of different strides take two calls,
+ *   each on one side as a key-only cache.
  *
  * hs2_kv_write stores the rows in the cache's type:
  *   F32 / BF16: the value, rounded to nearest even where bfloat16 is narrower.

@@ -478,27 +478,56 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     return _new(max(nbytes, 256), torch.uint8, device, stream)
 
 
+def _token_stride(rows, n: int, c: hs2_kv) -> int:
+    """Elements from one token of the rows to the next, or an error."""
+    shape, stride = rows.shape, rows.stride()
+    if shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
+        raise HS2Error("rows must be [n_rows][Hkv][d] with contiguous tokens")
+    return stride[0] if n > 1 else c.Hkv * c.d  # one token: its stride reaches nothing
+
+
+def _side(c: hs2_kv, v: bool) -> hs2_kv:
+    """The K (V) half of the cache as a key-only cache."""
+    half = hs2_kv.from_buffer_copy(c)
+    if v:
+        half.k, half.k_scale, half.k_sf = c.v, c.v_scale, c.v_sf
+    half.v = half.v_scale = half.v_sf = None
+    return half
+
+
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
     c, dev = kv._cached()[:2]
-    shape, stride, dtype = k_rows.shape, k_rows.stride(), k_rows.dtype
-    n = shape[0]
-    if dtype not in _ROW_DTYPES or shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
-        raise HS2Error("rows must be float32 or bfloat16 [n_rows][Hkv][d] with contiguous tokens")
+    n, dtype = k_rows.shape[0], k_rows.dtype
     if (v_rows is None) != (kv.v is None):
         raise HS2Error("v_rows goes with a cache that has V")
-    if v_rows is not None and (v_rows.dtype is not dtype or v_rows.shape != shape or v_rows.stride() != stride):
-        raise HS2Error("v_rows must have k_rows' dtype, shape and strides")
+    if dtype not in _ROW_DTYPES or (v_rows is not None and v_rows.dtype is not dtype):
+        raise HS2Error("rows must be float32 or bfloat16, K and V alike")
+    ks = _token_stride(k_rows, n, c)
+    vs = ks if v_rows is None else _token_stride(v_rows, n, c)
     _i32(row_start, "row_start", c.batch + 1)
     st = _launch_stream(stream, dev, k_rows, v_rows, row_start, dev_err)
-    _check(call(ctypes.byref(c), k_rows.data_ptr(), _ptr(v_rows), _ROW_DTYPES[dtype],
-                stride[0] if n > 1 else c.Hkv * c.d, row_start.data_ptr(), n, _ptr(dev_err), st))
+
+    def rows(c, k, v, stride):
+        _check(call(ctypes.byref(c), k.data_ptr(), _ptr(v), _ROW_DTYPES[dtype], stride, row_start.data_ptr(), n,
+                    _ptr(dev_err), st))
+
+    if vs == ks:
+        rows(c, k_rows, v_rows, ks)
+        return
+    # a call takes one stride: a call for each side, once it is sure that neither will be refused
+    for x, stride in ((k_rows, ks), (v_rows, vs)):
+        if (x.data_ptr() | stride * x.element_size()) % 16 or stride < c.Hkv * c.d:
+            raise HS2Error("rows must start on 16 bytes, their tokens a multiple of 16 bytes apart and disjoint")
+    rows(_side(c, False), k_rows, None, ks)
+    rows(_side(c, True), v_rows, None, vs)
 
 
 def hs2_kv_write(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor, dev_err=None,
                  stream=None) -> None:
     """Rows of a ragged batch into the cache, quantised to its type: rows [row_start[b],
     row_start[b+1]) are sequence b's last positions (seq_len already counts them). ``k_rows``
-    / ``v_rows``: float32 or bfloat16 [n_rows][Hkv][d], any token stride; the cache's
+    / ``v_rows``: float32 or bfloat16 (both alike) [n_rows][Hkv][d], each with a token stride
+    of its own (a multiple of 16 bytes; one launch where they agree, else two); the cache's
     k_scale / v_scale are inputs."""
     _kv_rows(load().hs2_kv_write, kv, k_rows, v_rows, row_start, dev_err, stream)
 
