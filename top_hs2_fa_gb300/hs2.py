@@ -502,24 +502,21 @@ def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
         raise HS2Error("v_rows goes with a cache that has V")
     if dtype not in _ROW_DTYPES or (v_rows is not None and v_rows.dtype is not dtype):
         raise HS2Error("rows must be float32 or bfloat16, K and V alike")
-    ks = _token_stride(k_rows, n, c)
-    vs = ks if v_rows is None else _token_stride(v_rows, n, c)
+    ks = vs = _token_stride(k_rows, n, c)
+    if v_rows is not None and (v_rows.stride() != k_rows.stride() or v_rows.shape != k_rows.shape):
+        vs = _token_stride(v_rows, n, c)
     _i32(row_start, "row_start", c.batch + 1)
     st = _launch_stream(stream, dev, k_rows, v_rows, row_start, dev_err)
-
-    def rows(c, k, v, stride):
-        _check(call(ctypes.byref(c), k.data_ptr(), _ptr(v), _ROW_DTYPES[dtype], stride, row_start.data_ptr(), n,
-                    _ptr(dev_err), st))
-
+    dt, rs, err = _ROW_DTYPES[dtype], row_start.data_ptr(), _ptr(dev_err)
     if vs == ks:
-        rows(c, k_rows, v_rows, ks)
+        _check(call(ctypes.byref(c), k_rows.data_ptr(), _ptr(v_rows), dt, ks, rs, n, err, st))
         return
     # a call takes one stride: a call for each side, once it is sure that neither will be refused
     for x, stride in ((k_rows, ks), (v_rows, vs)):
         if (x.data_ptr() | stride * x.element_size()) % 16 or stride < c.Hkv * c.d:
             raise HS2Error("rows must start on 16 bytes, their tokens a multiple of 16 bytes apart and disjoint")
-    rows(_side(c, False), k_rows, None, ks)
-    rows(_side(c, True), v_rows, None, vs)
+    for v, x, stride in ((False, k_rows, ks), (True, v_rows, vs)):
+        _check(call(ctypes.byref(_side(c, v)), x.data_ptr(), 0, dt, stride, rs, n, err, st))
 
 
 def hs2_kv_write(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor, dev_err=None,
