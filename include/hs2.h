@@ -294,9 +294,11 @@ hs2_status hs2_hier_reindex(hs2_idx_mode mode, const void* q_idx, const float* w
  *   The pages written must belong to their sequence alone.
  * hs2_kv_read writes the values those positions stand for to k_rows / v_rows (FP8 / FP4:
  *   code * scales in float32, rounded once; then to bfloat16 where that is row_dtype).
- * Device-side: t_b beyond max_pages * page_size, n_b > t_b or a descending row_start sets
- *   HS2_DEV_BAD_LENGTH, a table entry outside [0, num_pages) HS2_DEV_BAD_PAGE; such rows are
- *   left as they were (in the cache, or in k_rows / v_rows). */
+ * Device-side: t_b beyond max_pages * page_size, n_b > t_b, a sequence with rows outside
+ *   [0, n_rows) or a descending row_start sets HS2_DEV_BAD_LENGTH, a table entry outside
+ *   [0, num_pages) HS2_DEV_BAD_PAGE; such sequences' rows are left as they were (in the
+ *   cache, or in k_rows / v_rows; of a bad entry the rows of its page; where a start falls,
+ *   all or only some rows of the sequences about it are). */
 hs2_status hs2_kv_write(const hs2_kv* kv, const void* k_rows, const void* v_rows, hs2_dtype row_dtype,
                         int64_t row_stride, const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream);
 hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype row_dtype, int64_t row_stride,

@@ -37,10 +37,11 @@ __global__ void __launch_bounds__(kCcWarps * 32) chunk_cc_kernel(const ChunkArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int n1[1];
   warp_rows_at_most<1>(a.row_start, a.batch, r, n1);
-  const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, r, n1[0]);
+  if (r == 0 && h == 0 && warp == 0 && warp_bad_starts(a.row_start, a.batch, a.n_rows) && lane == 0)
+    flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
+  const RowPlace pl = row_place(a.row_start, a.seq_len, a.batch, a.max_pages, a.n_rows, r, n1[0]);
   if (pl.b < 0) return;
-  const int end = a.row_start[pl.b + 1];
-  if (pl.pos < 0 || a.seq_len[pl.b] > a.max_t || end - a.row_start[pl.b] > a.max_n || end > a.n_rows) {
+  if (pl.pos < 0 || a.seq_len[pl.b] > a.max_t || a.row_start[pl.b + 1] - a.row_start[pl.b] > a.max_n) {
     if (threadIdx.x == 0) flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
     return;
   }

@@ -6,6 +6,17 @@
 
 namespace hs2 {
 
+// Whether any sequence's rows are not within [0, n_rows), or a start falls, by one warp: what the
+// rows themselves cannot see, where no row of theirs exists.
+HS2_DEVI bool warp_bad_starts(const int32_t* row_start, int batch, int n_rows) {
+  bool bad = false;
+  for (int b = threadIdx.x & 31; b < batch; b += 32) {
+    const int r0 = row_start[b], r1 = row_start[b + 1];
+    bad |= r1 != r0 && (r1 < r0 || r0 < 0 || r1 > n_rows);
+  }
+  return __any_sync(0xffffffffu, bad);
+}
+
 // n[k] = number of entries of row_start[0 .. batch] that are <= r0 + k, by one warp: every
 // lane gets all of them. One round of independent loads per 32 entries (a binary search
 // would chain its loads).
@@ -29,14 +40,17 @@ struct RowPlace {
 };
 // Place of row r given n_le, the number of row_start entries <= r: the last sequence that starts at or
 // before r owns it (those before it that start there too have no rows).
-HS2_DEVI RowPlace row_place(const int32_t* row_start, const int32_t* seq_len, int batch, int max_pages, int r, int n_le) {
+HS2_DEVI RowPlace row_place(const int32_t* row_start, const int32_t* seq_len, int batch, int max_pages, int n_rows,
+                            int r, int n_le) {
   RowPlace p{n_le - 1, -1};
   if (p.b < 0 || p.b >= batch) {
     p.b = -1;
     return p;
   }
-  const int r0 = row_start[p.b], n = row_start[p.b + 1] - r0, t = seq_len[p.b];
-  if (r < r0 || n <= 0 || (uint32_t)(r - r0) >= (uint32_t)n) return p;  // a descending row_start
+  const int r0 = row_start[p.b], r1 = row_start[p.b + 1], t = seq_len[p.b];
+  if (r0 < 0 || r1 > n_rows) return p;  // rows that do not exist
+  if (r < r0 || r >= r1) return p;      // a descending row_start
+  const int n = r1 - r0;
   if (t >= n && t <= max_pages * kPage) p.pos = t - n + (r - r0);
   return p;
 }
