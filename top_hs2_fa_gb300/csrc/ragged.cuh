@@ -51,7 +51,7 @@ HS2_DEVI RowPlace row_place(const int32_t* row_start, const int32_t* seq_len, in
   if (r0 < 0 || r1 > n_rows) return p;  // rows that do not exist
   if (r < r0 || r >= r1) return p;      // a descending row_start
   const int n = r1 - r0;
-  if (t >= n && t <= max_pages * kPage) p.pos = t - n + (r - r0);
+  if (t >= n && t <= (long long)max_pages * kPage) p.pos = t - n + (r - r0);
   return p;
 }
 
