@@ -379,8 +379,9 @@ hs2_status hs2_pages_free(const hs2_pages* pages, const int32_t* block_table, co
  * child_table and child_len do not overlap the sources'. Where the free pages do not
  * suffice, HS2_DEV_BAD_PAGE is set and every branch has length 0 and no pages. src outside
  * [-1, batch) sets HS2_DEV_BAD_INDEX, a source length outside [0, max_pages * 64]
- * HS2_DEV_BAD_LENGTH: that branch is none. A source's bad table entry sets
- * HS2_DEV_BAD_PAGE and is -1 in the branch (a bad last page: nothing is copied). */
+ * HS2_DEV_BAD_LENGTH: that branch is none. A source's bad table entry (out of range, or a
+ * page without a reference) sets HS2_DEV_BAD_PAGE and is -1 in the branch (a bad last page:
+ * nothing is copied to the branch's own). */
 hs2_status hs2_pages_fork(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, const int32_t* src, int n_child,
                           int32_t* child_table, int32_t* child_len, int32_t* dev_err, void* stream);
 /* hs2_pages_compact: with L referenced pages, moves every referenced page >= L into a free

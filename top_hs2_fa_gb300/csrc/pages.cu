@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(256) pages_fork_copy_kernel(const PagesArgs a,
   if (rest == 0) return;
   const int to = child[full], of = par[full];
   if (to < 0) return;  // flagged by the plan
-  if (of < 0 || of >= a.num_pages) {
+  if (of < 0 || of >= a.num_pages || __ldcg(&a.ref[of]) <= 0) {  // as above
     if (slab == 0 && threadIdx.x == 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
     return;
   }
