@@ -389,7 +389,7 @@ hs2_status hs2_pages_fork(const hs2_pages* pages, int n_caches, const hs2_kv* kv
  * cache with its scales, and updates the references, the free list (the pages >= L, the
  * lowest taken first; entries behind are -1) and the entries of the caches' block table
  * below ceil(seq_len[b] / 64). That table must hold every sequence that has pages of the
- * pool. Bad entries (HS2_DEV_BAD_PAGE) and the rows of sequences with a bad length
+ * pool. Bad entries (out of range, or of a free page: HS2_DEV_BAD_PAGE) and the rows of sequences with a bad length
  * (HS2_DEV_BAD_LENGTH) are left as they are.
  * workspace: at least hs2_pages_compact_workspace(pages) bytes, 256-byte aligned, contents
  * ignored. */

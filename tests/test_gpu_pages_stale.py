@@ -35,3 +35,25 @@ def test_fork_of_a_free_last_page(H, dtype):  # noqa: F811
         np.testing.assert_array_equal(after[name][mine], before[name][mine], err_msg=name)
         rows = slice(None) if name.endswith("scale") else (slice(None), slice(0, 6))
         np.testing.assert_array_equal(after[name][other][rows], before[name][source][rows], err_msg=name)
+
+
+def test_compact_flags_entries_of_free_pages_below(H):  # noqa: F811
+    """An entry that points at a free page below the count of referenced ones, which another
+    sequence's page moves into: flagged and left as it is."""
+    import torch
+
+    rng = np.random.default_rng(36)
+    c = T.make_cache(rng, "bf16", 6, 1, 64)
+    pages = H.Pages.make(6)
+    pages.ref.copy_(dev([0, 1, 0, 0, 1, 0]))
+    dt, dl = dev([[4, 1], [0, -1], [1, -1]]), dev([128, 60, 64])
+    kv = T.device_cache(H, c, np.zeros((3, 2)), [0, 0, 0])
+    kv.block_table, kv.seq_len = dt, dl
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    H.hs2_pages_compact(pages, [kv], dev_err=err)
+    assert int(err.item()) == H.DEV_BAD_PAGE
+    assert dt.tolist() == [[0, 1], [0, -1], [1, -1]] and pages.ref.tolist() == [1, 1, 0, 0, 0, 0]
+    err.zero_()
+    dl[1] = 0  # the sequence that pointed there ends: nothing to flag
+    H.hs2_pages_compact(pages, [kv], dev_err=err)
+    assert int(err.item()) == 0 and dt.tolist() == [[0, 1], [0, -1], [1, -1]]

@@ -293,8 +293,8 @@ cudaError_t launch_pages_fork(const PagesArgs& a, const PageSlabs& sl, cudaStrea
 // ---------------------------------------------------------------------------- compact
 // First launch, one cluster: every block takes a slice of the pages. From the blocks' counts of
 // referenced pages come L and the ranks of its holes (free pages below L) and movers
-// (referenced pages from L on); the i-th mover goes to the i-th hole. The lists, a mover's
-// rank by page, and the free list are written; references and tables follow with the copies.
+// (referenced pages from L on); the i-th mover goes to the i-th hole. The lists, by page whether it is
+// free (-1) and a mover's rank, and the free list are written; references and tables follow with the copies.
 __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesThreads)
     pages_compact_plan_kernel(const PagesArgs a) {
   __shared__ int sums[33], live_s, hole_s, mover_s;
@@ -344,7 +344,7 @@ __global__ void __cluster_dims__(kPagesCluster, 1, 1) __launch_bounds__(kPagesTh
     mover_at += here >> 16;
     if (in && low && !live) dst[hi] = p;
     if (live && !low) src[mi] = p;
-    if (in && !low) rank_of[p] = live ? mi : -1;
+    if (in) rank_of[p] = live ? (low ? 0 : mi) : -1;
     if (in) a.free_list[a.num_pages - 1 - p] = low ? -1 : p;
   }
   if (rank == 0 && threadIdx.x == 0) {
@@ -407,13 +407,9 @@ __global__ void __launch_bounds__(256) pages_move_kernel(const PagesArgs a, cons
     for (int j = lane; j < pages_of(t); j += 32) {
       int32_t* e = a.bt + (size_t)b * a.max_pages + j;
       const int page = *e;
-      if (page < 0 || page >= a.num_pages) {
-        flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-      } else if (page >= L) {
-        const int r = rank_of[page];
-        if (r < 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-        else *e = dst[r];
-      }
+      const int r = page >= 0 && page < a.num_pages ? rank_of[page] : -1;
+      if (r < 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+      else if (page >= L) *e = dst[r];
     }
   }
 }
