@@ -456,7 +456,7 @@ def _launch_stream(stream, dev: int, *tensors) -> int:
     for t in tensors:
         if t is not None and t.get_device() != dev:
             raise HS2Error("tensors on several devices")
-    if dev < 0 or dev != torch.cuda.current_device() or (stream is not None and stream.device.index != dev):
+    if dev < 0 or dev != torch._C._cuda_getDevice() or (stream is not None and stream.device.index != dev):
         raise HS2Error("the tensors must be on the current CUDA device (and the stream's)")
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
@@ -478,9 +478,8 @@ def _scratch(nbytes: int, device, stream) -> torch.Tensor:
     return _new(max(nbytes, 256), torch.uint8, device, stream)
 
 
-def _token_stride(rows, n: int, c: hs2_kv) -> int:
-    """Elements from one token of the rows to the next, or an error."""
-    shape, stride = rows.shape, rows.stride()
+def _token_stride(shape, stride, n: int, c: hs2_kv) -> int:
+    """Elements from one token of rows to the next, or an error."""
     if shape != (n, c.Hkv, c.d) or stride[2] != 1 or (c.Hkv > 1 and stride[1] != c.d):
         raise HS2Error("rows must be [n_rows][Hkv][d] with contiguous tokens")
     return stride[0] if n > 1 else c.Hkv * c.d  # one token: its stride reaches nothing
@@ -497,14 +496,16 @@ def _side(c: hs2_kv, v: bool) -> hs2_kv:
 
 def _kv_rows(call, kv: KV, k_rows, v_rows, row_start, dev_err, stream) -> None:
     c, dev = kv._cached()[:2]
-    n, dtype = k_rows.shape[0], k_rows.dtype
+    dtype = k_rows.dtype
     if (v_rows is None) != (kv.v is None):
         raise HS2Error("v_rows goes with a cache that has V")
     if dtype not in _ROW_DTYPES or (v_rows is not None and v_rows.dtype is not dtype):
         raise HS2Error("rows must be float32 or bfloat16, K and V alike")
-    ks = vs = _token_stride(k_rows, n, c)
-    if v_rows is not None and (v_rows.stride() != k_rows.stride() or v_rows.shape != k_rows.shape):
-        vs = _token_stride(v_rows, n, c)
+    shape, stride = k_rows.shape, k_rows.stride()
+    n = shape[0]
+    ks = vs = _token_stride(shape, stride, n, c)
+    if v_rows is not None and (v_rows.stride() != stride or v_rows.shape != shape):
+        vs = _token_stride(v_rows.shape, v_rows.stride(), n, c)
     _i32(row_start, "row_start", c.batch + 1)
     st = _launch_stream(stream, dev, k_rows, v_rows, row_start, dev_err)
     dt, rs, err = _ROW_DTYPES[dtype], row_start.data_ptr(), _ptr(dev_err)
