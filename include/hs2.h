@@ -290,7 +290,8 @@ hs2_status hs2_hier_reindex(hs2_idx_mode mode, const void* q_idx, const float* w
  *     group holding a NaN stores s = NaN, i.e. all its 16 values read as NaN.
  *   Every code is the one exact arithmetic gives. k_scale / v_scale (one per page and KV
  *   head) are inputs: they are set before rows are written and apply to a page's older rows
- *   too. S outside [2^-60, 2^60] (or NaN): HS2_DEV_BAD_PAGE, the row is not written.
+ *   too. S outside [2^-60, 2^60] (or NaN): HS2_DEV_BAD_PAGE, and the row's part under that
+ *   scale (its KV head's K, or V) is not written.
  *   The pages written must belong to their sequence alone.
  * hs2_kv_read writes the values those positions stand for to k_rows / v_rows (FP8 / FP4:
  *   code * scales in float32, rounded once; then to bfloat16 where that is row_dtype).
@@ -320,14 +321,20 @@ hs2_status hs2_kv_read(const hs2_kv* kv, void* k_rows, void* v_rows, hs2_dtype r
  * Keys in pages whose table entry is bad are left out (HS2_DEV_BAD_PAGE; a row with no key
  * left and no sink gets o = 0, lse = -inf). A sequence whose n_b > max_n, t_b > max_t,
  * n_b > t_b, or rows beyond n_rows, sets HS2_DEV_BAD_LENGTH and its rows are not written
- * (a descending row_start: none or only some rows are).
+ * (a descending row_start: none or only some rows are). With n_rows = 0 or max_n = 0 nothing
+ * is launched and nothing flagged. HS2_ERR_UNSUPPORTED: pools of 2^31 rows (num_pages * Hkv *
+ * 64) or more, and declared sizes of more than 2^30 tiles (max_t / 128 + 2 for every 16 to 256
+ * of the n_rows * Hq rows and every sequence's KV head).
  * The weights enter P.V rounded to 16 bits whatever o_dtype is (float32 caches: not rounded): to
  * bfloat16, or, with few rows per KV head over an FP8 / FP4 cache, weight times V scale to float16
  * relative to the row's largest, of which 2^-30 and less is lost. Their sum and lse are float32.
  * V scales may differ from page to page; magnitudes in [2^-60, 2^60], or 0.
- * A V row that is not finite makes the rows of a chunk undefined that see any key of its
- * 128-key tile, as a weight of zero does not cancel it; values behind seq_len do not matter.
- * A K row or query that is not finite gives NaN in the rows that see it.
+ * Logits x(s) of finite inputs are taken to stay below 2^26 in magnitude (float32 caches: any):
+ * beyond, their float32 form has no fraction left and a row can come out as NaN or 0.
+ * A V row that is not finite can make every row of its sequence in the call undefined, as a
+ * weight of zero does not cancel it in the rows that share its tile; values behind seq_len do
+ * not matter. A NaN in a K row or a query, or a logit of +inf, gives NaN in the rows that see
+ * it; a logit of -inf is a weight of 0.
  * workspace: at least hs2_fa_chunk_workspace(...) bytes, 256-byte aligned, contents ignored;
  * what it gives for some n_rows, max_n and max_t also suffices where any of them is smaller
  * (same Hq, kv and w). Calls that run at the same time need workspaces of their own.
@@ -389,8 +396,8 @@ hs2_status hs2_pages_fork(const hs2_pages* pages, int n_caches, const hs2_kv* kv
  * cache with its scales, and updates the references, the free list (the pages >= L, the
  * lowest taken first; entries behind are -1) and the entries of the caches' block table
  * below ceil(seq_len[b] / 64). That table must hold every sequence that has pages of the
- * pool. Bad entries (out of range, or of a free page: HS2_DEV_BAD_PAGE) and the rows of sequences with a bad length
- * (HS2_DEV_BAD_LENGTH) are left as they are.
+ * pool. Bad entries (out of range, or of a free page: HS2_DEV_BAD_PAGE) and the rows of
+ * sequences with a bad length (HS2_DEV_BAD_LENGTH) are left as they are.
  * workspace: at least hs2_pages_compact_workspace(pages) bytes, 256-byte aligned, contents
  * ignored. */
 size_t hs2_pages_compact_workspace(const hs2_pages* pages);

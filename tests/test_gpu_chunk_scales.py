@@ -158,3 +158,29 @@ def test_long_ranges(H, dtype):  # noqa: F811
     # 2200 keys of 128 threads: below 2e-4 in all
     check_relative((o, lse), want, slice(None), lse_tol=2 * LSE_TOL, rel=REL + 2e-4)
     del rng
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("n", [2, 300])
+def test_logits_up_to_the_documented_size(H, dtype, n):  # noqa: F811
+    """Logits of nearly 2^26: finite, lse within the logits' own fp32 errors (a sum of d = 128 products in
+    fp32: 128 * 2^-23 * scale * sum |q k|), and where the largest leads by more than twice those, the
+    row is that key's V up to a weight's rounding to 16 bits."""
+    t = 700
+    rng, c, bt, rs, qraw, qval = case(86, dtype, [t], [n], 8, 1, 128)
+    page, line = bt[0, np.arange(t) // 64], np.arange(t) % 64
+    k, v = (T.values(c, side, page, 0, line) for side in ("k", "v"))
+    x = np.einsum("nhd,td->nht", qval, k)
+    scale = float(np.float32(0.99 * 2.0 ** 26 / np.abs(x).max()))
+    seen = np.arange(t) <= t - n + np.arange(n)[:, None, None]
+    x = np.where(seen, scale * x, -np.inf)
+    off = 128 * 2.0 ** -23 * scale * np.where(seen, np.einsum("nhd,td->nht", np.abs(qval), np.abs(k)), 0).max(-1)
+    o, lse, err = run(H, c, bt, [t], rs, qraw, scale)
+    assert err == 0 and np.isfinite(o).all()
+    assert (np.abs(lse - x.max(-1)) <= off + 10).all()  # (log of the number of keys: below 10)
+    top = np.sort(x, -1)
+    clear = top[..., -1] - top[..., -2] > 2 * off + 40
+    assert clear.mean() > 0.9
+    want = v[x.argmax(-1)][clear]
+    assert (np.abs(o[clear] - want) <= 2.0 ** -8 * np.abs(want) + 1e-12).all()
+    del rng

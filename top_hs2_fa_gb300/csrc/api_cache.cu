@@ -71,7 +71,8 @@ struct ChunkCuts {
 //     (256), 477 and 480 (64 long ones); 8 sequences of 8 to 160 rows 67 with both, 40 wide, 64 long
 //     ones 603 and 590.
 //   up to 256 rows: one sequence of 256 rows and 32K keys 68 narrow, 95 wide; at 512 rows 98 and 95;
-//     8 sequences of 8K to 16K keys with 256 rows 143 and 134, with 512 rows 247 and 166 (FP4).
+//     8 sequences of 8K to 16K keys with 256 rows 143 and 134, with 512 rows 247 and 166 (FP4). So
+//     one sequence alone sets the border; the rule does not count sequences, and several lose 6 % there.
 //   few rows times keys: 5 sequences of 32 to 352 rows over 1K to 6K keys 35 narrow, 39 wide, 55 both;
 //     one of 512 rows and 2K keys 31 and 35, and 16K keys 62 and 56.
 //   little to expand: 12 sequences of 32 to 22400 rows over 1K to 6K keys 132 wide, 161 both; 9 of up

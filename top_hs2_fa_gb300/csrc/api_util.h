@@ -42,7 +42,7 @@ inline bool valid_kv(const hs2_kv* kv, bool need_v) {
   return true;
 }
 
-// FP8 / FP4 caches (quantised codes with scales): decode only
+// FP8 / FP4 caches (quantised codes with scales)
 inline bool low_precision(const hs2_kv* kv) { return kv->dtype == HS2_FP8_E4M3 || kv->dtype == HS2_FP4_E2M1; }
 
 inline bool pow2_le32(int g) { return g == 1 || g == 2 || g == 4 || g == 8 || g == 16 || g == 32; }
