@@ -26,11 +26,14 @@
 //                where its values would leave f16's range
 // A bf16 cache skips the conversions: its TMA tiles are the operands (bf16 Q, P).
 // Measured, with plan and merge, 64 sequences of 16K to 32K keys, 32 heads over 4, d = 128: single tokens
-// of bf16 476 us (1.01 of the copy bandwidth), FP8 296 (0.81), FP4 261 (0.52); 4 tokens of FP4 279
-// (0.48). FP4 is bound by the instructions and waits around its operands, not by any one pipe:
+// of bf16 471 us (1.02 of the copy bandwidth), FP8 296 (0.82), FP4 260 (0.52); 4 tokens of FP4 275
+// (0.50). FP4 is bound by the instructions and waits around its operands, not by any one pipe:
 // conversions fill 23 % of a tile's time, the MMAs 26 %.
-// The page's K scale multiplies the logits; V's enters P. Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four
-// softmax warps of a tile leave their loop together (they meet at a hardware barrier).
+// The page's K scale multiplies the logits; V's enters P, which rounds to f16, K's and V's type here
+// (off by 2^-11 at most; over a bf16 cache to bf16, 2^-8). One V scale for all rows of a tile, P
+// relative to the largest so far, cost 1 to 5 % more and lost rows whose own scales lie far below it.
+// Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four softmax warps of a
+// tile leave their loop together (they meet at a hardware barrier).
 #include <cuda.h>
 #include <cuda_fp16.h>
 

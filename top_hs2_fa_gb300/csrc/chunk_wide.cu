@@ -14,7 +14,8 @@
 //               then S_{j+1} = Q K^T over it
 //   warps 4-7, 8-11  softmax of half a, b: a thread has a whole row. p = 2^(x c - m) with the
 //               reference m moving only when it is exceeded by 2^8, P rounded to bf16 over the
-//               tile's own S columns, the normaliser summed in fp32 from unrounded weights
+//               tile's own S columns (an MMA's operands have one type, and V is bf16: a weight
+//               is off by at most 2^-8 of itself), the normaliser summed in fp32 from unrounded weights
 // FP8 / FP4 caches come as expanded bf16 pages: their page factors scale the logits (c) and the
 // weights (2^lv) per page, at no cost per element.
 // TMEM: S of a [0,128), of b [128,256), O of a [256,384), of b [384,512). Every wait is bounded.

@@ -86,7 +86,7 @@ def run_chunk(a) -> float:
     shape = (pages, Hkv, 64)
     dt, width = (torch.bfloat16, d) if a.kv == "bf16" else (torch.uint8, d if a.kv == "fp8" else d // 2)
     new = lambda w, dtype=torch.uint8: torch.zeros((*shape, w), dtype=dtype, device="cuda")  # noqa: E731
-    scale = lambda: None if a.kv == "bf16" else torch.full((pages, Hkv), 1 / 16, device="cuda")  # noqa: E731
+    scale = lambda: None if a.kv == "bf16" else torch.full((pages, Hkv), a.slab, device="cuda")  # noqa: E731
     sf = lambda: new(d // 16) if a.kv == "fp4" else None  # noqa: E731
     kv = hs2.KV(k=new(width, dt), v=new(width, dt), block_table=torch.full((B, -(-int(lens.max()) // 64)), -1,
                                                                            dtype=torch.int32, device="cuda"),
@@ -115,6 +115,7 @@ def main() -> None:
     ap.add_argument("--sa-layers", type=int, default=5)
     ap.add_argument("--tokens", type=int, default=4, help="chunk: query tokens of a sequence")
     ap.add_argument("--kv", choices=("bf16", "fp8", "fp4"), default="fp4", help="chunk: the cache's type")
+    ap.add_argument("--slab", type=float, default=1 / 16, help="chunk: the FP8 / FP4 cache's slab scales")
     ap.add_argument("--kv-fp8", action="store_true", help="decode: FP8 E4M3 paged KV")
     a = ap.parse_args()
     build.build()
