@@ -89,7 +89,8 @@ typedef enum { HS2_F32 = 0, HS2_BF16 = 1, HS2_FP8_E4M3 = 2, HS2_FP4_E2M1 = 3 } h
  *              FP8 and FP4 caches are written and read back by hs2_kv_write / hs2_kv_read,
  *              and read by hs2_fa_select (decode), hs2_sa_reuse (decode) and hs2_fa_chunk;
  *              queries are bf16; the prefill selection and the KV append refuse them.
- * page_size must be 64; d must be 64 or 128.                                        */
+ * page_size must be 64; d must be 64 or 128, in a latent cache 576 or 320 (hs2_latent_write;
+ *              hs2_pages_fork and hs2_pages_compact take those too).                    */
 typedef struct {
   const void* k;
   const void* v;
@@ -345,6 +346,88 @@ size_t hs2_fa_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, i
 hs2_status hs2_fa_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
                         int max_t, int w, float scale, const float* sink, void* o, hs2_dtype o_dtype, float* lse,
                         void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rows rotated by their positions on the way into a cache (rotary position embedding).
+ * hs2_rot: table float32 [n_pos][dim] (device, 16-byte aligned): row p has the cosines of position
+ * p's dim / 2 angles, then their sines. The first dim channels of a head are rotated (dim a
+ * multiple of 32 up to d), in pairs (a, b) = (x_i, x_{i + dim/2}), with pairs = 1 (x_2i, x_2i+1):
+ *   a' = a cos_i - b sin_i,  b' = b cos_i + a sin_i,
+ * every product and sum rounded to float32 by itself, then the result to where it goes. */
+typedef struct {
+  const float* table;
+  int32_t n_pos;
+  int32_t dim;
+  int32_t pairs;
+} hs2_rot;
+
+/* hs2_kv_write with K, and optionally the queries of the same rows, rotated: rows, positions, types
+ * and errors as there; K and V rows have a token stride each. q: [n_rows][Hq][d] of row_dtype, token r
+ * at r * q_stride elements, or NULL with Hq = 0; q_out: the rotated queries as hs2_fa_chunk takes
+ * them, float32 for an F32 cache, else bfloat16, [n_rows][Hq][d] at q_out_stride; it may be q itself
+ * (same type and stride) and overlaps nothing else. Rows that are flagged or outside every sequence have
+ * neither their cache rows nor their q_out written. A position of n_pos or more sets
+ * HS2_DEV_BAD_INDEX. All cache types. */
+hs2_status hs2_kv_write_rot(const hs2_kv* kv, const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
+                            hs2_dtype row_dtype, const int32_t* row_start, int n_rows, const hs2_rot* rot, const void* q,
+                            int64_t q_stride, int Hq, void* q_out, int64_t q_out_stride, int32_t* dev_err, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Latent attention: keys and values of all heads from one latent vector a token, plus a key part
+ * that carries the position ([L10] §5.1: the V3.2 layers' latent of 512 + 64 channels).
+ * A latent cache is an hs2_kv with v = NULL, Hkv = 1 and d = dc + 64, dc 512 or 256: a row is dc
+ * latent channels c and 64 rotated channels r. F32 or BF16; FP8 / FP4: HS2_ERR_UNSUPPORTED.
+ *
+ * hs2_latent_write stores c_rows ([n_rows][dc]) as they are and r_rows ([n_rows][64]) rotated (rot->dim
+ * must be 64), and writes the queries' rotated part q ([n_rows][Hq][64], or NULL with Hq = 0) to
+ * q_out, of the cache's type. Token r of an array is at r times its stride (elements), head h of q and
+ * q_out at h times q_head / q_out_head; all 16-byte aligned with strides of a multiple of 16 bytes.
+ * q_out is typically the last 64 channels of [n_rows][Hq][dc + 64]; it may be q itself.
+ * hs2_latent_read gets rows back (c and r of row_dtype; r as stored, rotated), e.g. to expand them.
+ * Rows, positions and errors as in hs2_kv_write / hs2_kv_read / hs2_kv_write_rot. */
+hs2_status hs2_latent_write(const hs2_kv* kv, const void* c_rows, int64_t c_stride, const void* r_rows, int64_t r_stride,
+                            hs2_dtype row_dtype, const int32_t* row_start, int n_rows, const hs2_rot* rot, const void* q,
+                            int64_t q_stride, int64_t q_head, int Hq, void* q_out, int64_t q_out_stride,
+                            int64_t q_out_head, int32_t* dev_err, void* stream);
+hs2_status hs2_latent_read(const hs2_kv* kv, void* c_rows, int64_t c_stride, void* r_rows, int64_t r_stride,
+                           hs2_dtype row_dtype, const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream);
+
+/* hs2_latent_chunk, the absorbed form: causal attention of a ragged batch of query chunks over a
+ * latent cache, rows as in hs2_fa_chunk. q: [n_rows][Hq][dc + 64] of the cache's type, the queries
+ * taken into the latent space and their rotated part. Row at position p, head h:
+ *   x(s) = scale * q_h . [c_s, r_s], s <= p;  o = sum_s softmax(x)(s) c_s;  lse = log sum_s exp x(s).
+ * o: [n_rows][Hq][dc] of o_dtype (HS2_F32 or HS2_BF16), lse float32 [n_rows][Hq] or NULL. Hq a power
+ * of two up to 128. Bad pages and lengths, sizes, precision, workspace: as hs2_fa_chunk (bf16 caches:
+ * the weights enter the second product rounded to bfloat16; float32 caches: not rounded). */
+size_t hs2_latent_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t);
+hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
+                            int max_t, float scale, void* o, hs2_dtype o_dtype, float* lse, void* workspace,
+                            size_t ws_bytes, int32_t* dev_err, void* stream);
+
+/* hs2_latent_prefill, the expanded form: the same attention with K and V of every head expanded from
+ * the latents, for prompts (a fifth to a third of the absorbed form's operations per key). Keys are
+ * packed like rows: sequence b has keys [key_start[b], key_start[b+1]) and its rows
+ * [row_start[b], row_start[b+1]) are its LAST positions. Head h:
+ *   x(s) = scale * (q_h[0:128] . k_{s,h} + q_h[128:192] . r_s),  o = sum_s softmax(x)(s) v_{s,h}.
+ * hs2_latent_keys: k, v [n_keys][Hq][128] with token and head strides (elements; slices of the
+ * expansion's output fit), r [n_keys][64] shared by the heads; HS2_F32 or HS2_BF16, 16-byte aligned
+ * with strides of a multiple of 16 bytes. q: [n_rows][Hq][192] of the same type; o:
+ * [n_rows][Hq][128] of o_dtype. A sequence with n_b > max_n, more keys than max_t, fewer keys than rows,
+ * or rows or keys outside the arrays sets HS2_DEV_BAD_LENGTH and its rows are not written (a
+ * descending row_start or key_start: none or only some rows are). Precision and workspace as hs2_fa_chunk. */
+typedef struct {
+  const void* k;
+  const void* r;
+  const void* v;
+  int64_t k_token, k_head, r_token, v_token, v_head;
+  const int32_t* key_start; /* [batch + 1] */
+  int32_t n_keys;
+  hs2_dtype dtype;
+} hs2_latent_keys;
+size_t hs2_latent_prefill_workspace(int n_rows, int Hq, int batch, int max_n, int max_t);
+hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, int batch,
+                              const hs2_latent_keys* keys, int max_t, float scale, void* o, hs2_dtype o_dtype, float* lse,
+                              void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream);
 
 /* ---------------------------------------------------------------------------
  * Pages of a pool: room for sequences, branches that share pages, defragmentation. All on

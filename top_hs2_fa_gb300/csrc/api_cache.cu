@@ -234,7 +234,7 @@ bool page_caches(const hs2_pages* pages, int n_caches, const hs2_kv* kvs, hs2::P
   };
   for (int c = 0; c < n_caches; ++c) {
     const hs2_kv* kv = &kvs[c];
-    if (!valid_kv(kv, false) || (kv->v && !valid_kv(kv, true))) return false;
+    if (valid_latent(kv) ? low_precision(kv) : !valid_kv(kv, false) || (kv->v && !valid_kv(kv, true))) return false;
     if (kv->num_pages != pages->num_pages || kv->block_table != kvs[0].block_table || kv->seq_len != kvs[0].seq_len ||
         kv->batch != kvs[0].batch || kv->max_pages != kvs[0].max_pages)
       return false;

@@ -1,0 +1,238 @@
+// api_latent.cu — the extern "C" boundary of latent attention and of the rows that are rotated on
+// their way into a cache. Validation and launches as in api.cu.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/hs2.h"
+#include "api_util.h"
+#include "kernels.h"
+
+using namespace hs2::api;
+
+namespace {
+
+int elem_bytes(hs2_dtype t) { return t == HS2_F32 ? 4 : 2; }
+bool row_type(hs2_dtype t) { return t == HS2_F32 || t == HS2_BF16; }
+// a row array's base and a stride of it: 16-byte loads
+bool rows16(const void* p, int64_t stride, hs2_dtype t) { return p && aligned16(p) && stride * elem_bytes(t) % 16 == 0; }
+
+// Bounds on strides and counts that keep products within 64 bits.
+constexpr int64_t kMaxStride = 1LL << 31;
+
+bool valid_rot(const hs2_rot* r, int d) {
+  return r && r->table && aligned16(r->table) && r->n_pos >= 1 && r->dim >= 32 && r->dim <= d && r->dim % 32 == 0 &&
+         (r->pairs == 0 || r->pairs == 1);
+}
+hs2::RotTable rot_table(const hs2_rot* r) { return {r->table, r->n_pos, r->dim, r->pairs}; }
+
+hs2::RowsArgs rows_args(const hs2_kv* kv, const int32_t* row_start, int n_rows, int32_t* dev_err) {
+  hs2::RowsArgs a{};
+  a.k = const_cast<void*>(kv->k);
+  a.v = const_cast<void*>(kv->v);
+  a.k_scale = kv->k_scale;
+  a.v_scale = kv->v_scale;
+  a.k_sf = const_cast<uint8_t*>(kv->k_sf);
+  a.v_sf = const_cast<uint8_t*>(kv->v_sf);
+  a.bt = kv->block_table;
+  a.seq_len = kv->seq_len;
+  a.batch = kv->batch;
+  a.num_pages = kv->num_pages;
+  a.max_pages = kv->max_pages;
+  a.Hkv = kv->Hkv;
+  a.row_start = row_start;
+  a.n_rows = n_rows;
+  a.dev_err = dev_err;
+  return a;
+}
+
+hs2_status latent_rows(const hs2_kv* kv, const void* c_rows, int64_t c_stride, const void* r_rows, int64_t r_stride,
+                       hs2_dtype row_dtype, const int32_t* row_start, int n_rows, hs2::LatentRowsArgs& z, bool write,
+                       int32_t* dev_err, void* stream) {
+  z.rows = rows_args(kv, row_start, n_rows, dev_err);
+  z.c_rows = c_rows;
+  z.r_rows = r_rows;
+  z.c_stride = c_stride;
+  z.r_stride = r_stride;
+  const cudaError_t e = hs2::launch_latent_rows(z, kv->d - hs2::kLatentRot, kv->dtype == HS2_F32, row_dtype == HS2_F32,
+                                                write, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+// The checks that the reading and the writing of latent rows share; HS2_OK with *go = false: nothing to do.
+hs2_status check_latent_rows(const hs2_kv* kv, const void* c_rows, int64_t c_stride, const void* r_rows,
+                             int64_t r_stride, hs2_dtype row_dtype, const int32_t* row_start, int n_rows, bool* go) {
+  *go = false;
+  if (!valid_latent(kv) || !row_start || n_rows < 0 || !row_type(row_dtype)) return HS2_ERR_ARG;
+  if (low_precision(kv)) return HS2_ERR_UNSUPPORTED;
+  if (n_rows == 0) return HS2_OK;
+  if (!rows16(c_rows, c_stride, row_dtype) || !rows16(r_rows, r_stride, row_dtype)) return HS2_ERR_ARG;
+  if (c_stride < kv->d - hs2::kLatentRot || r_stride < hs2::kLatentRot || c_stride > kMaxStride || r_stride > kMaxStride)
+    return HS2_ERR_ARG;
+  *go = true;
+  return HS2_OK;
+}
+
+// What the two attention forms take alike.
+bool valid_attention(int n_rows, int max_n, int max_t, float scale, hs2_dtype o_dtype) {
+  return n_rows >= 0 && max_n >= 0 && max_n <= max_t && std::isfinite(scale) && scale > 0.f && row_type(o_dtype);
+}
+bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
+
+hs2::ChunkArgs chunk_args(const void* q, const int32_t* row_start, int n_rows, int max_n, int max_t, int batch, int Hq,
+                          float scale, void* o, hs2_dtype o_dtype, float* lse, int32_t* dev_err) {
+  hs2::ChunkArgs a{};
+  a.q = q;
+  a.row_start = row_start;
+  a.n_rows = n_rows;
+  a.max_n = max_n;
+  a.max_t = max_t;
+  a.batch = batch;
+  a.Hq = Hq;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.o = o;
+  a.o_bf16 = o_dtype == HS2_BF16;
+  a.lse = lse;
+  a.dev_err = dev_err;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+hs2_status hs2_kv_write_rot(const hs2_kv* kv, const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
+                            hs2_dtype row_dtype, const int32_t* row_start, int n_rows, const hs2_rot* rot, const void* q,
+                            int64_t q_stride, int Hq, void* q_out, int64_t q_out_stride, int32_t* dev_err, void* stream) {
+  if (!valid_kv(kv, false) || (kv->v && !valid_kv(kv, true))) return HS2_ERR_ARG;
+  if (!row_start || n_rows < 0 || !row_type(row_dtype) || !valid_rot(rot, kv->d)) return HS2_ERR_ARG;
+  if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
+  if (n_rows == 0) return HS2_OK;
+  const int64_t row = (int64_t)kv->Hkv * kv->d, q_row = (int64_t)Hq * kv->d;
+  if (!rows16(k_rows, k_stride, row_dtype) || k_stride < row || k_stride > kMaxStride) return HS2_ERR_ARG;
+  if (kv->v && (!rows16(v_rows, v_stride, row_dtype) || v_stride < row || v_stride > kMaxStride)) return HS2_ERR_ARG;
+  const hs2_dtype q_type = kv->dtype == HS2_F32 ? HS2_F32 : HS2_BF16;
+  if (q && (!rows16(q, q_stride, row_dtype) || q_stride < q_row || q_stride > kMaxStride ||
+            !rows16(q_out, q_out_stride, q_type) || q_out_stride < q_row || q_out_stride > kMaxStride))
+    return HS2_ERR_ARG;
+  if (q && q == q_out && (q_type != row_dtype || q_stride != q_out_stride)) return HS2_ERR_ARG;
+  if (kv->Hkv > 65535 || Hq > 65535) return HS2_ERR_UNSUPPORTED;
+  hs2::RotRowsArgs z{};
+  z.rows = rows_args(kv, row_start, n_rows, dev_err);
+  z.rows.k_rows = k_rows;
+  z.rows.v_rows = v_rows;
+  z.rows.row_stride = k_stride;
+  z.v_stride = v_stride;
+  z.rot = rot_table(rot);
+  z.q = q;
+  z.q_out = q_out;
+  z.q_stride = q_stride;
+  z.q_out_stride = q_out_stride;
+  z.Hq = Hq;
+  const cudaError_t e = hs2::launch_kv_write_rot(z, kv->d, kv->dtype, row_dtype == HS2_F32, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+hs2_status hs2_latent_write(const hs2_kv* kv, const void* c_rows, int64_t c_stride, const void* r_rows, int64_t r_stride,
+                            hs2_dtype row_dtype, const int32_t* row_start, int n_rows, const hs2_rot* rot, const void* q,
+                            int64_t q_stride, int64_t q_head, int Hq, void* q_out, int64_t q_out_stride,
+                            int64_t q_out_head, int32_t* dev_err, void* stream) {
+  if (!valid_rot(rot, hs2::kLatentRot) || rot->dim != hs2::kLatentRot) return HS2_ERR_ARG;
+  if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
+  bool go;
+  const hs2_status st = check_latent_rows(kv, c_rows, c_stride, r_rows, r_stride, row_dtype, row_start, n_rows, &go);
+  if (!go) return st;
+  if (q) {
+    // heads apart from one another, rows apart from one another
+    auto apart = [&](const void* p, int64_t stride, int64_t head, hs2_dtype t) {
+      return rows16(p, stride, t) && head * elem_bytes(t) % 16 == 0 && head >= hs2::kLatentRot && head <= kMaxStride &&
+             stride >= (Hq - 1) * head + hs2::kLatentRot && stride <= kMaxStride;
+    };
+    if (Hq > 65535 || !apart(q, q_stride, q_head, row_dtype) || !apart(q_out, q_out_stride, q_out_head, kv->dtype))
+      return HS2_ERR_ARG;
+    if (q == q_out && (kv->dtype != row_dtype || q_stride != q_out_stride || q_head != q_out_head)) return HS2_ERR_ARG;
+  }
+  hs2::LatentRowsArgs z{};
+  z.rot = rot_table(rot);
+  z.q = q;
+  z.q_out = q_out;
+  z.q_stride = q_stride;
+  z.q_head = q_head;
+  z.q_out_stride = q_out_stride;
+  z.q_out_head = q_out_head;
+  z.Hq = Hq;
+  return latent_rows(kv, c_rows, c_stride, r_rows, r_stride, row_dtype, row_start, n_rows, z, true, dev_err, stream);
+}
+
+hs2_status hs2_latent_read(const hs2_kv* kv, void* c_rows, int64_t c_stride, void* r_rows, int64_t r_stride,
+                           hs2_dtype row_dtype, const int32_t* row_start, int n_rows, int32_t* dev_err, void* stream) {
+  bool go;
+  const hs2_status st = check_latent_rows(kv, c_rows, c_stride, r_rows, r_stride, row_dtype, row_start, n_rows, &go);
+  if (!go) return st;
+  hs2::LatentRowsArgs z{};
+  return latent_rows(kv, c_rows, c_stride, r_rows, r_stride, row_dtype, row_start, n_rows, z, false, dev_err, stream);
+}
+
+size_t hs2_latent_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t) {
+  if (!valid_latent(kv) || n_rows < 0 || max_n < 0 || max_t < 0 || Hq < 1 || !heads_supported(Hq)) return 0;
+  return 256;
+}
+
+hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
+                            int max_t, float scale, void* o, hs2_dtype o_dtype, float* lse, void* workspace,
+                            size_t ws_bytes, int32_t* dev_err, void* stream) {
+  if (!valid_latent(kv) || !row_start || Hq < 1 || !valid_attention(n_rows, max_n, max_t, scale, o_dtype))
+    return HS2_ERR_ARG;
+  if (low_precision(kv) || !heads_supported(Hq)) return HS2_ERR_UNSUPPORTED;
+  if ((long long)max_t > (long long)kv->max_pages * 64) return HS2_ERR_ARG;
+  if (n_rows == 0 || max_n == 0) return HS2_OK;
+  if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < 256) return HS2_ERR_ARG;
+  hs2::ChunkArgs a = chunk_args(q, row_start, n_rows, max_n, max_t, kv->batch, Hq, scale, o, o_dtype, lse, dev_err);
+  a.k = kv->k;
+  a.bt = kv->block_table;
+  a.seq_len = kv->seq_len;
+  a.num_pages = kv->num_pages;
+  a.max_pages = kv->max_pages;
+  const cudaError_t e = hs2::launch_latent_cc(a, {}, kv->d - hs2::kLatentRot, kv->dtype == HS2_F32, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+size_t hs2_latent_prefill_workspace(int n_rows, int Hq, int batch, int max_n, int max_t) {
+  if (n_rows < 0 || Hq < 1 || batch < 1 || max_n < 0 || max_t < 0) return 0;
+  return 256;
+}
+
+hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, int batch,
+                              const hs2_latent_keys* keys, int max_t, float scale, void* o, hs2_dtype o_dtype, float* lse,
+                              void* workspace, size_t ws_bytes, int32_t* dev_err, void* stream) {
+  if (!row_start || !keys || Hq < 1 || batch < 1 || !valid_attention(n_rows, max_n, max_t, scale, o_dtype) ||
+      !row_type(keys->dtype) || !keys->key_start || keys->n_keys < 0)
+    return HS2_ERR_ARG;
+  if (n_rows == 0 || max_n == 0) return HS2_OK;
+  if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
+  if (keys->n_keys > 0) {
+    auto strided = [&](const void* p, int64_t token, int64_t head, int width) {
+      return rows16(p, token, keys->dtype) && head * elem_bytes(keys->dtype) % 16 == 0 && head >= width &&
+             head <= kMaxStride && token >= width && token <= kMaxStride;
+    };
+    if (!strided(keys->k, keys->k_token, keys->k_head, hs2::kLatentNope) ||
+        !strided(keys->v, keys->v_token, keys->v_head, hs2::kLatentValue) ||
+        !strided(keys->r, keys->r_token, hs2::kLatentRot, hs2::kLatentRot))
+      return HS2_ERR_ARG;
+  }
+  if (Hq > 65535) return HS2_ERR_UNSUPPORTED;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < 256) return HS2_ERR_ARG;
+  hs2::ChunkArgs a = chunk_args(q, row_start, n_rows, max_n, max_t, batch, Hq, scale, o, o_dtype, lse, dev_err);
+  a.k = keys->k;
+  a.v = keys->v;
+  a.key_start = keys->key_start;
+  a.n_keys = keys->n_keys;
+  const hs2::LatentKeys lk{keys->r, keys->k_token, keys->k_head, keys->v_token, keys->v_head, keys->r_token};
+  const cudaError_t e = hs2::launch_latent_cc(a, lk, 0, keys->dtype == HS2_F32, (cudaStream_t)stream);
+  return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+}
+
+}  // extern "C"

@@ -42,6 +42,14 @@ inline bool valid_kv(const hs2_kv* kv, bool need_v) {
   return true;
 }
 
+// A latent cache: key-only, one KV head, rows of 512 or 256 latent and 64 rotated channels.
+inline bool valid_latent(const hs2_kv* kv) {
+  return kv && kv->k && !kv->v && kv->block_table && kv->seq_len && kv->batch >= 1 && kv->num_pages >= 1 &&
+         kv->max_pages >= 1 && kv->Hkv == 1 && kv->page_size == 64 && (kv->d == 576 || kv->d == 320) &&
+         (kv->dtype == HS2_F32 || kv->dtype == HS2_BF16 || kv->dtype == HS2_FP8_E4M3 || kv->dtype == HS2_FP4_E2M1) &&
+         aligned16(kv->k);
+}
+
 // FP8 / FP4 caches (quantised codes with scales)
 inline bool low_precision(const hs2_kv* kv) { return kv->dtype == HS2_FP8_E4M3 || kv->dtype == HS2_FP4_E2M1; }
 

@@ -102,6 +102,36 @@ struct RowsArgs {
   int32_t* dev_err;
 };
 
+// cos and sin by position, float32 [n_pos][dim]: cos of the dim / 2 pairs, then sin.
+struct RotTable {
+  const float* table;  // null: none
+  int n_pos, dim;
+  int pairs;  // neighbours (2i, 2i + 1) instead of (i, i + dim / 2)
+};
+// hs2_kv_write with K and the queries rotated.
+struct RotRowsArgs {
+  RowsArgs rows;
+  long long v_stride;  // v_rows' token stride (rows.row_stride: k_rows')
+  RotTable rot;
+  const void* q;  // [n_rows][Hq][d] of the rows' type, or null (Hq = 0)
+  void* q_out;    // float32 for an F32 cache, else bfloat16; may be q
+  long long q_stride, q_out_stride;
+  int Hq;
+};
+// Rows of a latent cache ([num_pages][64][dc + 64]): rows.k is the pool.
+constexpr int kLatentRot = 64;
+struct LatentRowsArgs {
+  RowsArgs rows;
+  const void* c_rows;  // [n_rows][dc], [n_rows][64] (read: written to)
+  const void* r_rows;
+  long long c_stride, r_stride;
+  RotTable rot;
+  const void* q;  // [n_rows][Hq][64], or null (Hq = 0)
+  void* q_out;
+  long long q_stride, q_head, q_out_stride, q_out_head;
+  int Hq;
+};
+
 // Attention of a ragged batch of query chunks (the last rows of every sequence).
 struct ChunkArgs {
   const void* q;  // [n_rows][Hq][D]
@@ -124,6 +154,18 @@ struct ChunkArgs {
   int o_bf16;
   float* lse;  // [n_rows][Hq], or null
   int32_t* dev_err;
+  // keys packed like the rows instead of paged: sequence b's are [key_start[b], key_start[b+1]) of
+  // n_keys (null: paged, seq_len and bt)
+  const int32_t* key_start;
+  int n_keys;
+};
+
+// Expanded keys of latent attention: ChunkArgs' k [n_keys][Hq][128] and v [n_keys][Hq][128] with these
+// strides (elements), r [n_keys][64] shared by the heads.
+constexpr int kLatentNope = 128, kLatentValue = 128;
+struct LatentKeys {
+  const void* r;
+  long long k_token, k_head, v_token, v_head, r_token;
 };
 
 // The plan of a persistent chunk-attention kernel (device memory, written by the planning
@@ -300,6 +342,9 @@ struct SelectArgs {
 
 cudaError_t launch_fa_decode_mma(const AttnArgs& a, int Bq, cudaStream_t s);
 cudaError_t launch_kv_rows(const RowsArgs& a, int d, int dtype, bool write, bool row_f32, cudaStream_t s);
+cudaError_t launch_kv_write_rot(const RotRowsArgs& z, int d, int dtype, bool row_f32, cudaStream_t s);
+cudaError_t launch_latent_rows(const LatentRowsArgs& z, int dc, bool cache_f32, bool row_f32, bool write, cudaStream_t s);
+cudaError_t launch_latent_cc(const ChunkArgs& a, const LatentKeys& lk, int dc, bool f32, cudaStream_t s);
 cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s);
 cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s);
 cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, int dtype, void* ek, void* ev,

@@ -28,6 +28,8 @@ EXPORTS = (
     "hs2_kv_append", "hs2_fa_select_append", "hs2_fa_select_launches", "hs2_sa_reuse_launches",
     "hs2_kv_write", "hs2_kv_read", "hs2_fa_chunk_workspace", "hs2_fa_chunk", "hs2_pages_grow", "hs2_pages_free",
     "hs2_pages_fork", "hs2_pages_compact_workspace", "hs2_pages_compact",
+    "hs2_kv_write_rot", "hs2_latent_write", "hs2_latent_read", "hs2_latent_chunk_workspace", "hs2_latent_chunk",
+    "hs2_latent_prefill_workspace", "hs2_latent_prefill",
 )
 STAGE_FA_SCAN, STAGE_SA_GATHER, STAGE_INDEXER = 0, 1, 2
 SA_OVERLAP = 1  # HS2_SA_OVERLAP
@@ -46,6 +48,18 @@ class hs2_kv(ctypes.Structure):
 class hs2_pages(ctypes.Structure):
     _fields_ = [("ref", ctypes.c_void_p), ("free_list", ctypes.c_void_p), ("n_free", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32)]
+
+
+class hs2_rot(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("n_pos", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("pairs", ctypes.c_int32)]
+
+
+class hs2_latent_keys(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("r", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_token", ctypes.c_int64), ("k_head", ctypes.c_int64), ("r_token", ctypes.c_int64),
+                ("v_token", ctypes.c_int64), ("v_head", ctypes.c_int64), ("key_start", ctypes.c_void_p),
+                ("n_keys", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
 class HS2Error(RuntimeError):
@@ -123,6 +137,21 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.hs2_pages_compact_workspace.restype = sz
     lib.hs2_pages_compact.argtypes = [pgp, i32, kvp, vp, sz, vp, vp]
     lib.hs2_pages_compact.restype = i32
+    rotp, lkp = ctypes.POINTER(hs2_rot), ctypes.POINTER(hs2_latent_keys)
+    lib.hs2_kv_write_rot.argtypes = [kvp, vp, i64, vp, i64, i32, vp, i32, rotp, vp, i64, i32, vp, i64, vp, vp]
+    lib.hs2_kv_write_rot.restype = i32
+    lib.hs2_latent_write.argtypes = [kvp, vp, i64, vp, i64, i32, vp, i32, rotp, vp, i64, i64, i32, vp, i64, i64, vp, vp]
+    lib.hs2_latent_write.restype = i32
+    lib.hs2_latent_read.argtypes = [kvp, vp, i64, vp, i64, i32, vp, i32, vp, vp]
+    lib.hs2_latent_read.restype = i32
+    lib.hs2_latent_chunk_workspace.argtypes = [i32, i32, kvp, i32, i32]
+    lib.hs2_latent_chunk_workspace.restype = sz
+    lib.hs2_latent_chunk.argtypes = [vp, vp, i32, i32, i32, kvp, i32, f32, vp, i32, vp, vp, sz, vp, vp]
+    lib.hs2_latent_chunk.restype = i32
+    lib.hs2_latent_prefill_workspace.argtypes = [i32, i32, i32, i32, i32]
+    lib.hs2_latent_prefill_workspace.restype = sz
+    lib.hs2_latent_prefill.argtypes = [vp, vp, i32, i32, i32, i32, lkp, i32, f32, vp, i32, vp, vp, sz, vp, vp]
+    lib.hs2_latent_prefill.restype = i32
     if lib.hs2_abi_version() != ABI_VERSION:
         raise HS2Error(f"libhs2 ABI {lib.hs2_abi_version()} != binding ABI {ABI_VERSION}: rebuild the library")
     _lib = lib
@@ -587,6 +616,220 @@ def hs2_fa_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float,
     _check(lib.hs2_fa_chunk(q.data_ptr(), row_start.data_ptr(), n, max_n, Hq, ctypes.byref(c), max_t, w, scale,
                             _ptr(sink), o.data_ptr(), _ROW_DTYPES[o_dtype], _ptr(lse), ws.data_ptr(), ws.nbytes,
                             _ptr(dev_err), st))
+    return o, lse
+
+
+# ---------------------------------------------------------------------------- rotated rows, latent attention
+_STYLES = {"halves": 0, "pairs": 1}
+
+
+def _rot(rot: torch.Tensor, style: str) -> hs2_rot:
+    """The table of cosines and sines, float32 [positions][dim], and how channels pair up."""
+    if rot.dtype is not torch.float32 or rot.dim() != 2 or not rot.is_contiguous():
+        raise HS2Error("rot must be a contiguous float32 matrix")
+    if style not in _STYLES:
+        raise HS2Error("style must be 'halves' or 'pairs'")
+    return hs2_rot(rot.data_ptr(), rot.shape[0], rot.shape[1], _STYLES[style])
+
+
+def _strides(t: torch.Tensor, name: str, *shape):
+    """(token, head) strides of rows t [n][...][width] of that shape, the last channels contiguous."""
+    if t.shape != shape or t.stride(-1) != 1:
+        raise HS2Error(f"{name} must be of shape {list(shape)} with contiguous channels")
+    width = shape[-1]
+    head = (t.stride(1) if shape[1] > 1 else width) if len(shape) == 3 else width
+    # (one token: its stride reaches nothing)
+    return t.stride(0) if shape[0] > 1 else (shape[1] - 1) * head + width if len(shape) == 3 else width, head
+
+
+def hs2_kv_write_rot(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor,
+                     rot: torch.Tensor, style: str = "halves", q: torch.Tensor | None = None, q_out=None, dev_err=None,
+                     stream=None):
+    """hs2_kv_write with K, and the queries ``q`` [n_rows][Hq][d] of the same rows, rotated by their
+    positions. ``rot``: float32 [positions][dim], the cosines of each position's dim / 2 angles, then the
+    sines; the first ``dim`` channels of a head are rotated, channel i with i + dim / 2
+    (``style`` "halves") or 2i with 2i + 1 ("pairs"). Returns the rotated queries as hs2_fa_chunk
+    takes them (bfloat16; float32 for an F32 cache), in ``q_out`` if given (it may be ``q``)."""
+    lib = load()
+    c, dev = kv._cached()[:2]
+    dtype = k_rows.dtype
+    if (v_rows is None) != (kv.v is None):
+        raise HS2Error("v_rows goes with a cache that has V")
+    if dtype not in _ROW_DTYPES or any(x is not None and x.dtype is not dtype for x in (v_rows, q)):
+        raise HS2Error("rows must be float32 or bfloat16, K, V and q alike")
+    n = k_rows.shape[0]
+    ks = _token_stride(k_rows.shape, k_rows.stride(), n, c)
+    vs = ks if v_rows is None else _token_stride(v_rows.shape, v_rows.stride(), n, c)
+    _i32(row_start, "row_start", c.batch + 1)
+    Hq = qs = os_ = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs, qh = _strides(q, "q", n, Hq, c.d)
+        out_type = torch.float32 if c.dtype == F32 else torch.bfloat16
+        if q_out is None:
+            q_out = _new((n, Hq, c.d), out_type, q.device, stream)
+        os_, oh = _strides(q_out, "q_out", n, Hq, c.d)
+        if q_out.dtype is not out_type or qh != c.d or oh != c.d:
+            raise HS2Error("q and q_out must have contiguous tokens, q_out bfloat16 (float32 for an F32 cache)")
+    elif q_out is not None:
+        raise HS2Error("q_out goes with q")
+    r = _rot(rot, style)
+    st = _launch_stream(stream, dev, k_rows, v_rows, row_start, rot, q, q_out, dev_err)
+    _check(lib.hs2_kv_write_rot(ctypes.byref(c), k_rows.data_ptr(), ks, _ptr(v_rows), vs, _ROW_DTYPES[dtype],
+                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs, Hq,
+                                _ptr(q_out) if Hq else None, os_, _ptr(dev_err), st))
+    return q_out
+
+
+def _latent(c: hs2_kv) -> int:
+    """Latent channels of a latent cache, or an error."""
+    if c.v or c.Hkv != 1 or c.d not in (576, 320) or c.dtype not in (F32, BF16):
+        raise HS2Error("a latent cache has k [num_pages][1][64][576 or 320], float32 or bfloat16, and no v")
+    return c.d - 64
+
+
+def hs2_latent_write(kv: KV, c_rows: torch.Tensor, r_rows: torch.Tensor, row_start: torch.Tensor, rot: torch.Tensor,
+                     style: str = "pairs", q: torch.Tensor | None = None, q_out: torch.Tensor | None = None, dev_err=None,
+                     stream=None):
+    """Rows of a ragged batch into a latent cache (``kv.k`` [num_pages][1][64][dc + 64], no v): ``c_rows``
+    [n_rows][dc] as they are, ``r_rows`` [n_rows][64] rotated by their positions; and the queries'
+    rotated part ``q`` [n_rows][Hq][64] to ``q_out`` (of the cache's type; a slice of the queries that
+    hs2_latent_chunk takes, or ``q`` itself). ``rot`` and ``style`` as in hs2_kv_write_rot, over 64
+    channels. Returns ``q_out``."""
+    lib = load()
+    c, dev = kv._cached()[:2]
+    dc, dtype = _latent(c), c_rows.dtype
+    if dtype not in _ROW_DTYPES or any(x is not None and x.dtype is not dtype for x in (r_rows, q)):
+        raise HS2Error("rows must be float32 or bfloat16, c, r and q alike")
+    n = c_rows.shape[0]
+    cs, rs = _strides(c_rows, "c_rows", n, dc)[0], _strides(r_rows, "r_rows", n, 64)[0]
+    _i32(row_start, "row_start", c.batch + 1)
+    Hq = qs = qh = os_ = oh = 0
+    if q is not None:
+        Hq = q.shape[1] if q.dim() == 3 else 0
+        qs, qh = _strides(q, "q", n, Hq, 64)
+        out_type = torch.float32 if c.dtype == F32 else torch.bfloat16
+        if q_out is None:
+            q_out = _new((n, Hq, 64), out_type, q.device, stream)
+        os_, oh = _strides(q_out, "q_out", n, Hq, 64)
+        if q_out.dtype is not out_type:
+            raise HS2Error("q_out must be of the cache's type")
+    elif q_out is not None:
+        raise HS2Error("q_out goes with q")
+    r = _rot(rot, style)
+    st = _launch_stream(stream, dev, c_rows, r_rows, row_start, rot, q, q_out, dev_err)
+    _check(lib.hs2_latent_write(ctypes.byref(c), c_rows.data_ptr(), cs, r_rows.data_ptr(), rs, _ROW_DTYPES[dtype],
+                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs, qh, Hq,
+                                _ptr(q_out) if Hq else None, os_, oh, _ptr(dev_err), st))
+    return q_out
+
+
+def hs2_latent_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype = torch.bfloat16, out=None,
+                    dev_err=None, stream=None):
+    """The rows hs2_latent_write with this ``row_start`` would write, as (c [n_rows][dc], r
+    [n_rows][64]) of ``dtype``, r as stored (rotated). Rows outside every sequence are left as they
+    are in ``out``."""
+    c, dev = kv._cached()[:2]
+    dc = _latent(c)
+    if dtype not in _ROW_DTYPES:
+        raise HS2Error("dtype must be float32 or bfloat16")
+    if out is None:
+        out = _new((n_rows, dc), dtype, kv.k.device, stream), _new((n_rows, 64), dtype, kv.k.device, stream)
+    elif out[0].dtype is not dtype or out[1].dtype is not dtype:
+        raise HS2Error("out must be of the dtype")
+    cs, rs = _strides(out[0], "out[0]", n_rows, dc)[0], _strides(out[1], "out[1]", n_rows, 64)[0]
+    _i32(row_start, "row_start", c.batch + 1)
+    st = _launch_stream(stream, dev, row_start, out[0], out[1], dev_err)
+    _check(load().hs2_latent_read(ctypes.byref(c), out[0].data_ptr(), cs, out[1].data_ptr(), rs, _ROW_DTYPES[dtype],
+                                  row_start.data_ptr(), n_rows, _ptr(dev_err), st))
+    return out
+
+
+def _attention_out(out, n: int, Hq: int, dv: int, o_dtype, device, stream):
+    """(o, lse) of an attention call: new, or `out` checked."""
+    if o_dtype not in _ROW_DTYPES:
+        raise HS2Error("o_dtype must be float32 or bfloat16")
+    if out is None:
+        return _new((n, Hq, dv), o_dtype, device, stream), _new((n, Hq), torch.float32, device, stream)
+    o, lse = out
+    if o.dtype is not o_dtype or o.shape != (n, Hq, dv) or not o.is_contiguous() or (
+            lse is not None and (lse.dtype is not torch.float32 or lse.shape != (n, Hq) or not lse.is_contiguous())):
+        raise HS2Error("out must be contiguous (o [n_rows][Hq][dv] of o_dtype, lse float32 [n_rows][Hq] or None)")
+    return o, lse
+
+
+def hs2_latent_chunk_workspace(n_rows: int, Hq: int, kv: KV, max_n: int, max_t: int) -> int:
+    return load().hs2_latent_chunk_workspace(n_rows, Hq, ctypes.byref(kv.c()), max_n, max_t)
+
+
+def hs2_latent_chunk(q: torch.Tensor, row_start: torch.Tensor, kv: KV, scale: float, max_n: int,
+                     max_t: int | None = None, o_dtype: torch.dtype = torch.float32, out=None, workspace=None,
+                     dev_err=None, stream=None):
+    """Causal attention of a ragged batch of query chunks over a latent cache, in the latent space
+    (absorbed form); returns (o [n_rows][Hq][dc], lse float32 [n_rows][Hq]).
+
+    ``q`` [n_rows][Hq][dc + 64] of the cache's type: the queries' latent part, then the rotated part that
+    hs2_latent_write leaves there. Rows, ``max_n``, ``max_t`` and ``o_dtype`` as in hs2_fa_chunk; Hq
+    a power of two up to 128."""
+    lib = load()
+    c, dev = kv._cached()[:2]
+    dc = _latent(c)
+    n, Hq, d = q.shape
+    if max_t is None:
+        max_t = c.max_pages * c.page_size
+    if q.dtype is not (torch.float32 if c.dtype == F32 else torch.bfloat16) or d != c.d or not q.is_contiguous():
+        raise HS2Error("q must be contiguous [n_rows][Hq][dc + 64] of the cache's type")
+    _i32(row_start, "row_start", c.batch + 1)
+    o, lse = _attention_out(out, n, Hq, dc, o_dtype, q.device, stream)
+    st = _launch_stream(stream, dev, q, row_start, o, lse, workspace, dev_err)
+    ws = workspace
+    if ws is None:
+        ws = _scratch(lib.hs2_latent_chunk_workspace(n, Hq, ctypes.byref(c), max_n, max_t), q.device, stream)
+    _check(lib.hs2_latent_chunk(q.data_ptr(), row_start.data_ptr(), n, max_n, Hq, ctypes.byref(c), max_t, scale,
+                                o.data_ptr(), _ROW_DTYPES[o_dtype], _ptr(lse), ws.data_ptr(), ws.nbytes, _ptr(dev_err), st))
+    return o, lse
+
+
+def hs2_latent_prefill_workspace(n_rows: int, Hq: int, batch: int, max_n: int, max_t: int) -> int:
+    return load().hs2_latent_prefill_workspace(n_rows, Hq, batch, max_n, max_t)
+
+
+def hs2_latent_prefill(q: torch.Tensor, k: torch.Tensor, r: torch.Tensor, v: torch.Tensor, row_start: torch.Tensor,
+                       key_start: torch.Tensor, scale: float, max_n: int, max_t: int,
+                       o_dtype: torch.dtype = torch.float32, out=None, workspace=None, dev_err=None, stream=None):
+    """Causal attention of a ragged batch over keys and values expanded from the latents (expanded
+    form); returns (o [n_rows][Hq][128], lse float32 [n_rows][Hq]).
+
+    ``q`` [n_rows][Hq][192]: 128 channels against ``k`` [n_keys][Hq][128], 64 rotated ones against ``r``
+    [n_keys][64], which the heads share; ``v`` [n_keys][Hq][128]. All bfloat16 or all float32; k, v
+    and r may be slices of wider arrays. Sequence b has keys [key_start[b], key_start[b+1]), and its rows
+    [row_start[b], row_start[b+1]) are its last positions. ``max_n`` and ``max_t`` bound a sequence's
+    rows and keys."""
+    lib = load()
+    n, Hq, _ = q.shape
+    nk = r.shape[0]
+    if q.dtype not in _ROW_DTYPES or any(x.dtype is not q.dtype for x in (k, r, v)):
+        raise HS2Error("q, k, r and v must be bfloat16 or float32, all alike")
+    if q.shape[2] != 192 or not q.is_contiguous():
+        raise HS2Error("q must be contiguous [n_rows][Hq][192]")
+    kt, kh = _strides(k, "k", nk, Hq, 128)
+    vt, vh = _strides(v, "v", nk, Hq, 128)
+    rt = _strides(r, "r", nk, 64)[0]
+    batch = row_start.numel() - 1
+    if batch < 1:
+        raise HS2Error("row_start has batch + 1 entries")
+    _i32(row_start, "row_start", batch + 1)
+    _i32(key_start, "key_start", batch + 1)
+    o, lse = _attention_out(out, n, Hq, 128, o_dtype, q.device, stream)
+    st = _launch_stream(stream, q.get_device(), q, k, r, v, row_start, key_start, o, lse, workspace, dev_err)
+    ws = workspace
+    if ws is None:
+        ws = _scratch(lib.hs2_latent_prefill_workspace(n, Hq, batch, max_n, max_t), q.device, stream)
+    keys = hs2_latent_keys(k.data_ptr(), r.data_ptr(), v.data_ptr(), kt, kh, rt, vt, vh, key_start.data_ptr(), nk,
+                           _ROW_DTYPES[q.dtype])
+    _check(lib.hs2_latent_prefill(q.data_ptr(), row_start.data_ptr(), n, max_n, Hq, batch, ctypes.byref(keys), max_t,
+                                  scale, o.data_ptr(), _ROW_DTYPES[o_dtype], _ptr(lse), ws.data_ptr(), ws.nbytes,
+                                  _ptr(dev_err), st))
     return o, lse
 
 
