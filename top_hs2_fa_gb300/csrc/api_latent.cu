@@ -79,6 +79,62 @@ hs2_status check_latent_rows(const hs2_kv* kv, const void* c_rows, int64_t c_str
 bool valid_attention(int n_rows, int max_n, int max_t, float scale, hs2_dtype o_dtype) {
   return n_rows >= 0 && max_n >= 0 && max_n <= max_t && std::isfinite(scale) && scale > 0.f && row_type(o_dtype);
 }
+int sm_count() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 152;
+  }
+  return std::min(n, 512);  // the merge's blocks hold the list of cut units, one per CTA at most
+}
+
+// Workspace of an attention call: the plan and the parts of cut units.
+struct Layout {
+  hs2::ChunkPlan plan;  // pointers after bind()
+  size_t off[7], total;
+  long long tiles;  // an upper bound
+};
+
+// `heads` units beside one another per sequence, of G rows a token, parts of dv channels.
+Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t) {
+  Layout L{};
+  size_t at = 0;
+  auto take = [&](int i, size_t bytes) { L.off[i] = at, at = align256(at + bytes); };
+  hs2::ChunkPlan& p = L.plan;
+  p.ctas = ctas;
+  p.tile_rows = tile_rows;
+  p.max_rows = 0x7fffffff;
+  const long long units = heads * ((long long)n_rows * G / tile_rows + std::min(batch, n_rows));
+  p.max_units = (int)std::min<long long>(units, 1 << 30);
+  L.tiles = units * (max_t / 128 + 2);
+  take(0, 16);
+  take(1, 4 * (size_t)ctas);
+  take(2, 4 * (size_t)ctas);
+  take(6, 4 * (size_t)ctas);
+  take(3, 48 * (size_t)p.max_units);
+  take(4, 2 * (size_t)ctas * tile_rows * 8);
+  take(5, 2 * (size_t)ctas * tile_rows * dv * 4);
+  L.total = std::max<size_t>(at, 256);
+  return L;
+}
+void bind(Layout& L, char* ws) {
+  hs2::ChunkPlan& p = L.plan;
+  p.head = (int32_t*)(ws + L.off[0]);
+  p.cta_first = (int32_t*)(ws + L.off[1]);
+  p.cuts = (int32_t*)(ws + L.off[2]);
+  p.cta_begin = (int32_t*)(ws + L.off[6]);
+  p.units = (int32_t*)(ws + L.off[3]);
+  p.part_ml = (float*)(ws + L.off[4]);
+  p.part_o = (float*)(ws + L.off[5]);
+}
+
+// Rows of a unit of the absorbed form: the least width that holds a sequence's; 128 by pairs of CTAs.
+int chunk_width(long long top) { return top <= 16 ? 16 : top <= 32 ? 32 : top <= 64 ? 64 : 128; }
+Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t) {
+  const int sms = sm_count();
+  return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t);
+}
+
 bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
 
 hs2::ChunkArgs chunk_args(const void* q, const int32_t* row_start, int n_rows, int max_n, int max_t, int batch, int Hq,
@@ -177,7 +233,12 @@ hs2_status hs2_latent_read(const hs2_kv* kv, void* c_rows, int64_t c_stride, voi
 
 size_t hs2_latent_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t) {
   if (!valid_latent(kv) || n_rows < 0 || max_n < 0 || max_t < 0 || Hq < 1 || !heads_supported(Hq)) return 0;
-  return 256;
+  size_t need = 256;
+  // narrower units are more: what a call with fewer tokens a sequence would take, too
+  const int widest = chunk_width((long long)std::min(max_n, n_rows) * Hq);
+  for (int w = 16; kv->dtype != HS2_F32 && w <= widest; w *= 2)
+    if (Hq <= w) need = std::max(need, chunk_layout(n_rows, Hq, kv, w, max_t).total);
+  return need;
 }
 
 hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
@@ -189,14 +250,35 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
   if ((long long)max_t > (long long)kv->max_pages * 64) return HS2_ERR_ARG;
   if (n_rows == 0 || max_n == 0) return HS2_OK;
   if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
-  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < 256) return HS2_ERR_ARG;
+  const int dc = kv->d - hs2::kLatentRot;
+  Layout L = chunk_layout(n_rows, Hq, kv, chunk_width((long long)std::min(max_n, n_rows) * Hq), max_t);
+  // 32-bit tile counts and pool rows
+  if (kv->dtype != HS2_F32 && (L.tiles > 1LL << 30 || (long long)kv->num_pages * 64 > 0x7fffffff - 64 || kv->max_pages > (1 << 24)))
+    return HS2_ERR_UNSUPPORTED;
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < (kv->dtype == HS2_F32 ? 256 : L.total)) return HS2_ERR_ARG;
   hs2::ChunkArgs a = chunk_args(q, row_start, n_rows, max_n, max_t, kv->batch, Hq, scale, o, o_dtype, lse, dev_err);
   a.k = kv->k;
   a.bt = kv->block_table;
   a.seq_len = kv->seq_len;
   a.num_pages = kv->num_pages;
   a.max_pages = kv->max_pages;
-  const cudaError_t e = hs2::launch_latent_cc(a, {}, kv->d - hs2::kLatentRot, kv->dtype == HS2_F32, (cudaStream_t)stream);
+  a.Hkv = 1;
+  a.G = Hq;
+  while ((1 << a.log2G) < a.G) ++a.log2G;
+  cudaStream_t s = (cudaStream_t)stream;
+  if (kv->dtype == HS2_F32) {
+    const cudaError_t e = hs2::launch_latent_cc(a, {}, dc, true, s);
+    return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+  }
+  bind(L, (char*)workspace);
+  const int width = std::min(64, L.plan.tile_rows), box_heads = std::min(Hq, width);  // rows and heads of a CTA
+  CUtensorMap tq, tk;
+  if (!encode_3d_bf16(&tq, q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, box_heads, width / box_heads) ||
+      !encode_2d_bf16(&tk, kv->k, kv->d, (uint64_t)kv->num_pages * 64, 64))
+    return HS2_ERR_ARG;
+  cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
+  if (e == cudaSuccess) e = hs2::launch_latent_chunk(tq, tk, a, L.plan, dc, s);
+  if (e == cudaSuccess) e = hs2::launch_chunk_merge(a, &L.plan, 1, dc, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocks) chunk_merge_ke
   __syncthreads();
   const ChunkUnit u = load_unit(p, cut_s);
   const int rows = ((u.ntok << a.log2G) + blocks - 1) / blocks;
-  if (rows > MORE) merge_rows<D, 1, 8>(a, p, u, per, y, blocks, sum, sum_l);
+  if (D <= 128 && rows > MORE) merge_rows<D, 1, D <= 128 ? 8 : LPR>(a, p, u, per, y, blocks, sum, sum_l);  // (wider rows: registers)
   else if (rows > FEW) merge_rows<D, 1, LPR>(a, p, u, per, y, blocks, sum, sum_l);
   else merge_rows<D, kMergeShare, LPR>(a, p, u, per, y, blocks, sum, sum_l);
 }
@@ -134,7 +134,9 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocks) chunk_merge_ke
 cudaError_t launch_chunk_merge(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, int d, cudaStream_t s) {
   const ChunkPlan &p0 = plans[0], &p1 = plans[n_plans - 1];
   const dim3 grid(kMergeBlocks * p0.ctas, n_plans);  // every plan is cut among as many CTAs
-  return launch_pdl(d == 128 ? chunk_merge_kernel<128> : chunk_merge_kernel<64>, grid, dim3(kMergeWarps * 32), 0, s, a, p0, p1);
+  auto kern = d == 512 ? chunk_merge_kernel<512> : d == 256 ? chunk_merge_kernel<256> : d == 128 ? chunk_merge_kernel<128>
+                                                                                         : chunk_merge_kernel<64>;
+  return launch_pdl(kern, grid, dim3(kMergeWarps * 32), 0, s, a, p0, p1);
 }
 
 }  // namespace hs2
