@@ -135,6 +135,11 @@ Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t) 
   return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t);
 }
 
+// A unit of the expanded form is 256 tokens of a head.
+Layout prefill_layout(int n_rows, int Hq, int batch, int max_t) {
+  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t);
+}
+
 bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
 
 hs2::ChunkArgs chunk_args(const void* q, const int32_t* row_start, int n_rows, int max_n, int max_t, int batch, int Hq,
@@ -267,7 +272,7 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
   while ((1 << a.log2G) < a.G) ++a.log2G;
   cudaStream_t s = (cudaStream_t)stream;
   if (kv->dtype == HS2_F32) {
-    const cudaError_t e = hs2::launch_latent_cc(a, {}, dc, true, s);
+    const cudaError_t e = hs2::launch_latent_cc(a, {}, dc, s);
     return e == cudaSuccess ? HS2_OK : cuda_fail(e);
   }
   bind(L, (char*)workspace);
@@ -284,7 +289,7 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
 
 size_t hs2_latent_prefill_workspace(int n_rows, int Hq, int batch, int max_n, int max_t) {
   if (n_rows < 0 || Hq < 1 || batch < 1 || max_n < 0 || max_t < 0) return 0;
-  return 256;
+  return prefill_layout(n_rows, Hq, batch, max_t).total;
 }
 
 hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, int batch,
@@ -305,15 +310,34 @@ hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_row
         !strided(keys->r, keys->r_token, hs2::kLatentRot, hs2::kLatentRot))
       return HS2_ERR_ARG;
   }
-  if (Hq > 65535) return HS2_ERR_UNSUPPORTED;
-  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < 256) return HS2_ERR_ARG;
+  const bool f32 = keys->dtype == HS2_F32;
+  Layout L = prefill_layout(n_rows, Hq, batch, max_t);
+  if (Hq > 65535 || (!f32 && L.tiles > 1LL << 30)) return HS2_ERR_UNSUPPORTED;  // grid y; 32-bit tile counts
+  if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < (f32 ? 256 : L.total)) return HS2_ERR_ARG;
   hs2::ChunkArgs a = chunk_args(q, row_start, n_rows, max_n, max_t, batch, Hq, scale, o, o_dtype, lse, dev_err);
+  a.Hkv = Hq;
+  a.G = 1;
   a.k = keys->k;
   a.v = keys->v;
   a.key_start = keys->key_start;
   a.n_keys = keys->n_keys;
   const hs2::LatentKeys lk{keys->r, keys->k_token, keys->k_head, keys->v_token, keys->v_head, keys->r_token};
-  const cudaError_t e = hs2::launch_latent_cc(a, lk, 0, keys->dtype == HS2_F32, (cudaStream_t)stream);
+  cudaStream_t s = (cudaStream_t)stream;
+  if (f32 || keys->n_keys == 0) {  // (no keys: nothing but what there is to flag)
+    const cudaError_t e = hs2::launch_latent_cc(a, lk, 0, s);
+    return e == cudaSuccess ? HS2_OK : cuda_fail(e);
+  }
+  bind(L, (char*)workspace);
+  const uint64_t nk = keys->n_keys;
+  CUtensorMap tq, tk, tr, tv;
+  if (!encode_3d_bf16(&tq, q, 192, (uint64_t)Hq, (uint64_t)n_rows, 1, 128) ||
+      !encode_3d_bf16(&tk, keys->k, 128, (uint64_t)Hq, nk, 1, 128, keys->k_head, keys->k_token) ||
+      !encode_3d_bf16(&tr, keys->r, 64, 1, nk, 1, 128, keys->r_token, keys->r_token) ||
+      !encode_3d_bf16(&tv, keys->v, 128, (uint64_t)Hq, nk, 1, 128, keys->v_head, keys->v_token))
+    return HS2_ERR_ARG;
+  cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
+  if (e == cudaSuccess) e = hs2::launch_latent_prefill(tq, tk, tr, tv, a, L.plan, s);
+  if (e == cudaSuccess) e = hs2::launch_chunk_merge(a, &L.plan, 1, hs2::kLatentValue, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 

@@ -107,8 +107,9 @@ inline bool encode_2d_bytes(CUtensorMap* map, const void* base, uint32_t row_byt
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// d2 x d1 x d0 bf16 in tiles of b2 x b1 x 64, contiguous or with strides of s1 and s2 elements.
 inline bool encode_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1, uint64_t d2, uint32_t b1,
-                    uint32_t b2) {
+                    uint32_t b2, uint64_t s1 = 0, uint64_t s2 = 0) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -121,7 +122,7 @@ inline bool encode_3d_bf16(CUtensorMap* map, const void* base, uint64_t d0, uint
     encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
   }
   const cuuint64_t dims[3] = {d0, d1, d2};
-  const cuuint64_t strides[2] = {d0 * 2, d0 * d1 * 2};
+  const cuuint64_t strides[2] = {(s1 ? s1 : d0) * 2, (s2 ? s2 : d0 * d1) * 2};
   const cuuint32_t box[3] = {64, b1, b2};
   const cuuint32_t estr[3] = {1, 1, 1};
   return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,

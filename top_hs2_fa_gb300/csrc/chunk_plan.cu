@@ -32,11 +32,18 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   if (threadIdx.x == 0) n_cuts = longest = 0;
   // rows of two sequences at once would overrun what the host sized for n_rows rows
   bool descends = false;
-  int n = 0, t = 0, r0 = 0;  // this thread's sequence of the chunk
+  int n = 0, t = 0, r0 = 0, k0 = 0;  // this thread's sequence of the chunk
   auto load = [&](int b) {
-    n = t = r0 = 0;
+    n = t = r0 = k0 = 0;
     if (b >= a.batch) return;
-    r0 = a.row_start[b], t = a.seq_len[b];
+    r0 = a.row_start[b];
+    if (a.key_start) {  // packed keys; bad starts have no t that a row could have
+      k0 = a.key_start[b];
+      const int k1 = a.key_start[b + 1];
+      t = k0 >= 0 && k1 >= k0 && k1 <= a.n_keys ? k1 - k0 : -1;
+    } else {
+      t = a.seq_len[b];
+    }
     const int r1 = a.row_start[b + 1];
     descends |= r1 < r0;
     n = r1 - r0;
@@ -86,6 +93,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
       }
       s_exp[threadIdx.x] = pg - e0;  // expanded page of the sequence's page 0
     }
+    if (a.key_start) s_exp[threadIdx.x] = k0;
     __syncthreads();
     for (int u0 = 0; u0 < here; u0 += kPlanThreads) {
       const int u = u0 + threadIdx.x;
@@ -109,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
         const int last = (x.pos0 + x.ntok - 1) / kPage;
         x.ntiles = (last - x.page0) / 2 + 1;
         x.t = st;
-        x.slot_page = p.expand ? s_exp[lo] : 0;
+        x.slot_page = p.expand || a.key_start ? s_exp[lo] : 0;
         x.npages = (st + kPage - 1) / kPage;
         cost = x.ntiles;
       }

@@ -16,7 +16,7 @@ namespace hs2 {
 struct __align__(16) ChunkUnit {
   int b, g, row, ntok;                // row: packed row of the first token
   int pos0, page0, ntiles, prefix;    // position of the first token; first page; tiles before this unit
-  int t, slot_page, npages, pad;      // keys; the sequence's first expanded page; pages of the sequence
+  int t, slot_page, npages, pad;      // keys; the sequence's first expanded page (packed keys: its first key); pages of the sequence
 };
 
 // Where a CTA's range meets the units.

@@ -346,7 +346,9 @@ cudaError_t launch_kv_write_rot(const RotRowsArgs& z, int d, int dtype, bool row
 cudaError_t launch_latent_rows(const LatentRowsArgs& z, int dc, bool cache_f32, bool row_f32, bool write, cudaStream_t s);
 cudaError_t launch_latent_chunk(const CUtensorMap& tq, const CUtensorMap& tk, const ChunkArgs& a, const ChunkPlan& p, int dc,
                                 cudaStream_t s);
-cudaError_t launch_latent_cc(const ChunkArgs& a, const LatentKeys& lk, int dc, bool f32, cudaStream_t s);
+cudaError_t launch_latent_prefill(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tr, const CUtensorMap& tv,
+                                  const ChunkArgs& a, const ChunkPlan& p, cudaStream_t s);
+cudaError_t launch_latent_cc(const ChunkArgs& a, const LatentKeys& lk, int dc, cudaStream_t s);
 cudaError_t launch_chunk_cc(const ChunkArgs& a, int d, cudaStream_t s);
 cudaError_t launch_chunk_plan(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, cudaStream_t s);
 cudaError_t launch_chunk_expand(const ChunkArgs& a, const ChunkPlan& p, int d, int dtype, void* ek, void* ev,

@@ -15,17 +15,12 @@ namespace {
 constexpr int kLcWarps = 8;
 constexpr int kLcKeys = 4;  // keys per warp step: their loads and reductions overlap
 
-template <typename T>
-HS2_DEVI float2 load2(const T* p) {
-  if constexpr (sizeof(T) == 4) return *reinterpret_cast<const float2*>(p);
-  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-  return make_float2(bf16_lo(w), bf16_hi(w));
-}
+HS2_DEVI float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
 
 }  // namespace
 
 // grid (rows, query heads), 8 warps over the row's keys, merged through shared memory.
-template <typename T, int DN, int DV, bool PAGED>
+template <int DN, int DV, bool PAGED>
 __global__ void __launch_bounds__(kLcWarps * 32) latent_cc_kernel(const ChunkArgs a, const LatentKeys lk) {
   constexpr int DQ = DN + kLatentRot, NK = DN / 64, NV = DV / 64;  // steps of 64 channels
   __shared__ float sm_m[kLcWarps], sm_l[kLcWarps], sm_o[kLcWarps][DV];
@@ -55,7 +50,7 @@ __global__ void __launch_bounds__(kLcWarps * 32) latent_cc_kernel(const ChunkArg
   }
   const int pos = t - n + (r - r0);
   const int32_t* bt = PAGED ? a.bt + (size_t)b * a.max_pages : nullptr;
-  const T* qp = reinterpret_cast<const T*>(a.q) + ((size_t)r * a.Hq + h) * DQ + 2 * lane;
+  const float* qp = reinterpret_cast<const float*>(a.q) + ((size_t)r * a.Hq + h) * DQ + 2 * lane;
   float2 q[NK + 1];
 #pragma unroll
   for (int i = 0; i <= NK; ++i) q[i] = load2(qp + 64 * i);
@@ -65,27 +60,27 @@ __global__ void __launch_bounds__(kLcWarps * 32) latent_cc_kernel(const ChunkArg
   for (int i = 0; i < NV; ++i) o[i] = make_float2(0.f, 0.f);
   for (int s0 = warp * kLcKeys; s0 <= pos; s0 += kLcWarps * kLcKeys) {
     float x[kLcKeys];
-    const T* vp[kLcKeys];
+    const float* vp[kLcKeys];
 #pragma unroll
     for (int j = 0; j < kLcKeys; ++j) {
       x[j] = -INFINITY;
       vp[j] = nullptr;
       const int s = s0 + j;
       if (s > pos) continue;
-      const T *kp, *rp;
+      const float *kp, *rp;
       if (PAGED) {
         const int phys = bt[s / kPage];
         if (phys < 0 || phys >= a.num_pages) {
           if (lane == 0) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
           continue;
         }
-        kp = reinterpret_cast<const T*>(a.k) + ((size_t)phys * kPage + s % kPage) * DQ + 2 * lane;
+        kp = reinterpret_cast<const float*>(a.k) + ((size_t)phys * kPage + s % kPage) * DQ + 2 * lane;
         rp = kp + DN;
         vp[j] = kp;
       } else {
-        kp = reinterpret_cast<const T*>(a.k) + (long long)(key0 + s) * lk.k_token + h * lk.k_head + 2 * lane;
-        rp = reinterpret_cast<const T*>(lk.r) + (long long)(key0 + s) * lk.r_token + 2 * lane;
-        vp[j] = reinterpret_cast<const T*>(a.v) + (long long)(key0 + s) * lk.v_token + h * lk.v_head + 2 * lane;
+        kp = reinterpret_cast<const float*>(a.k) + (long long)(key0 + s) * lk.k_token + h * lk.k_head + 2 * lane;
+        rp = reinterpret_cast<const float*>(lk.r) + (long long)(key0 + s) * lk.r_token + 2 * lane;
+        vp[j] = reinterpret_cast<const float*>(a.v) + (long long)(key0 + s) * lk.v_token + h * lk.v_head + 2 * lane;
       }
       const float2 kr = load2(rp);
       float dot = fmaf(q[NK].x, kr.x, q[NK].y * kr.y);
@@ -142,15 +137,10 @@ __global__ void __launch_bounds__(kLcWarps * 32) latent_cc_kernel(const ChunkArg
   if (a.lse && threadIdx.x == 0) a.lse[at] = chunk_lse(L, M);
 }
 
-template <typename T>
-static cudaError_t launch_t(const ChunkArgs& a, const LatentKeys& lk, int dc, cudaStream_t s) {
-  auto kern = !a.bt ? latent_cc_kernel<T, kLatentNope, kLatentValue, false>
-                    : dc == 512 ? latent_cc_kernel<T, 512, 512, true> : latent_cc_kernel<T, 256, 256, true>;
+cudaError_t launch_latent_cc(const ChunkArgs& a, const LatentKeys& lk, int dc, cudaStream_t s) {
+  auto kern = !a.bt ? latent_cc_kernel<kLatentNope, kLatentValue, false>
+                    : dc == 512 ? latent_cc_kernel<512, 512, true> : latent_cc_kernel<256, 256, true>;
   return launch_pdl(kern, dim3(a.n_rows, a.Hq), dim3(kLcWarps * 32), 0, s, a, lk);
-}
-
-cudaError_t launch_latent_cc(const ChunkArgs& a, const LatentKeys& lk, int dc, bool f32, cudaStream_t s) {
-  return f32 ? launch_t<float>(a, lk, dc, s) : launch_t<__nv_bfloat16>(a, lk, dc, s);
 }
 
 }  // namespace hs2
