@@ -125,6 +125,7 @@ ChunkLayout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int max_n, int ma
       p.tile_rows = tile_rows;
       p.min_rows = lo;
       p.max_rows = hi;
+      p.snap = 2;
       const long long units = (long long)kv->Hkv * ((long long)n_rows * G / tile_rows + std::min(kv->batch, n_rows));
       p.max_units = (int)std::min<long long>(units, 1 << 30);
       L.tiles = std::max(L.tiles, units * (max_t / 128 + 2));

@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   // saves (4 sequences of up to 1500 keys 19.1 us against 16.2, 64 tokens over 2048 keys 25.3, 22.3)
   const int per = max(1, (total_tiles + p.ctas - 1) / p.ctas);
   __syncthreads();  // the records are visible to the block
-  const bool snap = 2 * longest <= per;
+  const bool snap = (long long)p.snap * longest <= per;
   // each CTA's range start and the unit there, and the list of units that a range border cuts (in
   // any order: the merge treats each by itself)
   auto place = [&](int u, int ntiles, int prefix) {

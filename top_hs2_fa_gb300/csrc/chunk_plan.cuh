@@ -44,6 +44,20 @@ HS2_DEVI ChunkUnit load_unit(const ChunkPlan& p, int u) {
   return x;
 }
 
+// A unit's record spread over a warp, a word a lane, so that the next unit's can be on its way while
+// this one's tiles are walked; `there`: whether there is one.
+HS2_DEVI int fetch_unit(const ChunkPlan& p, int u, bool there) {
+  const int lane = threadIdx.x & 31;
+  return there && lane < 12 ? __ldcg(p.units + 12 * (size_t)u + lane) : 0;
+}
+HS2_DEVI ChunkUnit spread_unit(int word) {
+  ChunkUnit x;
+  int* d = reinterpret_cast<int*>(&x);
+#pragma unroll
+  for (int i = 0; i < 11; ++i) d[i] = __shfl_sync(0xffffffffu, word, i);
+  return x;
+}
+
 // A row's results from its denominator, relative to 2^M: 0 where no key is left, NaN passes on.
 HS2_DEVI float chunk_lse(float den, float M) { return den == 0.f ? -INFINITY : (M + log2f(den)) / kLog2e; }
 HS2_DEVI float chunk_factor(float num, float den) { return den == 0.f ? 0.f : num / den; }

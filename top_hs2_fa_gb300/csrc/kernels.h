@@ -180,6 +180,7 @@ struct ChunkPlan {
   int max_units, ctas;
   int tile_rows;            // rows of a unit: 256 or the narrow kernel's width
   int min_rows, max_rows;   // of a sequence, times G
+  int snap;                 // borders move to units' where a range is this many times the longest unit, or more
   float* part_ml;           // [2 ctas][tile_rows][2] m (base 2) and l of the parts
   float* part_o;            // [2 ctas][tile_rows][D] their unnormalised outputs
   // sequences whose pages are expanded to bf16 first (wide kernel on FP8 / FP4), by ordinal

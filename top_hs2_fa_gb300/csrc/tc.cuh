@@ -129,6 +129,39 @@ HS2_DEVI void mma_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
       : "memory");
 }
+// Four MMAs of K = 16 each, the operands' descriptors (or tensor memory columns) A_STEP and B_STEP apart,
+// as mma_f16_warp / mma_f16_ts_warp: the issuing warp shares its scheduler with others, so its
+// instructions count.
+template <int A_STEP, int B_STEP>
+HS2_DEVI void mma4_f16_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                            uint32_t elected) {
+  asm volatile(
+      "{.reg .pred p, q, t; .reg .b64 a, b; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; setp.eq.u32 t, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 a, %1, %6; add.u64 b, %2, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, a, %6; add.u64 b, b, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;\n\t"
+      "add.u64 a, a, %6; add.u64 b, b, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, t;}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected), "n"(A_STEP), "n"(B_STEP)
+      : "memory");
+}
+template <int A_STEP, int B_STEP>
+HS2_DEVI void mma4_f16_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate,
+                               uint32_t elected) {
+  asm volatile(
+      "{.reg .pred p, q, t; .reg .b32 a; .reg .b64 b; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; setp.eq.u32 t, 0, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, %6; add.u64 b, %2, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, a, %6; add.u64 b, b, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;\n\t"
+      "add.u32 a, a, %6; add.u64 b, b, %7;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, t;}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected), "n"(A_STEP), "n"(B_STEP)
+      : "memory");
+}
 HS2_DEVI void mma_commit_warp(uint64_t* bar, uint32_t elected) {
   asm volatile(
       "{.reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
