@@ -8,15 +8,16 @@
 // O^T[DC][N] += C^T P^T, N = 16, 32 or 64 rows (tokens times heads), so that O of 512 channels
 // fits tensor memory (4 x 64 columns; with the rows as M it would take all 512) and a tile is read
 // once: the same shared-memory tile is S's K-major A operand and, MN-major, O's. Units of 128 rows
-// (Hq = 128, or chunks) go to a pair of neighbouring CTAs that walk the same tiles, 64 rows
-// each, so that the second finds the tile in L2.
+// (Hq = 128, or chunks) go to a cluster of two CTAs, 64 rows each, that fetch a page of every tile each
+// for both (each for itself, the reads from L2 were what bound it: single tokens of 128 heads, 32
+// sequences of 4K to 16K keys, 148 us).
 //   warp 0   producer: the tile in DC / 128 pieces of 128 channels (32 KB) and one of the 64 rotated ones,
 //            each with a barrier, through rings of pieces: with 64 rows of 512 channels a tile fills the
 //            ring, and a piece of the next one comes as soon as its channels' O is done
 //   warps 1, 3   MMA issuers, of S (piece by piece as they land) and of O (piece by piece, each
 //            committed to the ring)
 //   warp 2   Q of the next unit by TMA
-//   warps 4-7, 8-11  softmax, a key a thread, half of the rows each: p = 2^(x c + nm) with a reference nm per
+//   warps 4-7, 8-11 ...  softmax, a key a thread, 8 or 16 rows each: p = 2^(x c + nm) with a reference nm per
 //            row that moves only when a weight would exceed 2^14; P rounds to bf16, C's type (a weight is off
 //            by at most 2^-8 of itself), and goes where the tile's rotated channels were, which S
 //            alone needs; the normaliser is summed in fp32 from unrounded p, per thread
@@ -33,7 +34,12 @@ namespace hs2 {
 
 namespace {
 
-constexpr int kLThreads = 384;
+// `bytes` bytes from `src` on into L2 (both multiples of 16).
+HS2_DEVI void l2_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+constexpr int kAhead = 2;  // tiles
+
 constexpr uint32_t kPiece = 32768, kRotPiece = 16384;
 
 template <int DC, int N>
@@ -44,11 +50,13 @@ struct LatentSmem {
   static constexpr int RING = DC == 512 ? (N == 64 ? 4 : 5) : (N == 64 ? 4 : 5);
   static constexpr int ROT = DC == 512 ? (N == 64 ? 1 : N == 32 ? 1 : 2) : 2;
   static constexpr int O_BUFS = N == 64 ? 1 : 2;  // by the parity of the unit
+  static constexpr int GROUPS = N == 64 ? 4 : 2;  // of four softmax warps, N / GROUPS rows each
+  static constexpr int THREADS = 128 * (1 + GROUPS);
   uint8_t piece[RING][kPiece];   // [two blocks of 64 channels][128 keys][128 bytes]
   uint8_t rot[ROT][kRotPiece];   // [128 keys][128 bytes]: r, then P ([key][row])
   uint8_t q[BLOCKS * N * 128];
-  alignas(16) float nm[N], alpha[N];                    // by softmax group: half of the rows each
-  alignas(16) float warp_m[2][4][N / 2], sums[2][4][N / 2], factor[N];
+  alignas(16) float nm[N], alpha[N], factor[N];
+  alignas(16) float warp_m[GROUPS][4][N / GROUPS], sums[GROUPS][4][N / GROUPS];
   uint64_t full[RING], empty[RING], rot_full[ROT], rot_empty[ROT];
   uint64_t s_full[2], s_empty[2], p_ready[2], pv_done[2], o_empty[O_BUFS], q_full, q_empty;
   uint32_t tmem_base;
@@ -57,14 +65,15 @@ struct LatentSmem {
 
 }  // namespace
 
-// PAIR: CTAs 2i and 2i + 1 take rows [0, 64) and [64, 128) of the units of range i.
+// PAIR: a cluster's CTAs take rows [0, 64) and [64, 128) of the units of its range (the second also where
+// a unit has no such rows: the tiles come from both).
 template <int DC, int N, bool PAIR>
-__global__ void __launch_bounds__(kLThreads, 1)
+__global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     latent_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const ChunkArgs a,
                         const ChunkPlan p) {
   using Sm = LatentSmem<DC, N>;
   constexpr int PIECES = Sm::PIECES, BLOCKS = Sm::BLOCKS, RING = Sm::RING, ROT = Sm::ROT, OB = Sm::O_BUFS;
-  constexpr int C = N / 2;                 // columns (rows of the unit) of a softmax thread
+  constexpr int NG = Sm::GROUPS, C = N / NG;  // softmax groups; columns (rows of the unit) of a thread
   constexpr uint32_t kObuf = PIECES * N;   // tensor memory columns of an O
   static_assert(128 + OB * kObuf <= 512, "tensor memory");
   static_assert(RING < 3 * PIECES, "at most two tiles between their S and their O: two phases of p_ready");
@@ -75,19 +84,19 @@ __global__ void __launch_bounds__(kLThreads, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < RING; ++s) {
       tc::mbar_init(&sm.full[s], 1);
-      tc::mbar_init(&sm.empty[s], 1);
+      tc::mbar_init(&sm.empty[s], PAIR ? 2 : 1);  // of a pair: both are done with the piece
     }
     for (int s = 0; s < ROT; ++s) {
       tc::mbar_init(&sm.rot_full[s], 1);
-      tc::mbar_init(&sm.rot_empty[s], 1);
+      tc::mbar_init(&sm.rot_empty[s], PAIR ? 2 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.s_full[s], 1);
-      tc::mbar_init(&sm.s_empty[s], 256);
-      tc::mbar_init(&sm.p_ready[s], 256);
+      tc::mbar_init(&sm.s_empty[s], NG * 128);
+      tc::mbar_init(&sm.p_ready[s], NG * 128);
       tc::mbar_init(&sm.pv_done[s], 1);
     }
-    for (int s = 0; s < OB; ++s) tc::mbar_init(&sm.o_empty[s], 256);
+    for (int s = 0; s < OB; ++s) tc::mbar_init(&sm.o_empty[s], NG * 128);
     tc::mbar_init(&sm.q_full, 1);
     tc::mbar_init(&sm.q_empty, 1);
     sm.abort = 0;
@@ -95,24 +104,31 @@ __global__ void __launch_bounds__(kLThreads, 1)
   }
   if (warp == 1) tc::tmem_alloc(&sm.tmem_base, 512);
   tc::tc_fence_before();
-  __syncthreads();
+  if (PAIR) tc::cluster_sync();  // (the peer's barriers are set up)
+  else __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
   const ChunkRange rg = chunk_range(p, cta);
   const int per = p.head[1];
   const uint32_t tS = sm.tmem_base, tO = tS + 128;
-  // whether this CTA has rows of the unit
-  auto mine = [&](const ChunkUnit& u) { return !PAIR || (u.ntok << a.log2G) > row0; };
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
     int it = 0;
     bool ok = true;
     const int oob = a.num_pages * kPage;  // the row past the pool: zeros
+    // 64 channels of the tile's two pages: a pair's CTAs fetch one each for both
+    auto load = [&](uint8_t* to, int x, int ra, int rb, uint64_t* bar) {
+      if constexpr (PAIR) {
+        tc::tma_load_2d_multicast(to + (row0 ? 8192 : 0), &tm_k, x, row0 ? rb : ra, bar, 3);
+      } else {
+        tc::tma_load_2d(to, &tm_k, x, ra, bar);
+        tc::tma_load_2d(to + 8192, &tm_k, x, rb, bar);
+      }
+    };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      if (!mine(u)) continue;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
       const int page_end = min(u.npages, u.page0 + 2 * j1);
       // lane i has the table entry of page i of a block of 32 (16 tiles), and the next block's
@@ -126,10 +142,19 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (!there && u.page0 + 2 * c0 + lane < page_end) flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
         const int row = there ? raw * kPage : oob;
         raw = entry(c0 + 16);
+        const int row_next = raw >= 0 && raw < a.num_pages ? raw * kPage : oob;
         const int c1 = min(j1, c0 + 16);
         for (int j = c0; ok && j < c1; ++j, ++it) {
           const int l0 = 2 * (j - c0);
           const int ra = __shfl_sync(0xffffffffu, row, l0), rb = __shfl_sync(0xffffffffu, row, l0 + 1);
+          if constexpr (PAIR) {
+            // this CTA's page of the tile kAhead on into L2
+            const int l1 = l0 + 2 * kAhead + (row0 ? 1 : 0);
+            const int here = __shfl_sync(0xffffffffu, row, l1 & 31), later = __shfl_sync(0xffffffffu, row_next, l1 & 31);
+            const int ahead = l1 < 32 ? here : later;
+            if (lane == 0 && ahead != oob)
+              l2_prefetch(reinterpret_cast<const uint8_t*>(a.k) + (size_t)ahead * (2 * (DC + kLatentRot)), kPage * 2 * (DC + kLatentRot));
+          }
           for (int c = 0; c < PIECES; ++c) {
             const int n = it * PIECES + c, st = n % RING;
             ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.empty[st], ((n / RING) & 1) ^ 1));
@@ -137,10 +162,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
             if (lane == 0) {
               tc::mbar_arrive_expect_tx(&sm.full[st], kPiece);
 #pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                tc::tma_load_2d(sm.piece[st] + x * 16384, &tm_k, 128 * c + 64 * x, ra, &sm.full[st]);
-                tc::tma_load_2d(sm.piece[st] + x * 16384 + 8192, &tm_k, 128 * c + 64 * x, rb, &sm.full[st]);
-              }
+              for (int x = 0; x < 2; ++x) load(sm.piece[st] + x * 16384, 128 * c + 64 * x, ra, rb, &sm.full[st]);
             }
           }
           if (!ok) break;
@@ -148,8 +170,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
           ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.rot_empty[st], ((it / ROT) & 1) ^ 1));
           if (ok && lane == 0) {
             tc::mbar_arrive_expect_tx(&sm.rot_full[st], kRotPiece);
-            tc::tma_load_2d(sm.rot[st], &tm_k, DC, ra, &sm.rot_full[st]);
-            tc::tma_load_2d(sm.rot[st] + 8192, &tm_k, DC, rb, &sm.rot_full[st]);
+            load(sm.rot[st], DC, ra, rb, &sm.rot_full[st]);
           }
         }
       }
@@ -172,10 +193,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
-      if (!mine(u)) {
-        at = end;
-        continue;
-      }
       ok = all(tc::mbar_wait(&sm.q_full, seg & 1));
       for (; ok && at < end; ++at, ++it) {
         const int b = it & 1;
@@ -213,15 +230,15 @@ __global__ void __launch_bounds__(kLThreads, 1)
     // ------------------------------------------------------------------ O^T += C^T P^T
     constexpr uint32_t idO = narrow_idesc(true, N, true, true);
     const uint32_t el = tc::elect_one();
+    auto release = [&](uint64_t* bar) {
+      if constexpr (PAIR) tc::mma_commit_multicast_warp(bar, 3, el);
+      else tc::mma_commit_warp(bar, el);
+    };
     int it = 0, seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
-      if (!mine(u)) {
-        at = end;
-        continue;
-      }
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg % OB], ((seg / OB) & 1) ^ 1));
       const uint32_t o = tO + (seg % OB) * kObuf;
       for (int j = 0; ok && at < end; ++at, ++it, ++j) {
@@ -237,9 +254,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // 16 keys each
             tc::mma_f16_warp(o + c * N, vd + ks * 128, pd + ks * 128, idO, (j > 0 || ks > 0) ? 1u : 0u, el);
-          tc::mma_commit_warp(&sm.empty[st], el);
+          release(&sm.empty[st]);
         }
-        tc::mma_commit_warp(&sm.rot_empty[it % ROT], el);
+        release(&sm.rot_empty[it % ROT]);
         tc::mma_commit_warp(&sm.pv_done[b], el);
       }
       ++seg;
@@ -253,7 +270,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, un);
       at = min(rg.end, u.prefix + u.ntiles);
-      if (!mine(u)) continue;
       ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty, (seg & 1) ^ 1));
       if (!ok) break;
       if (lane == 0) {
@@ -279,7 +295,6 @@ __global__ void __launch_bounds__(kLThreads, 1)
       const ChunkUnit u = load_unit(p, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      if (!mine(u)) continue;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
       const uint32_t o = tO + (seg % OB) * kObuf + n0;
       float l[C];
@@ -406,9 +421,9 @@ __global__ void __launch_bounds__(kLThreads, 1)
         }
         if (kb + 128 > u.t && kb + key >= u.t) {
           // what lies behind the sequence in the pool may be anything, and 0 times a NaN is a NaN:
-          // each group clears half of the channels
-          for (int c = 0; c < PIECES; ++c) {
-            uint8_t* dead = sm.piece[(it * PIECES + c) % RING] + grp * 16384 + key * 128;
+          // each group clears its share of the channels
+          for (int c = grp; c < 2 * PIECES; c += NG) {
+            uint8_t* dead = sm.piece[(it * PIECES + (c >> 1)) % RING] + (c & 1) * 16384 + key * 128;
 #pragma unroll
             for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4*>(dead + 16 * i) = make_uint4(0, 0, 0, 0);
           }
@@ -480,7 +495,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
     if (!run && lane == 0) halt(sm, a.dev_err);
   }
   tc::tc_fence_before();
-  __syncthreads();
+  if (PAIR) tc::cluster_sync();  // neither leaves while the other may write to it
+  else __syncthreads();
   if (warp == 1) tc::tmem_dealloc(sm.tmem_base, 512);
 }
 
@@ -491,7 +507,7 @@ static cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const 
   auto kern = latent_chunk_kernel<DC, N, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(PAIR ? 2 * p.ctas : p.ctas), dim3(kLThreads), sm, s, tq, tk, a, p);
+  return launch_pdl_cluster(kern, PAIR ? 2 : 1, dim3(PAIR ? 2 * p.ctas : p.ctas), dim3(LatentSmem<DC, N>::THREADS), sm, s, tq, tk, a, p);
 }
 
 template <int DC>
