@@ -120,6 +120,20 @@ HS2_DEVI void check_starts(const RowsArgs& a) {
     flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
 }
 
+// 16 values as E4M3 codes under slab scale S, four to a word; whether S is one that rows are written under.
+HS2_DEVI bool fp8_codes(const RowsArgs& a, float S, const float (&x)[16], uint32_t (&w)[4]) {
+  if (!(S >= 0x1p-60f && S <= 0x1p60f)) {
+    flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+    return false;
+  }
+  const float inv = 1.f / S;
+  float q[16];
+  quotients<5>(x, inv, S, 0.f, q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = e4m3_codes(q[4 * i], q[4 * i + 1]) | (e4m3_codes(q[4 * i + 2], q[4 * i + 3]) << 16);
+  return true;
+}
+
 // One side's 16 channels to their place.
 template <int D, int FMT>
 HS2_DEVI void put16(const RowsArgs& a, int side, size_t slab, size_t line, int grp, const float (&x)[16]) {
@@ -137,19 +151,14 @@ HS2_DEVI void put16(const RowsArgs& a, int side, size_t slab, size_t line, int g
                           pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
   } else {
     const float S = (side ? a.v_scale : a.k_scale)[slab];
-    if (!(S >= 0x1p-60f && S <= 0x1p60f)) {
-      flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
-      return;
-    }
     if constexpr (FMT == HS2_FP8_E4M3) {
-      const float inv = 1.f / S;
-      float q[16];
-      quotients<5>(x, inv, S, 0.f, q);
       uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = e4m3_codes(q[4 * i], q[4 * i + 1]) | (e4m3_codes(q[4 * i + 2], q[4 * i + 3]) << 16);
-      *reinterpret_cast<uint4*>(pool + line * D + 16 * grp) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (fp8_codes(a, S, x, w)) *reinterpret_cast<uint4*>(pool + line * D + 16 * grp) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
+      if (!(S >= 0x1p-60f && S <= 0x1p60f)) {
+        flag_error(a.dev_err, HS2_DEV_BAD_PAGE);
+        return;
+      }
       float top = fabsf(x[0]);  // the largest magnitude, or NaN
 #pragma unroll
       for (int j = 1; j < 15; j += 2) top = max_nan3(top, fabsf(x[j]), fabsf(x[j + 1]));

@@ -1,4 +1,4 @@
-// rot.cuh — rotation of a head's channels by a token's position, 16 channels a lane.
+// rot.cuh — rotation of a head's channels by a token's position, 16 channels (8 pairs) a lane.
 //
 // Pair i of a position p with table row (cos_0 .. cos_{R/2-1}, sin_0 .. sin_{R/2-1}), R channels
 // rotated: a' = a cos_i - b sin_i, b' = b cos_i + a sin_i, (a, b) = (x_i, x_{i + R/2}) (halves) or
@@ -11,71 +11,71 @@
 
 namespace hs2 {
 
-// cos and sin of the 16 channels of group grp (of grp < R / 16 groups): one for each channel.
-HS2_DEVI void load_angles(const RotTable& t, int pos, int grp, float (&cs)[16], float (&sn)[16]) {
-  const int half = t.dim / 2;
-  const float* row = t.table + (size_t)pos * t.dim;
-  if (t.pairs) {
-    const float4* c = reinterpret_cast<const float4*>(row + 8 * grp);
-    const float4* s = reinterpret_cast<const float4*>(row + half + 8 * grp);
+// A lane's 16 channels of a head of D: 8 from `lo` and 8 from `hi` on, where neighbouring lanes' pieces of
+// 8 are neighbours (16 in a row made every access of bfloat16 rows half sectors: 26273 latent rows with 32
+// heads took 73 us). Lanes [0, R / 16) have 8 pairs, of halves x[i] with x[8 + i], the others channels
+// that are not rotated.
+struct LaneChannels {
+  int lo, hi;
+  bool turn;  // whether they are rotated
+};
+HS2_DEVI LaneChannels lane_channels(const RotTable& t, int D, int grp) {
+  const int n = t.dim / 16;
+  if (grp < n) return {8 * grp, 8 * grp + t.dim / 2, true};
+  return {t.dim + 8 * (grp - n), t.dim + 8 * (grp - n) + (D - t.dim) / 2, false};
+}
+
+// cos and sin of a lane's 8 pairs.
+HS2_DEVI void load_angles(const RotTable& t, int pos, int grp, float (&cs)[8], float (&sn)[8]) {
+  // halves: pairs [8 g, 8 g + 8); neighbours: 4 of either piece
+  const float* row = t.table + (size_t)pos * t.dim + (t.pairs ? 4 * grp : 8 * grp);
+  const int next = t.pairs ? t.dim / 4 : 4;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float4 u = __ldg(c + i), v = __ldg(s + i);
-      cs[8 * i] = cs[8 * i + 1] = u.x, cs[8 * i + 2] = cs[8 * i + 3] = u.y;
-      cs[8 * i + 4] = cs[8 * i + 5] = u.z, cs[8 * i + 6] = cs[8 * i + 7] = u.w;
-      sn[8 * i] = sn[8 * i + 1] = v.x, sn[8 * i + 2] = sn[8 * i + 3] = v.y;
-      sn[8 * i + 4] = sn[8 * i + 5] = v.z, sn[8 * i + 6] = sn[8 * i + 7] = v.w;
-    }
+  for (int i = 0; i < 2; ++i) {
+    const float4 u = __ldg(reinterpret_cast<const float4*>(row + i * next));
+    const float4 v = __ldg(reinterpret_cast<const float4*>(row + t.dim / 2 + i * next));
+    cs[4 * i] = u.x, cs[4 * i + 1] = u.y, cs[4 * i + 2] = u.z, cs[4 * i + 3] = u.w;
+    sn[4 * i] = v.x, sn[4 * i + 1] = v.y, sn[4 * i + 2] = v.z, sn[4 * i + 3] = v.w;
+  }
+}
+
+HS2_DEVI void turn_pair(float& a, float& b, float c, float s) {
+  const float x = a, y = b;
+  a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+  b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+}
+HS2_DEVI void rotate16(const RotTable& t, const float (&cs)[8], const float (&sn)[8], float (&x)[16]) {
+  if (t.pairs) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn_pair(x[2 * i], x[2 * i + 1], cs[i], sn[i]);
   } else {
-    const int at = 16 * grp < half ? 16 * grp : 16 * grp - half;
-    const float4* c = reinterpret_cast<const float4*>(row + at);
-    const float4* s = reinterpret_cast<const float4*>(row + half + at);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 u = __ldg(c + i), v = __ldg(s + i);
-      cs[4 * i] = u.x, cs[4 * i + 1] = u.y, cs[4 * i + 2] = u.z, cs[4 * i + 3] = u.w;
-      sn[4 * i] = v.x, sn[4 * i + 1] = v.y, sn[4 * i + 2] = v.z, sn[4 * i + 3] = v.w;
-    }
+    for (int i = 0; i < 8; ++i) turn_pair(x[i], x[8 + i], cs[i], sn[i]);
   }
 }
 
-// x rotated, for the lanes with `turn`; the whole warp calls it. Lanes of one head are neighbours,
-// lane - grp the first.
-HS2_DEVI void rotate16(const RotTable& t, int grp, bool turn, const float (&cs)[16], const float (&sn)[16], float (&x)[16]) {
-  if (t.pairs) {
-    if (!turn) return;
-#pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-      const float a = x[i], b = x[i + 1];
-      x[i] = __fsub_rn(__fmul_rn(a, cs[i]), __fmul_rn(b, sn[i]));
-      x[i + 1] = __fadd_rn(__fmul_rn(b, cs[i]), __fmul_rn(a, sn[i]));
-    }
-    return;
-  }
-  const int lane = threadIdx.x & 31, h = t.dim / 32;  // groups of a half
-  const bool first = grp < h;
-  const int other = lane + (first ? h : -h);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float y = __shfl_sync(0xffffffffu, x[i], other & 31);
-    const float p = __fmul_rn(x[i], cs[i]), q = __fmul_rn(y, sn[i]);
-    if (turn) x[i] = first ? __fsub_rn(p, q) : __fadd_rn(p, q);
-  }
-}
-
-// 16 channels to a row of floats or bfloat16.
+// 8 channels of a row of floats or bfloat16.
 template <bool F32>
-HS2_DEVI void store16(void* rows, long long at, const float (&x)[16]) {
+HS2_DEVI void load8(const void* rows, long long at, float* x) {
+  if constexpr (F32) {
+    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rows) + at);
+    const float4 u = p[0], v = p[1];
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  } else {
+    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(rows) + at);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[2 * j] = bf16_lo(w[j]), x[2 * j + 1] = bf16_hi(w[j]);
+  }
+}
+template <bool F32>
+HS2_DEVI void store8(void* rows, long long at, const float* x) {
   if constexpr (F32) {
     float4* p = reinterpret_cast<float4*>(reinterpret_cast<float*>(rows) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    p[0] = make_float4(x[0], x[1], x[2], x[3]), p[1] = make_float4(x[4], x[5], x[6], x[7]);
   } else {
-    uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(rows) + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      p[i] = make_uint4(pack_bf16(x[8 * i], x[8 * i + 1]), pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                        pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+    *reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(rows) + at) =
+        make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
   }
 }
 

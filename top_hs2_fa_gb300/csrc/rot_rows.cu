@@ -2,37 +2,19 @@
 // rotated by their positions on the way (rot.cuh), and the rows of a latent cache.
 //
 // Bound by the bytes: rows in, codes and queries out; a program that rotates first writes and reads
-// Q and K once more. A warp has a row (or several): it looks the row's place up once, loads the
+// Q and K once more. A warp has a row (or two): it looks the row's place up once, loads the
 // table's cos and sin once into registers (a lane keeps its channels from head to head), and takes
-// the heads of K, V and Q, 512 channels a step.
+// the heads of K and V and then those of Q, 512 channels a step and of Q two steps' loads at a time.
+// 32768 rows of 32 heads over 4, d = 128, bf16 to FP8 (653 MB): 120 us, 0.80 of the copy bandwidth; with K, V
+// and Q in one loop 163 (16 warps an SM: the registers of the quantisation), with more warps at fewer
+// registers 148 and 167. 26273 latent rows of 512 + 64 with 32 heads (282 MB): 60 us, 0.69, the queries' 128
+// bytes a head at a stride of 384 in and 1152 out; 73 with 16 channels in a row per lane.
 #include "kv_rows.cuh"
 #include "rot.cuh"
 
 namespace hs2 {
 
 namespace {
-
-// load16 without the read-only path: q may be rotated in place
-template <bool F32>
-HS2_DEVI void load16_rw(const void* rows, long long at, float (&x)[16]) {
-  if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(rows) + at);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = p[i];
-      x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(rows) + at);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 v = p[i];
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) x[8 * i + 2 * j] = bf16_lo(w[j]), x[8 * i + 2 * j + 1] = bf16_hi(w[j]);
-    }
-  }
-}
 
 // Where row r is: its position (-1: nowhere, or flagged), and the physical page.
 struct RowSpot {
@@ -69,9 +51,9 @@ HS2_DEVI RowSpot warp_spots(const RowsArgs& a, const RotTable& rot, int r0, bool
 
 }  // namespace
 
-// grid (1 + rows / (8 TOK), splits of a row's heads). Block (0, 0) checks the row starts.
+// grid (1 + rows / (8 TOK), splits of a row's steps). Block (0, 0) checks the row starts.
 template <int D, int FMT, bool ROW_F32, int TOK>
-__global__ void __launch_bounds__(kRowThreads) kv_write_rot_kernel(const RotRowsArgs z) {
+__global__ void __launch_bounds__(kRowThreads, 2) kv_write_rot_kernel(const RotRowsArgs z) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int GPR = D / 16, HPS = 32 / GPR;  // lanes of a head; heads of a step
@@ -84,31 +66,75 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_rot_kernel(const RotRows
   const int r0 = ((blockIdx.x - 1) * (kRowThreads / 32) + warp) * TOK;
   if (r0 >= a.n_rows) return;
   const RowSpot mine = warp_spots<TOK>(a, z.rot, r0, blockIdx.y == 0);
-  const int kv_heads = a.v ? 2 * a.Hkv : a.Hkv, heads = kv_heads + z.Hq;
-  const int steps = (heads + HPS - 1) / HPS, per = (steps + gridDim.y - 1) / gridDim.y;
+  const int kv_heads = a.v ? 2 * a.Hkv : a.Hkv, kv_steps = (kv_heads + HPS - 1) / HPS;
+  const int steps = kv_steps + (z.Hq + HPS - 1) / HPS, per = (steps + gridDim.y - 1) / gridDim.y;
   const int s0 = blockIdx.y * per, s1 = min(steps, s0 + per);
-  const bool in_rot = 16 * grp < z.rot.dim;
+  // V as it lies; an FP4 cache's groups are 16 channels in a row
+  constexpr bool FP4 = FMT == HS2_FP4_E2M1;
+  const LaneChannels ch = lane_channels(z.rot, D, grp), cv{FP4 ? 16 * grp : 8 * grp, FP4 ? 16 * grp + 8 : D / 2 + 8 * grp, false};
 #pragma unroll 1
   for (int k = 0; k < TOK; ++k) {
     const int pos = __shfl_sync(0xffffffffu, mine.pos, k), phys = __shfl_sync(0xffffffffu, mine.phys, k), r = r0 + k;
     if (pos < 0) continue;
-    float cs[16], sn[16];
-    if (in_rot) load_angles(z.rot, pos, grp, cs, sn);
-#pragma unroll 2
-    for (int s = s0; s < s1; ++s) {
-      const int head = s * HPS + sub, g = head < a.Hkv ? head : head - a.Hkv;
-      const bool is_q = head >= kv_heads && head < heads, is_v = head >= a.Hkv && head < kv_heads;
+    float cs[8], sn[8];
+    if (ch.turn) load_angles(z.rot, pos, grp, cs, sn);
+    int s = s0;
+#pragma unroll 1
+    for (; s < min(s1, kv_steps); ++s) {  // K and V
+      const int head = s * HPS + sub;
+      const bool is_k = head < a.Hkv;
+      const int g = is_k ? head : head - a.Hkv;
+      const LaneChannels c = is_k ? ch : cv;
       float x[16];
-      if (head < a.Hkv) load16<ROW_F32>(a.k_rows, (long long)r * a.row_stride + g * D + 16 * grp, x);
-      else if (is_v) load16<ROW_F32>(a.v_rows, (long long)r * z.v_stride + g * D + 16 * grp, x);
-      else if (is_q) load16_rw<ROW_F32>(z.q, (long long)r * z.q_stride + (head - kv_heads) * D + 16 * grp, x);
-      rotate16(z.rot, grp, in_rot && !is_v, cs, sn, x);  // (lanes without a head rotate what they have)
-      if (is_q) {
-        store16<FMT == HS2_F32>(z.q_out, (long long)r * z.q_out_stride + (head - kv_heads) * D + 16 * grp, x);
-      } else if (head < kv_heads) {
-        const size_t slab = (size_t)phys * a.Hkv + g;
-        put16<D, FMT>(a, is_v, slab, slab * kPage + pos % kPage, grp, x);
+      if (head < kv_heads) {
+        const void* rows = is_k ? a.k_rows : a.v_rows;
+        const long long at = r * (is_k ? a.row_stride : z.v_stride) + g * D;
+        load8<ROW_F32>(rows, at + c.lo, x);
+        load8<ROW_F32>(rows, at + c.hi, x + 8);
+        if (c.turn) rotate16(z.rot, cs, sn, x);
       }
+      if (FP4 && s * HPS < a.Hkv) {
+        // K's groups of 16 channels in a row: neighbours swap, the even one takes the lower pieces' group
+        const bool odd = grp & 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[8 + i], 1);
+          if (is_k && odd) x[i] = got;
+          if (is_k && !odd) x[8 + i] = got;
+        }
+      }
+      if (head >= kv_heads) continue;
+      const size_t slab = (size_t)phys * a.Hkv + g, line = slab * kPage + pos % kPage;
+      if constexpr (FP4) {
+        put16<D, FMT>(a, !is_k, slab, line, is_k ? (grp & 1 ? ch.hi - 8 : ch.lo) / 16 : grp, x);
+      } else {
+        void* pool = is_k ? a.k : a.v;
+        if constexpr (FMT == HS2_FP8_E4M3) {
+          uint32_t w[4];
+          uint8_t* to = reinterpret_cast<uint8_t*>(pool) + line * D;
+          if (!fp8_codes(a, (is_k ? a.k_scale : a.v_scale)[slab], x, w)) continue;
+          *reinterpret_cast<uint2*>(to + c.lo) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(to + c.hi) = make_uint2(w[2], w[3]);
+        } else {
+          store8<FMT == HS2_F32>(pool, (long long)line * D + c.lo, x);
+          store8<FMT == HS2_F32>(pool, (long long)line * D + c.hi, x + 8);
+        }
+      }
+    }
+#pragma unroll 1
+    for (; s < s1; s += 2) {  // the queries, two steps' loads at a time
+      float x[16], y[16];
+      const int h0 = (s - kv_steps) * HPS + sub, h1 = h0 + HPS;
+      const bool two = h1 < z.Hq && s + 1 < s1;
+      const long long at = r * z.q_stride + h0 * D, to = r * z.q_out_stride + h0 * D;
+      if (h0 < z.Hq) load8<ROW_F32>(z.q, at + ch.lo, x), load8<ROW_F32>(z.q, at + ch.hi, x + 8);
+      if (two) load8<ROW_F32>(z.q, at + HPS * D + ch.lo, y), load8<ROW_F32>(z.q, at + HPS * D + ch.hi, y + 8);
+      __syncwarp();  // they may be rotated in place: a head's lanes load before any stores
+      if (ch.turn) rotate16(z.rot, cs, sn, x);
+      if (ch.turn) rotate16(z.rot, cs, sn, y);
+      if (h0 < z.Hq) store8<FMT == HS2_F32>(z.q_out, to + ch.lo, x), store8<FMT == HS2_F32>(z.q_out, to + ch.hi, x + 8);
+      if (two)
+        store8<FMT == HS2_F32>(z.q_out, to + HPS * D + ch.lo, y), store8<FMT == HS2_F32>(z.q_out, to + HPS * D + ch.hi, y + 8);
     }
   }
 }
@@ -116,7 +142,7 @@ __global__ void __launch_bounds__(kRowThreads) kv_write_rot_kernel(const RotRows
 // A latent cache's row is DC channels as they are and 64 that are rotated; the queries' 64 rotated
 // channels go to their place. grid as above; step 0 takes the row itself, step s > 0 queries.
 template <int DC, bool CACHE_F32, bool ROW_F32, int TOK>
-__global__ void __launch_bounds__(kRowThreads) latent_write_kernel(const LatentRowsArgs z) {
+__global__ void __launch_bounds__(kRowThreads, 3) latent_write_kernel(const LatentRowsArgs z) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int GPR = kLatentRot / 16, HPS = 32 / GPR;
@@ -131,38 +157,59 @@ __global__ void __launch_bounds__(kRowThreads) latent_write_kernel(const LatentR
   const RowSpot mine = warp_spots<TOK>(a, z.rot, r0, blockIdx.y == 0);
   const int steps = 1 + (z.Hq + HPS - 1) / HPS, per = (steps + gridDim.y - 1) / gridDim.y;
   const int s0 = blockIdx.y * per, s1 = min(steps, s0 + per);
+  const LaneChannels ch = lane_channels(z.rot, kLatentRot, grp);
 #pragma unroll 1
   for (int k = 0; k < TOK; ++k) {
     const int pos = __shfl_sync(0xffffffffu, mine.pos, k), phys = __shfl_sync(0xffffffffu, mine.phys, k), r = r0 + k;
     if (pos < 0) continue;
-    float cs[16], sn[16];
+    float cs[8], sn[8];
     load_angles(z.rot, pos, grp, cs, sn);
     const long long line = ((long long)phys * kPage + pos % kPage) * (DC + kLatentRot);
-#pragma unroll 2
-    for (int s = s0; s < s1; ++s) {
-      float x[16];
-      if (s == 0) {
-        if (lane < DC / 16) {
-          load16<ROW_F32>(z.c_rows, (long long)r * z.c_stride + 16 * lane, x);
-          store16<CACHE_F32>(a.k, line + 16 * lane, x);
-        }
-        if (lane < GPR) load16<ROW_F32>(z.r_rows, (long long)r * z.r_stride + 16 * lane, x);
-        rotate16(z.rot, grp, true, cs, sn, x);
-        if (lane < GPR) store16<CACHE_F32>(a.k, line + DC + 16 * lane, x);
-        continue;
+    int s = s0;
+    if (s == 0) {
+      float x[16], y[16];
+      const bool in_c = lane < DC / 16, in_r = lane < GPR;
+      const long long cat = r * z.c_stride + 8 * lane, rat = r * z.r_stride;
+      if (in_c) load8<ROW_F32>(z.c_rows, cat, x), load8<ROW_F32>(z.c_rows, cat + DC / 2, x + 8);
+      if (in_r) load8<ROW_F32>(z.r_rows, rat + ch.lo, y), load8<ROW_F32>(z.r_rows, rat + ch.hi, y + 8);
+      if (in_c) store8<CACHE_F32>(a.k, line + 8 * lane, x), store8<CACHE_F32>(a.k, line + 8 * lane + DC / 2, x + 8);
+      if (in_r) {
+        rotate16(z.rot, cs, sn, y);
+        store8<CACHE_F32>(a.k, line + DC + ch.lo, y);
+        store8<CACHE_F32>(a.k, line + DC + ch.hi, y + 8);
       }
+      ++s;
+    }
+    auto fetch = [&](int s, float (&x)[16]) {
       const int head = (s - 1) * HPS + sub;
-      const bool have = head < z.Hq;
-      if (have) load16_rw<ROW_F32>(z.q, (long long)r * z.q_stride + head * z.q_head + 16 * grp, x);
-      rotate16(z.rot, grp, true, cs, sn, x);
-      if (have) store16<CACHE_F32>(z.q_out, (long long)r * z.q_out_stride + head * z.q_out_head + 16 * grp, x);
+      if (head >= z.Hq) return;
+      const long long at = r * z.q_stride + head * z.q_head;
+      load8<ROW_F32>(z.q, at + ch.lo, x);
+      load8<ROW_F32>(z.q, at + ch.hi, x + 8);
+    };
+    auto finish = [&](int s, float (&x)[16]) {
+      const int head = (s - 1) * HPS + sub;
+      rotate16(z.rot, cs, sn, x);
+      if (head >= z.Hq) return;
+      const long long at = r * z.q_out_stride + head * z.q_out_head;
+      store8<CACHE_F32>(z.q_out, at + ch.lo, x);
+      store8<CACHE_F32>(z.q_out, at + ch.hi, x + 8);
+    };
+#pragma unroll 1
+    for (; s < s1; s += 2) {
+      float x[16], y[16];
+      fetch(s, x);
+      if (s + 1 < s1) fetch(s + 1, y);
+      __syncwarp();  // q may be rotated in place: a head's lanes load before any stores
+      finish(s, x);
+      if (s + 1 < s1) finish(s + 1, y);
     }
   }
 }
 
 // Rows of a latent cache back to arrays: a warp has a row at a time, 16 channels a lane.
 template <int DC, bool CACHE_F32, bool ROW_F32, int TOK>
-__global__ void __launch_bounds__(kRowThreads) latent_read_kernel(const LatentRowsArgs z) {
+__global__ void __launch_bounds__(kRowThreads, 3) latent_read_kernel(const LatentRowsArgs z) {
   griddep_launch_dependents();
   griddep_wait();
   const RowsArgs& a = z.rows;
@@ -180,16 +227,20 @@ __global__ void __launch_bounds__(kRowThreads) latent_read_kernel(const LatentRo
     if (pos < 0) continue;
     const long long line = ((long long)phys * kPage + pos % kPage) * (DC + kLatentRot);
     float x[16], y[16];
-    if (lane < DC / 16) load16<CACHE_F32>(a.k, line + 16 * lane, x);
-    if (lane < kLatentRot / 16) load16<CACHE_F32>(a.k, line + DC + 16 * lane, y);
-    if (lane < DC / 16) store16<ROW_F32>(const_cast<void*>(z.c_rows), (long long)r * z.c_stride + 16 * lane, x);
-    if (lane < kLatentRot / 16) store16<ROW_F32>(const_cast<void*>(z.r_rows), (long long)r * z.r_stride + 16 * lane, y);
+    const bool in_c = lane < DC / 16, in_r = lane < kLatentRot / 16;
+    void *c = const_cast<void*>(z.c_rows), *rr = const_cast<void*>(z.r_rows);
+    const long long cat = r * z.c_stride + 8 * lane, rat = r * z.r_stride + 8 * lane, at = line + 8 * lane;
+    if (in_c) load8<CACHE_F32>(a.k, at, x), load8<CACHE_F32>(a.k, at + DC / 2, x + 8);
+    if (in_r) load8<CACHE_F32>(a.k, at + DC, y), load8<CACHE_F32>(a.k, at + DC + 32, y + 8);
+    if (in_c) store8<ROW_F32>(c, cat, x), store8<ROW_F32>(c, cat + DC / 2, x + 8);
+    if (in_r) store8<ROW_F32>(rr, rat, y), store8<ROW_F32>(rr, rat + 32, y + 8);
   }
 }
 
 namespace {
 
-// Rows of a warp and splits of a row's heads: few rows are spread over as many warps as there are steps.
+// Rows of a warp and splits of a row's heads: few rows are spread over as many warps as there are steps; of
+// many, a warp has two whole ones (32768 rows 120 us; with one 124, with eight 124).
 constexpr int kManyRows = 4096;
 constexpr int kRowsPerWarp = 4;
 
@@ -200,7 +251,7 @@ dim3 row_grid(int n_rows, int tok, int splits) {
 
 template <int D, int FMT, bool ROW_F32>
 cudaError_t launch_rot(const RotRowsArgs& z, cudaStream_t s) {
-  const int hps = 512 / D, steps = ((z.rows.v ? 2 : 1) * z.rows.Hkv + z.Hq + hps - 1) / hps;
+  const int hps = 512 / D, steps = ((z.rows.v ? 2 : 1) * z.rows.Hkv + hps - 1) / hps + (z.Hq + hps - 1) / hps;
   if (z.rows.n_rows >= kManyRows)
     return launch_pdl(kv_write_rot_kernel<D, FMT, ROW_F32, kRowsPerWarp>, row_grid(z.rows.n_rows, kRowsPerWarp, 1),
                       dim3(kRowThreads), 0, s, z);

@@ -627,19 +627,36 @@ def _rot(rot: torch.Tensor, style: str) -> hs2_rot:
     """The table of cosines and sines, float32 [positions][dim], and how channels pair up."""
     if rot.dtype is not torch.float32 or rot.dim() != 2 or not rot.is_contiguous():
         raise HS2Error("rot must be a contiguous float32 matrix")
-    if style not in _STYLES:
+    pairs = _STYLES.get(style)
+    if pairs is None:
         raise HS2Error("style must be 'halves' or 'pairs'")
-    return hs2_rot(rot.data_ptr(), rot.shape[0], rot.shape[1], _STYLES[style])
+    n, dim = rot.shape
+    return hs2_rot(rot.data_ptr(), n, dim, pairs)
 
 
-def _strides(t: torch.Tensor, name: str, *shape):
-    """(token, head) strides of rows t [n][...][width] of that shape, the last channels contiguous."""
-    if t.shape != shape or t.stride(-1) != 1:
+def _strides(t: torch.Tensor, name: str, shape: tuple):
+    """(token, head) strides of rows t [n][width] or [n][heads][width], the channels contiguous."""
+    st = t.stride()
+    if t.shape != shape or st[-1] != 1:
         raise HS2Error(f"{name} must be of shape {list(shape)} with contiguous channels")
-    width = shape[-1]
-    head = (t.stride(1) if shape[1] > 1 else width) if len(shape) == 3 else width
-    # (one token: its stride reaches nothing)
-    return t.stride(0) if shape[0] > 1 else (shape[1] - 1) * head + width if len(shape) == 3 else width, head
+    # (a stride along one element reaches nothing)
+    if len(shape) == 2:
+        return (st[0] if shape[0] > 1 else shape[1]), shape[1]
+    n, heads, width = shape
+    head = st[1] if heads > 1 else width
+    return (st[0] if n > 1 else (heads - 1) * head + width), head
+
+
+def _queries(q: torch.Tensor, q_out, n: int, width: int, c: hs2_kv, stream):
+    """(heads, q's strides, q_out or a new one, its strides) of the queries that go with n rows."""
+    Hq = q.shape[1] if q.dim() == 3 else 0
+    shape, out_type = (n, Hq, width), torch.float32 if c.dtype == F32 else torch.bfloat16
+    qs = _strides(q, "q", shape)
+    if q_out is None:
+        return Hq, qs, _new(shape, out_type, q.device, stream), (Hq * width, width)
+    if q_out.dtype is not out_type:
+        raise HS2Error("q_out must be bfloat16 (float32 for an F32 cache)")
+    return Hq, qs, q_out, _strides(q_out, "q_out", shape)
 
 
 def hs2_kv_write_rot(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, row_start: torch.Tensor,
@@ -652,32 +669,29 @@ def hs2_kv_write_rot(kv: KV, k_rows: torch.Tensor, v_rows: torch.Tensor | None, 
     takes them (bfloat16; float32 for an F32 cache), in ``q_out`` if given (it may be ``q``)."""
     lib = load()
     c, dev = kv._cached()[:2]
-    dtype = k_rows.dtype
+    dtype, shape, stride = k_rows.dtype, k_rows.shape, k_rows.stride()
     if (v_rows is None) != (kv.v is None):
         raise HS2Error("v_rows goes with a cache that has V")
-    if dtype not in _ROW_DTYPES or any(x is not None and x.dtype is not dtype for x in (v_rows, q)):
+    if dtype not in _ROW_DTYPES or (v_rows is not None and v_rows.dtype is not dtype) or (
+            q is not None and q.dtype is not dtype):
         raise HS2Error("rows must be float32 or bfloat16, K, V and q alike")
-    n = k_rows.shape[0]
-    ks = _token_stride(k_rows.shape, k_rows.stride(), n, c)
-    vs = ks if v_rows is None else _token_stride(v_rows.shape, v_rows.stride(), n, c)
+    n = shape[0]
+    ks = vs = _token_stride(shape, stride, n, c)
+    if v_rows is not None and (v_rows.stride() != stride or v_rows.shape != shape):
+        vs = _token_stride(v_rows.shape, v_rows.stride(), n, c)
     _i32(row_start, "row_start", c.batch + 1)
-    Hq = qs = os_ = 0
+    Hq, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs, qh = _strides(q, "q", n, Hq, c.d)
-        out_type = torch.float32 if c.dtype == F32 else torch.bfloat16
-        if q_out is None:
-            q_out = _new((n, Hq, c.d), out_type, q.device, stream)
-        os_, oh = _strides(q_out, "q_out", n, Hq, c.d)
-        if q_out.dtype is not out_type or qh != c.d or oh != c.d:
-            raise HS2Error("q and q_out must have contiguous tokens, q_out bfloat16 (float32 for an F32 cache)")
+        Hq, qs, q_out, os_ = _queries(q, q_out, n, c.d, c, stream)
+        if qs[1] != c.d or os_[1] != c.d:
+            raise HS2Error("q and q_out must have contiguous tokens")
     elif q_out is not None:
         raise HS2Error("q_out goes with q")
     r = _rot(rot, style)
     st = _launch_stream(stream, dev, k_rows, v_rows, row_start, rot, q, q_out, dev_err)
     _check(lib.hs2_kv_write_rot(ctypes.byref(c), k_rows.data_ptr(), ks, _ptr(v_rows), vs, _ROW_DTYPES[dtype],
-                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs, Hq,
-                                _ptr(q_out) if Hq else None, os_, _ptr(dev_err), st))
+                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs[0], Hq,
+                                _ptr(q_out) if Hq else None, os_[0], _ptr(dev_err), st))
     return q_out
 
 
@@ -699,28 +713,21 @@ def hs2_latent_write(kv: KV, c_rows: torch.Tensor, r_rows: torch.Tensor, row_sta
     lib = load()
     c, dev = kv._cached()[:2]
     dc, dtype = _latent(c), c_rows.dtype
-    if dtype not in _ROW_DTYPES or any(x is not None and x.dtype is not dtype for x in (r_rows, q)):
+    if dtype not in _ROW_DTYPES or r_rows.dtype is not dtype or (q is not None and q.dtype is not dtype):
         raise HS2Error("rows must be float32 or bfloat16, c, r and q alike")
     n = c_rows.shape[0]
-    cs, rs = _strides(c_rows, "c_rows", n, dc)[0], _strides(r_rows, "r_rows", n, 64)[0]
+    cs, rs = _strides(c_rows, "c_rows", (n, dc))[0], _strides(r_rows, "r_rows", (n, 64))[0]
     _i32(row_start, "row_start", c.batch + 1)
-    Hq = qs = qh = os_ = oh = 0
+    Hq, qs, os_ = 0, (0, 0), (0, 0)
     if q is not None:
-        Hq = q.shape[1] if q.dim() == 3 else 0
-        qs, qh = _strides(q, "q", n, Hq, 64)
-        out_type = torch.float32 if c.dtype == F32 else torch.bfloat16
-        if q_out is None:
-            q_out = _new((n, Hq, 64), out_type, q.device, stream)
-        os_, oh = _strides(q_out, "q_out", n, Hq, 64)
-        if q_out.dtype is not out_type:
-            raise HS2Error("q_out must be of the cache's type")
+        Hq, qs, q_out, os_ = _queries(q, q_out, n, 64, c, stream)
     elif q_out is not None:
         raise HS2Error("q_out goes with q")
     r = _rot(rot, style)
     st = _launch_stream(stream, dev, c_rows, r_rows, row_start, rot, q, q_out, dev_err)
     _check(lib.hs2_latent_write(ctypes.byref(c), c_rows.data_ptr(), cs, r_rows.data_ptr(), rs, _ROW_DTYPES[dtype],
-                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs, qh, Hq,
-                                _ptr(q_out) if Hq else None, os_, oh, _ptr(dev_err), st))
+                                row_start.data_ptr(), n, ctypes.byref(r), _ptr(q) if Hq else None, qs[0], qs[1], Hq,
+                                _ptr(q_out) if Hq else None, os_[0], os_[1], _ptr(dev_err), st))
     return q_out
 
 
@@ -737,7 +744,7 @@ def hs2_latent_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.d
         out = _new((n_rows, dc), dtype, kv.k.device, stream), _new((n_rows, 64), dtype, kv.k.device, stream)
     elif out[0].dtype is not dtype or out[1].dtype is not dtype:
         raise HS2Error("out must be of the dtype")
-    cs, rs = _strides(out[0], "out[0]", n_rows, dc)[0], _strides(out[1], "out[1]", n_rows, 64)[0]
+    cs, rs = _strides(out[0], "out[0]", (n_rows, dc))[0], _strides(out[1], "out[1]", (n_rows, 64))[0]
     _i32(row_start, "row_start", c.batch + 1)
     st = _launch_stream(stream, dev, row_start, out[0], out[1], dev_err)
     _check(load().hs2_latent_read(ctypes.byref(c), out[0].data_ptr(), cs, out[1].data_ptr(), rs, _ROW_DTYPES[dtype],
@@ -808,13 +815,13 @@ def hs2_latent_prefill(q: torch.Tensor, k: torch.Tensor, r: torch.Tensor, v: tor
     lib = load()
     n, Hq, _ = q.shape
     nk = r.shape[0]
-    if q.dtype not in _ROW_DTYPES or any(x.dtype is not q.dtype for x in (k, r, v)):
+    if q.dtype not in _ROW_DTYPES or not (k.dtype is r.dtype is v.dtype is q.dtype):
         raise HS2Error("q, k, r and v must be bfloat16 or float32, all alike")
     if q.shape[2] != 192 or not q.is_contiguous():
         raise HS2Error("q must be contiguous [n_rows][Hq][192]")
-    kt, kh = _strides(k, "k", nk, Hq, 128)
-    vt, vh = _strides(v, "v", nk, Hq, 128)
-    rt = _strides(r, "r", nk, 64)[0]
+    kt, kh = _strides(k, "k", (nk, Hq, 128))
+    vt, vh = _strides(v, "v", (nk, Hq, 128))
+    rt = _strides(r, "r", (nk, 64))[0]
     batch = row_start.numel() - 1
     if batch < 1:
         raise HS2Error("row_start has batch + 1 entries")
