@@ -160,75 +160,63 @@ __global__ void __launch_bounds__(kPThreads, 1)
       next = fetch_unit(p, un + 1, end < rg.end);
       const bool both = u.ntok > kWRows;
       // S of half h of the tile at the K ring's place
-      auto scores = [&](int h, bool last) {
-        int st = ks;
-#pragma unroll
-        for (int c = 0; c < kPBlocks; ++c) {
-          tc::mma4_f16_warp<2, 2>(tS + h * 128, q0 + h * (kPBlocks * kBlk) + c * kBlk, k0 + st * kBlk, idS, c > 0 ? 1u : 0u, el);
-          if (h == 1 || !both) tc::mma_commit_warp(&sm.k_empty[st], el);
-          if (++st == kPKRing) st = 0;
-        }
-        tc::mma_commit_warp(&sm.s_full[h], el);
-        if (last) tc::mma_commit_warp(&sm.q_empty[h], el);
-      };
-      auto k_landed = [&]() {
-        bool landed = true;
+      auto scores = [&](int h, bool last) -> bool {
         int st = ks, ph = kp;
 #pragma unroll
         for (int c = 0; c < kPBlocks; ++c) {
-          landed = landed && tc::mbar_wait(&sm.k_full[st], ph);
+          if (h == 0) {
+            if (!all(tc::mbar_wait(&sm.k_full[st], ph))) return false;
+            tc::tc_fence_after();
+          }
+          tc::mma4_f16_warp<2, 2>(tS + h * 128, q0 + h * (kPBlocks * kBlk) + c * kBlk, k0 + st * kBlk, idS, c > 0 ? 1u : 0u, el);
+          if (h == 1 || !both) tc::mma_commit_warp(&sm.k_empty[st], el);
           if (++st == kPKRing) st = 0, ph ^= 1;
         }
-        return all(landed);
+        tc::mma_commit_warp(&sm.s_full[h], el);
+        if (last) tc::mma_commit_warp(&sm.q_empty[h], el);
+        return true;
       };
       auto k_next = [&]() {
         ks += kPBlocks;
         if (ks >= kPKRing) ks -= kPKRing, kp ^= 1;
       };
-      ok = all(tc::mbar_wait(&sm.q_full[0], seg[0]++ & 1)) && k_landed();
-      if (ok) {
+      ok = all(tc::mbar_wait(&sm.q_full[0], seg[0]++ & 1)) && scores(0, at + 1 == end);
+      if (ok && both) {
+        ok = all(tc::mbar_wait(&sm.q_full[1], seg[1]++ & 1));
         tc::tc_fence_after();
-        scores(0, at + 1 == end);
-        if (both) {
-          ok = all(tc::mbar_wait(&sm.q_full[1], seg[1]++ & 1));
-          tc::tc_fence_after();
-          if (ok) scores(1, at + 1 == end);
-        }
-        k_next();
+        if (ok) (void)scores(1, at + 1 == end);
       }
+      k_next();
       // (the first P of a unit comes from the threads that have read the last unit out of O)
       for (int j = 0; ok && at < end; ++at, ++j) {
         const bool more = at + 1 < end, last = at + 2 == end;
-        auto products = [&](int h) {  // O += P V, 64 keys at a time
-          int st = vs;
+        // O += P V, 64 keys at a time (the second 64 may still be on their way)
+        auto products = [&](int h) -> bool {
+          int st = vs, ph = vp;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
+            if (h == 0) {
+              if (!all(tc::mbar_wait(&sm.v_full[st], ph))) return false;
+              tc::tc_fence_after();
+            }
             tc::mma4_f16_ts_warp<8, 128>(tO + h * 128, tS + h * 128 + c * 32, v0 + st * kVh, idO, (j > 0 || c > 0) ? 1u : 0u, el);
             if (h == 1 || !both) tc::mma_commit_warp(&sm.v_empty[st], el);
-            if (++st == kPVRing) st = 0;
+            if (++st == kPVRing) st = 0, ph ^= 1;
           }
           tc::mma_commit_warp(&sm.pv_done[h], el);
+          return true;
         };
-        const int v1 = vs + 1 == kPVRing ? 0 : vs + 1;
-        ok = all(tc::mbar_wait(&sm.v_full[vs], vp) && tc::mbar_wait(&sm.v_full[v1], v1 ? vp : vp ^ 1) &&
-                 tc::mbar_wait(&sm.p_full[0], mine[0] & 1));
+        ok = all(tc::mbar_wait(&sm.p_full[0], mine[0] & 1)) && products(0);
         if (!ok) break;
-        tc::tc_fence_after();
-        products(0);
         ++mine[0];
-        if (more) {
-          ok = k_landed();
-          if (!ok) break;
-          tc::tc_fence_after();
-          scores(0, last);
-        }
+        if (more && !(ok = scores(0, last))) break;
         if (both) {
           ok = all(tc::mbar_wait(&sm.p_full[1], mine[1] & 1));
           if (!ok) break;
           tc::tc_fence_after();
-          products(1);
+          (void)products(1);
           ++mine[1];
-          if (more) scores(1, last);
+          if (more) (void)scores(1, last);
         }
         if (more) k_next();
         vs += 2;
