@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, kMergeBlocks) chunk_merge_ke
 
 cudaError_t launch_chunk_merge(const ChunkArgs& a, const ChunkPlan* plans, int n_plans, int d, cudaStream_t s) {
   const ChunkPlan &p0 = plans[0], &p1 = plans[n_plans - 1];
-  const dim3 grid(kMergeBlocks * p0.ctas, n_plans);  // every plan is cut among as many CTAs
+  // every plan is cut among as many CTAs; a range of 128-row units is a pair's
+  const dim3 grid(kMergeBlocks * p0.ctas * (p0.tile_rows == 128 ? 2 : 1), n_plans);
   auto kern = d == 512 ? chunk_merge_kernel<512> : d == 256 ? chunk_merge_kernel<256> : d == 128 ? chunk_merge_kernel<128>
                                                                                          : chunk_merge_kernel<64>;
   return launch_pdl(kern, grid, dim3(kMergeWarps * 32), 0, s, a, p0, p1);
