@@ -88,6 +88,14 @@ int sm_count() {
   return std::min(n, 512);  // the merge's blocks hold the list of cut units, one per CTA at most
 }
 
+// Up to so many keys no unit is cut, and there is nothing to merge: a unit's two tiles (four of the expanded
+// form) take a CTA no longer than the parts take the merge. Cut and whole, us on the device:
+//   absorbed: 4 single tokens of 16 heads over 256 keys 19.2 and 17.0, 64 of them 20.2 and 19.1; over 500
+//     keys 19.6 and 20.9, 23.4 and 22.8, 16 sequences of 3 tokens of 32 heads 24.7 and 27.2.
+//   expanded: 3 prompts of 64 tokens, 16 heads, over 256 keys 15.0 and 12.5, over 500 15.8 and 15.2; 16 of 100
+//     28.0 and 24.4; one of 128 tokens over 700 keys 17.3 and 18.9.
+constexpr int kWholeAbsorbed = 256, kWholeExpanded = 512;
+
 // Workspace of an attention call: the plan and the parts of cut units.
 struct Layout {
   hs2::ChunkPlan plan;  // pointers after bind()
@@ -96,7 +104,7 @@ struct Layout {
 };
 
 // `heads` units beside one another per sequence, of G rows a token, parts of dv channels.
-Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t) {
+Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t, int whole) {
   Layout L{};
   size_t at = 0;
   auto take = [&](int i, size_t bytes) { L.off[i] = at, at = align256(at + bytes); };
@@ -104,7 +112,7 @@ Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, 
   p.ctas = ctas;
   p.tile_rows = tile_rows;
   p.max_rows = 0x7fffffff;
-  p.snap = 32;  // ranges differ by a unit at most: with 2 a prompt's by a third (16384 tokens of 16 heads 981 us)
+  p.snap = max_t <= whole ? 0 : 32;  // ranges differ by a unit at most: with 2 a prompt's by a third (16384 tokens of 16 heads 981 us)
   const long long units = heads * ((long long)n_rows * G / tile_rows + std::min(batch, n_rows));
   p.max_units = (int)std::min<long long>(units, 1 << 30);
   L.tiles = units * (max_t / 128 + 2);
@@ -133,12 +141,13 @@ void bind(Layout& L, char* ws) {
 int chunk_width(long long top) { return top <= 16 ? 16 : top <= 32 ? 32 : top <= 64 ? 64 : 128; }
 Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t) {
   const int sms = sm_count();
-  return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t);
+  return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t,
+                kWholeAbsorbed);
 }
 
 // A unit of the expanded form is 256 tokens of a head.
 Layout prefill_layout(int n_rows, int Hq, int batch, int max_t) {
-  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t);
+  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t, kWholeExpanded);
 }
 
 bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
@@ -284,7 +293,7 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
     return HS2_ERR_ARG;
   cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
   if (e == cudaSuccess) e = hs2::launch_latent_chunk(tq, tk, a, L.plan, dc, s);
-  if (e == cudaSuccess) e = hs2::launch_chunk_merge(a, &L.plan, 1, dc, s);
+  if (e == cudaSuccess && L.plan.snap) e = hs2::launch_chunk_merge(a, &L.plan, 1, dc, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 
@@ -338,7 +347,7 @@ hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_row
     return HS2_ERR_ARG;
   cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
   if (e == cudaSuccess) e = hs2::launch_latent_prefill(tq, tk, tr, tv, a, L.plan, s);
-  if (e == cudaSuccess) e = hs2::launch_chunk_merge(a, &L.plan, 1, hs2::kLatentValue, s);
+  if (e == cudaSuccess && L.plan.snap) e = hs2::launch_chunk_merge(a, &L.plan, 1, hs2::kLatentValue, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
 }
 
