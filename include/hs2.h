@@ -34,8 +34,8 @@
  *   into (HS2_DEV_*) when they meet an out-of-range block-table entry or index,
  *   or give up a bounded wait. Bad accesses are skipped, never performed. The
  *   caller zeroes it and reads it after synchronising.
- * - Outputs are float32 whatever the input dtype (fp32 accumulation); hs2_fa_chunk and
- *   hs2_kv_read take the output type as an argument.
+ * - Outputs are float32 whatever the input dtype (fp32 accumulation); hs2_fa_chunk, hs2_kv_read
+ *   and the latent operators take the output type as an argument.
  * - Index sets are written sorted ascending, padded with -1, with a count array.
  *   Among equal scores the lower position (or lower block id) wins.
  */
@@ -362,7 +362,8 @@ typedef struct {
 } hs2_rot;
 
 /* hs2_kv_write with K, and optionally the queries of the same rows, rotated: rows, positions, types
- * and errors as there; K and V rows have a token stride each. q: [n_rows][Hq][d] of row_dtype, token r
+ * and errors as there; K and V rows have a token stride each (strides here and below: at most 2^31
+ * elements). q: [n_rows][Hq][d] of row_dtype, token r
  * at r * q_stride elements, or NULL with Hq = 0; q_out: the rotated queries as hs2_fa_chunk takes
  * them, float32 for an F32 cache, else bfloat16, [n_rows][Hq][d] at q_out_stride; it may be q itself
  * (same type and stride) and overlaps nothing else. Rows that are flagged or outside every sequence have
@@ -374,7 +375,7 @@ hs2_status hs2_kv_write_rot(const hs2_kv* kv, const void* k_rows, int64_t k_stri
 
 /* ---------------------------------------------------------------------------
  * Latent attention: keys and values of all heads from one latent vector a token, plus a key part
- * that carries the position ([L10] §5.1: the V3.2 layers' latent of 512 + 64 channels).
+ * that carries the position.
  * A latent cache is an hs2_kv with v = NULL, Hkv = 1 and d = dc + 64, dc 512 or 256: a row is dc
  * latent channels c and 64 rotated channels r. F32 or BF16; FP8 / FP4: HS2_ERR_UNSUPPORTED.
  *
@@ -397,8 +398,9 @@ hs2_status hs2_latent_read(const hs2_kv* kv, void* c_rows, int64_t c_stride, voi
  * taken into the latent space and their rotated part. Row at position p, head h:
  *   x(s) = scale * q_h . [c_s, r_s], s <= p;  o = sum_s softmax(x)(s) c_s;  lse = log sum_s exp x(s).
  * o: [n_rows][Hq][dc] of o_dtype (HS2_F32 or HS2_BF16), lse float32 [n_rows][Hq] or NULL. Hq a power
- * of two up to 128. Bad pages and lengths, sizes, precision, workspace: as hs2_fa_chunk (bf16 caches:
- * the weights enter the second product rounded to bfloat16; float32 caches: not rounded). */
+ * of two up to 128. max_n and max_t, bad pages and lengths, values that are not finite, sizes and
+ * workspace (hs2_latent_chunk_workspace(...) bytes): as hs2_fa_chunk. BF16 caches: the weights enter the
+ * second product rounded to bfloat16; float32 caches: not rounded. */
 size_t hs2_latent_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_n, int max_t);
 hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows, int max_n, int Hq, const hs2_kv* kv,
                             int max_t, float scale, void* o, hs2_dtype o_dtype, float* lse, void* workspace,
@@ -414,7 +416,11 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
  * with strides of a multiple of 16 bytes. q: [n_rows][Hq][192] of the same type; o:
  * [n_rows][Hq][128] of o_dtype. A sequence with n_b > max_n, more keys than max_t, fewer keys than rows,
  * or rows or keys outside the arrays sets HS2_DEV_BAD_LENGTH and its rows are not written (a
- * descending row_start or key_start: none or only some rows are). Precision and workspace as hs2_fa_chunk. */
+ * descending row_start or key_start: none or only some rows are). Precision as hs2_latent_chunk; a V row
+ * that is not finite can make every row of its sequence undefined, what lies outside every sequence
+ * does not matter. HS2_ERR_UNSUPPORTED: n_keys above 2^31 - 257, and declared sizes of more than 2^30
+ * tiles (max_t / 128 + 2 for every 256 of the n_rows rows and every sequence, times Hq). workspace: at
+ * least hs2_latent_prefill_workspace(...) bytes, as there. */
 typedef struct {
   const void* k;
   const void* r;

@@ -270,6 +270,50 @@ def test_graph_and_streams(H):
         assert torch.equal(a, b) and torch.equal(b, c)
 
 
+def test_more_sequences_than_threads(H):
+    """1100 sequences: the plan takes them 1024 at a time, and as many units."""
+    lens = [1 + (i * 37) % 150 for i in range(1100)]
+    counts = [0 if i % 7 == 3 else 1 for i in range(1100)]
+    rng, pool, bt, rs, q = latent_case(40, "bf16", lens, counts, 4, 256)
+    want = L.absorbed(L.values(pool), L.values(q), rs, lens, bt, SCALE)
+    o, lse, err = run(H, pool, bt, lens, rs, q)
+    assert err == 0
+    check((o, lse), want, "bf16", 320)
+    rng, rs, ks, q, kv, r = expanded_case(40, "bf16", counts, lens, 2)
+    want = want_expanded(rs, ks, q, kv, r)
+    o, lse, err = run_expanded(H, rs, ks, q, kv, r)
+    assert err == 0
+    check((o, lse), want, "bf16", 192)
+
+
+@pytest.mark.parametrize("Hq", [16, 128])
+def test_two_calls_at_once(H, Hq):
+    """Two streams, a workspace each; and one after another in one workspace with other sizes."""
+    import torch
+
+    cases = [latent_case(48 + i, "bf16", lens, counts, Hq, 512) + (lens,) for i, (lens, counts) in
+             enumerate((([3000, 500], [2, 1]), ([129] * 30, [1] * 30)))]
+    ins = [(T.device(q), T.device(rs), latent_kv(H, pool, bt, lens), int(np.diff(rs).max()), max(lens))
+           for rng, pool, bt, rs, q, lens in cases]
+    alone = [H.hs2_latent_chunk(q, rs, kv, SCALE, mn, max_t=mt) for q, rs, kv, mn, mt in ins]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in ins]
+    got = [[] for _ in ins]
+    for _ in range(5):
+        for i, (q, rs, kv, mn, mt) in enumerate(ins):
+            got[i].append(H.hs2_latent_chunk(q, rs, kv, SCALE, mn, max_t=mt, stream=streams[i]))
+    torch.cuda.synchronize()
+    size = max(H.hs2_latent_chunk_workspace(q.shape[0], Hq, kv, mn, mt) for q, rs, kv, mn, mt in ins)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        for i, (q, rs, kv, mn, mt) in enumerate(ins):
+            got[i].append(H.hs2_latent_chunk(q, rs, kv, SCALE, mn, max_t=mt, workspace=ws))
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for x in runs:
+            assert torch.equal(x[0], want[0]) and torch.equal(x[1], want[1])
+
+
 # ---------------------------------------------------------------------------- expanded
 def expanded_case(seed, dtype, counts, keys, Hq, first=0, extra=0, key_first=0, key_extra=0):
     rng = np.random.default_rng(seed)

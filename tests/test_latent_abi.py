@@ -88,6 +88,7 @@ def test_latent_chunk_arguments(lib):
     for over in (dict(v=32), dict(Hkv=2), dict(d=128), dict(d=512), dict(page_size=16)):
         assert _chunk(lib, _latent(**over)) == -1, over
     assert _chunk(lib, _latent(dtype=2)) == -2
+    assert _chunk(lib, _latent(num_pages=1 << 25)) == -2  # 32-bit rows
     assert _chunk(lib, _latent(), n=0) == 0 and _chunk(lib, _latent(), max_n=0) == 0
     kv = _latent()
     assert lib.hs2_latent_chunk_workspace(4, 16, ctypes.byref(kv), 3, 300) > 0
@@ -115,6 +116,9 @@ def test_latent_prefill_arguments(lib):
                  dict(n_keys=-1), dict(dtype=2)):
         assert _prefill(lib, _keys(**over)) == -1, over
     assert _prefill(lib, None) == -1
+    assert _prefill(lib, _keys(n_keys=0x7fffffff)) == -2  # 32-bit rows
+    assert _prefill(lib, _keys(), Hq=1 << 16) == -2
+    assert _prefill(lib, _keys(), n=1 << 28, max_n=1 << 28, max_t=1 << 30) == -2  # 32-bit tile counts
     assert _prefill(lib, _keys(), n=0) == 0 and _prefill(lib, _keys(), max_n=0) == 0
     assert lib.hs2_latent_prefill_workspace(4, 4, 2, 3, 300) > 0
     for bad in ((-1, 4, 2, 3, 300), (4, 0, 2, 3, 300), (4, 4, 0, 3, 300), (4, 4, 2, -3, 300), (4, 4, 2, 3, -1)):

@@ -322,7 +322,8 @@ hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_row
   }
   const bool f32 = keys->dtype == HS2_F32;
   Layout L = prefill_layout(n_rows, Hq, batch, max_t);
-  if (Hq > 65535 || (!f32 && L.tiles > 1LL << 30)) return HS2_ERR_UNSUPPORTED;  // grid y; 32-bit tile counts
+  // grid y; 32-bit tile counts and rows
+  if (Hq > 65535 || (!f32 && (L.tiles > 1LL << 30 || keys->n_keys > 0x7fffffff - 256))) return HS2_ERR_UNSUPPORTED;
   if (!workspace || ((uintptr_t)workspace & 255u) || ws_bytes < (f32 ? 256 : L.total)) return HS2_ERR_ARG;
   hs2::ChunkArgs a = chunk_args(q, row_start, n_rows, max_n, max_t, batch, Hq, scale, o, o_dtype, lse, dev_err);
   a.Hkv = Hq;
