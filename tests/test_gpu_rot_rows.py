@@ -78,7 +78,7 @@ def test_write(H, dtype, row, d, Hkv, Hq, rot, pairs):
 
 
 @pytest.mark.parametrize("dtype,row", [("fp4", "bf16"), ("fp8", "f32"), ("bf16", "bf16")])
-@pytest.mark.parametrize("n", [4095, 4096, 4099, 9001])
+@pytest.mark.parametrize("n", [4096, 6999, 7000, 7003, 9001])
 def test_many_rows(H, dtype, row, n):
     """About the border where a warp takes several rows, page-unaligned, key and query of their own strides."""
     import torch
@@ -189,7 +189,7 @@ def test_flagged_rows(H):
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("row", ["f32", "bf16"])
 @pytest.mark.parametrize("dc,Hq,pairs,n1", [(512, 16, True, 3), (256, 1, False, 3), (512, 0, True, 3), (512, 9, False, 3),
-                                            (256, 128, True, 70), (512, 2, True, 4300)])
+                                            (256, 128, True, 70), (512, 2, True, 4300), (512, 9, True, 7103), (256, 0, False, 14100)])
 def test_latent_rows(H, dtype, row, dc, Hq, pairs, n1):
     import torch
 

@@ -239,10 +239,14 @@ __global__ void __launch_bounds__(kRowThreads, 3) latent_read_kernel(const Laten
 
 namespace {
 
-// Rows of a warp and splits of a row's heads: few rows are spread over as many warps as there are steps; of
-// many, a warp has two whole ones (32768 rows 120 us; with one 124, with eight 124).
-constexpr int kManyRows = 4096;
-constexpr int kRowsPerWarp = 4;
+// Rows of a warp and splits of a row's steps: few rows are spread over a warp a step, of many a warp has
+// two whole ones (32768 rows 120 us; with one 124, with eight 124). Spread and whole, by rows times steps:
+//   K, V and 32 heads over 4, d = 128 (10 steps): 256 rows 4.4 and 9.0 us, 1024 9.0 and 9.9, 2048 15.6 and 10.7,
+//   8192 68 and 34. Latent rows with 32 heads (5 steps): 1024 rows 4.9 and 7.4, 2048 7.0 and 8.9, 4096 12.1 and
+//   10.7, 16384 55 and 44. Reading (no steps to spread) 256 rows 2.3 and 2.5, 4096 3.1 and 3.3, 8192 4.1 and 3.6.
+constexpr long long kManySteps = 14000;
+constexpr int kReadSteps = 2;  // what a row of the reading counts as
+constexpr int kRowsPerWarp = 2;
 
 dim3 row_grid(int n_rows, int tok, int splits) {
   const int per = kRowThreads / 32 * tok;
@@ -252,7 +256,7 @@ dim3 row_grid(int n_rows, int tok, int splits) {
 template <int D, int FMT, bool ROW_F32>
 cudaError_t launch_rot(const RotRowsArgs& z, cudaStream_t s) {
   const int hps = 512 / D, steps = ((z.rows.v ? 2 : 1) * z.rows.Hkv + hps - 1) / hps + (z.Hq + hps - 1) / hps;
-  if (z.rows.n_rows >= kManyRows)
+  if ((long long)z.rows.n_rows * steps >= kManySteps)
     return launch_pdl(kv_write_rot_kernel<D, FMT, ROW_F32, kRowsPerWarp>, row_grid(z.rows.n_rows, kRowsPerWarp, 1),
                       dim3(kRowThreads), 0, s, z);
   return launch_pdl(kv_write_rot_kernel<D, FMT, ROW_F32, 1>, row_grid(z.rows.n_rows, 1, steps < 65535 ? steps : 65535),
@@ -273,7 +277,7 @@ cudaError_t launch_rot_d(const RotRowsArgs& z, int dtype, bool row_f32, cudaStre
 template <int DC, bool CACHE_F32, bool ROW_F32>
 cudaError_t launch_latent(const LatentRowsArgs& z, bool write, cudaStream_t s) {
   const int n = z.rows.n_rows, steps = 1 + (z.Hq + 7) / 8;
-  const bool many = n >= kManyRows;
+  const bool many = (long long)n * (write ? steps : kReadSteps) >= kManySteps;
   auto kern = write ? (many ? latent_write_kernel<DC, CACHE_F32, ROW_F32, kRowsPerWarp> : latent_write_kernel<DC, CACHE_F32, ROW_F32, 1>)
                     : (many ? latent_read_kernel<DC, CACHE_F32, ROW_F32, kRowsPerWarp> : latent_read_kernel<DC, CACHE_F32, ROW_F32, 1>);
   return launch_pdl(kern, row_grid(n, many ? kRowsPerWarp : 1, many || !write ? 1 : steps), dim3(kRowThreads), 0, s, z);
