@@ -565,9 +565,9 @@ def hs2_kv_read(kv: KV, row_start: torch.Tensor, n_rows: int, dtype: torch.dtype
     v_rows) of ``dtype`` [n_rows][Hkv][d] (v_rows None for a key-only cache). Rows outside
     every sequence are left as they are in ``out``."""
     if out is None:
-        c = kv.c()
-        k, v = (_new((n_rows, c.Hkv, c.d), dtype, kv.k.device, stream) if t is not None else None for t in (kv.k, kv.v))
-        out = (k, v)
+        c, device = kv._cached()[0], kv.k.device
+        shape = (n_rows, c.Hkv, c.d)
+        out = (_new(shape, dtype, device, stream), None if kv.v is None else _new(shape, dtype, device, stream))
     elif out[0].shape[0] != n_rows or out[0].dtype != dtype:
         raise HS2Error("out must hold n_rows rows of the dtype")
     _kv_rows(load().hs2_kv_read, kv, out[0], out[1], row_start, dev_err, stream)
