@@ -9,15 +9,20 @@
 // fits tensor memory (4 x 64 columns; with the rows as M it would take all 512) and a tile is read
 // once: the same shared-memory tile is S's K-major A operand and, MN-major, O's. Units of 128 rows
 // (Hq = 128, or chunks) go to a cluster of two CTAs, 64 rows each, that fetch a page of every tile each
-// for both (each for itself, the reads from L2 were what bound it: single tokens of 128 heads, 32
-// sequences of 4K to 16K keys, 148 us).
+// for both, and the pages two tiles ahead into L2 (for itself each, without L2: single tokens of 128 heads 148 us).
+//   64 single tokens of 16 heads over 16K to 32K keys (1.81 GB): 286 to 293 us with plan and merge, 0.91 to 0.93
+//     of the copy bandwidth.
+//   32 single tokens of 128 heads over 4K to 16K keys: 128 us, 0.71 PFLOP/s; 12 sequences of 1 to 200 tokens of
+//     32 heads 231 us, 0.82. A tile takes 5300 cycles there, 3700 of them products (48 cycles an MMA of 64 rows,
+//     whose 6 KB of operands come from shared memory); with 64 rows of 512 channels a tile fills what
+//     Q leaves of it, so that the softmax between them is not hidden.
 //   warp 0   producer: the tile in DC / 128 pieces of 128 channels (32 KB) and one of the 64 rotated ones,
 //            each with a barrier, through rings of pieces: with 64 rows of 512 channels a tile fills the
 //            ring, and a piece of the next one comes as soon as its channels' O is done
 //   warps 1, 3   MMA issuers, of S (piece by piece as they land) and of O (piece by piece, each
 //            committed to the ring)
 //   warp 2   Q of the next unit by TMA
-//   warps 4-7, 8-11 ...  softmax, a key a thread, 8 or 16 rows each: p = 2^(x c + nm) with a reference nm per
+//   warps 4-7, 8-11 (64 rows: to 19)  softmax, a key a thread, 8 or 16 rows each (32 rows each: 4 % slower): p = 2^(x c + nm) with a reference nm per
 //            row that moves only when a weight would exceed 2^14; P rounds to bf16, C's type (a weight is off
 //            by at most 2^-8 of itself), and goes where the tile's rotated channels were, which S
 //            alone needs; the normaliser is summed in fp32 from unrounded p, per thread

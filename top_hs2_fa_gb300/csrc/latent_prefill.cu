@@ -7,6 +7,10 @@
 // 96 KB of shared memory, a tile of K and V 80, and a half is done with one most of a tile's time after
 // the other: K comes in blocks of 64 channels through a ring of five, V 64 keys at a time through a
 // ring of three, so that about 2200 cycles pass from the release of a piece to the next use of its place.
+// A prompt of 16384 tokens of 16 heads: 923 to 937 us, 1.48 PFLOP/s, 0.77 of the burst rate; chunks of 333 to 1200
+// tokens over up to 6100 keys, 32 heads, 404 to 411 us, 1.08. A tile takes 3100 cycles (2560 at the tensor
+// pipe's rate, which the MMAs' operands, 8 KB of shared memory in 64 cycles, allow barely), the end of a unit as
+// much as two or three more.
 //   warps 0, 1, 3   TMA producers of the K blocks, of V, of Q (each half as soon as its last S is done)
 //   warp 2      issues all MMAs, the halves in turn: O_a += P_j V_j with P_j read from tensor memory, then
 //               S_a of tile j + 1 over it, then b's. (A warp for each half let their instructions
