@@ -314,6 +314,77 @@ def test_two_calls_at_once(H, Hq):
             assert torch.equal(x[0], want[0]) and torch.equal(x[1], want[1])
 
 
+def spread(batch, top, low=1):
+    """Lengths from low to top, in no order, the longest somewhere in the middle."""
+    lens = [low + (top - low) * ((i * 7919 + 13) % 101) // 101 for i in range(batch)]
+    lens[batch // 2] = top
+    return lens
+
+
+# What decides who plans: at most 32 sequences, 512 keys (expanded 1024), 16 units a block (of a pair of
+# blocks: 76 pairs; else 152 blocks, with a unit more for each sequence). Batches and lengths on both sides.
+@pytest.mark.parametrize("batch,top,tokens,Hq", [(32, 256, 1, 64), (33, 256, 1, 64), (32, 257, 2, 16), (33, 257, 2, 16),
+                                                 (32, 512, 1, 32), (33, 512, 1, 32), (32, 513, 1, 128), (1, 512, 1, 128),
+                                                 (32, 300, 37, 128), (32, 300, 38, 128), (40, 1300, 25, 16),
+                                                 (150, 2000, 9, 16), (60, 900, 2, 64)])
+def test_who_plans(H, batch, top, tokens, Hq):
+    lens = spread(batch, top)
+    counts = [0 if i % 9 == 4 else min(t, tokens) for i, t in enumerate(lens)]
+    rng, pool, bt, rs, q = latent_case(50, "bf16", lens, counts, Hq, 256, first=1, extra=1)
+    pool = poison(pool, bt, lens)
+    want = L.absorbed(L.values(pool), L.values(q), rs, lens, bt, SCALE)
+    o, lse, err = run(H, pool, bt, lens, rs, q, max_n=tokens)
+    assert err == 0
+    check((o, lse), want, "bf16", 320, rows=slice(rs[0], rs[-1]))
+    for outside in (slice(0, rs[0]), slice(rs[-1], None)):
+        assert (o[outside] == 9).all() and (lse[outside] == 9).all()
+    again = run(H, pool, bt, lens, rs, q, max_n=tokens)
+    assert (o == again[0]).all() and (lse == again[1]).all()
+
+
+@pytest.mark.parametrize("Hq", [16, 128])
+def test_bad_books_of_short_sequences(H, Hq):
+    """As test_bad_lengths and test_bad_pages where a block finds its units itself."""
+    lens, counts = [100, 200, 5, 300, 0, 64], [2, 9, 4, 1, 0, 1]
+    rng, pool, bt, rs, q = latent_case(51, "bf16", lens, counts, Hq, 512)
+    bt[0, 0], bt[5, 0] = len(pool), -1
+    want = L.absorbed(L.values(pool), L.values(q), rs, lens, bt, SCALE)
+    o, lse, err = run(H, pool, bt, [100, 200, 3, 300, 0, 64], rs, q, max_n=8)  # rows 9 > 8, 4 > 3
+    assert err == H.DEV_BAD_LENGTH | H.DEV_BAD_PAGE
+    good = np.r_[rs[0]:rs[1], rs[3]:rs[6]]
+    check((o[good], lse[good]), tuple(x[good] for x in want), "bf16", 576)
+    assert (o[rs[1]:rs[3]] == 9).all() and (lse[rs[1]:rs[3]] == 9).all()
+    assert (o[rs[5]:] == 0).all() and (lse[rs[5]:] == -np.inf).all()
+    falling = rs.copy()
+    falling[2] = 1  # rows of two sequences at once: nobody's are computed
+    o, lse, err = run(H, pool, bt, lens, falling, q, max_n=9)
+    assert err == H.DEV_BAD_LENGTH and (o == 9).all() and (lse == 9).all()
+    beyond = rs.copy()
+    beyond[6] += 5  # rows that do not exist
+    o, lse, err = run(H, pool, bt, lens, beyond, q, max_n=9, max_t=300)
+    assert err & H.DEV_BAD_LENGTH and (o[rs[5]:] == 9).all() and (o[rs[1]:rs[2]] != 9).any()
+
+
+@pytest.mark.parametrize("tiles", [1023, 1024])
+def test_longest_whole_units(H, tiles):
+    """160 single tokens over up to 131072 keys, every page the same one: the softmax of its 64 keys, and
+    lse log(pages) more. The sums are of 128 * tiles terms in fp32, each addition off by at most 2^-24 of
+    the sum so far."""
+    import torch
+
+    pages, Hq, batch = 2 * tiles, 16, 160
+    rng = np.random.default_rng(52)
+    page = T.bf16_round(rng.standard_normal((1, 64, 320)))
+    q = T.bf16_round(rng.standard_normal((batch, Hq, 320)))
+    ro, rlse, mag = L.absorbed(T.widen(page), T.widen(q), T.starts([1] * batch), [64] * batch, np.zeros((batch, 1), int), SCALE)
+    kv = H.KV(k=T.device(page[:, None]), v=None, block_table=torch.zeros((batch, pages), dtype=torch.int32, device="cuda"),
+              seq_len=torch.full((batch,), 64 * pages, dtype=torch.int32, device="cuda"))
+    o, lse = H.hs2_latent_chunk(T.device(q), T.device(T.starts([1] * batch)), kv, SCALE, 1, max_t=64 * pages)
+    slack = 128 * tiles * 2.0 ** -24
+    assert np.abs(lse.cpu().numpy() - rlse - np.log(pages)).max() <= slack + lse_tol(320)
+    assert (np.abs(o.double().cpu().numpy() - ro) <= (2.0 ** -8 + 2 * lse_tol(320) + 2 * slack) * mag + 1e-6).all()
+
+
 # ---------------------------------------------------------------------------- expanded
 def expanded_case(seed, dtype, counts, keys, Hq, first=0, extra=0, key_first=0, key_extra=0):
     rng = np.random.default_rng(seed)
@@ -460,6 +531,24 @@ def test_expanded_graph(H):
     eager = H.hs2_latent_prefill(dq, d[..., :128], dr, d[..., 128:], drs, dks, SCALE, 300, 500)
     for a, b in zip(got, eager):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("batch,top,tokens,Hq", [(32, 1024, 70, 4), (33, 1024, 70, 4), (32, 1025, 70, 4), (31, 512, 300, 3),
+                                                 (33, 512, 300, 3), (32, 200, 48, 64), (32, 200, 56, 64), (36, 1500, 30, 8),
+                                                 (70, 1500, 40, 16), (3, 1024, 1, 1)])
+def test_expanded_who_plans(H, batch, top, tokens, Hq):
+    """As test_who_plans; 64 heads of 32 sequences are 16 units a block up to 1536 rows."""
+    keys = spread(batch, top, low=56 if Hq == 64 else 1)
+    counts = [0 if Hq != 64 and i % 9 == 4 else min(t, tokens) for i, t in enumerate(keys)]
+    rng, rs, ks, q, kv, r = expanded_case(53, "bf16", counts, keys, Hq, first=1, extra=1)
+    want = want_expanded(rs, ks, q, kv, r)
+    o, lse, err = run_expanded(H, rs, ks, q, kv, r, max_n=tokens)
+    assert err == 0
+    check((o, lse), want, "bf16", 192, rows=slice(rs[0], rs[-1]))
+    for outside in (slice(0, rs[0]), slice(rs[-1], None)):
+        assert (o[outside] == 9).all() and (lse[outside] == 9).all()
+    again = run_expanded(H, rs, ks, q, kv, r, max_n=tokens)
+    assert (o == again[0]).all() and (lse == again[1]).all()
 
 
 # ---------------------------------------------------------------------------- together

@@ -88,23 +88,35 @@ int sm_count() {
   return std::min(n, 512);  // the merge's blocks hold the list of cut units, one per CTA at most
 }
 
-// Up to so many keys no unit is cut, and there is nothing to merge: a unit's two tiles (four of the expanded
-// form) take a CTA no longer than the parts take the merge. Cut and whole, us on the device:
-//   absorbed: 4 single tokens of 16 heads over 256 keys 19.2 and 17.0, 64 of them 20.2 and 19.1; over 500
-//     keys 19.6 and 20.9, 23.4 and 22.8, 16 sequences of 3 tokens of 32 heads 24.7 and 27.2.
-//   expanded: 3 prompts of 64 tokens, 16 heads, over 256 keys 15.0 and 12.5, over 500 15.8 and 15.2; 16 of 100
-//     28.0 and 24.4; one of 128 tokens over 700 keys 17.3 and 18.9.
-constexpr int kWholeAbsorbed = 256, kWholeExpanded = 512;
+// Calls with few keys cut no unit, and there is nothing to merge: a unit's few tiles take a CTA no longer than
+// its parts take the merge. With up to `own` keys and no more sequences than a warp has lanes and 16 units a CTA
+// there is no planning kernel either, every CTA finds its units itself; other calls plan, and cut none up to
+// `planned` keys. us on the device:
+//   absorbed, planned, cut and whole: 4 single tokens of 16 heads over 256 keys 19.2 and 17.0, 64 of them 20.2
+//     and 19.1; over 500 keys 19.6 and 20.9, 16 sequences of 3 tokens of 32 heads 24.7 and 27.2.
+//   absorbed, cut and own: 4 single tokens of 16 heads over 500 keys 19.7 and 17.0, of 128 heads 24.7 and 23.0,
+//     8 chunks of 100 of 32 heads 57 and 40; over 700 keys 18.9 and 20.3, 24.1 and 27.1, 61 and 48.
+//   expanded, planned, cut and whole: 3 prompts of 64 tokens, 16 heads, over 256 keys 15.0 and 12.5, over 500 15.8
+//     and 15.2; 16 of 100 28.0 and 24.4; one of 128 tokens over 700 keys 17.3 and 18.9.
+//   expanded, cut and own: one of 128 tokens over 1000 keys 17.6 and 17.2, 3 of 64 18.2 and 17.8, 16 of 400 of
+//     32 heads 119 and 92. With up to 4 units a CTA instead of 16 these over 500 keys 77.9, not 71.4.
+struct Whole {
+  int planned, own;
+};
+constexpr Whole kWholeAbsorbed{256, 512}, kWholeExpanded{512, 1024};
+// What being cut costs a CTA, in tiles (chunk_plan.cu has the figures).
+constexpr int kCutAbsorbed = 4, kCutExpanded = 8;
 
 // Workspace of an attention call: the plan and the parts of cut units.
 struct Layout {
   hs2::ChunkPlan plan;  // pointers after bind()
-  size_t off[7], total;
+  size_t off[8], total;
   long long tiles;  // an upper bound
 };
 
 // `heads` units beside one another per sequence, of G rows a token, parts of dv channels.
-Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t, int whole) {
+Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t, Whole whole,
+              int cut_tiles) {
   Layout L{};
   size_t at = 0;
   auto take = [&](int i, size_t bytes) { L.off[i] = at, at = align256(at + bytes); };
@@ -112,10 +124,14 @@ Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, 
   p.ctas = ctas;
   p.tile_rows = tile_rows;
   p.max_rows = 0x7fffffff;
-  p.snap = max_t <= whole ? 0 : 32;  // ranges differ by a unit at most: with 2 a prompt's by a third (16384 tokens of 16 heads 981 us)
+  p.cut_tiles = cut_tiles;
   const long long units = heads * ((long long)n_rows * G / tile_rows + std::min(batch, n_rows));
   p.max_units = (int)std::min<long long>(units, 1 << 30);
   L.tiles = units * (max_t / 128 + 2);
+  p.own = max_t <= whole.own && batch <= hs2::kOwnPlanSeqs && units <= hs2::kOwnPlanUnits * (long long)ctas;
+  // ranges differ by a unit at most: with 2 a prompt's by a third (16384 tokens of 16 heads 981 us)
+  p.snap = p.own || max_t <= whole.planned ? 0 : 32;
+  if (p.own) p.ctas = std::max(1, (int)std::min<long long>(units, ctas));  // no more CTAs than there can be units
   take(0, 16);
   take(1, 4 * (size_t)ctas);
   take(2, 4 * (size_t)ctas);
@@ -123,6 +139,7 @@ Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, 
   take(3, 48 * (size_t)p.max_units);
   take(4, 2 * (size_t)ctas * tile_rows * 8);
   take(5, 2 * (size_t)ctas * tile_rows * dv * 4);
+  if (!p.own) take(7, 8 * (size_t)std::min<long long>(units, hs2::kOwnPlanUnits * (long long)ctas));
   L.total = std::max<size_t>(at, 256);
   return L;
 }
@@ -133,6 +150,7 @@ void bind(Layout& L, char* ws) {
   p.cuts = (int32_t*)(ws + L.off[2]);
   p.cta_begin = (int32_t*)(ws + L.off[6]);
   p.units = (int32_t*)(ws + L.off[3]);
+  p.order = p.own ? nullptr : (int2*)(ws + L.off[7]);
   p.part_ml = (float*)(ws + L.off[4]);
   p.part_o = (float*)(ws + L.off[5]);
 }
@@ -142,12 +160,12 @@ int chunk_width(long long top) { return top <= 16 ? 16 : top <= 32 ? 32 : top <=
 Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t) {
   const int sms = sm_count();
   return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t,
-                kWholeAbsorbed);
+                kWholeAbsorbed, kCutAbsorbed);
 }
 
 // A unit of the expanded form is 256 tokens of a head.
 Layout prefill_layout(int n_rows, int Hq, int batch, int max_t) {
-  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t, kWholeExpanded);
+  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t, kWholeExpanded, kCutExpanded);
 }
 
 bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
@@ -291,7 +309,7 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
   if (!encode_3d_bf16(&tq, q, kv->d, (uint64_t)Hq, (uint64_t)n_rows, box_heads, width / box_heads) ||
       !encode_2d_bf16(&tk, kv->k, kv->d, (uint64_t)kv->num_pages * 64, 64))
     return HS2_ERR_ARG;
-  cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
+  cudaError_t e = L.plan.own ? cudaSuccess : hs2::launch_chunk_plan(a, &L.plan, 1, s);
   if (e == cudaSuccess) e = hs2::launch_latent_chunk(tq, tk, a, L.plan, dc, s);
   if (e == cudaSuccess && L.plan.snap) e = hs2::launch_chunk_merge(a, &L.plan, 1, dc, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);
@@ -346,7 +364,7 @@ hs2_status hs2_latent_prefill(const void* q, const int32_t* row_start, int n_row
       !encode_3d_bf16(&tr, keys->r, 64, 1, nk, 1, 128, keys->r_token, keys->r_token) ||
       !encode_3d_bf16(&tv, keys->v, 128, (uint64_t)Hq, nk, 1, 64, keys->v_head, keys->v_token))
     return HS2_ERR_ARG;
-  cudaError_t e = hs2::launch_chunk_plan(a, &L.plan, 1, s);
+  cudaError_t e = L.plan.own ? cudaSuccess : hs2::launch_chunk_plan(a, &L.plan, 1, s);
   if (e == cudaSuccess) e = hs2::launch_latent_prefill(tq, tk, tr, tv, a, L.plan, s);
   if (e == cudaSuccess && L.plan.snap) e = hs2::launch_chunk_merge(a, &L.plan, 1, hs2::kLatentValue, s);
   return e == cudaSuccess ? HS2_OK : cuda_fail(e);

@@ -10,6 +10,7 @@ namespace hs2 {
 namespace {
 
 constexpr int kPlanThreads = 1024;
+constexpr int kLengths = kPlanThreads;  // of whole units: tiles below this
 
 // The first key a token at position p sees.
 HS2_DEVI int first_key(int p, int w) { return w > 0 ? max(0, p - w + 1) : 0; }
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) p.cta_begin[c] = 0;
     if (threadIdx.x == 0) {
       flag_error(a.dev_err, HS2_DEV_BAD_LENGTH);
-      p.head[0] = p.head[2] = 0;
+      p.head[0] = p.head[2] = p.head[3] = 0;
       p.head[1] = 1;
       if (p.expand) p.exp_head[0] = 0;
     }
@@ -140,6 +141,51 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   // saves (4 sequences of up to 1500 keys 19.1 us against 16.2, 64 tokens over 2048 keys 25.3, 22.3)
   const int per = max(1, (total_tiles + p.ctas - 1) / p.ctas);
   __syncthreads();  // the records are visible to the block
+  // Whole units by falling length, the CTAs taking them in turn there and back, where the longest of the CTAs'
+  // sums is at most `whole`: cuts cost a CTA two parts, another start and the merge, cut_tiles tiles or more,
+  // and units that share keys run at the same time. Whole and cut, us on the device, with that longest sum and
+  // the range, in tiles: absorbed, 8 sequences of 100 tokens of 32 heads over 2000 keys (26, 25) 89 and 100,
+  // but 60 of 2 tokens of 64 heads (16, 10) 68 and 62, 16 of 3 of 32 heads over 1000 (8, 2) 38 and 30;
+  // expanded, 16 of 400 of 32 heads over 6000 (216, 204) 400 and 454, 6 of 500 of 16 over 2000 (20, 14) 49 and
+  // 58, but one of 1000 over 2000 (16, 6) 38 and 33. The sort takes 1 to 2 us.
+  const int whole = per + per / 8 + p.cut_tiles;
+  if (p.order && units > 0 && units <= kOwnUnits * p.ctas && longest <= whole && longest < kLengths) {
+    __shared__ int place_of[kLengths], span;
+    auto tiles_of = [&](int u) {
+      return a.batch <= kPlanThreads && units <= kPlanThreads ? my_tiles : p.units[12 * (size_t)u + 6];
+    };
+    place_of[threadIdx.x] = 0;
+    if (threadIdx.x == 0) span = 0;
+    __syncthreads();
+    for (int u = threadIdx.x; u < units; u += kPlanThreads) atomicAdd(&place_of[kLengths - 1 - tiles_of(u)], 1);
+    __syncthreads();
+    int all;
+    place_of[threadIdx.x] = block_prefix(place_of[threadIdx.x], sums, all);  // of units longer than this
+    __syncthreads();
+    for (int u = threadIdx.x; u < units; u += kPlanThreads) {
+      const int k = tiles_of(u);
+      p.order[atomicAdd(&place_of[kLengths - 1 - k], 1)] = make_int2(u, k);
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.ctas; c += kPlanThreads) {
+      int sum = 0;
+      for (int i = 0; i < kOwnUnits; ++i) {
+        const int k = ordered_unit(i, c, p.ctas);
+        if (k < units) sum += p.order[k].y;
+      }
+      atomicMax(&span, sum);
+    }
+    __syncthreads();
+    if (span <= whole) {
+      if (threadIdx.x == 0) {
+        p.head[0] = total_tiles;
+        p.head[1] = per;
+        p.head[2] = 0;
+        p.head[3] = units;
+      }
+      return;
+    }
+  }
   const bool snap = (long long)p.snap * longest <= per;
   // each CTA's range start and the unit there, and the list of units that a range border cuts (in
   // any order: the merge treats each by itself)
@@ -166,6 +212,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
     p.head[0] = total_tiles;
     p.head[1] = per;
     p.head[2] = n_cuts;
+    p.head[3] = 0;
     if (p.expand) p.exp_head[0] = n_exp;
   }
 }

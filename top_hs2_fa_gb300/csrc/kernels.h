@@ -180,8 +180,10 @@ struct LatentKeys {
 // The plan of a persistent chunk-attention kernel (device memory, written by the planning
 // kernel of the same call). rows: the packed rows of a unit; sequences with rows in
 // (min_rows, max_rows] are the kernel's.
+// (own: calls of up to so many sequences, and of so many units a CTA)
+constexpr int kOwnPlanSeqs = 32, kOwnPlanUnits = 16;
 struct ChunkPlan {
-  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units
+  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units, [3] whether `order` is what the CTAs follow
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
   int32_t* cta_begin;  // [ctas] the range start
   int32_t* cuts;       // [ctas] units that a range border cuts: one per border at most
@@ -189,6 +191,9 @@ struct ChunkPlan {
   int max_units, ctas;
   int tile_rows;            // rows of a unit: 256 or the narrow kernel's width
   int min_rows, max_rows;   // of a sequence, times G
+  int cut_tiles;            // what being cut costs a CTA, in tiles (see chunk_plan.cu)
+  int2* order;              // null, or room for [kOwnPlanUnits ctas] units by falling length: (unit, tiles)
+  int own;                  // 1: no planning kernel, every CTA finds its units itself (plan_own); none is cut
   int snap;                 // borders move to units' where a range is this many times the longest unit, or more
   float* part_ml;           // [2 ctas][tile_rows][2] m (base 2) and l of the parts
   float* part_o;            // [2 ctas][tile_rows][D] their unnormalised outputs

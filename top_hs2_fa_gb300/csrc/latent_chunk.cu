@@ -22,10 +22,10 @@
 //   warps 1, 3   MMA issuers, of S (piece by piece as they land) and of O (piece by piece, each
 //            committed to the ring)
 //   warp 2   Q of the next unit by TMA
-//   warps 4-7, 8-11 (64 rows: to 19)  softmax, a key a thread, 8 or 16 rows each (32 rows each: 4 % slower): p = 2^(x c + nm) with a reference nm per
-//            row that moves only when a weight would exceed 2^14; P rounds to bf16, C's type (a weight is off
-//            by at most 2^-8 of itself), and goes where the tile's rotated channels were, which S
-//            alone needs; the normaliser is summed in fp32 from unrounded p, per thread
+//   warps 4-7, 8-11 (64 rows: to 19)  softmax, a key a thread, 8 or 16 rows each (32 each: 4 % slower):
+//            p = 2^(x c + nm) with a reference nm per row that moves only when a weight would exceed 2^14; P
+//            rounds to bf16, C's type (a weight is off by at most 2^-8 of itself), and goes where the tile's
+//            rotated channels were, which S alone needs; the normaliser is summed in fp32 from unrounded p
 // Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four warps of a softmax
 // group leave their loop together (they meet at a hardware barrier).
 #include <cuda.h>
@@ -64,6 +64,8 @@ struct LatentSmem {
   alignas(16) float warp_m[GROUPS][4][N / GROUPS], sums[GROUPS][4][N / GROUPS];
   uint64_t full[RING], empty[RING], rot_full[ROT], rot_empty[ROT];
   uint64_t s_full[2], s_empty[2], p_ready[2], pv_done[2], o_empty[O_BUFS], q_full, q_empty;
+  ChunkUnit own[kOwnUnits];
+  int own_end, listed;
   uint32_t tmem_base;
   int abort;
 };
@@ -113,8 +115,8 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
   else __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
-  const ChunkRange rg = chunk_range(p, cta);
-  const int per = p.head[1];
+  const ChunkRange rg = plan_range(a, p, cta, sm.own, &sm.own_end, &sm.listed);
+  const int per = sm.listed ? 1 : p.head[1];
   const uint32_t tS = sm.tmem_base, tO = tS + 128;
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
@@ -131,7 +133,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
       }
     };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, un);
+      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
@@ -196,7 +198,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, un);
+      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
       ok = all(tc::mbar_wait(&sm.q_full, seg & 1));
       for (; ok && at < end; ++at, ++it) {
@@ -242,7 +244,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int it = 0, seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, un);
+      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg % OB], ((seg / OB) & 1) ^ 1));
       const uint32_t o = tO + (seg % OB) * kObuf;
@@ -273,7 +275,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, un);
+      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
       at = min(rg.end, u.prefix + u.ntiles);
       ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty, (seg & 1) ^ 1));
       if (!ok) break;
@@ -297,7 +299,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int it = 0, seg = 0;
     bool run = true;
     for (int at = rg.begin, un = rg.first_unit; run && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, un);
+      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;

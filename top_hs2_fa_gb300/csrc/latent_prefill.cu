@@ -3,12 +3,14 @@
 // x = scale (q_n . k + q_r . r), o = softmax(x) v per head: 192 channels of K (128 of the head's, 64 that
 // the heads share) and 128 of V, causal over packed sequences. Bound by the tensor pipe, 2 (192 + 128)
 // flops per (row, key); a head's keys are read once per 256 rows. The scheme is chunk_wide.cu's: a
-// unit is 256 tokens of a head, two halves of 128 rows that take turns on the tensor pipe, P as bf16 (a weight is off by at most 2^-8 of itself) over its tile's S. Q takes
-// 96 KB of shared memory, a tile of K and V 80, and a half is done with one most of a tile's time after
-// the other: K comes in blocks of 64 channels through a ring of five, V 64 keys at a time through a
-// ring of three, so that about 2200 cycles pass from the release of a piece to the next use of its place.
-// A prompt of 16384 tokens of 16 heads: 923 to 937 us, 1.48 PFLOP/s, 0.77 of the burst rate; chunks of 333 to 1200
-// tokens over up to 6100 keys, 32 heads, 404 to 411 us, 1.08. A tile takes 3100 cycles (2560 at the tensor
+// unit is 256 tokens of a head, two halves of 128 rows that take turns on the tensor pipe, P as bf16 (a
+// weight is off by at most 2^-8 of itself) over its tile's S. Q takes 96 KB of shared memory, a tile of
+// K and V 80, and a half is done with one most of a tile's time after the other: K comes in blocks of 64
+// channels through a ring of five, V 64 keys at a time through a ring of three, so that 1300 to 1500 cycles at
+// least are left from the release of a piece to the next use of its place.
+// A prompt of 16384 tokens of 16 heads: 850 to 856 us, 1.61 PFLOP/s, 0.84 of the burst rate; chunks of 333 to 1200
+// tokens over up to 6100 keys, 32 heads, 349 to 356 us, 1.25 (their units whole by falling length; in equal
+// ranges 923 to 937 and 404 to 411). A tile takes 3100 cycles (2560 at the tensor
 // pipe's rate, which the MMAs' operands, 8 KB of shared memory in 64 cycles, allow barely), the end of a unit as
 // much as two or three more.
 //   warps 0, 1, 3   TMA producers of the K blocks, of V, of Q (each half as soon as its last S is done)
@@ -46,6 +48,8 @@ struct PrefillSmem {
   // by half
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
   float row[2][128];  // by half: what a row's two threads tell one another
+  ChunkUnit own[kOwnUnits];
+  int own_end, listed;
   uint32_t tmem_base;
   int abort;
 };
@@ -91,14 +95,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc::fence_mbar_init();
   }
   griddep_wait();
-  const ChunkRange rg = chunk_range(p, blockIdx.x);
+  const ChunkRange rg = plan_range(a, p, blockIdx.x, sm.own, &sm.own_end, &sm.listed);
   if (rg.begin >= rg.end) return;  // nothing for this CTA (the whole block leaves)
   if (warp == 1) tc::tmem_alloc(&sm.tmem_base, kWTmem);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tS = sm.tmem_base, tO = tS + 256;
-  const int per = p.head[1];
+  const int per = sm.listed ? 1 : p.head[1];
 
   if (warp == 0) {
     // ------------------------------------------------------------------ K
@@ -107,7 +111,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int issued = 0;  // blocks
       bool ok = true;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, un);
+        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
         for (int j = j0; ok && j < j1; ++j)
@@ -130,7 +134,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int issued = 0;
       bool ok = true;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, un);
+        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
         for (int j = 2 * j0; j < 2 * j1; ++j, ++issued) {
@@ -157,11 +161,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr uint32_t kBlk = kPBlock >> 4, kVh = kPVHalf >> 4;
     // the places of the rings, and the phases that they are in
     int ks = 0, kp = 0, vs = 0, vp = 0;
-    int next = fetch_unit(p, rg.first_unit, true);
+    int next = fetch_unit(p, sm.listed, sm.own, rg.first_unit, true);
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = spread_unit(next);
       const int end = min(rg.end, u.prefix + u.ntiles);
-      next = fetch_unit(p, un + 1, end < rg.end);
+      next = fetch_unit(p, sm.listed, sm.own, un + 1, end < rg.end);
       const bool both = u.ntok > kWRows;
       // S of half h of the tile at the K ring's place
       auto scores = [&](int h, bool last) -> bool {
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         return true;
       };
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, un);
+        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
         at = min(rg.end, u.prefix + u.ntiles);
         ok = load(0, na, u);
         na += ok;
@@ -271,12 +275,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tr = h * kWRows + r;  // the row's token of the unit
     const float c = a.scale_log2;
     const bool wide_out = ((uintptr_t)a.o & 31) == 0;
-    int next = fetch_unit(p, rg.first_unit, true);
+    int next = fetch_unit(p, sm.listed, sm.own, rg.first_unit, true);
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = spread_unit(next);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      next = fetch_unit(p, un + 1, at < rg.end);
+      next = fetch_unit(p, sm.listed, sm.own, un + 1, at < rg.end);
       if (h == 1 && u.ntok <= kWRows) {  // no second half
         it += j1 - j0;
         continue;
