@@ -322,11 +322,15 @@ def spread(batch, top, low=1):
 
 
 # What decides who plans: at most 32 sequences, 512 keys (expanded 1024), 16 units a block (of a pair of
-# blocks: 76 pairs; else 152 blocks, with a unit more for each sequence). Batches and lengths on both sides.
+# blocks: 76 pairs; else 152 blocks, with a unit more for each sequence); or at most 128 sequences of up to 64
+# rows (pairs: 32 of up to 128). Batches and lengths on both sides.
 @pytest.mark.parametrize("batch,top,tokens,Hq", [(32, 256, 1, 64), (33, 256, 1, 64), (32, 257, 2, 16), (33, 257, 2, 16),
                                                  (32, 512, 1, 32), (33, 512, 1, 32), (32, 513, 1, 128), (1, 512, 1, 128),
                                                  (32, 300, 37, 128), (32, 300, 38, 128), (40, 1300, 25, 16),
-                                                 (150, 2000, 9, 16), (60, 900, 2, 64)])
+                                                 (150, 2000, 9, 16), (60, 900, 2, 64), (128, 2000, 1, 16),
+                                                 (129, 2000, 1, 16), (64, 5000, 4, 32), (5, 3100, 1, 128), (128, 257, 4, 16),
+                                                 (32, 2000, 1, 128), (33, 2000, 1, 128), (32, 900, 8, 16), (33, 900, 8, 16),
+                                                 (100, 9000, 16, 1), (3, 700, 9, 16)])
 def test_who_plans(H, batch, top, tokens, Hq):
     lens = spread(batch, top)
     counts = [0 if i % 9 == 4 else min(t, tokens) for i, t in enumerate(lens)]
@@ -342,27 +346,49 @@ def test_who_plans(H, batch, top, tokens, Hq):
     assert (o == again[0]).all() and (lse == again[1]).all()
 
 
-@pytest.mark.parametrize("Hq", [16, 128])
-def test_bad_books_of_short_sequences(H, Hq):
-    """As test_bad_lengths and test_bad_pages where a block finds its units itself."""
-    lens, counts = [100, 200, 5, 300, 0, 64], [2, 9, 4, 1, 0, 1]
+@pytest.mark.parametrize("Hq,top,more", [(16, 300, 9), (128, 300, 9), (8, 2900, 9), (128, 2900, 1), (1, 2900, 9)])
+def test_bad_books_where_blocks_plan(H, Hq, top, more):
+    """As test_bad_lengths and test_bad_pages where a block finds its units or its range itself."""
+    lens, counts = [100, 200, 5, top, 0, 64], [min(2, more), more, min(4, more), 1, 0, 1]
     rng, pool, bt, rs, q = latent_case(51, "bf16", lens, counts, Hq, 512)
     bt[0, 0], bt[5, 0] = len(pool), -1
     want = L.absorbed(L.values(pool), L.values(q), rs, lens, bt, SCALE)
-    o, lse, err = run(H, pool, bt, [100, 200, 3, 300, 0, 64], rs, q, max_n=8)  # rows 9 > 8, 4 > 3
+    # rows 9 > 8, 4 > 3; of single tokens: keys beyond max_t, none
+    bad = [100, 200, 3, top, 0, 64] if more > 1 else [100, top + 1, 0, top, 0, 64]
+    o, lse, err = run(H, pool, bt, bad, rs, q, max_n=min(8, more), max_t=top)
     assert err == H.DEV_BAD_LENGTH | H.DEV_BAD_PAGE
     good = np.r_[rs[0]:rs[1], rs[3]:rs[6]]
     check((o[good], lse[good]), tuple(x[good] for x in want), "bf16", 576)
     assert (o[rs[1]:rs[3]] == 9).all() and (lse[rs[1]:rs[3]] == 9).all()
     assert (o[rs[5]:] == 0).all() and (lse[rs[5]:] == -np.inf).all()
     falling = rs.copy()
-    falling[2] = 1  # rows of two sequences at once: nobody's are computed
-    o, lse, err = run(H, pool, bt, lens, falling, q, max_n=9)
+    falling[2] = rs[1] - 1  # rows of two sequences at once: nobody's are computed
+    o, lse, err = run(H, pool, bt, lens, falling, q, max_n=more)
     assert err == H.DEV_BAD_LENGTH and (o == 9).all() and (lse == 9).all()
     beyond = rs.copy()
-    beyond[6] += 5  # rows that do not exist
-    o, lse, err = run(H, pool, bt, lens, beyond, q, max_n=9, max_t=300)
+    beyond[6] += 1  # rows that do not exist
+    o, lse, err = run(H, pool, bt, lens, beyond, q, max_n=max(more, 2), max_t=top)
     assert err & H.DEV_BAD_LENGTH and (o[rs[5]:] == 9).all() and (o[rs[1]:rs[2]] != 9).any()
+
+
+def test_workspace_grows_with_the_call(H):
+    """Whoever plans: more rows, more rows of a sequence or more keys never need less."""
+    import torch
+
+    for batch in (1, 32, 33, 64, 128, 129):
+        kv = H.KV(k=torch.zeros((1, 1, 64, 576), dtype=torch.bfloat16, device="cuda"), v=None,
+                  block_table=torch.zeros((batch, 2000), dtype=torch.int32, device="cuda"),
+                  seq_len=torch.ones(batch, dtype=torch.int32, device="cuda"))
+        for Hq in (1, 16, 64, 128):
+            def size(n, mn, mt):
+                return H.hs2_latent_chunk_workspace(n, Hq, kv, mn, mt)
+            steps = [(16, 64), (64, 256), (256, 512), (512, 513), (513, 100000)]
+            for n in (1, 16, 128, 4000):
+                for mn in (1, 2, 8, 9):
+                    for lo, hi in steps:
+                        assert size(n, mn, lo) <= size(n, mn, hi)
+                    for mt in (64, 256, 512, 100000):
+                        assert size(n, mn, mt) <= size(n + 1, mn, mt) and size(n, mn, mt) <= size(n, mn + 1, mt)
 
 
 @pytest.mark.parametrize("tiles", [1023, 1024])

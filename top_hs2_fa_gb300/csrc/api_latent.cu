@@ -94,12 +94,17 @@ int sm_count() {
 // `planned` keys. us on the device:
 //   absorbed, planned, cut and whole: 4 single tokens of 16 heads over 256 keys 19.2 and 17.0, 64 of them 20.2
 //     and 19.1; over 500 keys 19.6 and 20.9, 16 sequences of 3 tokens of 32 heads 24.7 and 27.2.
-//   absorbed, cut and own: 4 single tokens of 16 heads over 500 keys 19.7 and 17.0, of 128 heads 24.7 and 23.0,
-//     8 chunks of 100 of 32 heads 57 and 40; over 700 keys 18.9 and 20.3, 24.1 and 27.1, 61 and 48.
+//   absorbed, cut and own: 8 chunks of 100 of 32 heads over 500 keys 57 and 40, over 700 61 and 48; but 4 single
+//     tokens of 128 heads over 700 24.1 and 27.1.
 //   expanded, planned, cut and whole: 3 prompts of 64 tokens, 16 heads, over 256 keys 15.0 and 12.5, over 500 15.8
 //     and 15.2; 16 of 100 28.0 and 24.4; one of 128 tokens over 700 keys 17.3 and 18.9.
 //   expanded, cut and own: one of 128 tokens over 1000 keys 17.6 and 17.2, 3 of 64 18.2 and 17.8, 16 of 400 of
 //     32 heads 119 and 92. With up to 4 units a CTA instead of 16 these over 500 keys 77.9, not 71.4.
+// Where a sequence has one unit (absorbed, up to 128 rows) every CTA finds its range of the line itself: planned and
+// not, 16 single tokens of 16 heads over 2000 keys 23.1 and 18.8, 8 of 128 heads over 8000 47.1 and 41.5, 128 of 16
+// over 500 25.3 and 23.7; of pairs with up to 32 sequences (64 single tokens of 128 heads over 300 keys 28.1 and
+// 31.1, and 128 over 4000 156 and 159: whole units fit there). Up to `planned` keys the units stay whole (4
+// single tokens of 16 heads over 256 keys 13.3, as ranges 15.2; over 512 17.0 and 15.4).
 struct Whole {
   int planned, own;
 };
@@ -114,9 +119,10 @@ struct Layout {
   long long tiles;  // an upper bound
 };
 
-// `heads` units beside one another per sequence, of G rows a token, parts of dv channels.
+// `heads` units beside one another per sequence, of G rows a token, parts of dv channels; one: a sequence has one
+// unit at most.
 Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, int dv, int max_t, Whole whole,
-              int cut_tiles) {
+              int cut_tiles, bool one) {
   Layout L{};
   size_t at = 0;
   auto take = [&](int i, size_t bytes) { L.off[i] = at, at = align256(at + bytes); };
@@ -128,10 +134,12 @@ Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, 
   const long long units = heads * ((long long)n_rows * G / tile_rows + std::min(batch, n_rows));
   p.max_units = (int)std::min<long long>(units, 1 << 30);
   L.tiles = units * (max_t / 128 + 2);
-  p.own = max_t <= whole.own && batch <= hs2::kOwnPlanSeqs && units <= hs2::kOwnPlanUnits * (long long)ctas;
+  const bool own = max_t <= (one ? whole.planned : whole.own) && batch <= hs2::kOwnPlanSeqs &&
+                   units <= hs2::kOwnPlanUnits * (long long)ctas;
+  p.own = own ? 1 : one && batch <= hs2::line_seqs(tile_rows == 128) ? 2 : 0;
   // ranges differ by a unit at most: with 2 a prompt's by a third (16384 tokens of 16 heads 981 us)
-  p.snap = p.own || max_t <= whole.planned ? 0 : 32;
-  if (p.own) p.ctas = std::max(1, (int)std::min<long long>(units, ctas));  // no more CTAs than there can be units
+  p.snap = own || (p.own == 0 && max_t <= whole.planned) ? 0 : 32;
+  if (p.own == 1) p.ctas = std::max(1, (int)std::min<long long>(units, ctas));  // no more CTAs than there can be units
   take(0, 16);
   take(1, 4 * (size_t)ctas);
   take(2, 4 * (size_t)ctas);
@@ -139,7 +147,7 @@ Layout layout(int n_rows, int heads, int G, int batch, int tile_rows, int ctas, 
   take(3, 48 * (size_t)p.max_units);
   take(4, 2 * (size_t)ctas * tile_rows * 8);
   take(5, 2 * (size_t)ctas * tile_rows * dv * 4);
-  if (!p.own) take(7, 8 * (size_t)std::min<long long>(units, hs2::kOwnPlanUnits * (long long)ctas));
+  take(7, 8 * (size_t)std::min<long long>(units, hs2::kOwnPlanUnits * (long long)ctas));
   L.total = std::max<size_t>(at, 256);
   return L;
 }
@@ -157,15 +165,15 @@ void bind(Layout& L, char* ws) {
 
 // Rows of a unit of the absorbed form: the least width that holds a sequence's; 128 by pairs of CTAs.
 int chunk_width(long long top) { return top <= 16 ? 16 : top <= 32 ? 32 : top <= 64 ? 64 : 128; }
-Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t) {
+Layout chunk_layout(int n_rows, int Hq, const hs2_kv* kv, int width, int max_t, long long top) {
   const int sms = sm_count();
   return layout(n_rows, 1, Hq, kv->batch, width, width == 128 ? std::max(1, sms / 2) : sms, kv->d - hs2::kLatentRot, max_t,
-                kWholeAbsorbed, kCutAbsorbed);
+                kWholeAbsorbed, kCutAbsorbed, top <= width);
 }
 
 // A unit of the expanded form is 256 tokens of a head.
 Layout prefill_layout(int n_rows, int Hq, int batch, int max_t) {
-  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t, kWholeExpanded, kCutExpanded);
+  return layout(n_rows, Hq, 1, batch, 256, sm_count(), hs2::kLatentValue, max_t, kWholeExpanded, kCutExpanded, false);
 }
 
 bool heads_supported(int Hq) { return Hq <= 128 && (Hq & (Hq - 1)) == 0; }
@@ -268,9 +276,10 @@ size_t hs2_latent_chunk_workspace(int n_rows, int Hq, const hs2_kv* kv, int max_
   if (!valid_latent(kv) || n_rows < 0 || max_n < 0 || max_t < 0 || Hq < 1 || !heads_supported(Hq)) return 0;
   size_t need = 256;
   // narrower units are more: what a call with fewer tokens a sequence would take, too
-  const int widest = chunk_width((long long)std::min(max_n, n_rows) * Hq);
+  const long long top = (long long)std::min(max_n, n_rows) * Hq;
+  const int widest = chunk_width(top);
   for (int w = 16; kv->dtype != HS2_F32 && w <= widest; w *= 2)
-    if (Hq <= w) need = std::max(need, chunk_layout(n_rows, Hq, kv, w, max_t).total);
+    if (Hq <= w) need = std::max(need, chunk_layout(n_rows, Hq, kv, w, max_t, top).total);
   return need;
 }
 
@@ -284,7 +293,8 @@ hs2_status hs2_latent_chunk(const void* q, const int32_t* row_start, int n_rows,
   if (n_rows == 0 || max_n == 0) return HS2_OK;
   if (!q || !aligned16(q) || !o || !aligned16(o)) return HS2_ERR_ARG;
   const int dc = kv->d - hs2::kLatentRot;
-  Layout L = chunk_layout(n_rows, Hq, kv, chunk_width((long long)std::min(max_n, n_rows) * Hq), max_t);
+  const long long top = (long long)std::min(max_n, n_rows) * Hq;  // rows of a sequence
+  Layout L = chunk_layout(n_rows, Hq, kv, chunk_width(top), max_t, top);
   // 32-bit tile counts and pool rows
   if (kv->dtype != HS2_F32 && (L.tiles > 1LL << 30 || (long long)kv->num_pages * 64 > 0x7fffffff - 64 || kv->max_pages > (1 << 24)))
     return HS2_ERR_UNSUPPORTED;

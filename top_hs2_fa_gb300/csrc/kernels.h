@@ -180,8 +180,10 @@ struct LatentKeys {
 // The plan of a persistent chunk-attention kernel (device memory, written by the planning
 // kernel of the same call). rows: the packed rows of a unit; sequences with rows in
 // (min_rows, max_rows] are the kernel's.
-// (own: calls of up to so many sequences, and of so many units a CTA)
+// (own: 1 in calls of up to so many sequences, and of so many units a CTA; 2: of up to line_seqs(a range is a
+// pair's) sequences)
 constexpr int kOwnPlanSeqs = 32, kOwnPlanUnits = 16;
+constexpr int line_seqs(bool pair) { return pair ? 32 : 128; }
 struct ChunkPlan {
   int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units, [3] whether `order` is what the CTAs follow
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
@@ -193,7 +195,7 @@ struct ChunkPlan {
   int min_rows, max_rows;   // of a sequence, times G
   int cut_tiles;            // what being cut costs a CTA, in tiles (see chunk_plan.cu)
   int2* order;              // null, or room for [kOwnPlanUnits ctas] units by falling length: (unit, tiles)
-  int own;                  // 1: no planning kernel, every CTA finds its units itself (plan_own); none is cut
+  int own;                  // no planning kernel, every CTA finds its units itself: 1 whole ones (plan_own), 2 a range (plan_line)
   int snap;                 // borders move to units' where a range is this many times the longest unit, or more
   float* part_ml;           // [2 ctas][tile_rows][2] m (base 2) and l of the parts
   float* part_o;            // [2 ctas][tile_rows][D] their unnormalised outputs

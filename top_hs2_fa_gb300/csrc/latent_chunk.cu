@@ -64,8 +64,8 @@ struct LatentSmem {
   alignas(16) float warp_m[GROUPS][4][N / GROUPS], sums[GROUPS][4][N / GROUPS];
   uint64_t full[RING], empty[RING], rot_full[ROT], rot_empty[ROT];
   uint64_t s_full[2], s_empty[2], p_ready[2], pv_done[2], o_empty[O_BUFS], q_full, q_empty;
-  ChunkUnit own[kOwnUnits];
-  int own_end, listed;
+  ChunkUnit own[line_seqs(false)];
+  ChunkRange own_range;
   uint32_t tmem_base;
   int abort;
 };
@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
   else __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
-  const ChunkRange rg = plan_range(a, p, cta, sm.own, &sm.own_end, &sm.listed);
-  const int per = sm.listed ? 1 : p.head[1];
+  bool listed;
+  const ChunkRange rg = plan_range<line_seqs(PAIR)>(a, p, cta, sm.own, &sm.own_range, listed);
   const uint32_t tS = sm.tmem_base, tO = tS + 128;
   if (warp == 0) {
     // ------------------------------------------------------------------ producer
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
       }
     };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+      const ChunkUnit u = load_unit(p, listed, sm.own, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v); };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+      const ChunkUnit u = load_unit(p, listed, sm.own, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
       ok = all(tc::mbar_wait(&sm.q_full, seg & 1));
       for (; ok && at < end; ++at, ++it) {
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int it = 0, seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+      const ChunkUnit u = load_unit(p, listed, sm.own, un);
       const int end = min(rg.end, u.prefix + u.ntiles);
       ok = __all_sync(0xffffffffu, tc::mbar_wait(&sm.o_empty[seg % OB], ((seg / OB) & 1) ^ 1));
       const uint32_t o = tO + (seg % OB) * kObuf;
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+      const ChunkUnit u = load_unit(p, listed, sm.own, un);
       at = min(rg.end, u.prefix + u.ntiles);
       ok = __all_sync(0xffffffffu, !halted(sm) && tc::mbar_wait(&sm.q_empty, (seg & 1) ^ 1));
       if (!ok) break;
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int it = 0, seg = 0;
     bool run = true;
     for (int at = rg.begin, un = rg.first_unit; run && at < rg.end; ++un) {
-      const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+      const ChunkUnit u = load_unit(p, listed, sm.own, un);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
       const int32_t* bt = a.bt + (size_t)u.b * a.max_pages;
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
       auto out_row = [&](int n) -> size_t {
         return (size_t)(u.row + ((row0 + n) >> a.log2G)) * a.Hq + ((row0 + n) & (a.G - 1));
       };
-      const size_t slot = whole ? 0 : (size_t)part_slot(u, per, cta) * p.tile_rows + row0 + n0;
+      const size_t slot = whole ? 0 : (size_t)part_slot(u, rg.per, cta) * p.tile_rows + row0 + n0;
       if (tid < C) {
         const float M = nm[tid] == kUnset ? -INFINITY : -nm[tid];
         const float L = sm.sums[grp][0][tid] + sm.sums[grp][1][tid] + sm.sums[grp][2][tid] + sm.sums[grp][3][tid];

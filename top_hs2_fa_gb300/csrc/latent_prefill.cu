@@ -49,7 +49,7 @@ struct PrefillSmem {
   uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], pv_done[2];
   float row[2][128];  // by half: what a row's two threads tell one another
   ChunkUnit own[kOwnUnits];
-  int own_end, listed;
+  ChunkRange own_range;
   uint32_t tmem_base;
   int abort;
 };
@@ -95,14 +95,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     tc::fence_mbar_init();
   }
   griddep_wait();
-  const ChunkRange rg = plan_range(a, p, blockIdx.x, sm.own, &sm.own_end, &sm.listed);
+  bool listed;
+  const ChunkRange rg = plan_range<0>(a, p, blockIdx.x, sm.own, &sm.own_range, listed);
   if (rg.begin >= rg.end) return;  // nothing for this CTA (the whole block leaves)
   if (warp == 1) tc::tmem_alloc(&sm.tmem_base, kWTmem);
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tS = sm.tmem_base, tO = tS + 256;
-  const int per = sm.listed ? 1 : p.head[1];
 
   if (warp == 0) {
     // ------------------------------------------------------------------ K
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int issued = 0;  // blocks
       bool ok = true;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+        const ChunkUnit u = load_unit(p, listed, sm.own, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
         for (int j = j0; ok && j < j1; ++j)
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
       int issued = 0;
       bool ok = true;
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+        const ChunkUnit u = load_unit(p, listed, sm.own, un);
         const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
         at = u.prefix + j1;
         for (int j = 2 * j0; j < 2 * j1; ++j, ++issued) {
@@ -161,11 +161,11 @@ __global__ void __launch_bounds__(kPThreads, 1)
     constexpr uint32_t kBlk = kPBlock >> 4, kVh = kPVHalf >> 4;
     // the places of the rings, and the phases that they are in
     int ks = 0, kp = 0, vs = 0, vp = 0;
-    int next = fetch_unit(p, sm.listed, sm.own, rg.first_unit, true);
+    int next = fetch_unit(p, listed, sm.own, rg.first_unit, true);
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = spread_unit(next);
       const int end = min(rg.end, u.prefix + u.ntiles);
-      next = fetch_unit(p, sm.listed, sm.own, un + 1, end < rg.end);
+      next = fetch_unit(p, listed, sm.own, un + 1, end < rg.end);
       const bool both = u.ntok > kWRows;
       // S of half h of the tile at the K ring's place
       auto scores = [&](int h, bool last) -> bool {
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
         return true;
       };
       for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
-        const ChunkUnit u = load_unit(p, sm.listed, sm.own, un);
+        const ChunkUnit u = load_unit(p, listed, sm.own, un);
         at = min(rg.end, u.prefix + u.ntiles);
         ok = load(0, na, u);
         na += ok;
@@ -275,12 +275,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
     const int tr = h * kWRows + r;  // the row's token of the unit
     const float c = a.scale_log2;
     const bool wide_out = ((uintptr_t)a.o & 31) == 0;
-    int next = fetch_unit(p, sm.listed, sm.own, rg.first_unit, true);
+    int next = fetch_unit(p, listed, sm.own, rg.first_unit, true);
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = spread_unit(next);
       const int j0 = at - u.prefix, j1 = min(u.ntiles, rg.end - u.prefix);
       at = u.prefix + j1;
-      next = fetch_unit(p, sm.listed, sm.own, un + 1, at < rg.end);
+      next = fetch_unit(p, listed, sm.own, un + 1, at < rg.end);
       if (h == 1 && u.ntok <= kWRows) {  // no second half
         it += j1 - j0;
         continue;
@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
           }
         }
       } else {
-        const size_t at_p = (size_t)part_slot(u, per, blockIdx.x) * 2 * kWRows + tr;
+        const size_t at_p = (size_t)part_slot(u, rg.per, blockIdx.x) * 2 * kWRows + tr;
         if (cg == 0) reinterpret_cast<float2*>(p.part_ml)[at_p] = make_float2(m_used, l);
         float* po = p.part_o + at_p * D + cg * 64;
 #pragma unroll 1
