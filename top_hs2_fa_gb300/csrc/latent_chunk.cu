@@ -10,10 +10,10 @@
 // once: the same shared-memory tile is S's K-major A operand and, MN-major, O's. Units of 128 rows
 // (Hq = 128, or chunks) go to a cluster of two CTAs, 64 rows each, that fetch a page of every tile each
 // for both, and the pages two tiles ahead into L2 (for itself each, without L2: single tokens of 128 heads 148 us).
-//   64 single tokens of 16 heads over 16K to 32K keys (1.81 GB): 286 to 293 us with plan and merge, 0.91 to 0.93
+//   64 single tokens of 16 heads over 16K to 32K keys (1.81 GB): 286 to 290 us with the merge, 0.92 to 0.93
 //     of the copy bandwidth.
-//   32 single tokens of 128 heads over 4K to 16K keys: 128 us, 0.71 PFLOP/s; 12 sequences of 1 to 200 tokens of
-//     32 heads 231 us, 0.82. A tile takes 5300 cycles there, 3700 of them products (48 cycles an MMA of 64 rows,
+//   32 single tokens of 128 heads over 4K to 16K keys: 123 us, 0.74 PFLOP/s; 12 sequences of 1 to 200 tokens of
+//     32 heads 231 to 235 us, 0.82. A tile takes 5300 cycles there, 3700 of them products (48 cycles an MMA of 64 rows,
 //     whose 6 KB of operands come from shared memory); with 64 rows of 512 channels a tile fills what
 //     Q leaves of it, so that the softmax between them is not hidden.
 //   warp 0   producer: the tile in DC / 128 pieces of 128 channels (32 KB) and one of the 64 rotated ones,
@@ -26,8 +26,8 @@
 //            p = 2^(x c + nm) with a reference nm per row that moves only when a weight would exceed 2^14; P
 //            rounds to bf16, C's type (a weight is off by at most 2^-8 of itself), and goes where the tile's
 //            rotated channels were, which S alone needs; the normaliser is summed in fp32 from unrounded p
-// Units, ranges and merging as in chunk_plan.cuh. Every wait is bounded; the four warps of a softmax
-// group leave their loop together (they meet at a hardware barrier).
+// Units, ranges and merging as in chunk_plan.cuh, the plan found here where a call has few keys or few rows. Every
+// wait is bounded; the four warps of a softmax group leave their loop together (they meet at a hardware barrier).
 #include <cuda.h>
 
 #include "chunk_plan.cuh"
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
       auto out_row = [&](int n) -> size_t {
         return (size_t)(u.row + ((row0 + n) >> a.log2G)) * a.Hq + ((row0 + n) & (a.G - 1));
       };
-      const size_t slot = whole ? 0 : (size_t)part_slot(u, rg.per, cta) * p.tile_rows + row0 + n0;
+      const size_t slot = whole ? 0 : (size_t)part_slot(u, listed ? sm.own_range.per : p.head[1], cta) * p.tile_rows + row0 + n0;
       if (tid < C) {
         const float M = nm[tid] == kUnset ? -INFINITY : -nm[tid];
         const float L = sm.sums[grp][0][tid] + sm.sums[grp][1][tid] + sm.sums[grp][2][tid] + sm.sums[grp][3][tid];
