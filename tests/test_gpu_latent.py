@@ -270,6 +270,45 @@ def test_graph_and_streams(H):
         assert torch.equal(a, b) and torch.equal(b, c)
 
 
+@pytest.mark.parametrize("Hq,top", [(16, 200), (128, 200), (16, 3000), (128, 3000)])
+def test_graphs_of_few_rows(H, Hq, top):
+    """Two graphs of calls that plan in their blocks, in one workspace and replayed in turn while the lengths
+    move, so that other units are cut each time."""
+    import torch
+
+    lens, counts = [top, 64, 1, top // 2 + 3], [1, 1, 0, 1]
+    rng, pool, bt, rs, q = latent_case(54, "bf16", lens, counts, Hq, 256)
+    n = q.shape[0]
+    size = 0
+    calls = []
+    for seqs in (4, 2):  # all, and the first two with one row
+        kv = latent_kv(H, pool, bt[:seqs], lens[:seqs])
+        rows = T.device(q[:int(rs[seqs])].copy())
+        calls.append((kv, rows, T.device(rs[:seqs + 1].copy())))
+        size = max(size, H.hs2_latent_chunk_workspace(n, Hq, kv, 1, top))
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for kv, rows, drs in calls:
+        out = torch.zeros((rows.shape[0], Hq, 256), device="cuda"), torch.zeros((rows.shape[0], Hq), device="cuda")
+        run_it = lambda: H.hs2_latent_chunk(rows, drs, kv, SCALE, 1, max_t=top, out=out, workspace=ws)  # noqa: B023, E731
+        run_it()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            run_it()
+        graphs.append((g, out))
+    for now in ([top, 64, 1, top // 2 + 3], [1, 1, 1, 130], [top - 129, 20, 1, 64], [top, 63, 0, 2]):
+        for kv, _, _ in calls:
+            kv.seq_len.copy_(torch.tensor(now[:kv.seq_len.numel()], dtype=torch.int32))
+        for g, _ in graphs * 2:
+            g.replay()
+        torch.cuda.synchronize()
+        for (kv, rows, drs), (_, out) in zip(calls, graphs):
+            seqs = kv.seq_len.numel()
+            want = L.absorbed(L.values(pool), L.values(q[:rows.shape[0]]), rs[:seqs + 1], now[:seqs], bt[:seqs], SCALE)
+            check((out[0].double().cpu().numpy(), out[1].cpu().numpy()), want, "bf16", 320)
+
+
 def test_more_sequences_than_threads(H):
     """1100 sequences: the plan takes them 1024 at a time, and as many units."""
     lens = [1 + (i * 37) % 150 for i in range(1100)]
