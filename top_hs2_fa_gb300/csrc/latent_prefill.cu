@@ -8,7 +8,7 @@
 // K and V 80, and a half is done with one most of a tile's time after the other: K comes in blocks of 64
 // channels through a ring of five, V 64 keys at a time through a ring of three, so that 1300 to 1500 cycles at
 // least are left from the release of a piece to the next use of its place.
-// A prompt of 16384 tokens of 16 heads: 850 to 862 us, 1.60 PFLOP/s, 0.84 of the burst rate; chunks of 333 to 1200
+// A prompt of 16384 tokens of 16 heads: 843 to 867 us, 1.61 PFLOP/s, 0.84 of the burst rate; chunks of 333 to 1200
 // tokens over up to 6100 keys, 32 heads, 349 to 357 us, 1.25 (their units whole by falling length; in equal
 // ranges 923 to 937 and 404 to 411). A tile takes 3100 cycles (2560 at the tensor
 // pipe's rate, which the MMAs' operands, 8 KB of shared memory in 64 cycles, allow barely), the end of a unit as
