@@ -10,29 +10,20 @@ namespace hs2 {
 // launch on the stream finishes, so it must call griddep_wait before reading anything that
 // launch may write (and griddep_launch_dependents to let the next one begin early).
 template <typename... Params, typename... Args>
-inline cudaError_t launch_pdl_cluster(void (*kern)(Params...), int cluster, dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                      Args&&... args) {
+inline cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args&&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[2];
+  cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  cfg.numAttrs = 1;
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
   return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-template <typename... Params, typename... Args>
-inline cudaError_t launch_pdl(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                              Args&&... args) {
-  return launch_pdl_cluster(kern, 1, grid, block, smem, s, static_cast<Args&&>(args)...);
 }
 
 constexpr int kCombineThreads = 512;

@@ -8,12 +8,14 @@
 // O^T[DC][N] += C^T P^T, N = 16, 32 or 64 rows (tokens times heads), so that O of 512 channels
 // fits tensor memory (4 x 64 columns; with the rows as M it would take all 512) and a tile is read
 // once: the same shared-memory tile is S's K-major A operand and, MN-major, O's. Units of 128 rows
-// (Hq = 128, or chunks) go to a cluster of two CTAs, 64 rows each, that fetch a page of every tile each
-// for both, and the pages two tiles ahead into L2 (for itself each, without L2: single tokens of 128 heads 148 us).
+// (Hq = 128, or chunks) go to a pair of CTAs, 64 rows each, that walk the same tiles side by side: either loads them
+// whole, by plain copies, and fetches one of the two pages two tiles ahead into L2, so that HBM is read once
+// (without: single tokens of 128 heads 142 us; both pages by either CTA 128, the mixed batch 243). Nothing passes
+// from one CTA to the other.
 //   64 single tokens of 16 heads over 16K to 32K keys (1.81 GB): 286 to 290 us with the merge, 0.92 to 0.93
 //     of the copy bandwidth.
-//   32 single tokens of 128 heads over 4K to 16K keys: 123 us, 0.74 PFLOP/s; 12 sequences of 1 to 200 tokens of
-//     32 heads 231 to 235 us, 0.82. A tile takes 5300 cycles there, 3700 of them products (48 cycles an MMA of 64 rows,
+//   32 single tokens of 128 heads over 4K to 16K keys: 128 us, 0.71 PFLOP/s; 12 sequences of 1 to 200 tokens of
+//     32 heads 239 us, 0.79. A tile takes some 5500 cycles there, 3700 of them products (48 cycles an MMA of 64 rows,
 //     whose 6 KB of operands come from shared memory); with 64 rows of 512 channels a tile fills what
 //     Q leaves of it, so that the softmax between them is not hidden.
 //   warp 0   producer: the tile in DC / 128 pieces of 128 channels (32 KB) and one of the 64 rotated ones,
@@ -72,8 +74,9 @@ struct LatentSmem {
 
 }  // namespace
 
-// PAIR: a cluster's CTAs take rows [0, 64) and [64, 128) of the units of its range (the second also where
-// a unit has no such rows: the tiles come from both).
+// PAIR: CTAs 2i and 2i + 1 take rows [0, 64) and [64, 128) of the units of range i. The second walks a unit's tiles
+// also where it has no such rows: where it went ahead to its next unit the two no longer met in L2 (mixed batch
+// 248 us against 239).
 template <int DC, int N, bool PAIR>
 __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     latent_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const ChunkArgs a,
@@ -91,11 +94,11 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < RING; ++s) {
       tc::mbar_init(&sm.full[s], 1);
-      tc::mbar_init(&sm.empty[s], PAIR ? 2 : 1);  // of a pair: both are done with the piece
+      tc::mbar_init(&sm.empty[s], 1);
     }
     for (int s = 0; s < ROT; ++s) {
       tc::mbar_init(&sm.rot_full[s], 1);
-      tc::mbar_init(&sm.rot_empty[s], PAIR ? 2 : 1);
+      tc::mbar_init(&sm.rot_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&sm.s_full[s], 1);
@@ -111,8 +114,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
   }
   if (warp == 1) tc::tmem_alloc(&sm.tmem_base, 512);
   tc::tc_fence_before();
-  if (PAIR) tc::cluster_sync();  // (the peer's barriers are set up)
-  else __syncthreads();
+  __syncthreads();
   tc::tc_fence_after();
   griddep_wait();
   bool listed;
@@ -123,14 +125,10 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     int it = 0;
     bool ok = true;
     const int oob = a.num_pages * kPage;  // the row past the pool: zeros
-    // 64 channels of the tile's two pages: a pair's CTAs fetch one each for both
+    // 64 channels of the tile's two pages
     auto load = [&](uint8_t* to, int x, int ra, int rb, uint64_t* bar) {
-      if constexpr (PAIR) {
-        tc::tma_load_2d_multicast(to + (row0 ? 8192 : 0), &tm_k, x, row0 ? rb : ra, bar, 3);
-      } else {
-        tc::tma_load_2d(to, &tm_k, x, ra, bar);
-        tc::tma_load_2d(to + 8192, &tm_k, x, rb, bar);
-      }
+      tc::tma_load_2d(to, &tm_k, x, ra, bar);
+      tc::tma_load_2d(to + 8192, &tm_k, x, rb, bar);
     };
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
       const ChunkUnit u = load_unit(p, listed, sm.own, un);
@@ -237,10 +235,6 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     // ------------------------------------------------------------------ O^T += C^T P^T
     constexpr uint32_t idO = narrow_idesc(true, N, true, true);
     const uint32_t el = tc::elect_one();
-    auto release = [&](uint64_t* bar) {
-      if constexpr (PAIR) tc::mma_commit_multicast_warp(bar, 3, el);
-      else tc::mma_commit_warp(bar, el);
-    };
     int it = 0, seg = 0;
     bool ok = true;
     for (int at = rg.begin, un = rg.first_unit; ok && at < rg.end; ++un) {
@@ -261,9 +255,9 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)  // 16 keys each
             tc::mma_f16_warp(o + c * N, vd + ks * 128, pd + ks * 128, idO, (j > 0 || ks > 0) ? 1u : 0u, el);
-          release(&sm.empty[st]);
+          tc::mma_commit_warp(&sm.empty[st], el);
         }
-        release(&sm.rot_empty[it % ROT]);
+        tc::mma_commit_warp(&sm.rot_empty[it % ROT], el);
         tc::mma_commit_warp(&sm.pv_done[b], el);
       }
       ++seg;
@@ -502,8 +496,7 @@ __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     if (!run && lane == 0) halt(sm, a.dev_err);
   }
   tc::tc_fence_before();
-  if (PAIR) tc::cluster_sync();  // neither leaves while the other may write to it
-  else __syncthreads();
+  __syncthreads();
   if (warp == 1) tc::tmem_dealloc(sm.tmem_base, 512);
 }
 
@@ -514,7 +507,7 @@ static cudaError_t launch_n(const CUtensorMap& tq, const CUtensorMap& tk, const 
   auto kern = latent_chunk_kernel<DC, N, PAIR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, PAIR ? 2 : 1, dim3(PAIR ? 2 * p.ctas : p.ctas), dim3(LatentSmem<DC, N>::THREADS), sm, s, tq, tk, a, p);
+  return launch_pdl(kern, dim3(PAIR ? 2 * p.ctas : p.ctas), dim3(LatentSmem<DC, N>::THREADS), sm, s, tq, tk, a, p);
 }
 
 template <int DC>

@@ -170,26 +170,6 @@ HS2_DEVI void mma_commit_warp(uint64_t* bar, uint32_t elected) {
       : "memory");
 }
 
-// Clusters: the copy, or the arrival, goes to the same shared-memory offset in every CTA of `mask`.
-HS2_DEVI void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-HS2_DEVI void tma_load_2d_multicast(void* smem, const CUtensorMap* map, int x, int y, uint64_t* bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, {%2, "
-      "%3}], [%4], %5;" ::"r"(smem_u32(smem)),
-      "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-HS2_DEVI void mma_commit_multicast_warp(uint64_t* bar, uint16_t mask, uint32_t elected) {
-  asm volatile(
-      "{.reg .pred q; setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;}" ::"r"(
-          smem_u32(bar)),
-      "r"(elected), "h"(mask)
-      : "memory");
-}
-
 // Instruction descriptor, kind::f16: bf16 A and B, fp32 D, both K-major, shape M x N.
 HS2_DEVI constexpr uint32_t idesc_bf16_f32(int M, int N) {
   return (1u << 4)                      // D format: f32
