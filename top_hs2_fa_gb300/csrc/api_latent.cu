@@ -205,8 +205,9 @@ hs2_status hs2_kv_write_rot(const hs2_kv* kv, const void* k_rows, int64_t k_stri
                             int64_t q_stride, int Hq, void* q_out, int64_t q_out_stride, int32_t* dev_err, void* stream) {
   if (!valid_kv(kv, false) || (kv->v && !valid_kv(kv, true))) return HS2_ERR_ARG;
   if (!row_start || n_rows < 0 || !row_type(row_dtype) || !valid_rot(rot, kv->d)) return HS2_ERR_ARG;
-  if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
+  if (Hq < 0) return HS2_ERR_ARG;
   if (n_rows == 0) return HS2_OK;
+  if ((Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
   const int64_t row = (int64_t)kv->Hkv * kv->d, q_row = (int64_t)Hq * kv->d;
   if (!rows16(k_rows, k_stride, row_dtype) || k_stride < row || k_stride > kMaxStride) return HS2_ERR_ARG;
   if (kv->v && (!rows16(v_rows, v_stride, row_dtype) || v_stride < row || v_stride > kMaxStride)) return HS2_ERR_ARG;
@@ -237,10 +238,11 @@ hs2_status hs2_latent_write(const hs2_kv* kv, const void* c_rows, int64_t c_stri
                             int64_t q_stride, int64_t q_head, int Hq, void* q_out, int64_t q_out_stride,
                             int64_t q_out_head, int32_t* dev_err, void* stream) {
   if (!valid_rot(rot, hs2::kLatentRot) || rot->dim != hs2::kLatentRot) return HS2_ERR_ARG;
-  if (Hq < 0 || (Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
+  if (Hq < 0) return HS2_ERR_ARG;
   bool go;
   const hs2_status st = check_latent_rows(kv, c_rows, c_stride, r_rows, r_stride, row_dtype, row_start, n_rows, &go);
   if (!go) return st;
+  if ((Hq > 0) != (q != nullptr) || (q != nullptr) != (q_out != nullptr)) return HS2_ERR_ARG;
   if (q) {
     // heads apart from one another, rows apart from one another
     auto apart = [&](const void* p, int64_t stride, int64_t head, hs2_dtype t) {
