@@ -367,8 +367,9 @@ typedef struct {
  * at r * q_stride elements, or NULL with Hq = 0; q_out: the rotated queries as hs2_fa_chunk takes
  * them, float32 for an F32 cache, else bfloat16, [n_rows][Hq][d] at q_out_stride; it may be q itself
  * (same type and stride) and overlaps nothing else. Rows that are flagged or outside every sequence have
- * neither their cache rows nor their q_out written. A position of n_pos or more sets
- * HS2_DEV_BAD_INDEX. n_rows = 0: nothing to do, q and q_out may be NULL. All cache types. */
+ * neither their cache rows nor their q_out written; but under a slab scale out of range only the part
+ * that hs2_kv_write leaves out is, not the row's other heads, its other side or its q_out. A position
+ * of n_pos or more sets HS2_DEV_BAD_INDEX. n_rows = 0: nothing to do, q and q_out may be NULL. All cache types. */
 hs2_status hs2_kv_write_rot(const hs2_kv* kv, const void* k_rows, int64_t k_stride, const void* v_rows, int64_t v_stride,
                             hs2_dtype row_dtype, const int32_t* row_start, int n_rows, const hs2_rot* rot, const void* q,
                             int64_t q_stride, int Hq, void* q_out, int64_t q_out_stride, int32_t* dev_err, void* stream);
