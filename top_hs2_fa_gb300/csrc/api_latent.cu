@@ -94,17 +94,17 @@ int sm_count() {
 // `planned` keys. us on the device:
 //   absorbed, planned, cut and whole: 4 single tokens of 16 heads over 256 keys 19.2 and 17.0, 64 of them 20.2
 //     and 19.1; over 500 keys 19.6 and 20.9, 16 sequences of 3 tokens of 32 heads 24.7 and 27.2.
-//   absorbed, cut and own: 8 chunks of 100 of 32 heads over 500 keys 57 and 40, over 700 61 and 48; but 4 single
-//     tokens of 128 heads over 700 24.1 and 27.1.
+//   absorbed, planned (whole by length) and own: 8 chunks of 100 of 32 heads over 500 keys 43.4 and 39.4, over 700
+//     48.7 and 47.9.
 //   expanded, planned, cut and whole: 3 prompts of 64 tokens, 16 heads, over 256 keys 15.0 and 12.5, over 500 15.8
 //     and 15.2; 16 of 100 28.0 and 24.4; one of 128 tokens over 700 keys 17.3 and 18.9.
 //   expanded, cut and own: one of 128 tokens over 1000 keys 17.6 and 17.2, 3 of 64 18.2 and 17.8, 16 of 400 of
 //     32 heads 119 and 92. With up to 4 units a CTA instead of 16 these over 500 keys 77.9, not 71.4.
 // Where a sequence has one unit (absorbed, up to 128 rows) every CTA finds its range of the line itself: planned and
-// not, 16 single tokens of 16 heads over 2000 keys 23.1 and 18.8, 8 of 128 heads over 8000 47.1 and 41.5, 128 of 16
-// over 500 25.3 and 23.7; of pairs with up to 32 sequences (64 single tokens of 128 heads over 300 keys 28.1 and
-// 31.1, and 128 over 4000 156 and 159: whole units fit there). Up to `planned` keys the units stay whole (4
-// single tokens of 16 heads over 256 keys 13.3, as ranges 15.2; over 512 17.0 and 15.4).
+// not, 16 single tokens of 16 heads over 2000 keys 23.1 and 18.8, 8 of 128 heads over 8000 46.9 and 40.8, 128 of 16
+// over 500 25.3 and 23.7; of pairs with up to 32 sequences (64 single tokens of 128 heads over 300 keys 26.7 and
+// 29.8, and 128 over 4000 159 and 165: whole units fit there; but 33 over 2000 46.1 and 42.7). Up to `planned` keys
+// the units stay whole (4 single tokens of 16 heads over 256 keys 13.3, as ranges 15.2; over 512 17.0 and 15.4).
 struct Whole {
   int planned, own;
 };

@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const ChunkArg
   // Whole units by falling length, the CTAs taking them in turn there and back, where the longest of the CTAs'
   // sums is at most `whole`: cuts cost a CTA two parts, another start and the merge, cut_tiles tiles or more,
   // and units that share keys run at the same time. Whole and cut, us on the device, with that longest sum and
-  // the range, in tiles: absorbed, 8 sequences of 100 tokens of 32 heads over 2000 keys (26, 25) 89 and 100,
-  // but 60 of 2 tokens of 64 heads (16, 10) 68 and 62, 16 of 3 of 32 heads over 1000 (8, 2) 38 and 30;
-  // expanded, 16 of 400 of 32 heads over 6000 (216, 204) 400 and 454, 6 of 500 of 16 over 2000 (20, 14) 49 and
-  // 58, but one of 1000 over 2000 (16, 6) 38 and 33. The sort takes 1 to 2 us.
+  // the range, in tiles: absorbed, 8 sequences of 100 tokens of 32 heads over 2000 keys (26, 25) 92 and 102,
+  // but 60 of 2 tokens of 64 heads (16, 10) 71 and 63; expanded, 16 of 400 of 32 heads over 6000 (216, 204) 400
+  // and 454, 6 of 500 of 16 over 2000 (20, 14) 49 and 58, but one of 1000 over 2000 (16, 6) 38 and 33. The sort
+  // takes 1 to 2 us.
   const int whole = per + per / 8 + p.cut_tiles;
   if (p.order && units > 0 && units <= kOwnUnits * p.ctas && longest <= whole && longest < kLengths) {
     __shared__ int place_of[kLengths], span;

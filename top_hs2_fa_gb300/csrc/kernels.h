@@ -176,7 +176,7 @@ struct LatentKeys {
 constexpr int kOwnPlanSeqs = 32, kOwnPlanUnits = 16;
 constexpr int line_seqs(bool pair) { return pair ? 32 : 128; }
 struct ChunkPlan {
-  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units, [3] whether `order` is what the CTAs follow
+  int32_t* head;       // [0] tiles in all, [1] tiles per CTA, [2] cut units, [3] units in `order`, which the CTAs then follow; 0: ranges of the line
   int32_t* cta_first;  // [ctas] the unit at each CTA's range start
   int32_t* cta_begin;  // [ctas] the range start
   int32_t* cuts;       // [ctas] units that a range border cuts: one per border at most

@@ -53,9 +53,9 @@ template <int DC, int N>
 struct LatentSmem {
   static constexpr int PIECES = DC / 128;  // of a tile
   static constexpr int BLOCKS = DC / 64 + 1;
-  // what 227 KB hold beside Q
-  static constexpr int RING = DC == 512 ? (N == 64 ? 4 : 5) : (N == 64 ? 4 : 5);
-  static constexpr int ROT = DC == 512 ? (N == 64 ? 1 : N == 32 ? 1 : 2) : 2;
+  // what 227 KB hold beside Q (of 256 channels: less than three tiles' pieces, see below)
+  static constexpr int RING = N == 64 ? 4 : 5;
+  static constexpr int ROT = DC == 512 && N >= 32 ? 1 : 2;
   static constexpr int O_BUFS = N == 64 ? 1 : 2;  // by the parity of the unit
   static constexpr int GROUPS = N == 64 ? 4 : 2;  // of four softmax warps, N / GROUPS rows each
   static constexpr int THREADS = 128 * (1 + GROUPS);
@@ -75,8 +75,7 @@ struct LatentSmem {
 }  // namespace
 
 // PAIR: CTAs 2i and 2i + 1 take rows [0, 64) and [64, 128) of the units of range i. The second walks a unit's tiles
-// also where it has no such rows: where it went ahead to its next unit the two no longer met in L2 (mixed batch
-// 248 us against 239).
+// also where it has no such rows: going ahead to its next unit instead took longer (mixed batch 248 us against 239).
 template <int DC, int N, bool PAIR>
 __global__ void __launch_bounds__(LatentSmem<DC, N>::THREADS, 1)
     latent_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k, const ChunkArgs a,

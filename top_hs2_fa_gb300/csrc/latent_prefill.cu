@@ -19,6 +19,7 @@
 //               mix, and both halves' softmaxes run at the same time: 5150 cycles a tile of 2560.)
 //   warps 4-11, 12-19  softmax of half a, b: a row is two threads', 64 keys of the tile each. The reference
 //               that they share moves only when it is exceeded by 2^8
+// The 96 registers of the launch leave 72 bytes of spill stores a thread.
 // TMEM: S of a [0,128), of b [128,256), O of a [256,384), of b [384,512). Every wait is bounded.
 #include <cuda.h>
 

@@ -7,8 +7,11 @@
 // the heads of K and V and then those of Q, 512 channels a step and of Q two steps' loads at a time.
 // 32768 rows of 32 heads over 4, d = 128, bf16 to FP8 (653 MB): 120 us, 0.80 of the copy bandwidth; with K, V
 // and Q in one loop 163 (16 warps an SM: the registers of the quantisation), with more warps at fewer
-// registers 148 and 167. 26273 latent rows of 512 + 64 with 32 heads (282 MB): 60 us, 0.69, the queries' 128
-// bytes a head at a stride of 384 in and 1152 out; 73 with 16 channels in a row per lane.
+// registers 148 and 167. The same to FP4 123, without the queries 43. 26273 latent rows of 512 + 64 with 32
+// heads (282 MB): 60 us, 0.69; HBM is 47 % busy, a third of the warps fit and wait for their loads, and at the 80
+// registers that three blocks an SM leave the two-row form spills (84 bytes stored and 40 loaded a thread, other
+// types up to 164 and 120); the queries are 128 bytes a head at a stride of 384 in and 1152 out. 73 us with 16 channels
+// in a row per lane.
 #include "kv_rows.cuh"
 #include "rot.cuh"
 
